@@ -23,6 +23,12 @@ from .api import (  # noqa: F401
     fa_lse_merge,
     fa_num_splits_heuristic,
     fa_num_splits_prefill,
+    fa_paged_plan,
+    fa_rope,
+    fa_rope_append_paged,
+    fa_rope_bwd,
+    fa_rope_inv_freq,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
+    fa_tree_mask,
 )

@@ -27,6 +27,11 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _ULL = ctypes.c_ulonglong
+_D = ctypes.c_double
+
+FA_DTYPE_BF16 = 0
+FA_DTYPE_F32 = 1
+FA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # name -> (restype, argtypes); mirrors include/fa_gb300.h
 SIGNATURES = {
@@ -49,6 +54,15 @@ SIGNATURES = {
     "fa_decode_paged": (
         _I,
         [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _SZ, _P],
+    ),
+    "fa_paged_plan": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "fa_tree_mask": (_I, [_P, _P, _P, _P, _P, _I, _I, _P]),
+    "fa_rope_inv_freq": (_I, [_P, ctypes.POINTER(_F), _I, _D, _I, _D, _D, _D, _D]),
+    "fa_rope": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_rope_append_paged": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     ),
     "fa_get_last_device_error": (_I, [_P, ctypes.POINTER(_I)]),
     "fa_set_wait_timeout_ns": (None, [_ULL]),

@@ -13,7 +13,7 @@ import math
 
 import torch
 
-from ._lib import FAError, check, lib
+from ._lib import FA_DTYPE_BF16, FA_DTYPE_F32, FA_ROPE_SCALINGS, FAError, check, lib
 
 
 def _ptr(t: torch.Tensor | None):
@@ -287,6 +287,182 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bool = Tr
     return o, lse
 
 
+def _need_ints(name: str, t: torch.Tensor, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) \
+            or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+
+
+def fa_paged_plan(cached_lens, new_lens, free_pages, block_table, T: int, align_end: bool = False, seqlens=None,
+                  slots=None, positions=None, pages_used=None):
+    """Block tables, slot maps and positions of a step: cached_lens, new_lens [B], free_pages [F],
+    block_table [B][max_pages] (extended in place), all int32 on one device
+    -> (seqlens [B], slots [B][T], positions [B][T], pages_used [1])."""
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(cached_lens, "cached_lens", torch.int32, 1)
+    _need(free_pages, "free_pages", torch.int32, 1)
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    _need_ints("cached_lens", cached_lens, (B,), dev)
+    _need_ints("new_lens", new_lens, (B,), dev)
+    if free_pages.device != dev:
+        raise ValueError(f"free_pages must be on {dev}")
+    _on_current_device(block_table)
+    T = int(T)
+    seqlens = _out(seqlens, "seqlens", (B,), torch.int32, block_table)
+    slots = _out(slots, "slots", (B, T), torch.int32, block_table)
+    positions = _out(positions, "positions", (B, T), torch.int32, block_table)
+    pages_used = _out(pages_used, "pages_used", (1,), torch.int32, block_table)
+    st = lib().fa_paged_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_pages), free_pages.shape[0],
+                             _ptr(block_table), _ptr(seqlens), _ptr(slots), _ptr(positions), _ptr(pages_used), B, T,
+                             max_pages, 16, int(align_end), _stream(block_table))
+    check(st, "fa_paged_plan")
+    return seqlens, slots, positions, pages_used
+
+
+def fa_tree_mask(parents, seqlens, tree_lens=None, mask=None, positions=None):
+    """Visibility mask and positions of drafted trees: parents [B][T], seqlens [B], tree_lens [B] or
+    None (T nodes each), int32 -> (mask [B][T][ceil(T/32)] int32, positions [B][T] int32)."""
+    _need(parents, "parents", torch.int32, 2)
+    B, T = parents.shape
+    _need_ints("seqlens", seqlens, (B,), parents.device)
+    if tree_lens is not None:
+        _need_ints("tree_lens", tree_lens, (B,), parents.device)
+    _on_current_device(parents)
+    mask = _out(mask, "mask", (B, T, (T + 31) // 32), torch.int32, parents)
+    positions = _out(positions, "positions", (B, T), torch.int32, parents)
+    st = lib().fa_tree_mask(_ptr(parents), _ptr(seqlens), _ptr(tree_lens), _ptr(mask), _ptr(positions), B, T,
+                            _stream(parents))
+    check(st, "fa_tree_mask")
+    return mask, positions
+
+
+def fa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Angles per position of rot_dim / 2 rotary pairs, stretched for long contexts by scaling in
+    {"none", "linear", "ntk", "yarn"} -> (inv_freq fp64 on device, mscale)."""
+    if scaling not in FA_ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(FA_ROPE_SCALINGS)}, got {scaling!r}")
+    rot_dim = int(rot_dim)
+    host = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
+    mscale = ctypes.c_float(1.0)
+    st = lib().fa_rope_inv_freq(_ptr(host), ctypes.byref(mscale), rot_dim, float(base), FA_ROPE_SCALINGS[scaling],
+                                float(factor), float(original_len), float(beta_fast), float(beta_slow))
+    check(st, "fa_rope_inv_freq")
+    return host.to(device), mscale.value
+
+
+_ROPE_DTYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float32: FA_DTYPE_F32}
+_Strides = ctypes.c_longlong * 12
+
+
+def _need_rows(t, name: str, dtype, device, shape=None):
+    """A [B][heads][T][d] operand whose rows of d are dense; the strides between rows are free."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 4 or t.device != device or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a 4-D {dtype} tensor on {device} whose last stride is 1")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows_out(t, name: str, like: torch.Tensor):
+    """A caller's output of like's shape, no two of its rows on one another, or a new dense one."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _need_rows(t, name, like.dtype, like.device, like.shape)
+    if not t.is_contiguous():
+        reach = t.shape[3]  # values up to the end of the rows of the dimensions so far
+        for stride, size in sorted((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1):
+            if stride < reach:
+                raise ValueError(f"{name} has rows that overlap (shape {tuple(t.shape)}, strides {t.stride()})")
+            reach += stride * (size - 1)
+    return t
+
+
+def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool) -> int:
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != device \
+            or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous int32 tensor on {device}")
+    shape = tuple(positions.shape)
+    if shape != (B, T) and not (shared_ok and shape == (T,)):
+        raise ValueError(f"positions must be [{B}][{T}]{f' or [{T}]' if shared_ok else ''}, got {shape}")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.device != device \
+            or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {device} (fa_rope_inv_freq)")
+    return len(shape)
+
+
+def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out):
+    if not isinstance(q, torch.Tensor) or q.dtype not in _ROPE_DTYPES:
+        raise ValueError(f"{name}: q must be a bfloat16 or float32 tensor")
+    dev = q.device
+    _need_rows(q, "q", q.dtype, dev)
+    _on_current_device(q)
+    B, Hq, T, d = q.shape
+    pos_dim = _need_angles(positions, inv_freq, B, T, dev, True)
+    q_out = _rows_out(q_out, "q_out", q)
+    Hk = 0
+    none = (0, 0, 0)
+    sk = sko = none
+    if k is not None:
+        _need_rows(k, "k", q.dtype, dev)
+        Hk = k.shape[1]
+        if k.shape[0] != B or k.shape[2] != T or k.shape[3] != d:
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must share batch, length and head dimension")
+        k_out = _rows_out(k_out, "k_out", k)
+        sk, sko = k.stride()[:3], k_out.stride()[:3]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *sk, *sko)
+    st = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), strides, _ptr(positions), int(pos_dim == 1),
+                              _ptr(inv_freq), B, Hq, Hk, T, d, 2 * inv_freq.shape[0], int(interleaved), mscale,
+                              _ROPE_DTYPES[q.dtype], _stream(q))
+    check(st, name)
+    return q_out, k_out
+
+
+def fa_rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None):
+    """Rotary positions of q [B][Hq][T][d] and k [B][Hk][T][d] (or None), bf16 or fp32, any strides
+    between rows; positions [B][T] or [T] int32, inv_freq [rot/2] fp64 -> (q_out, k_out). Outputs are
+    dense [B][H][T][d] unless given; they may be q and k themselves."""
+    return _rope("fa_rope", q, k, positions, inv_freq, interleaved, mscale, q_out, k_out)
+
+
+def fa_rope_bwd(dq_out, dk_out, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, q_out=None,
+                k_out=None):
+    """Gradients of fa_rope: those of its outputs -> (dq, dk), into q_out and k_out where given."""
+    return _rope("fa_rope_bwd", dq_out, dk_out, positions, inv_freq, interleaved, mscale, q_out, k_out)
+
+
+def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved: bool = False,
+                         mscale: float = 1.0, q_out=None):
+    """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
+    and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
+    bf16 = torch.bfloat16
+    dev = q.device
+    _need_rows(q, "q", bf16, dev)
+    B, Hq, T, d = q.shape
+    _need(k_pages, "k_pages", bf16, 4)
+    _need(v_pages, "v_pages", bf16, 4)
+    P, page_size, Hkv, _ = k_pages.shape
+    if tuple(v_pages.shape) != tuple(k_pages.shape) or k_pages.shape[3] != d or k_pages.device != dev \
+            or v_pages.device != dev:
+        raise ValueError(f"k_pages and v_pages must both be [P][page_size][Hkv][{d}] on {dev}")
+    _need_rows(k, "k", bf16, dev, (B, Hkv, T, d))
+    _need_rows(v, "v", bf16, dev, (B, Hkv, T, d))
+    _on_current_device(q)
+    _need_angles(positions, inv_freq, B, T, dev, False)
+    _need_ints("slots", slots, (B, T), dev)
+    q_out = _rows_out(q_out, "q_out", q)
+    strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+    st = lib().fa_rope_append_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), strides, _ptr(positions), _ptr(slots),
+                                    _ptr(inv_freq), _ptr(k_pages), _ptr(v_pages), B, Hq, Hkv, T, page_size, P, d,
+                                    2 * inv_freq.shape[0], int(interleaved), mscale, _stream(q))
+    check(st, "fa_rope_append_paged")
+    return q_out
+
+
 def fa_get_last_device_error(device=None) -> tuple[int, int]:
     """Synchronise the current stream and read/clear the device error word -> (status, raw word)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -326,6 +502,12 @@ __all__ = [
     "fa_decode_splitkv_static",
     "fa_lse_merge",
     "fa_decode_paged",
+    "fa_paged_plan",
+    "fa_tree_mask",
+    "fa_rope_inv_freq",
+    "fa_rope",
+    "fa_rope_bwd",
+    "fa_rope_append_paged",
     "fa_get_last_device_error",
     "fa_set_wait_timeout_ns",
     "fa_get_wait_timeouts",

@@ -33,6 +33,14 @@ enum ErrSite : unsigned {
   SITE_KO_MMA = 13,
   SITE_KO_UPDATE = 14,
   SITE_BW_SMEM = 15,
+  SITE_PLAN = 16,
+  SITE_TREE_MASK = 17,
+  SITE_APPEND = 18,
+  SITE_TR_PRODUCER = 19,
+  SITE_TR_MMA = 20,
+  SITE_TR_SOFTMAX = 21,
+  SITE_TR_TABLE = 22,
+  SITE_TR_SMEM = 23,
 };
 
 __device__ __forceinline__ void record_error(unsigned* err, unsigned code, unsigned site) {

@@ -1,0 +1,38 @@
+// launch.cuh -- host-side launch helper shared by the cache and position kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace fa {
+
+// Accessors defined in api.cu.
+unsigned* device_error_word();
+int device_sm_count();
+unsigned long long wait_timeout_ns();
+
+// Launches `kfn` as a programmatic dependent of the launch before it on `stream`:
+// the kernel executes griddepcontrol.wait before its first global access.
+template <typename... KArgs, typename... Args>
+inline int launch_dependent(void (*kfn)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                            const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, args...);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  return launch_status();
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Only after pdl_wait(): a dependent launched early must not see the grid before this
+// one as complete while it still runs.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace fa

@@ -1,0 +1,230 @@
+// paged_plan.cu -- what a step over the paged cache needs before its first kernel:
+// block tables, slot maps and positions from request lengths, and the visibility
+// mask and positions of a tree of drafted tokens from its parent indexes.
+//
+// fa_paged_plan. Sequence b holds c = cached[b] tokens and gets n = new_lens[b] more.
+// It holds have = ceil(c / 16) pages and needs want = ceil((c + n) / 16). The pages
+// come from the front of the free list, sequence by sequence:
+//   block_table[b][have + i] = free_pages[first_b + i],  i < want - have,
+//   first_b = sum over b' < b of (want_b' - have_b').
+// The new token at position p = c + t goes to slot block_table[b][p / 16] * 16 + p % 16.
+//
+// How: one launch without any exchange between blocks. A block owns SEQS sequences
+// (one warp each) and sums the needs of every sequence before them by itself: 2 * B
+// lengths from L2, which for some thousand sequences costs less than a second launch
+// or a chain of flags between blocks. The slot of a token on a new page is formed from
+// the free list and not from the table entry that some warp is writing at that moment,
+// so blocks that share a sequence (blockIdx.y cuts long chunks) need no order. Bound by
+// launch latency for decode steps, by the 8 bytes written per token for prefill steps.
+//
+// fa_tree_mask. sees(i) = {i} + sees(parent(i)). One thread per node walks up the
+// parents in shared memory; as parent(i) < i the visited bits fall, so the thread
+// keeps one 32-bit word and stores it (and the empty ones it skips) when the walk
+// leaves it.
+#include "launch.cuh"
+
+namespace fa {
+
+constexpr int kPage = 16;
+constexpr int kPlanSeqs = 8;          // sequences per block, one warp each
+constexpr int kPlanThreads = kPlanSeqs * 32;
+constexpr int kPlanChunk = 512;       // tokens of a sequence per block
+
+struct PlanParams {
+  const int* cached;
+  const int* new_lens;
+  const int* free_pages;
+  int* block_table;
+  int* seqlens;
+  int* slots;
+  int* positions;
+  int* pages_used;
+  int B, T, max_pages, num_free, align_end;
+  unsigned* err;
+};
+
+// A sequence's lengths, clamped to what its table row and the T rows of a step hold.
+struct PlanSeq {
+  int c, n;
+  bool clamped;
+};
+__device__ __forceinline__ PlanSeq plan_seq(const PlanParams& p, int b) {
+  const int cap = p.max_pages * kPage;
+  const int c0 = __ldg(p.cached + b), n0 = __ldg(p.new_lens + b);
+  PlanSeq s;
+  s.c = max(0, min(c0, cap));
+  s.n = max(0, min(n0, min(p.T, cap - s.c)));
+  s.clamped = s.c != c0 || s.n != n0;
+  return s;
+}
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPage - 1) / kPage; }
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
+  __shared__ int partial[kPlanSeqs];
+  pdl_wait();
+  pdl_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b0 = blockIdx.x * kPlanSeqs;
+  const int b = b0 + warp;
+  // needs of every sequence before this block's, then of the block's own before this warp's
+  int sum = 0;
+  for (int i = threadIdx.x; i < b0; i += kPlanThreads) {
+    const PlanSeq s = plan_seq(p, i);
+    sum += pages_of(s.c + s.n) - pages_of(s.c);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) partial[warp] = sum;
+  __syncthreads();
+  int before = lane < kPlanSeqs ? partial[lane] : 0;
+  if (lane < warp && b0 + lane < p.B) {
+    const PlanSeq s = plan_seq(p, b0 + lane);
+    before += pages_of(s.c + s.n) - pages_of(s.c);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (b >= p.B) return;
+  const PlanSeq s = plan_seq(p, b);
+  const int have = pages_of(s.c), want = pages_of(s.c + s.n);
+  int* row = p.block_table + static_cast<size_t>(b) * p.max_pages;
+  if (blockIdx.y == 0) {
+    bool short_of = s.clamped;
+    for (int i = lane; i < want - have; i += 32) {
+      const int at = before + i;
+      const bool ok = at < p.num_free;
+      short_of |= !ok;
+      row[have + i] = ok ? __ldg(p.free_pages + at) : -1;
+    }
+    if (short_of) record_error(p.err, FA_ERR_BOUNDS, SITE_PLAN);
+    if (lane == 0) {
+      p.seqlens[b] = s.c + s.n;
+      if (b == p.B - 1) *p.pages_used = before + want - have;
+    }
+  }
+  // rows of the step: token t sits in row t, or (align_end) in row T - n + t
+  const int lead = p.align_end ? p.T - s.n : 0;
+  const int t0 = blockIdx.y * kPlanChunk;
+  const int t1 = min(p.T, t0 + kPlanChunk);
+  const size_t out = static_cast<size_t>(b) * p.T;
+  for (int r = t0 + lane; r < t1; r += 32) {
+    const int t = r - lead;
+    int slot = -1, pos = 0;
+    if (t >= 0 && t < s.n) {
+      pos = s.c + t;
+      const int pg = pos / kPage;
+      int page;
+      if (pg < have) {
+        page = row[pg];  // an entry that no block of this launch writes
+      } else {
+        const int at = before + pg - have;
+        page = at < p.num_free ? __ldg(p.free_pages + at) : -1;
+      }
+      slot = page >= 0 ? page * kPage + pos % kPage : -1;
+    }
+    p.slots[out + r] = slot;
+    p.positions[out + r] = pos;
+  }
+}
+
+constexpr int kTreeMaxNodes = 8192;  // parents of one sequence in shared memory
+
+__global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ parents,
+                                                        const int* __restrict__ seqlens,
+                                                        const int* __restrict__ tree_lens, int* __restrict__ mask,
+                                                        int* __restrict__ positions, int T, unsigned* err) {
+  extern __shared__ int up[];
+  pdl_wait();
+  pdl_launch();
+  const int b = blockIdx.y;
+  const int first = blockIdx.x * blockDim.x;
+  const int last = min(T, first + static_cast<int>(blockDim.x));  // nodes before it are all a walk from here visits
+  const int S = max(0, __ldg(seqlens + b));
+  const int n = max(0, min(tree_lens ? __ldg(tree_lens + b) : T, min(T, S)));
+  const int* prow = parents + static_cast<size_t>(b) * T;
+  for (int i = threadIdx.x; i < min(last, n); i += blockDim.x) {
+    const int q = __ldg(prow + i);
+    const bool ok = q >= -1 && q < i;  // anything else would not be a tree: the node becomes a root
+    if (!ok) record_error(err, FA_ERR_BOUNDS, SITE_TREE_MASK);
+    up[i] = ok ? q : -1;
+  }
+  __syncthreads();
+  const int i = first + threadIdx.x;
+  if (i >= T) return;
+  const int words = (T + 31) / 32;
+  int* out = mask + (static_cast<size_t>(b) * T + i) * words;
+  int at_word = words - 1;
+  unsigned cur = 0;
+  int depth = -1;
+  for (int at = i < n ? i : -1; at >= 0; at = up[at], ++depth) {
+    const int w = at >> 5;
+    for (; at_word > w; --at_word) {
+      out[at_word] = static_cast<int>(cur);
+      cur = 0;
+    }
+    cur |= 1u << (at & 31);
+  }
+  for (; at_word >= 0; --at_word) {
+    out[at_word] = static_cast<int>(cur);
+    cur = 0;
+  }
+  positions[static_cast<size_t>(b) * T + i] = i < n ? S - n + depth : 0;
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_pages, int num_free, int* block_table,
+                        int* seqlens, int* slots, int* positions, int* pages_used, int B, int T, int max_pages,
+                        int page_size, int align_end, void* stream) {
+  auto bad = [](const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 3u); };
+  if (bad(cached) || bad(new_lens) || bad(block_table) || bad(seqlens) || bad(slots) || bad(positions) ||
+      bad(pages_used))
+    return FA_ERR_INVALID_ARG;
+  if (num_free < 0 || (num_free > 0 && bad(free_pages))) return FA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page_size != kPage) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * T >= (1ll << 31) || static_cast<long long>(B) * max_pages >= (1ll << 31) ||
+      static_cast<long long>(max_pages) * kPage >= (1ll << 31) || T > 65535ll * kPlanChunk)
+    return FA_ERR_UNSUPPORTED;
+  PlanParams p;
+  p.cached = cached;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.slots = slots;
+  p.positions = positions;
+  p.pages_used = pages_used;
+  p.B = B;
+  p.T = T;
+  p.max_pages = max_pages;
+  p.num_free = num_free;
+  p.align_end = align_end ? 1 : 0;
+  p.err = device_error_word();
+  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  const dim3 grid((B + kPlanSeqs - 1) / kPlanSeqs, (T + kPlanChunk - 1) / kPlanChunk);
+  return static_cast<fa_status>(
+      launch_dependent(paged_plan_kernel, grid, dim3(kPlanThreads), 0, static_cast<cudaStream_t>(stream), p));
+}
+
+fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_lens, int* mask, int* positions, int B,
+                       int T, void* stream) {
+  auto bad = [](const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 3u); };
+  if (bad(parents) || bad(seqlens) || bad(mask) || bad(positions) || (tree_lens && bad(tree_lens)))
+    return FA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1) return FA_ERR_INVALID_ARG;
+  if (B > 65535 || T > kTreeMaxNodes) return FA_ERR_UNSUPPORTED;
+  unsigned* err = device_error_word();
+  if (!err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  const int threads = T >= 128 ? 128 : (T + 31) / 32 * 32;
+  const dim3 grid((T + threads - 1) / threads, B);
+  return static_cast<fa_status>(launch_dependent(tree_mask_kernel, grid, dim3(threads),
+                                                 static_cast<size_t>(T) * sizeof(int),
+                                                 static_cast<cudaStream_t>(stream), parents, seqlens, tree_lens, mask,
+                                                 positions, T, err));
+}
+
+}  // extern "C"

@@ -1,0 +1,382 @@
+// rope.cu -- rotary positions, forward and backward, and the same on the way into a
+// paged K/V cache.
+//
+// Pair i of a row at position p, (a, b), becomes
+//   (a cos t - b sin t, b cos t + a sin t) * mscale,  t = p * inv_freq[i];
+// the gradient is the transpose, the same with -t. Pairs are (x[i], x[i + rot/2])
+// ("half") or (x[2i], x[2i+1]) ("interleaved"), i < rot/2; values from rot on pass
+// through.
+//
+// Angles. A far position needs t to a small part of 2 pi, which p * inv_freq in 32
+// bits has not (at p = 10^6 it is off by 0.06). Here inv_freq / (2 pi) is a 64-bit
+// fraction of a turn, so the integer product p * that, modulo 2^64, IS the angle
+// modulo a turn, off by at most |p| * 2^-64 turns; its upper 32 bits go to sincospif.
+// No table of cosines, no largest position, no FP64 pipe (which is narrow here).
+//
+// How: bound by reading and writing each value once. A lane owns VEC pairs of a token
+// (16 bytes on each side) and makes their sines once, then walks over a chunk of the
+// token's heads, U of them in flight. A row's d * 2 bytes are whole 128-byte lines for
+// the layouts that matter, whatever the strides between rows, so no transpose through
+// shared memory is needed to go between [B][T][heads][d] and [B][heads][T][d].
+// Inputs whose rows are not whole aligned vectors take VEC = 1 (one pair, plain loads).
+#include <math.h>
+
+#include "launch.cuh"
+
+namespace fa {
+
+// One operand: rows [b][h][t], `heads` of them a token, strides in elements.
+struct RopeSide {
+  const void* src;
+  void* dst;
+  long long sb, sh, st;  // source strides
+  long long db, dh, dt;  // destination strides (unused where rows go to slots)
+  int heads;
+};
+
+struct RopeParams {
+  RopeSide q, k, v;         // v.heads = 0 but for appends
+  const int* positions;
+  long long pos_sb;         // 0: one row of positions for the whole batch
+  const double* inv_freq;
+  const int* slots;         // appends: k and v rows go to slot * slot_stride + head * d
+  long long slot_stride;
+  int num_slots;
+  long long tokens;         // B * T
+  int T, d, rot, lanes, head_chunk;
+  float mscale, sign;       // sign -1: the transposed rotation
+  unsigned* err;
+};
+
+template <typename E>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+};
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+};
+
+// VEC values at p as floats; VEC = 1 or a 16-byte vector
+template <typename E, int VEC>
+struct Pack {
+  float v[VEC];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (VEC == 1) {
+      v[0] = static_cast<float>(*p);
+    } else if constexpr (sizeof(E) == 2) {
+      const uint4 r = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+      const float4 r = *reinterpret_cast<const float4*>(p);
+      v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+    }
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (VEC == 1) {
+      *p = static_cast<E>(v[0]);
+    } else if constexpr (sizeof(E) == 2) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+};
+
+// f / (2 pi) modulo 1 as a 64-bit fraction, from the double's bits: its 53-bit mantissa
+// times floor(2^64 / (2 pi)), shifted by its exponent.
+__device__ __forceinline__ unsigned long long turns_of(double f) {
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(f));
+  const int e = static_cast<int>((bits >> 52) & 0x7ff);
+  if (e == 0) return 0;  // zero (a denormal's turn is far below 2^-64)
+  const unsigned long long m = (bits & 0xfffffffffffffull) | (1ull << 52);
+  constexpr unsigned long long kInv2Pi = 0x28BE60DB9391054Aull;
+  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int s = 1075 - e;  // f = m * 2^-s
+  unsigned long long r;
+  if (s <= 0)
+    r = s > -64 ? lo << -s : 0;
+  else if (s < 64)
+    r = (lo >> s) | (hi << (64 - s));
+  else
+    r = s < 128 ? hi >> (s - 64) : 0;
+  return (bits >> 63) ? 0ull - r : r;
+}
+
+template <typename E, int VEC, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+  pdl_wait();
+  pdl_launch();
+  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long token = id / p.lanes;
+  const int lane = static_cast<int>(id - token * p.lanes);
+  if (token >= p.tokens) return;
+  const int b = static_cast<int>(token / p.T);
+  const int t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+  const int half = p.rot / 2;
+  const bool turn = lane * VEC < half;  // else: the lane copies two vectors of the tail
+  int o0, o1;                           // the lane's two vectors in a row
+  bool two = true;
+  float c[VEC], s[VEC];
+  if (turn) {
+    const int i = lane * VEC;
+    o0 = INTER ? 2 * i : i;
+    o1 = INTER ? 2 * i + VEC : i + half;
+    const long long pos = __ldg(p.positions + b * p.pos_sb + t);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const unsigned long long a = static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + i + e));
+      // the signed upper half, in half turns
+      sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);
+      c[e] *= p.mscale;
+      s[e] *= p.mscale * p.sign;
+    }
+  } else {
+    o0 = p.rot + (lane - half / VEC) * 2 * VEC;
+    o1 = o0 + VEC;
+    two = o1 < p.d;
+  }
+  const int h_begin = blockIdx.y * p.head_chunk;
+  const int h_end = min(h_begin + p.head_chunk, p.q.heads + p.k.heads + p.v.heads);
+
+  long long slot = 0;
+  if (APPEND && h_end > p.q.heads) {
+    slot = __ldg(p.slots + token);
+    if (slot < -1 || slot >= p.num_slots) {
+      record_error(p.err, FA_ERR_BOUNDS, SITE_APPEND);
+      slot = -1;
+    }
+  }
+
+  // heads [h0, h1) of one operand, U rows in flight
+  auto rows = [&](const RopeSide& side, int h0, int h1, bool to_slot, bool rotate) {
+    const E* src = static_cast<const E*>(side.src) + b * side.sb + t * side.st;
+    E* dst = static_cast<E*>(side.dst) + (to_slot ? slot * p.slot_stride : b * side.db + t * side.dt);
+    const long long dh = to_slot ? p.d : side.dh;
+    constexpr int U = VEC == 1 ? 2 : 4;
+    for (int h = h0; h < h1; h += U) {
+      Pack<E, VEC> x[U], y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u < h1) {
+          x[u].load(src + (h + u) * side.sh + o0);
+          if (two) y[u].load(src + (h + u) * side.sh + o1);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u < h1) {
+          if (rotate) {
+            // the pair's two values: element e of x and y, or neighbours 2e, 2e + 1 of x then y
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              float& a = !INTER ? x[u].v[e] : (2 * e < VEC ? x[u].v[(2 * e) % VEC] : y[u].v[(2 * e) % VEC]);
+              float& g = !INTER ? y[u].v[e]
+                                : (2 * e + 1 < VEC ? x[u].v[(2 * e + 1) % VEC] : y[u].v[(2 * e + 1) % VEC]);
+              const float a0 = a, g0 = g;
+              a = a0 * c[e] - g0 * s[e];
+              g = g0 * c[e] + a0 * s[e];
+            }
+          }
+          x[u].store(dst + (h + u) * dh + o0);
+          if (two) y[u].store(dst + (h + u) * dh + o1);
+        }
+    }
+  };
+  const int hq = p.q.heads, hk = hq + p.k.heads;
+  if (h_begin < hq) rows(p.q, h_begin, min(h_end, hq), false, turn);
+  if (APPEND && slot < 0) return;
+  if (h_begin < hk && h_end > hq) rows(p.k, max(h_begin, hq) - hq, min(h_end, hk) - hq, APPEND, turn);
+  if (APPEND && h_end > hk) rows(p.v, max(h_begin, hk) - hk, h_end - hk, true, false);
+}
+
+static bool strides_ok(const RopeSide& s, int vec, bool slots) {
+  auto whole = [vec](long long x) { return x % vec == 0; };
+  return whole(s.sb) && whole(s.sh) && whole(s.st) && (slots || (whole(s.db) && whole(s.dh) && whole(s.dt))) &&
+         (reinterpret_cast<uintptr_t>(s.src) & 15u) == 0 && (reinterpret_cast<uintptr_t>(s.dst) & 15u) == 0;
+}
+
+template <typename E, bool APPEND>
+static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
+  constexpr int V = Vec16<E>::N;
+  // whole vectors on both sides of every pair, in the tail and in every row's start
+  const bool vec = (p.rot / 2) % V == 0 && p.d % V == 0 && strides_ok(p.q, V, false) &&
+                   (p.k.heads == 0 || strides_ok(p.k, V, APPEND)) && (p.v.heads == 0 || strides_ok(p.v, V, true));
+  const int w = vec ? V : 1;
+  p.lanes = p.rot / 2 / w + ((p.d - p.rot) / w + 1) / 2;
+  const int heads = p.q.heads + p.k.heads + p.v.heads;
+  const long long lanes = p.tokens * p.lanes;
+  if ((lanes + 255) / 256 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  // Heads per lane: as many as leave the SMs their threads, so that a lane's sines serve
+  // many rows, but not more than 16.
+  const long long room = static_cast<long long>(device_sm_count()) * 1024;
+  long long chunk = lanes * heads / room;
+  chunk = chunk < 1 ? 1 : (chunk > 16 ? 16 : chunk);
+  if (chunk > 4) chunk = chunk / 4 * 4;
+  while ((heads + chunk - 1) / chunk > 65535) chunk *= 2;
+  p.head_chunk = static_cast<int>(chunk);
+  const dim3 grid(static_cast<unsigned>((lanes + 255) / 256), static_cast<unsigned>((heads + chunk - 1) / chunk));
+  if (vec)
+    return interleaved ? launch_dependent(rope_kernel<E, V, true, APPEND>, grid, dim3(256), 0, stream, p)
+                       : launch_dependent(rope_kernel<E, V, false, APPEND>, grid, dim3(256), 0, stream, p);
+  return interleaved ? launch_dependent(rope_kernel<E, 1, true, APPEND>, grid, dim3(256), 0, stream, p)
+                     : launch_dependent(rope_kernel<E, 1, false, APPEND>, grid, dim3(256), 0, stream, p);
+}
+
+static bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// The stride of a dimension of one is never used; callers leave anything there.
+static RopeSide side_of(const void* src, void* dst, const long long* s, const long long* d, int B, int heads, int T) {
+  RopeSide r = {};
+  r.src = src;
+  r.dst = dst;
+  r.heads = heads;
+  r.sb = B > 1 ? s[0] : 0;
+  r.sh = heads > 1 ? s[1] : 0;
+  r.st = T > 1 ? s[2] : 0;
+  if (d) {
+    r.db = B > 1 ? d[0] : 0;
+    r.dh = heads > 1 ? d[1] : 0;
+    r.dt = T > 1 ? d[2] : 0;
+  }
+  return r;
+}
+
+static fa_status check_rope(const void* q, const void* q_out, const int* positions, const double* inv_freq, int B,
+                            int Hq, int Hk, int T, int d, int rot_dim, float mscale, unsigned elem) {
+  if (!q || !q_out || !positions || !inv_freq) return FA_ERR_INVALID_ARG;
+  if (misaligned(q, elem) || misaligned(q_out, elem) || misaligned(positions, 4) || misaligned(inv_freq, 8))
+    return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hk < 0 || T < 1 || d < 2 || rot_dim < 2 || (rot_dim & 1) || rot_dim > d)
+    return FA_ERR_INVALID_ARG;
+  if (!isfinite(mscale) || mscale <= 0.f) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * T >= (1ll << 31) || d > 1024 || Hq > 65535 || Hk > 65535) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+static fa_status rope_any(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                          const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk,
+                          int T, int d, int rot_dim, int interleaved, float mscale, int dtype, float sign,
+                          void* stream) {
+  if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_F32) return FA_ERR_UNSUPPORTED;
+  const unsigned elem = dtype == FA_DTYPE_F32 ? 4 : 2;
+  const fa_status st = check_rope(q, q_out, positions, inv_freq, B, Hq, Hk, T, d, rot_dim, mscale, elem);
+  if (st != FA_OK) return st;
+  if (!strides || (Hk > 0 && (!k || !k_out || misaligned(k, elem) || misaligned(k_out, elem))))
+    return FA_ERR_INVALID_ARG;
+  RopeParams p = {};
+  p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
+  if (Hk > 0) p.k = side_of(k, k_out, strides + 6, strides + 9, B, Hk, T);
+  p.positions = positions;
+  p.pos_sb = positions_shared ? 0 : T;
+  p.inv_freq = inv_freq;
+  p.tokens = static_cast<long long>(B) * T;
+  p.T = T;
+  p.d = d;
+  p.rot = rot_dim;
+  p.mscale = mscale;
+  p.sign = sign;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int rc = dtype == FA_DTYPE_F32 ? launch_rope<float, false>(p, interleaved != 0, cs)
+                                       : launch_rope<__nv_bfloat16, false>(p, interleaved != 0, cs);
+  return static_cast<fa_status>(rc);
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, double base, int scaling, double factor,
+                           double original_len, double beta_fast, double beta_slow) {
+  if (!inv_freq || !mscale) return FA_ERR_INVALID_ARG;
+  if (rot_dim < 2 || (rot_dim & 1) || !isfinite(base) || base <= 1.0) return FA_ERR_INVALID_ARG;
+  if (scaling < FA_ROPE_PLAIN || scaling > FA_ROPE_YARN) return FA_ERR_UNSUPPORTED;
+  if (scaling != FA_ROPE_PLAIN && (!isfinite(factor) || factor < 1.0)) return FA_ERR_INVALID_ARG;
+  const int n = rot_dim / 2;
+  const double two_pi = 6.283185307179586476925;
+  *mscale = 1.f;
+  // the base that stretches the longest wave by `factor` and leaves the shortest alone
+  const double b = scaling == FA_ROPE_NTK && n > 1 ? base * pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2)) : base;
+  double low = 0.0, high = 0.0;
+  if (scaling == FA_ROPE_YARN) {
+    if (!isfinite(original_len) || original_len < 1.0 || !isfinite(beta_fast) || !isfinite(beta_slow) ||
+        beta_slow <= 0.0 || beta_fast < beta_slow)
+      return FA_ERR_INVALID_ARG;
+    // the (fractional) pair index whose wave turns r times within the original length
+    auto pair_of = [&](double r) { return rot_dim * log(original_len / (r * two_pi)) / (2.0 * log(base)); };
+    low = floor(pair_of(beta_fast));
+    high = ceil(pair_of(beta_slow));
+    if (low < 0.0) low = 0.0;
+    if (high > rot_dim - 1) high = rot_dim - 1;
+    if (high <= low) high = low + 0.001;
+    if (factor > 1.0) *mscale = static_cast<float>(0.1 * log(factor) + 1.0);
+  }
+  for (int i = 0; i < n; ++i) {
+    double f = pow(b, -2.0 * i / rot_dim);
+    if (scaling == FA_ROPE_LINEAR) f /= factor;
+    if (scaling == FA_ROPE_YARN) {
+      double ramp = (i - low) / (high - low);  // 0: keeps its frequency, 1: stretched by `factor`
+      ramp = ramp < 0.0 ? 0.0 : (ramp > 1.0 ? 1.0 : ramp);
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    }
+    inv_freq[i] = f;
+  }
+  return FA_OK;
+}
+
+fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                  const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk, int T,
+                  int d, int rot_dim, int interleaved, float mscale, int dtype, void* stream) {
+  return rope_any(q, k, q_out, k_out, strides, positions, positions_shared, inv_freq, B, Hq, Hk, T, d, rot_dim,
+                  interleaved, mscale, dtype, 1.f, stream);
+}
+
+fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const long long* strides,
+                      const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk,
+                      int T, int d, int rot_dim, int interleaved, float mscale, int dtype, void* stream) {
+  return rope_any(dq_out, dk_out, dq, dk, strides, positions, positions_shared, inv_freq, B, Hq, Hk, T, d, rot_dim,
+                  interleaved, mscale, dtype, -1.f, stream);
+}
+
+fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void* q_out, const long long* strides,
+                               const int* positions, const int* slots, const double* inv_freq, void* k_pages,
+                               void* v_pages, int B, int Hq, int Hkv, int T, int page_size, int num_pages, int d,
+                               int rot_dim, int interleaved, float mscale, void* stream) {
+  const fa_status st = check_rope(q, q_out, positions, inv_freq, B, Hq, Hkv, T, d, rot_dim, mscale, 2);
+  if (st != FA_OK) return st;
+  if (!strides || !k || !v || !slots || !k_pages || !v_pages || Hkv < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(k_pages, 16) ||
+      misaligned(v_pages, 16))
+    return FA_ERR_INVALID_ARG;
+  if (page_size != 16 || static_cast<long long>(num_pages) * 16 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  RopeParams p = {};
+  p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
+  p.k = side_of(k, k_pages, strides + 6, nullptr, B, Hkv, T);
+  p.v = side_of(v, v_pages, strides + 9, nullptr, B, Hkv, T);
+  p.positions = positions;
+  p.pos_sb = T;
+  p.inv_freq = inv_freq;
+  p.slots = slots;
+  p.slot_stride = static_cast<long long>(Hkv) * d;
+  p.num_slots = num_pages * 16;
+  p.tokens = static_cast<long long>(B) * T;
+  p.T = T;
+  p.d = d;
+  p.rot = rot_dim;
+  p.mscale = mscale;
+  p.sign = 1.f;
+  p.err = device_error_word();
+  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  return static_cast<fa_status>(launch_rope<__nv_bfloat16, true>(p, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

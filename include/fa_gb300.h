@@ -68,8 +68,19 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2, /* valid but not implemented (e.g. head dim not in {64, 128}) */
   FA_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed; see fa_last_cuda_error_string() */
   FA_ERR_TIMEOUT = 4,     /* device side: a bounded wait ran out */
-  FA_ERR_BOUNDS = 5       /* device side: a block-table entry outside [0, num_pages) */
+  FA_ERR_BOUNDS = 5       /* device side: a block-table entry outside [0, num_pages), a length, slot or parent out of range */
 } fa_status;
+
+/* Element types of the calls that take more than one. */
+typedef enum { FA_DTYPE_BF16 = 0, FA_DTYPE_F32 = 1 } fa_dtype;
+
+/* How fa_rope_inv_freq stretches the angles for contexts longer than the trained one. */
+typedef enum {
+  FA_ROPE_PLAIN = 0,  /* base^(-2i / rot_dim) */
+  FA_ROPE_LINEAR = 1, /* every angle / factor (position interpolation) */
+  FA_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is stretched by factor */
+  FA_ROPE_YARN = 3    /* slow pairs / factor, fast pairs kept, a linear ramp between; mscale 0.1 ln factor + 1 */
+} fa_rope_scaling;
 
 /* Library version, major*10000 + minor*100 + patch. */
 FA_API int fa_version(void);
@@ -306,6 +317,102 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
                           int B, int Hq, int Hkv, int T, int max_pages, int page_size,
                           int num_pages, int d, float scale, int causal, int num_splits,
                           void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * fa_paged_plan -- block tables, slot maps and positions of a step over the paged
+ * cache, from its requests' lengths. Sequence b has cached[b] tokens in the cache
+ * and gets new_lens[b] <= T more. The pages that these need beyond the ones it has
+ * (ceil(tokens / 16)) come from the front of the free list, in the order of b:
+ *   block_table[b][have + i] = free_pages[first_b + i],
+ *   first_b = pages taken by the sequences before b.
+ * Entries that are not new are left as they are.
+ *   cached, new_lens [B] int32; free_pages [num_free] int32 (may be NULL when 0);
+ *   block_table [B][max_pages] int32, read and extended in place;
+ *   seqlens [B] int32 out: cached + new (what fa_decode_paged takes);
+ *   slots [B][T] int32 out: page * 16 + offset of each new token, -1 in rows without one;
+ *   positions [B][T] int32 out: cached[b] + its index, 0 in rows without one;
+ *   pages_used [1] int32 out: pages needed by all sequences together.
+ *   Row t of a sequence is its t-th new token or, with align_end, its new tokens are
+ *   the LAST new_lens[b] rows, where the bottom-right mask of fa_decode_paged wants
+ *   them (row i at position seqlens[b] - T + i).
+ *   Lengths outside [0, max_pages * 16] (cached) or [0, min(T, what is left of the
+ *   row)] (new) are clamped and FA_ERR_BOUNDS is recorded. When the free list is too
+ *   short, FA_ERR_BOUNDS is recorded, the pages past its end are -1 in the table and
+ *   their tokens' slots -1; pages_used says how many were needed.
+ *   block_table must not overlap any other argument.
+ */
+FA_API fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_pages, int num_free,
+                               int* block_table, int* seqlens, int* slots, int* positions, int* pages_used,
+                               int B, int T, int max_pages, int page_size, int align_end, void* stream);
+
+/*
+ * fa_tree_mask -- the visibility mask and the positions of trees of drafted tokens.
+ *   parents [B][T] int32: parent node of node i, in [-1, i); -1: it hangs on the
+ *     committed text. seqlens [B] int32: keys of each sequence, its nodes included.
+ *   tree_lens [B] int32: nodes n_b of each tree (NULL: T), clamped to [0, min(T, seqlens[b])].
+ *   mask [B][T][ceil(T / 32)] int32 out: bit j % 32 of word j / 32 of row i: node i sees
+ *     node j (itself or an ancestor). Rows from n_b on are 0.
+ *   positions [B][T] int32 out: seqlens[b] - n_b + depth (0 at a root); 0 from n_b on.
+ *   A parent outside [-1, i) records FA_ERR_BOUNDS and counts as -1. T <= 8192, B <= 65535.
+ */
+FA_API fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_lens, int* mask,
+                              int* positions, int B, int T, void* stream);
+
+/*
+ * fa_rope_inv_freq -- the angles per position of rotary pairs, plain or stretched for
+ * long contexts. Pure host arithmetic in fp64; inv_freq is HOST memory, rot_dim / 2
+ * values; *mscale what cos and sin are multiplied by (1 except for FA_ROPE_YARN).
+ *   factor >= 1 (not read for FA_ROPE_PLAIN); original_len, beta_fast, beta_slow are read
+ *   for FA_ROPE_YARN: pairs that turn more than beta_fast times within original_len
+ *   positions keep their angle, those that turn less than beta_slow times are stretched.
+ */
+FA_API fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, double base, int scaling,
+                                  double factor, double original_len, double beta_fast, double beta_slow);
+
+/*
+ * fa_rope -- rotary positions of q and k in one launch.
+ * Pair i of a row at position p, (a, b), becomes (a cos t - b sin t, b cos t + a sin t)
+ * * mscale with t = p * inv_freq[i]; it is (x[i], x[i + rot_dim/2]), or with interleaved
+ * (x[2i], x[2i+1]). Values from rot_dim on pass through.
+ *   q, q_out [B][Hq][T][d], k, k_out [B][Hk][T][d] (Hk = 0: no k), bf16 or fp32 (dtype, an
+ *   fa_dtype). Rows of d are dense; strides (HOST memory, 12 values, in elements) are those
+ *   of (batch, head, position) for q, q_out, k, k_out, so the rows may lie in a fused
+ *   projection [B][T][heads][d]. Pointers need the element's alignment only; rows that are
+ *   whole 16-byte vectors (and rot_dim / 2 a multiple of one) take the wider kernel.
+ *   q_out and k_out may be q and k with the same strides; otherwise no output may overlap
+ *   an input or another output. Inputs may have strides of 0.
+ *   positions [B][T] int32, or [T] with positions_shared; any int32 value.
+ *   inv_freq [rot_dim / 2] fp64 (device). The angle is exact to 2^-33 turns at any position.
+ *   2 <= rot_dim <= d <= 1024, rot_dim even. mscale > 0.
+ */
+FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                         const int* positions, int positions_shared, const double* inv_freq, int B, int Hq,
+                         int Hk, int T, int d, int rot_dim, int interleaved, float mscale, int dtype,
+                         void* stream);
+
+/* fa_rope_bwd -- gradients of fa_rope with respect to q and k from those of q_out and k_out:
+ * the transposed rotation. Arguments as fa_rope, dq_out and dk_out in the place of q and k. */
+FA_API fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const long long* strides,
+                             const int* positions, int positions_shared, const double* inv_freq, int B, int Hq,
+                             int Hk, int T, int d, int rot_dim, int interleaved, float mscale, int dtype,
+                             void* stream);
+
+/*
+ * fa_rope_append_paged -- the new rows of a step over the paged cache: q rotated, k rotated
+ * into its pages, v into its pages, in one launch.
+ *   q [B][Hq][T][d], k, v [B][Hkv][T][d] bf16 with strides (HOST, 12 values: q, q_out, k, v)
+ *   as fa_rope; q_out [B][Hq][T][d] may be q. positions, slots [B][T] int32 (fa_paged_plan).
+ *   k_pages, v_pages [num_pages][16][Hkv][d] bf16: row slots[b][t] of them is overwritten.
+ *   A slot of -1 writes nothing (q is rotated all the same); any other slot outside
+ *   [0, num_pages * 16) records FA_ERR_BOUNDS and writes nothing. Slots of one call must
+ *   differ: which of two rows for one slot stays is undefined.
+ *   page_size == 16.
+ */
+FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                                      const long long* strides, const int* positions, const int* slots,
+                                      const double* inv_freq, void* k_pages, void* v_pages, int B, int Hq,
+                                      int Hkv, int T, int page_size, int num_pages, int d, int rot_dim,
+                                      int interleaved, float mscale, void* stream);
 
 /*
  * fa_get_last_device_error -- synchronise `stream`, read and clear the

@@ -29,3 +29,10 @@ from .attention import (  # noqa: F401
     split_ranges,
     visible,
 )
+from .serving import (  # noqa: F401
+    pack_words,
+    paged_plan,
+    rope,
+    tree_attention,
+    tree_sees,
+)
