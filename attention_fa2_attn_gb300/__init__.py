@@ -30,5 +30,7 @@ from .api import (  # noqa: F401
     fa_rope_inv_freq,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
+    fa_tree_decode_paged,
     fa_tree_mask,
+    fa_tree_workspace_bytes,
 )

@@ -64,6 +64,11 @@ SIGNATURES = {
         _I,
         [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     ),
+    "fa_tree_decode_paged": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P],
+    ),
+    "fa_tree_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_get_last_device_error": (_I, [_P, ctypes.POINTER(_I)]),
     "fa_set_wait_timeout_ns": (None, [_ULL]),
     "fa_get_wait_timeouts": (None, [ctypes.POINTER(_ULL), ctypes.POINTER(_ULL)]),

@@ -9,6 +9,7 @@ in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -463,6 +464,61 @@ def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, 
     return q_out
 
 
+def fa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, max_pages: int, d: int,
+                            num_sms: int | None = None, device=None) -> int:
+    """Bytes of workspace fa_tree_decode_paged needs on a device with num_sms SMs (None: this one)."""
+    if num_sms is None:
+        num_sms = _sm_count(torch.cuda.current_device() if device is None else torch.device(device).index)
+    return int(lib().fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, int(num_sms)))
+
+
+@functools.lru_cache(maxsize=None)
+def _sm_count(index) -> int:
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+def fa_tree_decode_paged(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens=None,
+                         scale: float | None = None, workspace=None, out=None, lse=None):
+    """Attention of drafted trees over the paged cache: q [B][Hq][T][d], pools [P][16][Hkv][d] bf16,
+    block_table [B][max_pages], seqlens [B], tree_mask [B][T][ceil(T/32)] or [T][ceil(T/32)] (one for
+    all), tree_lens [B] or None (T nodes each), int32 -> (o, lse)."""
+    _need(q, "q", torch.bfloat16, 4)
+    _need(k_pages, "k_pages", torch.bfloat16, 4)
+    _need(v_pages, "v_pages", torch.bfloat16, 4)
+    _need(block_table, "block_table", torch.int32, 2)
+    B, Hq, T, d = q.shape
+    P, page_size, Hkv, _ = k_pages.shape
+    max_pages = block_table.shape[1]
+    dev = q.device
+    if not (dev == k_pages.device == v_pages.device == block_table.device):
+        raise ValueError("q, the pools and block_table must be on one device")
+    _on_current_device(q)
+    if tuple(k_pages.shape) != tuple(v_pages.shape) or k_pages.shape[3] != d:
+        raise ValueError(f"k_pages and v_pages must both be [P][page_size][Hkv][{d}]")
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}][max_pages]")
+    _need_ints("seqlens", seqlens, (B,), dev)
+    words = (T + 31) // 32
+    shared = isinstance(tree_mask, torch.Tensor) and tree_mask.dim() == 2
+    _need_ints("tree_mask", tree_mask, (T, words) if shared else (B, T, words), dev)
+    if tree_lens is not None:
+        _need_ints("tree_lens", tree_lens, (B,), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = lib().fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, _sm_count(dev.index))
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws_bytes = nbytes
+    else:
+        ws_bytes = _ws_bytes(workspace, nbytes, dev)
+    o = _out(out, "out", q.shape, torch.bfloat16, q)
+    lse = _out(lse, "lse", (B, Hq, T), torch.float32, q)
+    st = lib().fa_tree_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seqlens),
+                                    _ptr(tree_mask), int(shared), _ptr(tree_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T,
+                                    max_pages, page_size, P, d, scale, _ptr(workspace), ws_bytes, _stream(q))
+    check(st, "fa_tree_decode_paged")
+    return o, lse
+
+
 def fa_get_last_device_error(device=None) -> tuple[int, int]:
     """Synchronise the current stream and read/clear the device error word -> (status, raw word)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -508,6 +564,8 @@ __all__ = [
     "fa_rope",
     "fa_rope_bwd",
     "fa_rope_append_paged",
+    "fa_tree_decode_paged",
+    "fa_tree_workspace_bytes",
     "fa_get_last_device_error",
     "fa_set_wait_timeout_ns",
     "fa_get_wait_timeouts",

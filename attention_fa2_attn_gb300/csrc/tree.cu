@@ -1,0 +1,1037 @@
+// tree.cu -- attention of a tree of drafted tokens over the paged cache.
+//
+// What it computes. Sequence b has S = seqlens[b] keys, the last n of which are the
+// drafted nodes. Query row i < n is node i: it sees key j if j < S - n (the committed
+// text) or bit j - (S - n) of its mask row is set. O = softmax(scale * q K^T) V over
+// the keys it sees, lse = ln sum exp; a row that sees none, and rows from n on, get
+// O = 0 and lse = -inf. A KV head's g = Hq / Hkv query heads times T nodes are R = g * T
+// rows, dense in q, o and lse: row r is node r % T of head r / T.
+//
+// What bounds it. K and V are read once for R rows: R FLOP per byte. Up to some 256
+// rows that is HBM time, beyond it the tensor cores'. So the tensor cores run
+// (tcgen05, 128 rows a tile) whatever R is: a tile of 128 keys costs a tile of rows
+// about 1.1 us of S = Q K^T, softmax and O += P V in a row, and at full HBM rate an SM
+// gets such a K/V tile (64 KB at d = 128) every 1.5 us.
+//
+// How.
+//   * Work is cut into equal shares of key tiles, not of sequences: every CTA of the
+//     one-per-SM grid sums the batch's key tiles for itself and takes the share
+//     [c N / G, (c+1) N / G) of them. Lengths live on the device and may differ by any
+//     factor; every SM has the same number of tiles within one. A share that does not
+//     cover its (sequence, KV head) whole leaves fp32 partials (O, max, sums) in the
+//     workspace, at most two per CTA, and the merge kernel joins them. A list of the
+//     split ones, one entry per CTA, tells it which; what is whole is written at once.
+//   * R <= 128 (NARROW): two key tiles at a time for the one tile of rows. Softmax
+//     warps 0-3 take the even tiles, 4-7 the odd ones, each with its own S/P and O in
+//     TMEM, so that one's softmax runs under the other's MMAs; the two are joined in
+//     TMEM at the end of a share (a warp can read the other's lanes).
+//   * R > 128 (WIDE): two tiles of rows against each key tile, as the prefill kernel.
+//   * warp 8: K/V pages by TMA, 16-token boxes through the block table, into a ring of
+//     128-byte-swizzled tiles; the Q tile too (rows are dense: one plain box).
+//   * warp 9: TMEM and the MMA chain. S_t(x+1) is issued right behind PV_t(x).
+//   * the mask is looked at only in tiles that reach past S - n: a thread's row has
+//     its 128 bits of the tile in four registers. Rows of padding warps are skipped.
+// Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the
+// CTA unwinds. The softmax warps leave together by a vote at the barrier they share.
+#include "launch.cuh"
+
+namespace fa {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_tiled();  // defined in api.cu
+
+constexpr int kTrTile = 128;  // rows of a tile, keys of a tile
+
+template <int D, bool WIDE>
+struct TrCfg {
+  static constexpr int KCH = D / 64;             // 64-element (128-byte) chunks along d
+  static constexpr int CHUNK_BYTES = 128 * 128;  // 128 rows x 128 bytes, swizzled
+  static constexpr int Q_BYTES = kTrTile * D * 2;
+  static constexpr int KV_BYTES = kTrTile * D * 2;
+  static constexpr int QT = WIDE ? 2 : 1;
+  // stages of K and of V: 64 to 96 KB of each in flight (3 + 3 tiles of 32 KB fill the
+  // SM's shared memory beside one Q tile; HBM needs about 70 KB in flight an SM)
+  static constexpr int STAGES = D == 64 ? (WIDE ? 5 : 6) : (WIDE ? 2 : 3);
+  static constexpr int OFF_K = QT * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
+  static constexpr int OFF_EX = OFF_BAR + 384;
+  static constexpr int SMEM = OFF_EX + kTrTile * 5 * 4;  // at most 227 KB; the base is 1024-byte aligned
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
+  static constexpr int O_OFF = 128;
+  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, producer, MMA issuer, two idle warps
+  static constexpr int SOFTMAX_REGS = 192;  // 256 * 192 + 128 * 120 = 384 * 168
+  static constexpr int AUX_REGS = 120;
+  static_assert(SMEM <= 232448, "shared memory of an SM");
+};
+
+struct TrParams {
+  __nv_bfloat16* o;
+  float* lse;  // may be null
+  const int* block_table;
+  const int* seqlens;
+  const int* tree_lens;  // may be null: T nodes each
+  const int* mask;
+  long long mask_sb;  // words from a sequence's mask to the next's; 0: one for all
+  int B, Hkv, T, R, U;  // U: row units of a (sequence, KV head)
+  int words;            // of a mask row
+  int max_pages, num_pages;
+  float c;  // scale * log2(e)
+  float* part;     // [2 * grid][128 * QT][D]: unnormalised O of partial shares
+  float4* part_ml; // [2 * grid][128 * QT]: (max in log2 units, sum as P V saw it, sum, -)
+  int4* split;     // [grid]: (first row, rows, last CTA, -) of the unit that CTA c begins and does not end; z < 0: none
+  unsigned* err;
+  unsigned long long timeout_ns;
+};
+
+struct TrBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  // where this CTA's share begins
+  int b0, off0, begin, end, total, grid;
+};
+static_assert(sizeof(TrBars) <= 384, "barrier area");
+
+// Lengths of a sequence, clamped to what the table and the step hold.
+struct TrSeq {
+  int S, n;
+  int tiles;  // key tiles to go through
+};
+__device__ __forceinline__ TrSeq tr_seq(const TrParams& p, int b) {
+  TrSeq s;
+  s.S = max(0, min(__ldg(p.seqlens + b), p.max_pages * 16));
+  s.n = max(0, min(p.tree_lens ? __ldg(p.tree_lens + b) : p.T, min(p.T, s.S)));
+  s.tiles = s.n > 0 ? (s.S + kTrTile - 1) / kTrTile : 0;
+  return s;
+}
+// Steps of one (KV head, row unit): a key tile, or (narrow) a pair of them; a unit
+// without keys is one step, so that somebody writes its zeros.
+template <bool WIDE>
+__device__ __forceinline__ int tr_steps(const TrSeq& s) {
+  return max(1, WIDE ? s.tiles : (s.tiles + 1) / 2);
+}
+
+// A run of steps of one unit inside a CTA's share.
+struct TrSeg {
+  int b, kvh, u;
+  int S, n;
+  int x0, nt;    // first key tile and how many
+  bool from_start, to_end;
+  int unit_end;  // global index behind the unit's last step
+};
+
+// Walks a share segment by segment; each role walks by itself.
+template <bool WIDE>
+struct TrWalk {
+  int b, off, at, end;  // sequence, steps into it; global step; the share's end
+  __device__ __forceinline__ TrWalk(const TrBars* s) : b(s->b0), off(s->off0), at(s->begin), end(s->end) {}
+  __device__ __forceinline__ bool next(const TrParams& p, TrSeg& g) {
+    if (at >= end) return false;
+    const TrSeq q = tr_seq(p, b);
+    const int steps = tr_steps<WIDE>(q);
+    const int hu = off / steps;
+    const int j0 = off - hu * steps;
+    const int ns = min(steps - j0, end - at);
+    constexpr int PER = WIDE ? 1 : 2;
+    g.b = b;
+    g.kvh = hu / p.U;
+    g.u = hu - g.kvh * p.U;
+    g.S = q.S;
+    g.n = q.n;
+    g.x0 = j0 * PER;
+    g.nt = max(0, min(q.tiles, (j0 + ns) * PER) - g.x0);
+    g.from_start = j0 == 0;
+    g.to_end = j0 + ns == steps;
+    g.unit_end = at - j0 + steps;
+    off += ns;
+    at += ns;
+    if (off == steps * p.Hkv * p.U) {
+      ++b;
+      off = 0;
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// 32 visibility bits of a row for keys off .. off + 31, counted from the first node
+// (negative: committed text). `row`: the row's mask words, n nodes.
+__device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, int off) {
+  if (off <= -32) return 0xffffffffu;
+  if (off >= n) return 0u;
+  auto word = [&](int w) -> uint32_t {  // words past the last node are not read
+    return w >= 0 && w < words ? static_cast<uint32_t>(__ldg(row + w)) : 0u;
+  };
+  uint32_t v;
+  if (off < 0) {
+    v = ((1u << -off) - 1u) | (word(0) << -off);
+  } else {
+    v = __funnelshift_r(word(off >> 5), word((off >> 5) + 1), off & 31);
+  }
+  const int left = n - off;  // nodes from here on
+  return left < 32 ? v & ((1u << left) - 1u) : v;
+}
+
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(384, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const TrParams p) {
+  using C = TrCfg<D, WIDE>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  TrBars* bars = reinterpret_cast<TrBars*>(smem + C::OFF_BAR);
+  float* ex = reinterpret_cast<float*>(smem + C::OFF_EX);  // [5][128]: max and sum of both slots, lse sum of slot 1
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  if (smem_u32(smem) & 1023u) {  // the swizzle atoms' alignment; the block's only shared memory starts at a multiple
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      record_error(p.err, FA_ERR_TIMEOUT, SITE_TR_SMEM);
+      p.split[cta] = make_int4(0, 0, -1, 0);
+    }
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 128);
+      mbar_init(&bars->pv_done[t], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
+  pdl_wait();
+
+  // ---- this CTA's share of all steps: a block-wide scan over the sequences
+  {
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
+    const int lo = min(p.B, static_cast<int>(threadIdx.x) * per), hi = min(p.B, lo + per);
+    int mine = 0;  // all steps of a batch are below 2^31
+    for (int b = lo; b < hi; ++b) mine += tr_steps<WIDE>(tr_seq(p, b));
+    mine *= p.Hkv * p.U;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    // totals per warp go through the exchange area, which nothing uses yet
+    int* wsum = reinterpret_cast<int*>(ex);
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int before = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < 12; ++w) {
+      if (w < warp) before += wsum[w];
+      total += wsum[w];
+    }
+    // as many CTAs share the work as there are steps
+    const int G = min(static_cast<int>(gridDim.x), total);
+    const int begin = cta < G ? static_cast<int>(static_cast<long long>(cta) * total / G) : total;
+    const int end = cta < G ? static_cast<int>((cta + 1ll) * total / G) : total;
+    if (threadIdx.x == 0) {
+      bars->begin = begin;
+      bars->end = end;
+      bars->total = total;
+      bars->grid = G;
+    }
+    if (begin >= before && begin < before + mine) {  // one thread: its sequences hold the first step
+      int off = begin - before;
+      int b = lo;
+      for (; b < hi; ++b) {
+        const int s = tr_steps<WIDE>(tr_seq(p, b)) * p.Hkv * p.U;
+        if (off < s) break;
+        off -= s;
+      }
+      bars->b0 = b;
+      bars->off0 = off;
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+  const uint64_t tmo = p.timeout_ns;
+  const uint64_t tmo_unwind = unwind_timeout(tmo);
+  auto fail = [&](unsigned site) {
+    record_error(p.err, FA_ERR_TIMEOUT, site);
+    *abort_flag = 1;
+  };
+
+  if (warp >= 8) {
+    warpgroup_reg_dealloc<C::AUX_REGS>();
+    if (warp == 8) {
+      // ======================= producer =======================
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+      }
+      TrWalk<WIDE> walk(bars);
+      TrSeg w;
+      uint32_t g = 0;  // key tiles loaded so far (ring position)
+      uint32_t q_loads = 0;
+      const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
+      bool ok = true;
+      while (ok && !*abort_flag && walk.next(p, w)) {
+        if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, C::QT * C::Q_BYTES);
+          for (int t = 0; t < C::QT; ++t)
+            for (int c = 0; c < C::KCH; ++c)
+              tma_load_3d(sQ + t * C::Q_BYTES + c * C::CHUNK_BYTES, &tmQ, &bars->q_full, c * 64,
+                          (w.u * C::QT + t) * kTrTile, w.b * p.Hkv + w.kvh);
+        }
+        ++q_loads;
+        const int* trow = p.block_table + static_cast<size_t>(w.b) * p.max_pages;
+        const int n_pages = (w.S + 15) >> 4;
+        // lane i < 8 holds the entry of page 8x + i; the next tile's are fetched meanwhile
+        auto fetch = [&](int x) -> int {
+          const int pg = (w.x0 + x) * 8 + lane;
+          return lane < 8 && x < w.nt && pg < n_pages ? __ldg(trow + pg) : -1;
+        };
+        int ent_next = fetch(0);
+        for (int x = 0; x < w.nt; ++x, ++g) {
+          const int s = g % ST;
+          const uint32_t u = g / ST;
+          int ent = ent_next;
+          ent_next = fetch(x + 1);
+          const int npg = min(8, n_pages - (w.x0 + x) * 8);  // pages past the end are not loaded
+          if (lane < npg && (ent < 0 || ent >= p.num_pages)) {
+            // never dereferenced: page 0 is loaded in its place, the output is undefined
+            record_error(p.err, FA_ERR_BOUNDS, SITE_TR_TABLE);
+            ent = 0;
+          }
+          const uint32_t bytes = static_cast<uint32_t>(npg) * 16 * 128 * C::KCH;
+          const int pe = __shfl_sync(0xffffffffu, ent, pi & 7);
+          if (g >= ST && !mbar_wait(&bars->k_empty[s], (u - 1) & 1, tmo, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], bytes);
+          __syncwarp();
+          if (pi < npg)
+            tma_load_3d(sK + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, &tmK, &bars->k_full[s], pc * 64,
+                        w.kvh, pe * 16);
+          if (g >= ST && !mbar_wait(&bars->v_empty[s], (u - 1) & 1, tmo, abort_flag)) {
+            ok = false;
+            mbar_wait(&bars->k_full[s], u & 1, tmo_unwind);  // K was issued: let it land
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[s], bytes);
+          __syncwarp();
+          if (pi < npg)
+            tma_load_3d(sV + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, &tmV, &bars->v_full[s], pc * 64,
+                        w.kvh, pe * 16);
+        }
+      }
+      if (!ok) fail(SITE_TR_PRODUCER);
+      if (*abort_flag) {  // copies in flight must land before the CTA exits
+        if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) {
+          mbar_wait(&bars->k_full[x % ST], (x / ST) & 1, tmo_unwind);
+          mbar_wait(&bars->v_full[x % ST], (x / ST) & 1, tmo_unwind);
+        }
+      }
+    } else if (warp == 9) {
+      // ======================= MMA issuer =======================
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kTrTile, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sV), C::CHUNK_BYTES, 1024);
+      // S of slot t = Q (row tile t, or the only one) K^T, K in ring stage st
+      auto qk = [=](int t, int st) {
+        const uint64_t a0 = dQ + static_cast<uint64_t>((WIDE ? t * C::Q_BYTES : 0) >> 4);
+        const uint64_t b0 = dK + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+        const uint32_t dS = tmem + t * C::SLOT_COLS;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4);
+            tc_mma_ss(dS, a0 + off, b0 + off, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+        }
+      };
+      auto pv = [=](int t, int st, bool first) {
+        const uint64_t b0 = dV + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+        const uint32_t dO = tmem + t * C::SLOT_COLS + C::O_OFF;
+        const uint32_t aP = tmem + t * C::SLOT_COLS;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kTrTile / 16; ++kk)
+            tc_mma_ts(dO, aP + kk * 8, b0 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv,
+                      (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      auto commit = [=](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+      };
+      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, tmo, abort_flag); };
+      auto wait_k = [&](uint32_t x) -> bool {
+        const bool r = wwait(&bars->k_full[x % ST], (x / ST) & 1);
+        tc_fence_after();
+        return r;
+      };
+      auto wait_v = [&](uint32_t x) -> bool {
+        const bool r = wwait(&bars->v_full[x % ST], (x / ST) & 1);
+        tc_fence_after();
+        return r;
+      };
+      uint32_t pph[2] = {0, 0};  // p_full phase parities
+      auto wait_p = [&](int t) -> bool {
+        const bool r = wwait(&bars->p_full[t], t ? pph[1] : pph[0]);
+        if (t) pph[1] ^= 1; else pph[0] ^= 1;
+        tc_fence_after();
+        return r;
+      };
+      TrWalk<WIDE> walk(bars);
+      TrSeg w;
+      uint32_t g = 0;      // key tiles of earlier segments (ring position)
+      uint32_t seg_i = 0;
+      bool ok = true;
+      for (; ok && walk.next(p, w); ++seg_i, g += w.nt) {
+        const int nt = w.nt;
+        if (!wwait(&bars->q_full, seg_i & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (nt == 0) {
+          if (leader) mbar_arrive(&bars->q_empty);
+          continue;
+        }
+        if constexpr (!WIDE) {
+          // slots take the tiles in turn: tile x in slot x & 1
+          for (int x = 0; x < 2 && x < nt; ++x) {
+            if (!wait_k(g + x)) {
+              ok = false;
+              break;
+            }
+            qk(x, (g + x) % ST);
+            commit(&bars->s_full[x]);
+            commit(&bars->k_empty[(g + x) % ST]);
+            if (x + 1 == nt) commit(&bars->q_empty);
+          }
+          for (int x = 0; ok && x < nt; ++x) {
+            const int t = x & 1;
+            if (!wait_p(t) || !wait_v(g + x)) {
+              ok = false;
+              break;
+            }
+            pv(t, (g + x) % ST, x < 2);
+            commit(&bars->v_empty[(g + x) % ST]);
+            if (x + 2 >= nt) {
+              commit(&bars->pv_done[t]);
+            } else {
+              // S of this slot overwrites the columns P was read from; one thread's MMAs run in order
+              if (!wait_k(g + x + 2)) {
+                ok = false;
+                break;
+              }
+              qk(t, (g + x + 2) % ST);
+              commit(&bars->s_full[t]);
+              commit(&bars->k_empty[(g + x + 2) % ST]);
+              if (x + 3 == nt) commit(&bars->q_empty);  // the segment's last S
+            }
+          }
+        } else {
+          const bool two = (w.u * 2 + 1) * kTrTile < p.R;  // the unit's second row tile exists
+          if (!wait_k(g)) {
+            ok = false;
+            break;
+          }
+          qk(0, g % ST);
+          commit(&bars->s_full[0]);
+          if (two) {
+            qk(1, g % ST);
+            commit(&bars->s_full[1]);
+          }
+          commit(&bars->k_empty[g % ST]);
+          if (nt == 1) commit(&bars->q_empty);
+          for (int x = 0; ok && x < nt; ++x) {
+            const int sv = (g + x) % ST, sk = (g + x + 1) % ST;
+            const bool more = x + 1 < nt;
+            if (!wait_p(0) || !wait_v(g + x)) {
+              ok = false;
+              break;
+            }
+            pv(0, sv, x == 0);
+            if (!two) commit(&bars->v_empty[sv]);
+            if (more) {
+              if (!wait_k(g + x + 1)) {
+                ok = false;
+                break;
+              }
+              qk(0, sk);
+              commit(&bars->s_full[0]);
+            } else {
+              commit(&bars->pv_done[0]);
+            }
+            if (two) {
+              if (!wait_p(1)) {
+                ok = false;
+                break;
+              }
+              pv(1, sv, x == 0);
+              commit(&bars->v_empty[sv]);
+              if (more) {
+                qk(1, sk);
+                commit(&bars->s_full[1]);
+              } else {
+                commit(&bars->pv_done[1]);
+              }
+            }
+            if (more) {
+              commit(&bars->k_empty[sk]);
+              if (x + 2 == nt) commit(&bars->q_empty);
+            }
+          }
+        }
+      }
+      if (!ok && leader) fail(SITE_TR_MMA);
+      commit(&bars->drain);  // every MMA must finish before TMEM is released
+      mbar_wait(&bars->drain, 0, tmo_unwind);
+    }
+  } else {
+    // ======================= softmax: warps 0-3 (slot 0), 4-7 (slot 1) =======================
+    warpgroup_reg_alloc<C::SOFTMAX_REGS>();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * C::SLOT_COLS;
+    const uint32_t tO = tS + C::O_OFF;
+    const float2 c2 = make_float2(p.c, p.c);
+    // The reference maximum m is raised only when a row's maximum climbs more than this
+    // above it; until then the exponentials stay below 2^8 and carry one constant factor
+    // that O / l cancels.
+    constexpr float kRescaleSlack = 8.f;
+    bool ok = true;
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+    };
+    TrWalk<WIDE> walk(bars);
+    TrSeg w;
+    uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
+    uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
+    uint32_t gkv = 0;   // ring position at the segment's start
+    bool listed = false;
+    while (walk.next(p, w)) {
+      const int row = WIDE ? (w.u * 2 + t) * kTrTile + r : r;  // of the R rows
+      const bool has_rows = row - lane < p.R;                  // some row of this warp exists (warp-uniform)
+      const bool tile_exists = !WIDE || (w.u * 2 + t) * kTrTile < p.R;
+      const int node = row % p.T;
+      const bool live = row < p.R && node < w.n;
+      const int base = w.S - w.n;  // first node's key
+      const int* mrow = p.mask + w.b * p.mask_sb + static_cast<size_t>(node) * p.words;
+      const int step = WIDE ? 1 : 2;
+      const int x_first = WIDE ? 0 : t;
+      const int mine = !tile_exists || w.nt <= x_first ? 0 : (w.nt - x_first + step - 1) / step;  // tiles of this slot
+      float m = -INFINITY;
+      float l = 0.f;   // sum of the unrounded p: the lse's
+      float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
+
+      for (int i = 0; i < mine; ++i, ++cnt) {
+        const int x = x_first + i * step;  // tile of the segment
+        if (!wwait(&bars->s_full[t], cnt & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int key0 = (w.x0 + x) * kTrTile;
+        if (has_rows) {
+          uint32_t raw[4][32];
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, raw[cc]);
+          tmem_ld_wait();
+          float s[128];
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(raw[k >> 5][k & 31]);
+          if (key0 + kTrTile > base) {
+#pragma unroll
+            for (int wd = 0; wd < 4; ++wd) {
+              const uint32_t bits = live ? tr_bits(mrow, p.words, w.n, key0 + 32 * wd - base) : 0u;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((bits >> k) & 1u)) s[32 * wd + k] = -INFINITY;
+            }
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float a = fmax3(s[16 * k], s[16 * k + 1], s[16 * k + 2]);
+#pragma unroll
+            for (int e = 3; e < 15; e += 2) a = fmax3(a, s[16 * k + e], s[16 * k + e + 1]);
+            mx8[k] = fmaxf(a, s[16 * k + 15]);
+          }
+          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+          const float m_tile = mx * p.c;
+          const float m_new = (m_tile > m + kRescaleSlack) ? m_tile : m;
+          const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+          const float alpha = ex2_approx(m - m_use);
+          // the largest p is not 1 against a stale reference: O's normaliser counts it as
+          // the bf16 product sees it, so that a nearly one-hot row is not off by its rounding
+          const float p_top = ex2_approx(fmaf(mx, p.c, -m_use));
+          const float p_top_err = __bfloat162float(__float2bfloat16_rn(p_top)) - p_top;
+          const float2 nm2 = make_float2(-m_use, -m_use);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int e = cc * 32 + 2 * k;
+              const float2 v = ffma2(make_float2(s[e], s[e + 1]), c2, nm2);
+              const float2 ev = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              acc[k & 3] = fadd2(acc[k & 3], ev);
+              pk[k] = pack_bf16x2(ev.x, ev.y);
+            }
+            tmem_st16(tS + cc * 16, pk);
+          }
+          const float2 at = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+          l = fmaf(l, alpha, at.x + at.y);
+          lc = fmaf(lc, alpha, p_top_err);
+          m = m_new;
+          // PV of this slot's previous tile is complete: S of this one was issued behind it
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int cc = 0; cc < D / 32; cc += 2) {
+              uint32_t o0[32], o1[32];
+              tmem_ld32(tO + cc * 32, o0);
+              tmem_ld32(tO + cc * 32 + 32, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 v0 = fmul2(make_float2(__uint_as_float(o0[k]), __uint_as_float(o0[k + 1])), al2);
+                const float2 v1 = fmul2(make_float2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), al2);
+                o0[k] = __float_as_uint(v0.x);
+                o0[k + 1] = __float_as_uint(v0.y);
+                o1[k] = __float_as_uint(v1.x);
+                o1[k + 1] = __float_as_uint(v1.y);
+              }
+              tmem_st32(tO + cc * 32, o0);
+              tmem_st32(tO + cc * 32 + 32, o1);
+            }
+          }
+        }
+        // V rows past the sequence's end hold whatever the pool or an earlier tile left
+        // there, and 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
+        if (key0 + kTrTile > w.S && (!WIDE || t == 0)) {
+          const uint32_t xg = gkv + x;
+          if (!wwait(&bars->v_full[xg % ST], (xg / ST) & 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vt = sV + (xg % ST) * C::KV_BYTES;
+          const int r0 = w.S - key0;
+          for (int idx = r; idx < (kTrTile - r0) * C::KCH * 8; idx += 128) {
+            const int vr = r0 + idx / (C::KCH * 8);
+            const int rem = idx % (C::KCH * 8);
+            *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::CHUNK_BYTES + vr * 128 + (rem & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
+      }
+      gkv += w.nt;
+      if (ok && mine > 0) {
+        if (!wwait(&bars->pv_done[t], ecnt & 1)) ok = false;
+        ++ecnt;
+        tc_fence_after();
+      }
+      if (!ok) fail(SITE_TR_SOFTMAX);
+
+      // ---- the segment's end: final rows, or a partial
+      if (!live) {
+        m = -INFINITY;
+        l = lc = 0.f;
+      }
+      const bool whole = w.from_start && w.to_end;
+      const int slot = 2 * cta + (w.from_start ? 1 : 0);
+      const size_t out_row = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + row;
+      const size_t part_row = static_cast<size_t>(slot) * (kTrTile * C::QT) + (WIDE ? t * kTrTile : 0) + r;
+      if (threadIdx.x == 0 && w.from_start && !w.to_end && ok) {
+        // this CTA begins the unit: the last CTA with a share of it is the one that holds its last step
+        const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
+        const int first_row = w.u * C::QT * kTrTile;
+        p.split[cta] = make_int4((w.b * p.Hkv + w.kvh) * p.R + first_row, min(p.R - first_row, C::QT * kTrTile),
+                                 static_cast<int>(last), 0);
+        listed = true;
+      }
+      float m_all = m, sum = l + lc, lsum = l;
+      float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
+      if constexpr (!WIDE) {
+        ex[t * 128 + r] = m;
+        ex[(2 + t) * 128 + r] = l + lc;
+        if (t == 1) ex[4 * 128 + r] = l;
+        if (!vote_all(1, 256, ok)) break;  // all eight warps leave in the same segment
+        const float m0 = ex[r], m1 = ex[128 + r];
+        m_all = fmaxf(m0, m1);
+        const float m_use = m_all == -INFINITY ? 0.f : m_all;
+        f0 = ex2_approx(m0 - m_use);
+        f1 = ex2_approx(m1 - m_use);
+        sum = f0 * ex[256 + r] + f1 * ex[384 + r];
+        if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
+      } else if (!ok) {
+        break;
+      }
+      if (whole) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        f0 *= inv;
+        f1 *= inv;
+      }
+      if (has_rows && tile_exists) {
+        // narrow: each slot's warps write half the columns of the joined O
+        constexpr int COLS = WIDE ? D : D / 2;
+        const int col0 = WIDE ? 0 : t * COLS;
+        const bool take0 = (WIDE ? mine > 0 : w.nt > 0) && f0 != 0.f;
+        const bool take1 = !WIDE && w.nt > 1 && f1 != 0.f;
+        const uint32_t o_base = tmem + lane_base + (WIDE ? t * C::SLOT_COLS : 0) + C::O_OFF;
+        const bool write = row < p.R;
+#pragma unroll
+        for (int cc = 0; cc < COLS / 32; ++cc) {
+          uint32_t a[32], b[32];
+          tmem_ld32(o_base + col0 + cc * 32, a);
+          if constexpr (!WIDE) tmem_ld32(o_base + C::SLOT_COLS + col0 + cc * 32, b);
+          tmem_ld_wait();
+          float o[32];
+          // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
+            if constexpr (!WIDE) o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
+          }
+          if (!write) continue;
+          if (whole) {
+            __nv_bfloat16* dst = p.o + out_row * D + col0 + cc * 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(dst + 8 * q) =
+                  live ? make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                                    pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]))
+                       : make_uint4(0u, 0u, 0u, 0u);
+          } else if (live) {
+            float* dst = p.part + part_row * D + col0 + cc * 32;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+        if (write && (WIDE || t == 0)) {
+          if (whole) {
+            if (p.lse) p.lse[out_row] = lsum > 0.f ? (m_all + log2f(lsum)) * kLn2 : -INFINITY;
+          } else {
+            p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
+          }
+        }
+      }
+      tc_fence_before();
+      // narrow: both slots' O have been read by all before either is overwritten, and the
+      // exchange area before the next segment fills it
+      if constexpr (!WIDE) named_bar_sync(2, 256);
+    }
+    if (threadIdx.x == 0 && !listed) p.split[cta] = make_int4(0, 0, -1, 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the partials of the units that several CTAs share: lse = log2 sum 2^(m_s - m) l_s
+// + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. A block reads the list of split
+// units, and takes rows of them in turn, MW warps to a row, each with every MW-th partial.
+template <int D, int QT>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
+                                                         const float4* __restrict__ part_ml,
+                                                         const int4* __restrict__ split, int grid,
+                                                         __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+  constexpr int MW = 4;        // warps to a row
+  constexpr int N = D / 32;    // columns of a lane
+  constexpr int UNITS = 1024;  // most CTAs a grid may have
+  __shared__ int units[UNITS];
+  __shared__ int n_units;
+  __shared__ float red[8][D];
+  __shared__ float red_m[8], red_s[8], red_l[8];
+  if (threadIdx.x == 0) n_units = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_launch();
+  // every block makes the list in the order of the CTAs, so that all agree on it
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int c0 = 0; c0 < grid; c0 += 32) {
+      const int c = c0 + threadIdx.x;
+      const bool is = c < grid && split[c].z >= 0;
+      const unsigned all = __ballot_sync(0xffffffffu, is);
+      if (is) units[n + __popc(all & ((1u << threadIdx.x) - 1u))] = c;
+      n += __popc(all);
+    }
+    if (threadIdx.x == 0) n_units = n;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % MW, pair = warp / MW;  // two rows at a time
+  constexpr int ROWS = 128 * QT;
+  const int total = n_units * (ROWS / 2);
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    const int c = units[item / (ROWS / 2)];
+    const int4 un = split[c];
+    const int row = item % (ROWS / 2) * 2 + pair;
+    if (item % (ROWS / 2) * 2 >= un.y) continue;  // block-uniform
+    float m = -INFINITY, s = 0.f, l = 0.f;
+    float acc[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    if (row < un.y) {
+      // partial 0 is CTA c's last, the others are the later CTAs' first
+      constexpr int IN = 4;
+      for (int i0 = sub; i0 <= un.z - c; i0 += MW * IN) {
+        float4 ml[IN];
+        float v[IN][N];
+#pragma unroll
+        for (int k = 0; k < IN; ++k) {
+          const int i = i0 + k * MW;
+          ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+          if (i <= un.z - c) {
+            const size_t at = static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + row;
+            ml[k] = part_ml[at];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[k][e] = part[at * D + lane * N + e];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < IN; ++k) {
+          if (ml[k].x == -INFINITY) continue;  // a share without a key this row sees: its O was not written
+          const float mn = fmaxf(m, ml[k].x);
+          const float fa = ex2_approx(m - mn), fb = ex2_approx(ml[k].x - mn);
+          s = s * fa + ml[k].y * fb;
+          l = l * fa + ml[k].z * fb;
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[e] = acc[e] * fa + v[k][e] * fb;
+          m = mn;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc[e];
+    if (lane == 0) {
+      red_m[warp] = m;
+      red_s[warp] = s;
+      red_l[warp] = l;
+    }
+    __syncthreads();
+    if (sub == 0 && row < un.y) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < MW; ++k) mm = fmaxf(mm, red_m[warp + k]);
+      const float m_use = mm == -INFINITY ? 0.f : mm;
+      float st = 0.f, lt = 0.f, ot[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) ot[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < MW; ++k) {
+        const float f = ex2_approx(red_m[warp + k] - m_use);
+        st += f * red_s[warp + k];
+        lt += f * red_l[warp + k];
+#pragma unroll
+        for (int e = 0; e < N; ++e) ot[e] += f * red[warp + k][lane * N + e];
+      }
+      const float inv = st > 0.f ? 1.f / st : 0.f;
+      const size_t out = static_cast<size_t>(un.x) + row;
+      __nv_bfloat16* dst = o + out * D + lane * N;
+      if constexpr (N == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(ot[0] * inv, ot[1] * inv), pack_bf16x2(ot[2] * inv, ot[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(ot[0] * inv, ot[1] * inv);
+      if (lse && lane == 0) lse[out] = lt > 0.f ? (mm + log2f(lt)) * kLn2 : -INFINITY;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static bool tr_wide(int R) { return R > kTrTile; }
+
+// Row units of all (sequence, KV head)s and the most steps they can have, 0 from 2^31 on.
+static long long tr_most_steps(int B, int Hkv, int R, int max_pages) {
+  const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
+  const long long tiles = (static_cast<long long>(max_pages) * 16 + kTrTile - 1) / kTrTile;
+  const long long steps = tr_wide(R) ? tiles : (tiles + 1) / 2;
+  const long long n = static_cast<long long>(B) * Hkv * U;
+  return n > ((1ll << 31) - 1) / steps ? 0 : n * steps;
+}
+
+static int tr_grid(long long steps, int sms) { return static_cast<int>(steps < sms ? steps : sms); }
+
+static size_t tr_part_bytes(int grid, int R, int d) {
+  return static_cast<size_t>(2) * grid * (tr_wide(R) ? 256 : 128) * d * 4;
+}
+static size_t tr_ml_bytes(int grid, int R) { return static_cast<size_t>(2) * grid * (tr_wide(R) ? 256 : 128) * 16; }
+
+template <int D, bool WIDE>
+static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TrParams& p,
+                       int grid, cudaStream_t stream) {
+  using C = TrCfg<D, WIDE>;
+  auto kfn = tree_kernel<D, WIDE>;
+  const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
+  if (rc != FA_OK) return rc;
+  const long long items = static_cast<long long>(grid) * (kTrTile * C::QT / 2);
+  const int merge_grid = static_cast<int>(items < 2 * grid ? items : 2 * grid);
+  return launch_dependent(tree_merge_kernel<D, C::QT>, dim3(merge_grid), dim3(256), 0, stream,
+                          static_cast<const float*>(p.part), static_cast<const float4*>(p.part_ml),
+                          static_cast<const int4*>(p.split), grid, p.o, p.lse);
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || d < 1 || num_sms < 1 || Hq % Hkv != 0) return 0;
+  const long long R = static_cast<long long>(Hq / Hkv) * T;
+  if (R >= (1ll << 31)) return 0;
+  const long long steps = tr_most_steps(B, Hkv, static_cast<int>(R), max_pages);
+  if (steps == 0) return 0;
+  const int grid = tr_grid(steps, num_sms);
+  return tr_part_bytes(grid, static_cast<int>(R), d) + tr_ml_bytes(grid, static_cast<int>(R)) +
+         static_cast<size_t>(grid) * 16;
+}
+
+fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                               const int* seqlens, const int* tree_mask, int mask_shared, const int* tree_lens,
+                               void* o, float* lse, int B, int Hq, int Hkv, int T, int max_pages, int page_size,
+                               int num_pages, int d, float scale, void* workspace, size_t ws_bytes, void* stream) {
+  auto mis = [](const void* x, uintptr_t m) { return (reinterpret_cast<uintptr_t>(x) & (m - 1)) != 0; };
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !tree_mask || !o || !workspace)
+    return FA_ERR_INVALID_ARG;
+  if (mis(q, 16) || mis(k_pages, 16) || mis(v_pages, 16) || mis(o, 16) || mis(block_table, 4) || mis(seqlens, 4) ||
+      mis(tree_mask, 4) || (tree_lens && mis(tree_lens, 4)) || (lse && mis(lse, 4)) || mis(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || num_pages < 1 || Hq % Hkv != 0 || !(scale > 0.f) ||
+      !(scale < INFINITY))
+    return FA_ERR_INVALID_ARG;
+  if (page_size != 16 || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * 16 >= (1ll << 31) || static_cast<long long>(max_pages) * 16 >= (1ll << 31) ||
+      static_cast<long long>(B) * Hq * T >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  const int R = Hq / Hkv * T;
+  const long long steps = tr_most_steps(B, Hkv, R, max_pages);
+  if (steps == 0) return FA_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  if (sms > 1024) return FA_ERR_UNSUPPORTED;
+  if (ws_bytes < fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, sms)) return FA_ERR_INVALID_ARG;
+  const int grid = tr_grid(steps, sms);
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return FA_ERR_CUDA;
+
+  CUtensorMap tq, tk, tv;
+  {
+    // a KV head's R rows are dense; rows past R read as zeros
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)R, (cuuint64_t)B * Hkv};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)R * d * 2};
+    cuuint32_t box[3] = {64, 128, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
+  }
+  for (int i = 0; i < 2; ++i) {
+    // one 16-token page of one KV head per box
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)num_pages * 16};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2};
+    cuuint32_t box[3] = {64, 1, 16};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (enc(i == 0 ? &tk : &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(i == 0 ? k_pages : v_pages),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
+  }
+  TrParams p;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.tree_lens = tree_lens;
+  p.mask = tree_mask;
+  p.words = (T + 31) / 32;
+  p.mask_sb = mask_shared ? 0 : static_cast<long long>(T) * p.words;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.R = R;
+  p.U = tr_wide(R) ? (R + 2 * kTrTile - 1) / (2 * kTrTile) : 1;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.c = scale * kLog2e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float4*>(ws + tr_part_bytes(grid, R, d));
+  p.split = reinterpret_cast<int4*>(ws + tr_part_bytes(grid, R, d) + tr_ml_bytes(grid, R));
+  p.err = device_error_word();
+  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  p.timeout_ns = wait_timeout_ns();
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int rc;
+  if (tr_wide(R))
+    rc = d == 128 ? launch_tree<128, true>(tq, tk, tv, p, grid, cs) : launch_tree<64, true>(tq, tk, tv, p, grid, cs);
+  else
+    rc = d == 128 ? launch_tree<128, false>(tq, tk, tv, p, grid, cs) : launch_tree<64, false>(tq, tk, tv, p, grid, cs);
+  return static_cast<fa_status>(rc);
+}
+
+}  // extern "C"

@@ -415,6 +415,38 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
                                       int interleaved, float mscale, void* stream);
 
 /*
+ * fa_tree_decode_paged -- attention of a tree of drafted tokens over the paged cache, the
+ * tree's own keys included: the step that verifies drafts in one pass.
+ *   Sequence b has S = seqlens[b] keys; its last n = tree_lens[b] (NULL: T; clamped to
+ *   [0, min(T, S)]) are the drafted nodes, node i at position S - n + i. Query row i < n
+ *   is node i. It sees key j if j < S - n, or if bit (j - (S - n)) % 32 of word
+ *   (j - (S - n)) / 32 of its mask row is set (so itself only if its own bit is).
+ *   O and lse as fa_decode_paged; a row that sees no key, and rows from n on, get O = 0
+ *   and lse = -inf.
+ *   q [B][Hq][T][d] bf16; pools, block_table, seqlens as fa_decode_paged;
+ *   tree_mask [B][T][ceil(T / 32)] int32 (fa_tree_mask), or [T][ceil(T / 32)] for the whole
+ *   batch with mask_shared; o, lse as fa_decode_paged (lse may be NULL).
+ *   d in {64, 128}, page_size == 16, any Hq / Hkv and T with B * Hq * T < 2^31.
+ *   workspace: at least fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count)
+ *   bytes, 256-byte aligned; its contents need no initialisation, and calls that may
+ *   overlap on the GPU need one each.
+ *   Keys and values inside a sequence must be finite, as for every call here: a row's weight
+ *   of 0 does not cancel a NaN value that the mask hides from it. Pool rows past a
+ *   sequence's end are never used, whatever they hold.
+ *   A table entry outside [0, num_pages) is not dereferenced: FA_ERR_BOUNDS is recorded and
+ *   that sequence's output is undefined.
+ */
+FA_API fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* block_table, const int* seqlens, const int* tree_mask,
+                                      int mask_shared, const int* tree_lens, void* o, float* lse, int B, int Hq,
+                                      int Hkv, int T, int max_pages, int page_size, int num_pages, int d,
+                                      float scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* fa_tree_workspace_bytes -- two fp32 partials (O, max, sums) of a row tile for each CTA that
+ * the call launches on num_sms SMs, and its list of split work; 0 for invalid sizes. */
+FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
+
+/*
  * fa_get_last_device_error -- synchronise `stream`, read and clear the
  * device-side error word. Returns FA_OK, FA_ERR_TIMEOUT or FA_ERR_BOUNDS
  * (or FA_ERR_CUDA if the read itself fails). *detail (may be NULL) receives
