@@ -17,10 +17,12 @@
 // so blocks that share a sequence (blockIdx.y cuts long chunks) need no order. Bound by
 // launch latency for decode steps, by the 8 bytes written per token for prefill steps.
 //
-// fa_tree_mask. sees(i) = {i} + sees(parent(i)). One thread per node walks up the
-// parents in shared memory; as parent(i) < i the visited bits fall, so the thread
-// keeps one 32-bit word and stores it (and the empty ones it skips) when the walk
-// leaves it.
+// fa_tree_mask. sees(i) = {i} + sees(parent(i)). Trees of up to 128 nodes: a thread per
+// node, and every round joins to its set that of the node its own ends at, so that the
+// rounds are the logarithm of the depth and not the depth. Larger ones (their sets do not
+// fit in registers): a thread walks up the parents in shared memory; as parent(i) < i the
+// visited bits fall, so it keeps one 32-bit word and stores it (and the empty ones it
+// skips) when the walk leaves it.
 #include "launch.cuh"
 
 namespace fa {
@@ -126,6 +128,62 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   }
 }
 
+// What a block knows of its tree, with the lengths clamped as the attention call clamps them.
+struct TreeLens {
+  int S, n;
+};
+__device__ __forceinline__ TreeLens tree_lens_of(const int* seqlens, const int* tree_lens, int b, int T) {
+  TreeLens l;
+  l.S = max(0, __ldg(seqlens + b));
+  l.n = max(0, min(tree_lens ? __ldg(tree_lens + b) : T, min(T, l.S)));
+  return l;
+}
+__device__ __forceinline__ int parent_of(const int* prow, int i, unsigned* err) {
+  const int q = __ldg(prow + i);
+  if (q >= -1 && q < i) return q;
+  record_error(err, FA_ERR_BOUNDS, SITE_TREE_MASK);  // not a tree: the node becomes a root
+  return -1;
+}
+
+template <int W>
+__global__ void __launch_bounds__(128) tree_mask_small_kernel(const int* __restrict__ parents,
+                                                              const int* __restrict__ seqlens,
+                                                              const int* __restrict__ tree_lens,
+                                                              int* __restrict__ mask, int* __restrict__ positions,
+                                                              int T, unsigned* err) {
+  __shared__ unsigned set[W][128];
+  __shared__ int up[128];
+  pdl_wait();
+  pdl_launch();
+  const int b = blockIdx.y, i = threadIdx.x;
+  const TreeLens l = tree_lens_of(seqlens, tree_lens, b, T);
+  // mine: the nodes from i up to, but without, `at`
+  int at = i < l.n ? parent_of(parents + static_cast<size_t>(b) * T, i, err) : -1;
+  unsigned mine[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) mine[w] = i < l.n && i / 32 == w ? 1u << (i & 31) : 0u;
+  while (__syncthreads_or(at >= 0)) {
+    up[i] = at;
+#pragma unroll
+    for (int w = 0; w < W; ++w) set[w][i] = mine[w];
+    __syncthreads();
+    if (at >= 0) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) mine[w] |= set[w][at];
+      at = up[at];
+    }
+  }
+  if (i >= T) return;
+  const size_t row = static_cast<size_t>(b) * T + i;
+  int seen = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    mask[row * W + w] = static_cast<int>(mine[w]);
+    seen += __popc(mine[w]);
+  }
+  positions[row] = i < l.n ? l.S - l.n + seen - 1 : 0;
+}
+
 constexpr int kTreeMaxNodes = 8192;  // parents of one sequence in shared memory
 
 __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ parents,
@@ -138,15 +196,10 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ 
   const int b = blockIdx.y;
   const int first = blockIdx.x * blockDim.x;
   const int last = min(T, first + static_cast<int>(blockDim.x));  // nodes before it are all a walk from here visits
-  const int S = max(0, __ldg(seqlens + b));
-  const int n = max(0, min(tree_lens ? __ldg(tree_lens + b) : T, min(T, S)));
+  const TreeLens l = tree_lens_of(seqlens, tree_lens, b, T);
+  const int n = l.n;
   const int* prow = parents + static_cast<size_t>(b) * T;
-  for (int i = threadIdx.x; i < min(last, n); i += blockDim.x) {
-    const int q = __ldg(prow + i);
-    const bool ok = q >= -1 && q < i;  // anything else would not be a tree: the node becomes a root
-    if (!ok) record_error(err, FA_ERR_BOUNDS, SITE_TREE_MASK);
-    up[i] = ok ? q : -1;
-  }
+  for (int i = threadIdx.x; i < min(last, n); i += blockDim.x) up[i] = parent_of(prow, i, err);
   __syncthreads();
   const int i = first + threadIdx.x;
   if (i >= T) return;
@@ -167,7 +220,7 @@ __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ 
     out[at_word] = static_cast<int>(cur);
     cur = 0;
   }
-  positions[static_cast<size_t>(b) * T + i] = i < n ? S - n + depth : 0;
+  positions[static_cast<size_t>(b) * T + i] = i < n ? l.S - n + depth : 0;
 }
 
 }  // namespace fa
@@ -219,12 +272,18 @@ fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_l
   if (B > 65535 || T > kTreeMaxNodes) return FA_ERR_UNSUPPORTED;
   unsigned* err = device_error_word();
   if (!err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
-  const int threads = T >= 128 ? 128 : (T + 31) / 32 * 32;
-  const dim3 grid((T + threads - 1) / threads, B);
-  return static_cast<fa_status>(launch_dependent(tree_mask_kernel, grid, dim3(threads),
-                                                 static_cast<size_t>(T) * sizeof(int),
-                                                 static_cast<cudaStream_t>(stream), parents, seqlens, tree_lens, mask,
-                                                 positions, T, err));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (T <= 128) {
+    const int words = (T + 31) / 32;
+    auto kfn = words == 1 ? tree_mask_small_kernel<1>
+                          : (words == 2 ? tree_mask_small_kernel<2>
+                                        : (words == 3 ? tree_mask_small_kernel<3> : tree_mask_small_kernel<4>));
+    return static_cast<fa_status>(launch_dependent(kfn, dim3(1, B), dim3(words * 32), 0, cs, parents, seqlens,
+                                                   tree_lens, mask, positions, T, err));
+  }
+  return static_cast<fa_status>(launch_dependent(tree_mask_kernel, dim3((T + 127) / 128, B), dim3(128),
+                                                 static_cast<size_t>(T) * sizeof(int), cs, parents, seqlens, tree_lens,
+                                                 mask, positions, T, err));
 }
 
 }  // extern "C"

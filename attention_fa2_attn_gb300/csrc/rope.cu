@@ -14,12 +14,16 @@
 // No table of cosines, no largest position, no FP64 pipe (which is narrow here).
 //
 // How: bound by reading and writing each value once. A lane owns VEC pairs of a token
-// (16 bytes on each side) and makes their sines once, then walks over a chunk of the
-// token's heads, U of them in flight. A row's d * 2 bytes are whole 128-byte lines for
-// the layouts that matter, whatever the strides between rows, so no transpose through
-// shared memory is needed to go between [B][T][heads][d] and [B][heads][T][d].
+// (16 bytes on each side of a row); a block owns 32 such token-lanes and a chunk of the
+// heads, one head to a warp at a time. The block makes the sines of its 32 token-lanes
+// once (VEC angles to a warp, shared memory) while the first U rows of every warp are
+// already on their way. A row's d * 2 bytes are whole 128-byte lines for the layouts
+// that matter, whatever the strides between rows, so no transpose through shared memory
+// is needed to go between [B][T][heads][d] and [B][heads][T][d].
 // Inputs whose rows are not whole aligned vectors take VEC = 1 (one pair, plain loads).
 #include <math.h>
+
+#include <type_traits>
 
 #include "launch.cuh"
 
@@ -44,6 +48,7 @@ struct RopeParams {
   int num_slots;
   long long tokens;         // B * T
   int T, d, rot, lanes, head_chunk;
+  bool small;
   float mscale, sign;       // sign -1: the transposed rotation
   unsigned* err;
 };
@@ -59,34 +64,32 @@ struct Vec16<float> {
   static constexpr int N = 4;
 };
 
-// VEC values at p as floats; VEC = 1 or a 16-byte vector
+// VEC values as they lie in memory, and as floats
 template <typename E, int VEC>
-struct Pack {
-  float v[VEC];
-  __device__ __forceinline__ void load(const E* p) {
+struct Raw {
+  using T = typename std::conditional<VEC == 1, E, uint4>::type;
+  T r;
+  __device__ __forceinline__ void load(const E* p) { r = *reinterpret_cast<const T*>(p); }
+  __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<T*>(p) = r; }
+  __device__ __forceinline__ void get(float (&v)[VEC]) const {
     if constexpr (VEC == 1) {
-      v[0] = static_cast<float>(*p);
-    } else if constexpr (sizeof(E) == 2) {
-      const uint4 r = *reinterpret_cast<const uint4*>(p);
+      v[0] = static_cast<float>(r);
+    } else {
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const float4 r = *reinterpret_cast<const float4*>(p);
-      v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+      for (int i = 0; i < VEC; ++i)
+        v[i] = sizeof(E) == 4 ? __uint_as_float(w[i % 4])
+                              : __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
   }
-  __device__ __forceinline__ void store(E* p) const {
+  __device__ __forceinline__ void set(const float (&v)[VEC]) {
     if constexpr (VEC == 1) {
-      *p = static_cast<E>(v[0]);
+      r = static_cast<E>(v[0]);
     } else if constexpr (sizeof(E) == 2) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      r = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7]));
     } else {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     }
   }
 };
@@ -111,90 +114,112 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
   return (bits >> 63) ? 0ull - r : r;
 }
 
+constexpr int kRopeWarps = 8;
+
 template <typename E, int VEC, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
+  constexpr int U = 4;  // rows of a warp in flight
+  __shared__ float cs[2][VEC][32];
   pdl_wait();
   pdl_launch();
-  const long long id = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long token = id / p.lanes;
-  const int lane = static_cast<int>(id - token * p.lanes);
-  if (token >= p.tokens) return;
-  const int b = static_cast<int>(token / p.T);
-  const int t = static_cast<int>(token - static_cast<long long>(b) * p.T);
+  const int warp = threadIdx.x >> 5, id = threadIdx.x & 31;
+  const long long at = static_cast<long long>(blockIdx.x) * 32 + id;  // this thread's token-lane
+  // 32-bit division where the launch has fewer of them than 2^31
+  const long long token = p.small ? static_cast<long long>(static_cast<unsigned>(at) / static_cast<unsigned>(p.lanes))
+                                  : at / p.lanes;
+  const int lane = static_cast<int>(at - token * p.lanes);
+  const bool there = token < p.tokens;
+  const int b = there ? static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.T)) : 0;
+  const int t = there ? static_cast<int>(token - static_cast<long long>(b) * p.T) : 0;
   const int half = p.rot / 2;
   const bool turn = lane * VEC < half;  // else: the lane copies two vectors of the tail
-  int o0, o1;                           // the lane's two vectors in a row
-  bool two = true;
-  float c[VEC], s[VEC];
-  if (turn) {
-    const int i = lane * VEC;
-    o0 = INTER ? 2 * i : i;
-    o1 = INTER ? 2 * i + VEC : i + half;
-    const long long pos = __ldg(p.positions + b * p.pos_sb + t);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const unsigned long long a = static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + i + e));
-      // the signed upper half, in half turns
-      sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s[e], &c[e]);
-      c[e] *= p.mscale;
-      s[e] *= p.mscale * p.sign;
-    }
-  } else {
-    o0 = p.rot + (lane - half / VEC) * 2 * VEC;
-    o1 = o0 + VEC;
-    two = o1 < p.d;
-  }
+  const int o0 = turn ? (INTER ? 2 * lane * VEC : lane * VEC) : p.rot + (lane - half / VEC) * 2 * VEC;
+  const int o1 = turn && !INTER ? o0 + half : o0 + VEC;
+  const bool two = turn || o1 < p.d;
+  const int hq = p.q.heads, hk = hq + p.k.heads;
   const int h_begin = blockIdx.y * p.head_chunk;
-  const int h_end = min(h_begin + p.head_chunk, p.q.heads + p.k.heads + p.v.heads);
+  const int h_end = min(h_begin + p.head_chunk, hk + p.v.heads);
 
   long long slot = 0;
-  if (APPEND && h_end > p.q.heads) {
+  if (APPEND && there && h_end > hq) {
     slot = __ldg(p.slots + token);
     if (slot < -1 || slot >= p.num_slots) {
       record_error(p.err, FA_ERR_BOUNDS, SITE_APPEND);
       slot = -1;
     }
   }
+  // the operand of head h (the same for a whole warp) and the row's place in it
+  auto side_of_head = [&](int h) -> const RopeSide& { return h < hq ? p.q : (h < hk ? p.k : p.v); };
+  auto head_in_side = [&](int h) { return h < hq ? h : (h < hk ? h - hq : h - hk); };
+  auto wanted = [&](int h) { return there && h < h_end && !(APPEND && h >= hq && slot < 0); };
 
-  // heads [h0, h1) of one operand, U rows in flight
-  auto rows = [&](const RopeSide& side, int h0, int h1, bool to_slot, bool rotate) {
-    const E* src = static_cast<const E*>(side.src) + b * side.sb + t * side.st;
-    E* dst = static_cast<E*>(side.dst) + (to_slot ? slot * p.slot_stride : b * side.db + t * side.dt);
-    const long long dh = to_slot ? p.d : side.dh;
-    constexpr int U = VEC == 1 ? 2 : 4;
-    for (int h = h0; h < h1; h += U) {
-      Pack<E, VEC> x[U], y[U];
+  Raw<E, VEC> x[U], y[U];
+  auto load = [&](int h0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h + u < h1) {
-          x[u].load(src + (h + u) * side.sh + o0);
-          if (two) y[u].load(src + (h + u) * side.sh + o1);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h + u < h1) {
-          if (rotate) {
-            // the pair's two values: element e of x and y, or neighbours 2e, 2e + 1 of x then y
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              float& a = !INTER ? x[u].v[e] : (2 * e < VEC ? x[u].v[(2 * e) % VEC] : y[u].v[(2 * e) % VEC]);
-              float& g = !INTER ? y[u].v[e]
-                                : (2 * e + 1 < VEC ? x[u].v[(2 * e + 1) % VEC] : y[u].v[(2 * e + 1) % VEC]);
-              const float a0 = a, g0 = g;
-              a = a0 * c[e] - g0 * s[e];
-              g = g0 * c[e] + a0 * s[e];
-            }
-          }
-          x[u].store(dst + (h + u) * dh + o0);
-          if (two) y[u].store(dst + (h + u) * dh + o1);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * kRopeWarps;
+      if (wanted(h)) {
+        const RopeSide& s = side_of_head(h);
+        const E* src = static_cast<const E*>(s.src) + b * s.sb + head_in_side(h) * s.sh + t * s.st;
+        x[u].load(src + o0);
+        if (two) y[u].load(src + o1);
+      }
     }
   };
-  const int hq = p.q.heads, hk = hq + p.k.heads;
-  if (h_begin < hq) rows(p.q, h_begin, min(h_end, hq), false, turn);
-  if (APPEND && slot < 0) return;
-  if (h_begin < hk && h_end > hq) rows(p.k, max(h_begin, hq) - hq, min(h_end, hk) - hq, APPEND, turn);
-  if (APPEND && h_end > hk) rows(p.v, max(h_begin, hk) - hk, h_end - hk, true, false);
+  load(h_begin + warp);
+
+  if (turn && there) {
+    const long long pos = __ldg(p.positions + b * p.pos_sb + t);
+    for (int e = warp; e < VEC; e += kRopeWarps) {
+      const unsigned long long a =
+          static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + lane * VEC + e));
+      float s, c;  // of the signed upper half, in half turns
+      sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
+      cs[0][e][id] = c * p.mscale;
+      cs[1][e][id] = s * p.mscale * p.sign;
+    }
+  }
+  __syncthreads();
+  if (!there) return;
+  float c[VEC], s[VEC];
+  if (turn) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      c[e] = cs[0][e][id];
+      s[e] = cs[1][e][id];
+    }
+  }
+  for (int h0 = h_begin + warp; h0 < h_end; h0 += U * kRopeWarps) {
+    if (h0 != h_begin + warp) load(h0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * kRopeWarps;
+      if (!wanted(h)) continue;
+      const RopeSide& side = side_of_head(h);
+      const bool to_slot = APPEND && h >= hq;
+      if (turn && h < hk) {
+        float xv[VEC], yv[VEC];
+        x[u].get(xv);
+        y[u].get(yv);
+        // the pair's two values: element e of x and of y, or neighbours 2e, 2e + 1 of x, then y
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float& a = !INTER ? xv[e] : (2 * e < VEC ? xv[(2 * e) % VEC] : yv[(2 * e) % VEC]);
+          float& g = !INTER ? yv[e] : (2 * e + 1 < VEC ? xv[(2 * e + 1) % VEC] : yv[(2 * e + 1) % VEC]);
+          const float a0 = a, g0 = g;
+          a = a0 * c[e] - g0 * s[e];
+          g = g0 * c[e] + a0 * s[e];
+        }
+        x[u].set(xv);
+        y[u].set(yv);
+      }
+      const long long hs = head_in_side(h);
+      E* dst = static_cast<E*>(side.dst) +
+               (to_slot ? slot * p.slot_stride + hs * p.d : b * side.db + hs * side.dh + t * side.dt);
+      x[u].store(dst + o0);
+      if (two) y[u].store(dst + o1);
+    }
+  }
 }
 
 static bool strides_ok(const RopeSide& s, int vec, bool slots) {
@@ -212,17 +237,17 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   const int w = vec ? V : 1;
   p.lanes = p.rot / 2 / w + ((p.d - p.rot) / w + 1) / 2;
   const int heads = p.q.heads + p.k.heads + p.v.heads;
-  const long long lanes = p.tokens * p.lanes;
-  if ((lanes + 255) / 256 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  // Heads per lane: as many as leave the SMs their threads, so that a lane's sines serve
-  // many rows, but not more than 16.
-  const long long room = static_cast<long long>(device_sm_count()) * 1024;
-  long long chunk = lanes * heads / room;
-  chunk = chunk < 1 ? 1 : (chunk > 16 ? 16 : chunk);
-  if (chunk > 4) chunk = chunk / 4 * 4;
+  const long long blocks = (p.tokens * p.lanes + 31) / 32;
+  if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  p.small = blocks * 32 < (1ll << 31);
+  // Heads of a block: a whole round of rows in flight for its eight warps, fewer where the
+  // blocks would leave SMs idle (a decode step).
+  const long long want = 2ll * device_sm_count();
+  int chunk = 4 * kRopeWarps;
+  while (chunk > kRopeWarps && blocks * ((heads + chunk - 1) / chunk) < want) chunk /= 2;
   while ((heads + chunk - 1) / chunk > 65535) chunk *= 2;
-  p.head_chunk = static_cast<int>(chunk);
-  const dim3 grid(static_cast<unsigned>((lanes + 255) / 256), static_cast<unsigned>((heads + chunk - 1) / chunk));
+  p.head_chunk = chunk;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + chunk - 1) / chunk));
   if (vec)
     return interleaved ? launch_dependent(rope_kernel<E, V, true, APPEND>, grid, dim3(256), 0, stream, p)
                        : launch_dependent(rope_kernel<E, V, false, APPEND>, grid, dim3(256), 0, stream, p);

@@ -785,114 +785,138 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Joins the partials of the units that several CTAs share: lse = log2 sum 2^(m_s - m) l_s
-// + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. A block reads the list of split
-// units, and takes rows of them in turn, MW warps to a row, each with every MW-th partial.
+// + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Every block makes the list of split
+// units from the CTAs' entries (in their order, so that all agree) and takes items of it
+// in turn: eight rows, a warp each, or, where a unit has many partials (few KV heads and
+// long keys), one row whose partials the eight warps share out.
+template <int D>
+struct TrRow {
+  static constexpr int N = D / 32;  // columns of a lane
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float o[N] = {};
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float (&o2)[N]) {
+    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = o[e] * fa + o2[e] * fb;
+    m = mn;
+  }
+};
+
+constexpr int kTrManyParts = 12;   // a warp reads them four at a time
+constexpr int kTrMaxGrid = 1024;   // CTAs the list has room for
+
 template <int D, int QT>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
                                                          const float4* __restrict__ part_ml,
                                                          const int4* __restrict__ split, int grid,
                                                          __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
-  constexpr int MW = 4;        // warps to a row
-  constexpr int N = D / 32;    // columns of a lane
-  constexpr int UNITS = 1024;  // most CTAs a grid may have
-  __shared__ int units[UNITS];
-  __shared__ int n_units;
+  constexpr int N = TrRow<D>::N;
+  constexpr int ROWS = kTrTile * QT;
+  __shared__ int first_item[kTrMaxGrid + 1];  // of CTA c's entry
+  __shared__ int warp_sum[8];
   __shared__ float red[8][D];
   __shared__ float red_m[8], red_s[8], red_l[8];
-  if (threadIdx.x == 0) n_units = 0;
-  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();
-  // every block makes the list in the order of the CTAs, so that all agree on it
-  if (threadIdx.x < 32) {
-    int n = 0;
-    for (int c0 = 0; c0 < grid; c0 += 32) {
-      const int c = c0 + threadIdx.x;
-      const bool is = c < grid && split[c].z >= 0;
-      const unsigned all = __ballot_sync(0xffffffffu, is);
-      if (is) units[n + __popc(all & ((1u << threadIdx.x) - 1u))] = c;
-      n += __popc(all);
+  int total = 0;
+  for (int c0 = 0; c0 < grid; c0 += 256) {
+    const int c = c0 + threadIdx.x;
+    int items = 0;
+    if (c < grid) {
+      const int4 un = split[c];
+      if (un.z >= 0) items = un.z - c >= kTrManyParts ? un.y : (un.y + 7) / 8;
     }
-    if (threadIdx.x == 0) n_units = n;
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp % MW, pair = warp / MW;  // two rows at a time
-  constexpr int ROWS = 128 * QT;
-  const int total = n_units * (ROWS / 2);
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
-    const int c = units[item / (ROWS / 2)];
-    const int4 un = split[c];
-    const int row = item % (ROWS / 2) * 2 + pair;
-    if (item % (ROWS / 2) * 2 >= un.y) continue;  // block-uniform
-    float m = -INFINITY, s = 0.f, l = 0.f;
-    float acc[N];
+    int inc = items;
 #pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    for (int k = 1; k < 32; k <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = total;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k < warp) before += warp_sum[k];
+      total += warp_sum[k];
+    }
+    if (c < grid) first_item[c] = before + inc - items;
+    __syncthreads();
+  }
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int c = 0, hi = grid;  // the last entry that begins at or before the item: entries without items begin with the next
+    while (hi - c > 1) {
+      const int mid = (c + hi) / 2;
+      if (first_item[mid] <= item) c = mid; else hi = mid;
+    }
+    const int4 un = split[c];
+    const int parts = un.z - c + 1;
+    const bool many = parts > kTrManyParts;
+    const int row = many ? item - first_item[c] : (item - first_item[c]) * 8 + warp;
+    const int step = many ? 8 : 1;
+    TrRow<D> acc;
     if (row < un.y) {
       // partial 0 is CTA c's last, the others are the later CTAs' first
       constexpr int IN = 4;
-      for (int i0 = sub; i0 <= un.z - c; i0 += MW * IN) {
+      for (int i0 = many ? warp : 0; i0 < parts; i0 += step * IN) {
         float4 ml[IN];
         float v[IN][N];
 #pragma unroll
         for (int k = 0; k < IN; ++k) {
-          const int i = i0 + k * MW;
+          const int i = i0 + k * step;
           ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-          if (i <= un.z - c) {
+          if (i < parts) {
             const size_t at = static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + row;
             ml[k] = part_ml[at];
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[k][e] = part[at * D + lane * N + e];
+            const float* src = part + at * D + lane * N;
+            if constexpr (N == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[k][0] = x.x; v[k][1] = x.y;
+            }
           }
         }
 #pragma unroll
-        for (int k = 0; k < IN; ++k) {
-          if (ml[k].x == -INFINITY) continue;  // a share without a key this row sees: its O was not written
-          const float mn = fmaxf(m, ml[k].x);
-          const float fa = ex2_approx(m - mn), fb = ex2_approx(ml[k].x - mn);
-          s = s * fa + ml[k].y * fb;
-          l = l * fa + ml[k].z * fb;
+        for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
+      }
+    }
+    if (many) {  // block-uniform
 #pragma unroll
-          for (int e = 0; e < N; ++e) acc[e] = acc[e] * fa + v[k][e] * fb;
-          m = mn;
+      for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc.o[e];
+      if (lane == 0) {
+        red_m[warp] = acc.m;
+        red_s[warp] = acc.s;
+        red_l[warp] = acc.l;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        for (int k = 1; k < 8; ++k) {
+          float v[N];
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] = red[k][lane * N + e];
+          acc.add(red_m[k], red_s[k], red_l[k], v);
         }
       }
+      __syncthreads();
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc[e];
-    if (lane == 0) {
-      red_m[warp] = m;
-      red_s[warp] = s;
-      red_l[warp] = l;
-    }
-    __syncthreads();
-    if (sub == 0 && row < un.y) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < MW; ++k) mm = fmaxf(mm, red_m[warp + k]);
-      const float m_use = mm == -INFINITY ? 0.f : mm;
-      float st = 0.f, lt = 0.f, ot[N];
-#pragma unroll
-      for (int e = 0; e < N; ++e) ot[e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < MW; ++k) {
-        const float f = ex2_approx(red_m[warp + k] - m_use);
-        st += f * red_s[warp + k];
-        lt += f * red_l[warp + k];
-#pragma unroll
-        for (int e = 0; e < N; ++e) ot[e] += f * red[warp + k][lane * N + e];
-      }
-      const float inv = st > 0.f ? 1.f / st : 0.f;
+    if (row < un.y && (!many || warp == 0)) {
+      const float inv = acc.s > 0.f ? 1.f / acc.s : 0.f;
       const size_t out = static_cast<size_t>(un.x) + row;
       __nv_bfloat16* dst = o + out * D + lane * N;
       if constexpr (N == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(ot[0] * inv, ot[1] * inv), pack_bf16x2(ot[2] * inv, ot[3] * inv));
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16x2(acc.o[0] * inv, acc.o[1] * inv), pack_bf16x2(acc.o[2] * inv, acc.o[3] * inv));
       else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(ot[0] * inv, ot[1] * inv);
-      if (lse && lane == 0) lse[out] = lt > 0.f ? (mm + log2f(lt)) * kLn2 : -INFINITY;
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc.o[0] * inv, acc.o[1] * inv);
+      if (lse && lane == 0) lse[out] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * kLn2 : -INFINITY;
     }
-    __syncthreads();
   }
 }
 
@@ -926,8 +950,8 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   if (e != cudaSuccess) return record_cuda_failure(e);
   int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (rc != FA_OK) return rc;
-  const long long items = static_cast<long long>(grid) * (kTrTile * C::QT / 2);
-  const int merge_grid = static_cast<int>(items < 2 * grid ? items : 2 * grid);
+  // four blocks to an SM: a warp for most rows that can be split
+  const int merge_grid = 4 * grid;
   return launch_dependent(tree_merge_kernel<D, C::QT>, dim3(merge_grid), dim3(256), 0, stream,
                           static_cast<const float*>(p.part), static_cast<const float4*>(p.part_ml),
                           static_cast<const int4*>(p.split), grid, p.o, p.lse);
@@ -972,7 +996,7 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
   if (steps == 0) return FA_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
-  if (sms > 1024) return FA_ERR_UNSUPPORTED;
+  if (sms > kTrMaxGrid) return FA_ERR_UNSUPPORTED;
   if (ws_bytes < fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, sms)) return FA_ERR_INVALID_ARG;
   const int grid = tr_grid(steps, sms);
   EncodeTiledFn enc = get_encode_tiled();
