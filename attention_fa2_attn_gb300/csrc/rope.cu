@@ -240,12 +240,13 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   const long long blocks = (p.tokens * p.lanes + 31) / 32;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   p.small = blocks * 32 < (1ll << 31);
-  // Heads of a block: a whole round of rows in flight for its eight warps, fewer where the
-  // blocks would leave SMs idle (a decode step).
-  const long long want = 2ll * device_sm_count();
-  int chunk = 4 * kRopeWarps;
-  while (chunk > kRopeWarps && blocks * ((heads + chunk - 1) / chunk) < want) chunk /= 2;
-  while ((heads + chunk - 1) / chunk > 65535) chunk *= 2;
+  // Heads of a block: a round of rows in flight for its eight warps (a warp's U heads are
+  // kRopeWarps apart), in even chunks; one row a warp where the blocks would leave SMs idle
+  // (a decode step).
+  int cuts = (heads + 4 * kRopeWarps - 1) / (4 * kRopeWarps);
+  const int most = (heads + kRopeWarps - 1) / kRopeWarps;
+  while (cuts < most && blocks * cuts < 2ll * device_sm_count()) cuts = cuts * 2 < most ? cuts * 2 : most;
+  const int chunk = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps * kRopeWarps;
   p.head_chunk = chunk;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + chunk - 1) / chunk));
   if (vec)

@@ -112,10 +112,12 @@ __device__ __forceinline__ TrSeq tr_seq(const TrParams& p, int b) {
   return s;
 }
 // Steps of one (KV head, row unit): a key tile, or (narrow) a pair of them; a unit
-// without keys is one step, so that somebody writes its zeros.
+// without keys is one step, so that somebody writes its zeros. What a unit costs beside
+// its tiles (Q, the first S, writing O) counts as kTrExtra steps at its front.
+constexpr int kTrExtra = 1;
 template <bool WIDE>
 __device__ __forceinline__ int tr_steps(const TrSeq& s) {
-  return max(1, WIDE ? s.tiles : (s.tiles + 1) / 2);
+  return kTrExtra + max(1, WIDE ? s.tiles : (s.tiles + 1) / 2);
 }
 
 // A run of steps of one unit inside a CTA's share.
@@ -133,21 +135,26 @@ struct TrWalk {
   int b, off, at, end;  // sequence, steps into it; global step; the share's end
   __device__ __forceinline__ TrWalk(const TrBars* s) : b(s->b0), off(s->off0), at(s->begin), end(s->end) {}
   __device__ __forceinline__ bool next(const TrParams& p, TrSeg& g) {
-    if (at >= end) return false;
-    const TrSeq q = tr_seq(p, b);
-    const int steps = tr_steps<WIDE>(q);
-    const int hu = off / steps;
-    const int j0 = off - hu * steps;
-    const int ns = min(steps - j0, end - at);
+    TrSeq q;
+    int steps, hu, j0, ns;
+    do {  // a share that ends inside a unit's front leaves the whole unit to the next CTA
+      if (at >= end) return false;
+      q = tr_seq(p, b);
+      steps = tr_steps<WIDE>(q);
+      hu = off / steps;
+      j0 = off - hu * steps;
+      ns = min(steps - j0, end - at);
+      if (j0 + ns <= kTrExtra) at += ns;
+    } while (j0 + ns <= kTrExtra);
     constexpr int PER = WIDE ? 1 : 2;
     g.b = b;
     g.kvh = hu / p.U;
     g.u = hu - g.kvh * p.U;
     g.S = q.S;
     g.n = q.n;
-    g.x0 = j0 * PER;
-    g.nt = max(0, min(q.tiles, (j0 + ns) * PER) - g.x0);
-    g.from_start = j0 == 0;
+    g.x0 = max(0, j0 - kTrExtra) * PER;
+    g.nt = max(0, min(q.tiles, (j0 + ns - kTrExtra) * PER) - g.x0);
+    g.from_start = g.x0 == 0;
     g.to_end = j0 + ns == steps;
     g.unit_end = at - j0 + steps;
     off += ns;
@@ -159,6 +166,19 @@ struct TrWalk {
     return true;
   }
 };
+
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 __device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
   uint32_t r;
@@ -309,39 +329,58 @@ __global__ void __launch_bounds__(384, 1)
       const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
       bool ok = true;
       while (ok && !*abort_flag && walk.next(p, w)) {
-        if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&bars->q_full, C::QT * C::Q_BYTES);
-          for (int t = 0; t < C::QT; ++t)
-            for (int c = 0; c < C::KCH; ++c)
-              tma_load_3d(sQ + t * C::Q_BYTES + c * C::CHUNK_BYTES, &tmQ, &bars->q_full, c * 64,
-                          (w.u * C::QT + t) * kTrTile, w.b * p.Hkv + w.kvh);
-        }
-        ++q_loads;
         const int* trow = p.block_table + static_cast<size_t>(w.b) * p.max_pages;
         const int n_pages = (w.S + 15) >> 4;
-        // lane i < 8 holds the entry of page 8x + i; the next tile's are fetched meanwhile
+        // a lane holds one of 32 entries, four tiles' worth; the next 32 are fetched meanwhile
+        // (one tile ahead would leave an L2 round trip in every tile)
         auto fetch = [&](int x) -> int {
           const int pg = (w.x0 + x) * 8 + lane;
-          return lane < 8 && x < w.nt && pg < n_pages ? __ldg(trow + pg) : -1;
+          return pg < n_pages && pg < (w.x0 + w.nt) * 8 ? __ldg(trow + pg) : -1;
         };
-        int ent_next = fetch(0);
+        int ent = -1, ent_next = fetch(0);
+        // The last segment's Q is in use until its last S: this one's first tiles go ahead
+        // of its Q (all but one stage of the ring, which that segment's own end frees).
+        bool q_due = true;
+        auto load_q = [&]() {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full, C::QT * C::Q_BYTES);
+            for (int t = 0; t < C::QT; ++t)
+              for (int c = 0; c < C::KCH; ++c)
+                tma_load_3d(sQ + t * C::Q_BYTES + c * C::CHUNK_BYTES, &tmQ, &bars->q_full, c * 64,
+                            (w.u * C::QT + t) * kTrTile, w.b * p.Hkv + w.kvh);
+          }
+          ++q_loads;
+          q_due = false;
+        };
+        auto q_free = [&]() {  // uniform: every lane asks, and one answer counts
+          return q_loads == 0 || __all_sync(0xffffffffu, mbar_test(&bars->q_empty, (q_loads - 1) & 1));
+        };
         for (int x = 0; x < w.nt; ++x, ++g) {
+          if (q_due) {
+            if (q_free()) {
+              load_q();
+            } else if (x == ST - 1) {
+              if (!mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
+                ok = false;
+                break;
+              }
+              load_q();
+            }
+          }
           const int s = g % ST;
           const uint32_t u = g / ST;
-          int ent = ent_next;
-          ent_next = fetch(x + 1);
+          if ((x & 3) == 0) {
+            ent = ent_next;
+            ent_next = fetch(x + 4);
+          }
           const int npg = min(8, n_pages - (w.x0 + x) * 8);  // pages past the end are not loaded
-          if (lane < npg && (ent < 0 || ent >= p.num_pages)) {
+          const uint32_t bytes = static_cast<uint32_t>(npg) * 16 * 128 * C::KCH;
+          int pe = __shfl_sync(0xffffffffu, ent, (x & 3) * 8 + (pi & 7));
+          if (pi < npg && (pe < 0 || pe >= p.num_pages)) {
             // never dereferenced: page 0 is loaded in its place, the output is undefined
             record_error(p.err, FA_ERR_BOUNDS, SITE_TR_TABLE);
-            ent = 0;
+            pe = 0;
           }
-          const uint32_t bytes = static_cast<uint32_t>(npg) * 16 * 128 * C::KCH;
-          const int pe = __shfl_sync(0xffffffffu, ent, pi & 7);
           if (g >= ST && !mbar_wait(&bars->k_empty[s], (u - 1) & 1, tmo, abort_flag)) {
             ok = false;
             break;
@@ -361,6 +400,12 @@ __global__ void __launch_bounds__(384, 1)
           if (pi < npg)
             tma_load_3d(sV + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, &tmV, &bars->v_full[s], pc * 64,
                         w.kvh, pe * 16);
+        }
+        if (ok && q_due) {
+          if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
+            ok = false;
+          else
+            load_q();
         }
       }
       if (!ok) fail(SITE_TR_PRODUCER);
@@ -572,12 +617,18 @@ __global__ void __launch_bounds__(384, 1)
 
       for (int i = 0; i < mine; ++i, ++cnt) {
         const int x = x_first + i * step;  // tile of the segment
+        const int key0 = (w.x0 + x) * kTrTile;
+        const bool masked = key0 + kTrTile > base;
+        uint32_t bits[4];  // fetched while S is being computed
+        if (masked) {
+#pragma unroll
+          for (int wd = 0; wd < 4; ++wd) bits[wd] = live ? tr_bits(mrow, p.words, w.n, key0 + 32 * wd - base) : 0u;
+        }
         if (!wwait(&bars->s_full[t], cnt & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int key0 = (w.x0 + x) * kTrTile;
         if (has_rows) {
           uint32_t raw[4][32];
 #pragma unroll
@@ -586,14 +637,10 @@ __global__ void __launch_bounds__(384, 1)
           float s[128];
 #pragma unroll
           for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(raw[k >> 5][k & 31]);
-          if (key0 + kTrTile > base) {
+          if (masked) {
 #pragma unroll
-            for (int wd = 0; wd < 4; ++wd) {
-              const uint32_t bits = live ? tr_bits(mrow, p.words, w.n, key0 + 32 * wd - base) : 0u;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((bits >> k) & 1u)) s[32 * wd + k] = -INFINITY;
-            }
+            for (int k = 0; k < 128; ++k)
+              if (!((bits[k / 32] >> (k % 32)) & 1u)) s[k] = -INFINITY;
           }
           float mx8[8];
 #pragma unroll
@@ -787,7 +834,7 @@ __global__ void __launch_bounds__(384, 1)
 // Joins the partials of the units that several CTAs share: lse = log2 sum 2^(m_s - m) l_s
 // + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Every block makes the list of split
 // units from the CTAs' entries (in their order, so that all agree) and takes items of it
-// in turn: eight rows, a warp each, or, where a unit has many partials (few KV heads and
+// in turn: rows, two to a warp, or, where a unit has many partials (few KV heads and
 // long keys), one row whose partials the eight warps share out.
 template <int D>
 struct TrRow {
@@ -806,16 +853,18 @@ struct TrRow {
   }
 };
 
-constexpr int kTrManyParts = 12;   // a warp reads them four at a time
+constexpr int kTrManyParts = 6;    // up to here a warp reads them two at a time
+constexpr int kTrRowsPerWarp = 2;  // ... of two rows
 constexpr int kTrMaxGrid = 1024;   // CTAs the list has room for
 
 template <int D, int QT>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const float* __restrict__ part,
                                                          const float4* __restrict__ part_ml,
                                                          const int4* __restrict__ split, int grid,
                                                          __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
   constexpr int N = TrRow<D>::N;
   constexpr int ROWS = kTrTile * QT;
+  constexpr int RW = kTrRowsPerWarp;
   __shared__ int first_item[kTrMaxGrid + 1];  // of CTA c's entry
   __shared__ int warp_sum[8];
   __shared__ float red[8][D];
@@ -829,7 +878,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
     int items = 0;
     if (c < grid) {
       const int4 un = split[c];
-      if (un.z >= 0) items = un.z - c >= kTrManyParts ? un.y : (un.y + 7) / 8;
+      if (un.z >= 0) items = un.z - c >= kTrManyParts ? un.y : (un.y + 8 * RW - 1) / (8 * RW);
     }
     int inc = items;
 #pragma unroll
@@ -856,38 +905,67 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
     }
     const int4 un = split[c];
     const int parts = un.z - c + 1;
-    const bool many = parts > kTrManyParts;
-    const int row = many ? item - first_item[c] : (item - first_item[c]) * 8 + warp;
-    const int step = many ? 8 : 1;
-    TrRow<D> acc;
-    if (row < un.y) {
-      // partial 0 is CTA c's last, the others are the later CTAs' first
+    // partial 0 is CTA c's last, the others are the later CTAs' first
+    auto at = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS; };
+    auto get = [&](float4& ml, float (&v)[N], size_t row_at) {
+      ml = part_ml[row_at];
+      const float* src = part + row_at * D + lane * N;
+      if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x; v[1] = x.y;
+      }
+    };
+    auto put = [&](const TrRow<D>& r, int row) {
+      const float inv = r.s > 0.f ? 1.f / r.s : 0.f;
+      const size_t out = static_cast<size_t>(un.x) + row;
+      __nv_bfloat16* dst = o + out * D + lane * N;
+      if constexpr (N == 4)
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16x2(r.o[0] * inv, r.o[1] * inv), pack_bf16x2(r.o[2] * inv, r.o[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(r.o[0] * inv, r.o[1] * inv);
+      if (lse && lane == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
+    };
+    if (parts <= kTrManyParts) {
+      constexpr int IN = 2;
+      const int row0 = ((item - first_item[c]) * 8 + warp) * RW;
+      TrRow<D> acc[RW];
+      for (int i0 = 0; i0 < parts; i0 += IN) {
+        float4 ml[IN][RW];
+        float v[IN][RW][N];
+#pragma unroll
+        for (int k = 0; k < IN; ++k)
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            ml[k][r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            if (i0 + k < parts && row0 + r < un.y) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r);
+          }
+#pragma unroll
+        for (int k = 0; k < IN; ++k)
+#pragma unroll
+          for (int r = 0; r < RW; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
+      }
+#pragma unroll
+      for (int r = 0; r < RW; ++r)
+        if (row0 + r < un.y) put(acc[r], row0 + r);
+    } else {  // block-uniform: one row, each warp with every eighth partial
       constexpr int IN = 4;
-      for (int i0 = many ? warp : 0; i0 < parts; i0 += step * IN) {
+      const int row = item - first_item[c];
+      TrRow<D> acc;
+      for (int i0 = warp; i0 < parts; i0 += 8 * IN) {
         float4 ml[IN];
         float v[IN][N];
 #pragma unroll
         for (int k = 0; k < IN; ++k) {
-          const int i = i0 + k * step;
           ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-          if (i < parts) {
-            const size_t at = static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS + row;
-            ml[k] = part_ml[at];
-            const float* src = part + at * D + lane * N;
-            if constexpr (N == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src);
-              v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-            } else {
-              const float2 x = *reinterpret_cast<const float2*>(src);
-              v[k][0] = x.x; v[k][1] = x.y;
-            }
-          }
+          if (i0 + 8 * k < parts) get(ml[k], v[k], at(i0 + 8 * k) + row);
         }
 #pragma unroll
         for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
       }
-    }
-    if (many) {  // block-uniform
 #pragma unroll
       for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc.o[e];
       if (lane == 0) {
@@ -903,19 +981,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const float* __restrict
           for (int e = 0; e < N; ++e) v[e] = red[k][lane * N + e];
           acc.add(red_m[k], red_s[k], red_l[k], v);
         }
+        put(acc, row);
       }
       __syncthreads();
-    }
-    if (row < un.y && (!many || warp == 0)) {
-      const float inv = acc.s > 0.f ? 1.f / acc.s : 0.f;
-      const size_t out = static_cast<size_t>(un.x) + row;
-      __nv_bfloat16* dst = o + out * D + lane * N;
-      if constexpr (N == 4)
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack_bf16x2(acc.o[0] * inv, acc.o[1] * inv), pack_bf16x2(acc.o[2] * inv, acc.o[3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc.o[0] * inv, acc.o[1] * inv);
-      if (lse && lane == 0) lse[out] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * kLn2 : -INFINITY;
     }
   }
 }
@@ -929,7 +997,7 @@ static bool tr_wide(int R) { return R > kTrTile; }
 static long long tr_most_steps(int B, int Hkv, int R, int max_pages) {
   const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
   const long long tiles = (static_cast<long long>(max_pages) * 16 + kTrTile - 1) / kTrTile;
-  const long long steps = tr_wide(R) ? tiles : (tiles + 1) / 2;
+  const long long steps = kTrExtra + (tr_wide(R) ? tiles : (tiles + 1) / 2);
   const long long n = static_cast<long long>(B) * Hkv * U;
   return n > ((1ll << 31) - 1) / steps ? 0 : n * steps;
 }
@@ -950,8 +1018,7 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   if (e != cudaSuccess) return record_cuda_failure(e);
   int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (rc != FA_OK) return rc;
-  // four blocks to an SM: a warp for most rows that can be split
-  const int merge_grid = 4 * grid;
+  const int merge_grid = 3 * grid;  // what an SM holds of it
   return launch_dependent(tree_merge_kernel<D, C::QT>, dim3(merge_grid), dim3(256), 0, stream,
                           static_cast<const float*>(p.part), static_cast<const float4*>(p.part_ml),
                           static_cast<const int4*>(p.split), grid, p.o, p.lse);
