@@ -33,6 +33,8 @@
 //     its 128 bits of the tile in four registers. Rows of padding warps are skipped.
 // Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the
 // CTA unwinds. The softmax warps leave together by a vote at the barrier they share.
+#include <atomic>
+
 #include "launch.cuh"
 
 namespace fa {
@@ -59,6 +61,7 @@ struct TrCfg {
   static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
   static constexpr int OFF_EX = OFF_BAR + 384;
   static constexpr int SMEM = OFF_EX + kTrTile * 5 * 4;  // at most 227 KB; the base is 1024-byte aligned
+  static constexpr int LEAST = WIDE ? 4 : 1;
   static constexpr int TMEM_COLS = 512;
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
@@ -280,8 +283,10 @@ __global__ void __launch_bounds__(384, 1)
       if (w < warp) before += wsum[w];
       total += wsum[w];
     }
-    // as many CTAs share the work as there are steps
-    const int G = min(static_cast<int>(gridDim.x), total);
+    // A CTA gets LEAST steps at least: each more that shares a unit writes and the merge
+    // reads a partial of its rows, which costs as much as some steps when the rows are many.
+    // No CTA gets two units while others get none.
+    const int G = min(static_cast<int>(gridDim.x), max(total / C::LEAST, p.B * p.Hkv * p.U));
     const int begin = cta < G ? static_cast<int>(static_cast<long long>(cta) * total / G) : total;
     const int end = cta < G ? static_cast<int>((cta + 1ll) * total / G) : total;
     if (threadIdx.x == 0) {
@@ -833,9 +838,11 @@ __global__ void __launch_bounds__(384, 1)
 
 // Joins the partials of the units that several CTAs share: lse = log2 sum 2^(m_s - m) l_s
 // + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Every block makes the list of split
-// units from the CTAs' entries (in their order, so that all agree) and takes items of it
-// in turn: rows, two to a warp, or, where a unit has many partials (few KV heads and
-// long keys), one row whose partials the eight warps share out.
+// units from the CTAs' entries (in their order, so that all agree), keeps it in shared
+// memory and takes items of it in turn. What a row costs is round trips to L2, so: units
+// of up to four partials go two rows to a warp, all of them in flight; the others one
+// row to 1, 2, 4 or 8 warps (as many as the rows leave warps for), four partials each in
+// flight.
 template <int D>
 struct TrRow {
   static constexpr int N = D / 32;  // columns of a lane
@@ -853,58 +860,87 @@ struct TrRow {
   }
 };
 
-constexpr int kTrManyParts = 6;    // up to here a warp reads them two at a time
-constexpr int kTrRowsPerWarp = 2;  // ... of two rows
-constexpr int kTrMaxGrid = 1024;   // CTAs the list has room for
+constexpr int kTrMaxGrid = 1024;  // CTAs the list has room for
+constexpr int kTrFewParts = 4;
+constexpr int kTrMergeBlocks = 3;  // per SM
+
+struct TrUnit {
+  int first_item, row0, rows, parts;
+};
+
+// Block-wide inclusive scan of 256 values; *total gets their sum.
+__device__ __forceinline__ int scan256(int v, int* warp_sum, int* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, k);
+    if (lane >= k) v += y;
+  }
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k < warp) v += warp_sum[k];
+    all += warp_sum[k];
+  }
+  __syncthreads();
+  *total = all;
+  return v;
+}
 
 template <int D, int QT>
-__global__ void __launch_bounds__(256, 3) tree_merge_kernel(const float* __restrict__ part,
-                                                         const float4* __restrict__ part_ml,
-                                                         const int4* __restrict__ split, int grid,
-                                                         __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+__global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const float* __restrict__ part,
+                                                                         const float4* __restrict__ part_ml,
+                                                                         const int4* __restrict__ split, int grid,
+                                                                         __nv_bfloat16* __restrict__ o,
+                                                                         float* __restrict__ lse) {
   constexpr int N = TrRow<D>::N;
   constexpr int ROWS = kTrTile * QT;
-  constexpr int RW = kTrRowsPerWarp;
-  __shared__ int first_item[kTrMaxGrid + 1];  // of CTA c's entry
+  __shared__ TrUnit unit[kTrMaxGrid];  // by CTA; those of CTAs without an entry have no items
   __shared__ int warp_sum[8];
   __shared__ float red[8][D];
   __shared__ float red_m[8], red_s[8], red_l[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();
+  int many_rows = 0;  // rows of units with more than a few partials
+  for (int c0 = 0; c0 < grid; c0 += 256) {
+    const int c = c0 + threadIdx.x;
+    TrUnit u = {0, 0, 0, 0};
+    if (c < grid) {
+      const int4 un = split[c];
+      if (un.z >= 0) u = {0, un.x, un.y, un.z - c + 1};
+      unit[c] = u;
+    }
+    int sum;
+    scan256(u.parts > kTrFewParts ? u.rows : 0, warp_sum, &sum);
+    many_rows += sum;
+  }
+  int wpr = 8;  // warps to a row
+  while (wpr > 1 && many_rows * wpr > 16 * static_cast<int>(gridDim.x)) wpr >>= 1;
+  const int few_rows = 8 * 2, many_step = 8 / wpr;  // rows of an item
   int total = 0;
   for (int c0 = 0; c0 < grid; c0 += 256) {
     const int c = c0 + threadIdx.x;
     int items = 0;
     if (c < grid) {
-      const int4 un = split[c];
-      if (un.z >= 0) items = un.z - c >= kTrManyParts ? un.y : (un.y + 8 * RW - 1) / (8 * RW);
+      const int per = unit[c].parts > kTrFewParts ? many_step : few_rows;
+      items = (unit[c].rows + per - 1) / per;
     }
-    int inc = items;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, k);
-      if (lane >= k) inc += y;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = total;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k < warp) before += warp_sum[k];
-      total += warp_sum[k];
-    }
-    if (c < grid) first_item[c] = before + inc - items;
-    __syncthreads();
+    int sum;
+    const int inc = scan256(items, warp_sum, &sum);
+    if (c < grid) unit[c].first_item = total + inc - items;
+    total += sum;
   }
+  __syncthreads();
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int c = 0, hi = grid;  // the last entry that begins at or before the item: entries without items begin with the next
     while (hi - c > 1) {
       const int mid = (c + hi) / 2;
-      if (first_item[mid] <= item) c = mid; else hi = mid;
+      if (unit[mid].first_item <= item) c = mid; else hi = mid;
     }
-    const int4 un = split[c];
-    const int parts = un.z - c + 1;
+    const TrUnit un = unit[c];
     // partial 0 is CTA c's last, the others are the later CTAs' first
     auto at = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS; };
     auto get = [&](float4& ml, float (&v)[N], size_t row_at) {
@@ -920,7 +956,7 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const float* __restr
     };
     auto put = [&](const TrRow<D>& r, int row) {
       const float inv = r.s > 0.f ? 1.f / r.s : 0.f;
-      const size_t out = static_cast<size_t>(un.x) + row;
+      const size_t out = static_cast<size_t>(un.row0) + row;
       __nv_bfloat16* dst = o + out * D + lane * N;
       if constexpr (N == 4)
         *reinterpret_cast<uint2*>(dst) =
@@ -929,61 +965,64 @@ __global__ void __launch_bounds__(256, 3) tree_merge_kernel(const float* __restr
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(r.o[0] * inv, r.o[1] * inv);
       if (lse && lane == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
     };
-    if (parts <= kTrManyParts) {
+    if (un.parts <= kTrFewParts) {
       constexpr int IN = 2;
-      const int row0 = ((item - first_item[c]) * 8 + warp) * RW;
-      TrRow<D> acc[RW];
-      for (int i0 = 0; i0 < parts; i0 += IN) {
-        float4 ml[IN][RW];
-        float v[IN][RW][N];
+      const int row0 = (item - un.first_item) * few_rows + warp * 2;
+      TrRow<D> acc[2];
+      for (int i0 = 0; i0 < un.parts; i0 += IN) {
+        float4 ml[IN][2];
+        float v[IN][2][N];
 #pragma unroll
         for (int k = 0; k < IN; ++k)
 #pragma unroll
-          for (int r = 0; r < RW; ++r) {
+          for (int r = 0; r < 2; ++r) {
             ml[k][r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            if (i0 + k < parts && row0 + r < un.y) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r);
+            if (i0 + k < un.parts && row0 + r < un.rows) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r);
           }
 #pragma unroll
         for (int k = 0; k < IN; ++k)
 #pragma unroll
-          for (int r = 0; r < RW; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
+          for (int r = 0; r < 2; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
       }
 #pragma unroll
-      for (int r = 0; r < RW; ++r)
-        if (row0 + r < un.y) put(acc[r], row0 + r);
-    } else {  // block-uniform: one row, each warp with every eighth partial
+      for (int r = 0; r < 2; ++r)
+        if (row0 + r < un.rows) put(acc[r], row0 + r);
+    } else {
       constexpr int IN = 4;
-      const int row = item - first_item[c];
+      const int sub = warp & (wpr - 1);
+      const int row = (item - un.first_item) * many_step + warp / wpr;
       TrRow<D> acc;
-      for (int i0 = warp; i0 < parts; i0 += 8 * IN) {
+      for (int i0 = sub; i0 < un.parts; i0 += wpr * IN) {
         float4 ml[IN];
         float v[IN][N];
 #pragma unroll
         for (int k = 0; k < IN; ++k) {
           ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-          if (i0 + 8 * k < parts) get(ml[k], v[k], at(i0 + 8 * k) + row);
+          if (i0 + wpr * k < un.parts && row < un.rows) get(ml[k], v[k], at(i0 + wpr * k) + row);
         }
 #pragma unroll
         for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
       }
+      if (wpr > 1) {  // block-uniform
 #pragma unroll
-      for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc.o[e];
-      if (lane == 0) {
-        red_m[warp] = acc.m;
-        red_s[warp] = acc.s;
-        red_l[warp] = acc.l;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        for (int k = 1; k < 8; ++k) {
-          float v[N];
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = red[k][lane * N + e];
-          acc.add(red_m[k], red_s[k], red_l[k], v);
+        for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc.o[e];
+        if (lane == 0) {
+          red_m[warp] = acc.m;
+          red_s[warp] = acc.s;
+          red_l[warp] = acc.l;
         }
-        put(acc, row);
+        __syncthreads();
+        if (sub == 0) {
+          for (int k = warp + 1; k < warp + wpr; ++k) {
+            float v[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = red[k][lane * N + e];
+            acc.add(red_m[k], red_s[k], red_l[k], v);
+          }
+        }
+        __syncthreads();
       }
-      __syncthreads();
+      if (sub == 0 && row < un.rows) put(acc, row);
     }
   }
 }
@@ -1014,11 +1053,20 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
                        int grid, cudaStream_t stream) {
   using C = TrCfg<D, WIDE>;
   auto kfn = tree_kernel<D, WIDE>;
-  const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  // the attribute holds for the life of the device's context: asked for once per device
+  static std::atomic<unsigned long long> asked{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return record_cuda_failure(e);
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return record_cuda_failure(e);
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
   int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (rc != FA_OK) return rc;
-  const int merge_grid = 3 * grid;  // what an SM holds of it
+  const int merge_grid = kTrMergeBlocks * grid;
   return launch_dependent(tree_merge_kernel<D, C::QT>, dim3(merge_grid), dim3(256), 0, stream,
                           static_cast<const float*>(p.part), static_cast<const float4*>(p.part_ml),
                           static_cast<const int4*>(p.split), grid, p.o, p.lse);
