@@ -8,6 +8,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 
@@ -101,6 +102,21 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
         f.argtypes = args
     _lib = l
     return l
+
+
+_fast_calls = None
+
+
+def fast():
+    """The extension module ``_fast`` (the step calls from Python objects to the library),
+    loaded after the library it is linked to."""
+    global _fast_calls
+    if _fast_calls is None:
+        lib()
+        spec = importlib.util.spec_from_file_location("_fast", _build.FAST_PATH)
+        _fast_calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fast_calls)
+    return _fast_calls
 
 
 class FAError(RuntimeError):

@@ -9,13 +9,11 @@ in the library's kernels.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
-import struct
 
 import torch
 
-from ._lib import FA_DTYPE_BF16, FA_DTYPE_F32, FA_ROPE_SCALINGS, FAError, check, lib
+from ._lib import FA_DTYPE_BF16, FA_DTYPE_F32, FA_ROPE_SCALINGS, FAError, check, fast, lib
 
 
 def _ptr(t: torch.Tensor | None):
@@ -290,11 +288,16 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bool = Tr
 
 
 # What follows is called between the layers of a decode step, where a microsecond of the
-# host counts: each call tests its arguments in one expression first, and only where that
-# fails goes through the checks one by one, for the error that names the argument.
+# host counts. With no output given, a call goes through the extension module first
+# (fast(): the same tests, outputs and library call, in one step); it answers None where
+# an argument is not plainly right, and the checks below then name it.
 _BF16, _I32, _F64 = torch.bfloat16, torch.int32, torch.float64
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_ODD = (AttributeError, TypeError, ValueError, RuntimeError)  # what a wrong argument raises in such a test
+
+
+def _answer(got, name: str):
+    if type(got) is int:
+        check(got, name)
+    return got
 
 
 def _need_ints(name: str, t: torch.Tensor, shape, device):
@@ -303,88 +306,56 @@ def _need_ints(name: str, t: torch.Tensor, shape, device):
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
 
 
-def _ints(t, shape, dev: int) -> bool:
-    return t.dtype is _I32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-
-
-def _check_plan(cached_lens, new_lens, free_pages, block_table):
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(free_pages, "free_pages", torch.int32, 1)
-    _need_ints("cached_lens", cached_lens, block_table.shape[:1], block_table.device)
-    _need_ints("new_lens", new_lens, block_table.shape[:1], block_table.device)
-    if free_pages.device != block_table.device:
-        raise ValueError(f"free_pages must be on {block_table.device}")
-    _on_current_device(block_table)
-
-
 def fa_paged_plan(cached_lens, new_lens, free_pages, block_table, T: int, align_end: bool = False, seqlens=None,
                   slots=None, positions=None, pages_used=None):
     """Block tables, slot maps and positions of a step: cached_lens, new_lens [B], free_pages [F],
     block_table [B][max_pages] (extended in place), all int32 on one device
-    -> (seqlens [B], slots [B][T], positions [B][T], pages_used [1]), new ones as parts of one buffer."""
-    try:
-        dev = block_table.get_device()
-        B, max_pages = block_table.shape
-        num_free, = free_pages.shape
-        fine = (dev == _current_device() and _ints(block_table, (B, max_pages), dev)
-                and _ints(free_pages, (num_free,), dev) and _ints(cached_lens, (B,), dev) and _ints(new_lens, (B,), dev))
-    except _ODD:
-        fine = False
-    if not fine:
-        _check_plan(cached_lens, new_lens, free_pages, block_table)
+    -> (seqlens [B], slots [B][T], positions [B][T], pages_used [1])."""
+    if seqlens is None and slots is None and positions is None and pages_used is None:
+        got = fast().paged_plan(cached_lens, new_lens, free_pages, block_table, T, align_end)
+        if got is not None:
+            return _answer(got, "fa_paged_plan")
+    _need(block_table, "block_table", _I32, 2)
+    _need(free_pages, "free_pages", _I32, 1)
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    _need_ints("cached_lens", cached_lens, (B,), dev)
+    _need_ints("new_lens", new_lens, (B,), dev)
+    if free_pages.device != dev:
+        raise ValueError(f"free_pages must be on {dev}")
+    _on_current_device(block_table)
     T = int(T)
-    if seqlens is None and slots is None and positions is None and pages_used is None and T > 0:
-        # one allocation; rows of slots and positions start at 16-byte borders
-        n, head = (B * T + 3) & ~3, (B + 4) & ~3
-        buf = torch.empty(head + 2 * n, dtype=_I32, device=block_table.device)
-        seqlens, pages_used = buf.as_strided((B,), (1,)), buf.as_strided((1,), (1,), head - 1)
-        slots, positions = buf.as_strided((B, T), (T, 1), head), buf.as_strided((B, T), (T, 1), head + n)
-    else:
-        seqlens = _out(seqlens, "seqlens", (B,), _I32, block_table)
-        slots = _out(slots, "slots", (B, T), _I32, block_table)
-        positions = _out(positions, "positions", (B, T), _I32, block_table)
-        pages_used = _out(pages_used, "pages_used", (1,), _I32, block_table)
-    st = lib().fa_paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), num_free,
-                             block_table.data_ptr(), seqlens.data_ptr(), slots.data_ptr(), positions.data_ptr(),
-                             pages_used.data_ptr(), B, T, max_pages, 16, bool(align_end), _stream(block_table))
-    if st:
-        check(st, "fa_paged_plan")
+    if T < 1:
+        raise ValueError(f"T must be at least 1, got {T}")
+    seqlens = _out(seqlens, "seqlens", (B,), _I32, block_table)
+    slots = _out(slots, "slots", (B, T), _I32, block_table)
+    positions = _out(positions, "positions", (B, T), _I32, block_table)
+    pages_used = _out(pages_used, "pages_used", (1,), _I32, block_table)
+    st = lib().fa_paged_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_pages), free_pages.shape[0],
+                             _ptr(block_table), _ptr(seqlens), _ptr(slots), _ptr(positions), _ptr(pages_used), B, T,
+                             max_pages, 16, int(align_end), _stream(block_table))
+    check(st, "fa_paged_plan")
     return seqlens, slots, positions, pages_used
-
-
-def _check_tree_mask(parents, seqlens, tree_lens):
-    _need(parents, "parents", torch.int32, 2)
-    _need_ints("seqlens", seqlens, parents.shape[:1], parents.device)
-    if tree_lens is not None:
-        _need_ints("tree_lens", tree_lens, parents.shape[:1], parents.device)
-    _on_current_device(parents)
 
 
 def fa_tree_mask(parents, seqlens, tree_lens=None, mask=None, positions=None):
     """Visibility mask and positions of drafted trees: parents [B][T], seqlens [B], tree_lens [B] or
-    None (T nodes each), int32 -> (mask [B][T][ceil(T/32)] int32, positions [B][T] int32), new ones as
-    parts of one buffer."""
-    try:
-        dev = parents.get_device()
-        B, T = parents.shape
-        fine = (dev == _current_device() and _ints(parents, (B, T), dev) and _ints(seqlens, (B,), dev)
-                and (tree_lens is None or _ints(tree_lens, (B,), dev)))
-    except _ODD:
-        fine = False
-    if not fine:
-        _check_tree_mask(parents, seqlens, tree_lens)
-    words = (T + 31) // 32
+    None (T nodes each), int32 -> (mask [B][T][ceil(T/32)] int32, positions [B][T] int32)."""
     if mask is None and positions is None:
-        n = (B * T * words + 3) & ~3
-        buf = torch.empty(n + B * T, dtype=_I32, device=parents.device)
-        mask, positions = buf.as_strided((B, T, words), (T * words, words, 1)), buf.as_strided((B, T), (T, 1), n)
-    else:
-        mask = _out(mask, "mask", (B, T, words), _I32, parents)
-        positions = _out(positions, "positions", (B, T), _I32, parents)
-    st = lib().fa_tree_mask(parents.data_ptr(), seqlens.data_ptr(), _ptr(tree_lens), mask.data_ptr(),
-                            positions.data_ptr(), B, T, _stream(parents))
-    if st:
-        check(st, "fa_tree_mask")
+        got = fast().tree_mask(parents, seqlens, tree_lens)
+        if got is not None:
+            return _answer(got, "fa_tree_mask")
+    _need(parents, "parents", _I32, 2)
+    B, T = parents.shape
+    _need_ints("seqlens", seqlens, (B,), parents.device)
+    if tree_lens is not None:
+        _need_ints("tree_lens", tree_lens, (B,), parents.device)
+    _on_current_device(parents)
+    mask = _out(mask, "mask", (B, T, (T + 31) // 32), _I32, parents)
+    positions = _out(positions, "positions", (B, T), _I32, parents)
+    st = lib().fa_tree_mask(_ptr(parents), _ptr(seqlens), _ptr(tree_lens), _ptr(mask), _ptr(positions), B, T,
+                            _stream(parents))
+    check(st, "fa_tree_mask")
     return mask, positions
 
 
@@ -395,7 +366,7 @@ def fa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     if scaling not in FA_ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(FA_ROPE_SCALINGS)}, got {scaling!r}")
     rot_dim = int(rot_dim)
-    host = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
+    host = torch.empty(max(rot_dim, 0) // 2, dtype=_F64)
     mscale = ctypes.c_float(1.0)
     st = lib().fa_rope_inv_freq(_ptr(host), ctypes.byref(mscale), rot_dim, float(base), FA_ROPE_SCALINGS[scaling],
                                 float(factor), float(original_len), float(beta_fast), float(beta_slow))
@@ -404,14 +375,14 @@ def fa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 
 
 _ROPE_DTYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float32: FA_DTYPE_F32}
-_strides = struct.Struct("12q").pack  # host memory of the C call's strides
+_Strides = ctypes.c_longlong * 12  # host memory of the C call's strides
 
 
 def _need_rows(t, name: str, dtype, device, shape=None):
     """A [B][heads][T][d] operand whose rows of d are dense; the strides between rows are free."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 4 or t.device != device or (t.stride(3) != 1 and t.shape[3] > 1):
+    if t.dtype != dtype or t.dim() != 4 or t.device != device or t.stride(3) != 1:
         raise ValueError(f"{name} must be a 4-D {dtype} tensor on {device} whose last stride is 1")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -431,67 +402,47 @@ def _rows_out(t, name: str, like: torch.Tensor):
     return t
 
 
-def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool):
-    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != device \
+def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool) -> bool:
+    if not isinstance(positions, torch.Tensor) or positions.dtype != _I32 or positions.device != device \
             or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous int32 tensor on {device}")
     shape = tuple(positions.shape)
     if shape != (B, T) and not (shared_ok and shape == (T,)):
         raise ValueError(f"positions must be [{B}][{T}]{f' or [{T}]' if shared_ok else ''}, got {shape}")
-    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or inv_freq.device != device \
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != _F64 or inv_freq.device != device \
             or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {device} (fa_rope_inv_freq)")
-
-
-def _check_rope(name: str, q, k, positions, inv_freq):
-    if not isinstance(q, torch.Tensor) or q.dtype not in _ROPE_DTYPES:
-        raise ValueError(f"{name}: q must be a bfloat16 or float32 tensor")
-    _need_rows(q, "q", q.dtype, q.device)
-    _on_current_device(q)
-    B, Hq, T, d = q.shape
-    _need_angles(positions, inv_freq, B, T, q.device, True)
-    if k is not None:
-        _need_rows(k, "k", q.dtype, q.device)
-        if k.shape[0] != B or k.shape[2] != T or k.shape[3] != d:
-            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must share batch, length and head dimension")
+    return len(shape) == 1
 
 
 def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out):
-    try:
-        dev, dtype = q.get_device(), q.dtype
-        B, Hq, T, d = q.shape
-        q0, q1, q2, last = q.stride()
-        per_seq = positions.dim() == 2
-        half, = inv_freq.shape
-        fine = (dev == _current_device() and dtype in _ROPE_DTYPES and last == 1
-                and _ints(positions, (B, T) if per_seq else (T,), dev)
-                and inv_freq.dtype is _F64 and inv_freq.get_device() == dev and inv_freq.is_contiguous())
-        k0 = k1 = k2 = kb = kt = kd = Hk = 0
-        if fine and k is not None:
-            kb, Hk, kt, kd = k.shape
-            k0, k1, k2, last = k.stride()
-            fine = (k.dtype is dtype and k.get_device() == dev and last == 1 and kb == B and kt == T and kd == d)
-    except _ODD:
-        fine = False
-    if not fine:
-        _check_rope(name, q, k, positions, inv_freq)
-        q0, q1, q2, _ = q.stride()  # (a last stride that does not matter: d is 1)
-        k0, k1, k2, Hk = (0, 0, 0, 0) if k is None else (*k.stride()[:3], k.shape[1])
-        per_seq, half = positions.dim() == 2, inv_freq.shape[0]
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
+    if q_out is None and k_out is None:
+        got = fast().rope(q, k, positions, inv_freq, interleaved, mscale, name == "fa_rope_bwd")
+        if got is not None:
+            return _answer(got, name)
+    if not isinstance(q, torch.Tensor) or q.dtype not in _ROPE_DTYPES:
+        raise ValueError(f"{name}: q must be a bfloat16 or float32 tensor")
+    dev = q.device
+    _need_rows(q, "q", q.dtype, dev)
+    _on_current_device(q)
+    B, Hq, T, d = q.shape
+    shared = _need_angles(positions, inv_freq, B, T, dev, True)
     q_out = _rows_out(q_out, "q_out", q)
-    o0, o1, o2, _ = q_out.stride()
-    p0 = p1 = p2 = 0
+    Hk, sk, sko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
+        _need_rows(k, "k", q.dtype, dev)
+        Hk = k.shape[1]
+        if k.shape[0] != B or k.shape[2] != T or k.shape[3] != d:
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must share batch, length and head dimension")
         k_out = _rows_out(k_out, "k_out", k)
-        p0, p1, p2, _ = k_out.stride()
-    st = getattr(lib(), name)(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out),
-                              _strides(q0, q1, q2, o0, o1, o2, k0, k1, k2, p0, p1, p2), positions.data_ptr(),
-                              not per_seq, inv_freq.data_ptr(), B, Hq, Hk, T, d, 2 * half, bool(interleaved), float(mscale),
-                              _ROPE_DTYPES[dtype], _stream(q))
-    if st:
-        check(st, name)
+        sk, sko = k.stride()[:3], k_out.stride()[:3]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *sk, *sko)
+    st = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), strides, _ptr(positions), int(shared),
+                              _ptr(inv_freq), B, Hq, Hk, T, d, 2 * inv_freq.shape[0], int(interleaved), float(mscale),
+                              _ROPE_DTYPES[q.dtype], _stream(q))
+    check(st, name)
     return q_out, k_out
 
 
@@ -508,7 +459,14 @@ def fa_rope_bwd(dq_out, dk_out, positions, inv_freq, interleaved: bool = False, 
     return _rope("fa_rope_bwd", dq_out, dk_out, positions, inv_freq, interleaved, mscale, q_out, k_out)
 
 
-def _check_append(q, k, v, positions, slots, inv_freq, k_pages, v_pages):
+def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved: bool = False,
+                         mscale: float = 1.0, q_out=None):
+    """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
+    and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
+    if q_out is None:
+        got = fast().rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale)
+        if got is not None:
+            return _answer(got, "fa_rope_append_paged")
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a CUDA tensor")
     dev = q.device
@@ -516,48 +474,21 @@ def _check_append(q, k, v, positions, slots, inv_freq, k_pages, v_pages):
     B, Hq, T, d = q.shape
     _need(k_pages, "k_pages", _BF16, 4)
     _need(v_pages, "v_pages", _BF16, 4)
+    P, page_size, Hkv, _ = k_pages.shape
     if tuple(v_pages.shape) != tuple(k_pages.shape) or k_pages.shape[3] != d or k_pages.device != dev \
             or v_pages.device != dev:
         raise ValueError(f"k_pages and v_pages must both be [P][page_size][Hkv][{d}] on {dev}")
-    Hkv = k_pages.shape[2]
     _need_rows(k, "k", _BF16, dev, (B, Hkv, T, d))
     _need_rows(v, "v", _BF16, dev, (B, Hkv, T, d))
     _on_current_device(q)
     _need_angles(positions, inv_freq, B, T, dev, False)
     _need_ints("slots", slots, (B, T), dev)
-
-
-def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved: bool = False,
-                         mscale: float = 1.0, q_out=None):
-    """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
-    and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
-    try:
-        dev = q.get_device()
-        B, Hq, T, d = q.shape
-        P, page_size, Hkv, _ = k_pages.shape
-        half, = inv_freq.shape
-        q0, q1, q2, q3 = q.stride()
-        k0, k1, k2, k3 = k.stride()
-        v0, v1, v2, v3 = v.stride()
-        fine = (dev == _current_device() and q.dtype is k.dtype is v.dtype is k_pages.dtype is v_pages.dtype is _BF16
-                and q3 == k3 == v3 == 1 and k.shape == v.shape == (B, Hkv, T, d)
-                and k_pages.shape == v_pages.shape == (P, page_size, Hkv, d)
-                and k.get_device() == v.get_device() == k_pages.get_device() == v_pages.get_device() == dev
-                and k_pages.is_contiguous() and v_pages.is_contiguous()
-                and _ints(positions, (B, T), dev) and _ints(slots, (B, T), dev)
-                and inv_freq.dtype is _F64 and inv_freq.get_device() == dev and inv_freq.is_contiguous())
-    except _ODD:
-        fine = False
-    if not fine:
-        _check_append(q, k, v, positions, slots, inv_freq, k_pages, v_pages)
     q_out = _rows_out(q_out, "q_out", q)
-    o0, o1, o2, _ = q_out.stride()
-    st = lib().fa_rope_append_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                                    _strides(q0, q1, q2, o0, o1, o2, k0, k1, k2, v0, v1, v2), positions.data_ptr(),
-                                    slots.data_ptr(), inv_freq.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B,
-                                    Hq, Hkv, T, page_size, P, d, 2 * half, bool(interleaved), float(mscale), _stream(q))
-    if st:
-        check(st, "fa_rope_append_paged")
+    strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+    st = lib().fa_rope_append_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), strides, _ptr(positions), _ptr(slots),
+                                    _ptr(inv_freq), _ptr(k_pages), _ptr(v_pages), B, Hq, Hkv, T, page_size, P, d,
+                                    2 * inv_freq.shape[0], int(interleaved), float(mscale), _stream(q))
+    check(st, "fa_rope_append_paged")
     return q_out
 
 
@@ -565,22 +496,27 @@ def fa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, max_pages: int, d
                             num_sms: int | None = None, device=None) -> int:
     """Bytes of workspace fa_tree_decode_paged needs on a device with num_sms SMs (None: this one)."""
     if num_sms is None:
-        index = None if device is None else torch.device(device).index
-        num_sms = _sm_count(torch.cuda.current_device() if index is None else index)
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        num_sms = torch.cuda.get_device_properties(dev).multi_processor_count
     return int(lib().fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, int(num_sms)))
 
 
-@functools.lru_cache(maxsize=None)
-def _sm_count(index) -> int:
-    return torch.cuda.get_device_properties(index).multi_processor_count
-
-
-def _check_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens):
+def fa_tree_decode_paged(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens=None,
+                         scale: float | None = None, workspace=None, out=None, lse=None):
+    """Attention of drafted trees over the paged cache: q [B][Hq][T][d], pools [P][16][Hkv][d] bf16,
+    block_table [B][max_pages], seqlens [B], tree_mask [B][T][ceil(T/32)] or [T][ceil(T/32)] (one for
+    all), tree_lens [B] or None (T nodes each), int32 -> (o, lse)."""
+    if workspace is None and out is None and lse is None:
+        got = fast().tree_decode_paged(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens, scale)
+        if got is not None:
+            return _answer(got, "fa_tree_decode_paged")
     _need(q, "q", _BF16, 4)
     _need(k_pages, "k_pages", _BF16, 4)
     _need(v_pages, "v_pages", _BF16, 4)
-    _need(block_table, "block_table", torch.int32, 2)
+    _need(block_table, "block_table", _I32, 2)
     B, Hq, T, d = q.shape
+    P, page_size, Hkv, _ = k_pages.shape
+    max_pages = block_table.shape[1]
     dev = q.device
     if not (dev == k_pages.device == v_pages.device == block_table.device):
         raise ValueError("q, the pools and block_table must be on one device")
@@ -595,46 +531,17 @@ def _check_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens)
     _need_ints("tree_mask", tree_mask, (T, words) if shared else (B, T, words), dev)
     if tree_lens is not None:
         _need_ints("tree_lens", tree_lens, (B,), dev)
-
-
-def fa_tree_decode_paged(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens=None,
-                         scale: float | None = None, workspace=None, out=None, lse=None):
-    """Attention of drafted trees over the paged cache: q [B][Hq][T][d], pools [P][16][Hkv][d] bf16,
-    block_table [B][max_pages], seqlens [B], tree_mask [B][T][ceil(T/32)] or [T][ceil(T/32)] (one for
-    all), tree_lens [B] or None (T nodes each), int32 -> (o, lse)."""
-    try:
-        dev = q.get_device()
-        B, Hq, T, d = q.shape
-        P, page_size, Hkv, _ = k_pages.shape
-        rows, max_pages = block_table.shape
-        shared = tree_mask.dim() == 2
-        words = (T + 31) // 32
-        fine = (dev == _current_device() and q.dtype is k_pages.dtype is v_pages.dtype is _BF16
-                and k_pages.shape == v_pages.shape == (P, page_size, Hkv, d)
-                and k_pages.get_device() == v_pages.get_device() == dev
-                and q.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-                and _ints(block_table, (B, max_pages), dev) and _ints(seqlens, (B,), dev)
-                and _ints(tree_mask, (T, words) if shared else (B, T, words), dev)
-                and (tree_lens is None or _ints(tree_lens, (B,), dev)))
-    except _ODD:
-        fine = False
-    if not fine:
-        _check_tree(q, k_pages, v_pages, block_table, seqlens, tree_mask, tree_lens)
-    L = lib()
-    nbytes = L.fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, _sm_count(dev))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, device=dev)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        ws_bytes = nbytes
-    else:
-        ws_bytes = _ws_bytes(workspace, nbytes, q.device)
-    o = torch.empty_like(q) if out is None else _out(out, "out", q.shape, _BF16, q)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws_bytes = _ws_bytes(workspace, nbytes, dev)
+    o = _out(out, "out", q.shape, _BF16, q)
     lse = _out(lse, "lse", (B, Hq, T), torch.float32, q)
-    st = L.fa_tree_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-                                seqlens.data_ptr(), tree_mask.data_ptr(), shared, _ptr(tree_lens), o.data_ptr(),
-                                lse.data_ptr(), B, Hq, Hkv, T, max_pages, page_size, P, d,
-                                d ** -0.5 if scale is None else float(scale), workspace.data_ptr(), ws_bytes, _stream(q))
-    if st:
-        check(st, "fa_tree_decode_paged")
+    st = lib().fa_tree_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seqlens),
+                                    _ptr(tree_mask), int(shared), _ptr(tree_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T,
+                                    max_pages, page_size, P, d, scale, _ptr(workspace), ws_bytes, _stream(q))
+    check(st, "fa_tree_decode_paged")
     return o, lse
 
 

@@ -2,8 +2,11 @@
 
 Each ``csrc/*.cu`` translation unit is compiled in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a`` and the objects are linked
-into one shared library next to this file. A rebuild happens only when a
-source or header is newer than the library (or ``force=True``).
+into one shared library next to this file. ``csrc/fast_calls.cpp`` (the step
+calls' way from Python objects to that library) is compiled beside them with
+the host compiler against the installed torch and becomes the extension module
+``_fast``. A rebuild happens only when a source or header is newer than what
+was built from it (or ``force=True``).
 """
 
 from __future__ import annotations
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+FAST_SRC = os.path.join(CSRC, "fast_calls.cpp")
+FAST_PATH = os.path.join(HERE, "_fast.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [
@@ -46,17 +52,56 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    files = sources()
+    files = [*sources(), FAST_SRC]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
+    built = (LIB_PATH, FAST_PATH)
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in _deps())
+
+
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
+
+
+def _cuda_include() -> str:
+    home = os.environ.get("CUDA_HOME") or os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    return os.path.join(home, "include")
+
+
+def _compile_fast() -> str:
+    """Object file of the extension module, against the headers of the torch that runs."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "fast_calls.o")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], _cuda_include()]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in inc), "-c",
+          FAST_SRC, "-o", obj], "compiling fast_calls.cpp")
+    return obj
+
+
+def _link_fast(obj: str) -> None:
+    """Linked against the library beside it and the torch that is installed here."""
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FAST_PATH + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{HERE}", f"-l:{LIB_NAME}", f"-L{lib}",
+          "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+          f"-Wl,-rpath,{lib}"], "linking _fast")
+    os.replace(tmp, FAST_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -74,13 +119,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 4)) as ex:
+        fast = ex.submit(_compile_fast)
         results = list(ex.map(compile_one, sources()))
+        fast_obj = fast.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-lcuda"]
+    cmd = [nvcc, ARCH, "-shared", f"-Xlinker=-soname={LIB_NAME}", "-o", tmp, *[o for o, _ in results], "-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         # libcuda is only needed at run time through the runtime's entry-point
@@ -90,6 +137,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_fast(fast_obj)
     return LIB_PATH
 
 
