@@ -61,7 +61,8 @@ struct TrCfg {
   static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
   static constexpr int OFF_EX = OFF_BAR + 384;
   static constexpr int SMEM = OFF_EX + kTrTile * 5 * 4;  // at most 227 KB; the base is 1024-byte aligned
-  static constexpr int LEAST = WIDE ? 4 : 1;
+  static constexpr int LEAST = WIDE ? 4 : 1;  // steps of a share
+  static constexpr int STEP = WIDE ? 2 : 3, FRONT = WIDE ? 3 : 1;  // TrCost
   static constexpr int TMEM_COLS = 512;
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
@@ -90,6 +91,16 @@ struct TrParams {
   unsigned long long timeout_ns;
 };
 
+// What shares are cut in: `step` for a step and, ahead of a unit's first, `front` for what
+// a unit costs beside its tiles (Q, the first S, writing O). Measured: a narrow unit about
+// a third of its pair of tiles, a wide one 1.5 tiles. Batches of so few steps that a CTA
+// has hardly more than one are cut by steps alone.
+struct TrCost {
+  int step, front;
+  // the steps whose cost ends within the first `at` of a unit
+  __device__ __forceinline__ int steps_in(int at) const { return at < front ? 0 : (at - front) / step; }
+};
+
 struct TrBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
@@ -99,6 +110,7 @@ struct TrBars {
   int abort_flag;
   // where this CTA's share begins
   int b0, off0, begin, end, total, grid;
+  TrCost cost;
 };
 static_assert(sizeof(TrBars) <= 384, "barrier area");
 
@@ -115,12 +127,10 @@ __device__ __forceinline__ TrSeq tr_seq(const TrParams& p, int b) {
   return s;
 }
 // Steps of one (KV head, row unit): a key tile, or (narrow) a pair of them; a unit
-// without keys is one step, so that somebody writes its zeros. What a unit costs beside
-// its tiles (Q, the first S, writing O) counts as kTrExtra steps at its front.
-constexpr int kTrExtra = 1;
+// without keys is one step, so that somebody writes its zeros.
 template <bool WIDE>
 __device__ __forceinline__ int tr_steps(const TrSeq& s) {
-  return kTrExtra + max(1, WIDE ? s.tiles : (s.tiles + 1) / 2);
+  return max(1, WIDE ? s.tiles : (s.tiles + 1) / 2);
 }
 
 // A run of steps of one unit inside a CTA's share.
@@ -129,40 +139,44 @@ struct TrSeg {
   int S, n;
   int x0, nt;    // first key tile and how many
   bool from_start, to_end;
-  int unit_end;  // global index behind the unit's last step
+  int unit_end;  // where the unit ends in the whole batch's cost
 };
 
 // Walks a share segment by segment; each role walks by itself.
 template <bool WIDE>
 struct TrWalk {
-  int b, off, at, end;  // sequence, steps into it; global step; the share's end
-  __device__ __forceinline__ TrWalk(const TrBars* s) : b(s->b0), off(s->off0), at(s->begin), end(s->end) {}
+  int b, off, at, end;  // sequence, cost into it; cost into the batch; the share's end
+  TrCost c;
+  __device__ __forceinline__ TrWalk(const TrBars* s) : b(s->b0), off(s->off0), at(s->begin), end(s->end), c(s->cost) {}
   __device__ __forceinline__ bool next(const TrParams& p, TrSeg& g) {
     TrSeq q;
-    int steps, hu, j0, ns;
-    do {  // a share that ends inside a unit's front leaves the whole unit to the next CTA
+    int cost, hu, from, to, j0, j1;
+    do {
       if (at >= end) return false;
       q = tr_seq(p, b);
-      steps = tr_steps<WIDE>(q);
-      hu = off / steps;
-      j0 = off - hu * steps;
-      ns = min(steps - j0, end - at);
-      if (j0 + ns <= kTrExtra) at += ns;
-    } while (j0 + ns <= kTrExtra);
+      cost = c.front + c.step * tr_steps<WIDE>(q);
+      hu = off / cost;
+      from = off - hu * cost;
+      to = min(cost, from + end - at);
+      j0 = c.steps_in(from);
+      j1 = c.steps_in(to);
+      // a share that ends inside a unit's first step leaves all of it to the next CTA
+      if (j0 == j1) at += to - from;
+    } while (j0 == j1);
     constexpr int PER = WIDE ? 1 : 2;
     g.b = b;
     g.kvh = hu / p.U;
     g.u = hu - g.kvh * p.U;
     g.S = q.S;
     g.n = q.n;
-    g.x0 = max(0, j0 - kTrExtra) * PER;
-    g.nt = max(0, min(q.tiles, (j0 + ns - kTrExtra) * PER) - g.x0);
-    g.from_start = g.x0 == 0;
-    g.to_end = j0 + ns == steps;
-    g.unit_end = at - j0 + steps;
-    off += ns;
-    at += ns;
-    if (off == steps * p.Hkv * p.U) {
+    g.x0 = j0 * PER;
+    g.nt = max(0, min(q.tiles, j1 * PER) - g.x0);
+    g.from_start = j0 == 0;
+    g.to_end = to == cost;
+    g.unit_end = at - from + cost;
+    off += to - from;
+    at += to - from;
+    if (off == cost * p.Hkv * p.U) {
       ++b;
       off = 0;
     }
@@ -181,6 +195,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// 32 bytes in one store: a warp whose threads each write a row of their own spends a
+// wavefront per row and store, so half as many as with 16 bytes.
+__device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 __device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
@@ -260,13 +282,14 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 9) tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
   pdl_wait();
 
-  // ---- this CTA's share of all steps: a block-wide scan over the sequences
+  // ---- this CTA's share of the batch's cost: a block-wide scan over the sequences
   {
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
     const int lo = min(p.B, static_cast<int>(threadIdx.x) * per), hi = min(p.B, lo + per);
-    int mine = 0;  // all steps of a batch are below 2^31
+    int mine = 0;  // a batch's whole cost is below 2^31
     for (int b = lo; b < hi; ++b) mine += tr_steps<WIDE>(tr_seq(p, b));
-    mine *= p.Hkv * p.U;
+    const int units = p.Hkv * p.U;  // of a sequence
+    mine *= units;
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -277,16 +300,21 @@ __global__ void __launch_bounds__(384, 1)
     int* wsum = reinterpret_cast<int*>(ex);
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int before = inc - mine, total = 0;
+    int before = inc - mine, steps = 0;
 #pragma unroll
     for (int w = 0; w < 12; ++w) {
       if (w < warp) before += wsum[w];
-      total += wsum[w];
+      steps += wsum[w];
     }
-    // A CTA gets LEAST steps at least: each more that shares a unit writes and the merge
-    // reads a partial of its rows, which costs as much as some steps when the rows are many.
-    // No CTA gets two units while others get none.
-    const int G = min(static_cast<int>(gridDim.x), max(total / C::LEAST, p.B * p.Hkv * p.U));
+    // Each CTA that shares a unit writes, and the merge reads, a partial of its rows, which
+    // for 256 rows costs as much as some tiles: a CTA gets LEAST steps at least, but no two
+    // units while others get none. A share is a step's cost or more either way, so that every
+    // CTA between a unit's first and last has a step of it.
+    const int grid = static_cast<int>(gridDim.x);
+    const bool few = steps <= 2 * C::LEAST * grid;
+    const TrCost cost = few ? TrCost{1, 0} : TrCost{C::STEP, C::FRONT};
+    const int G = few ? min(grid, max(steps / C::LEAST, p.B * units)) : grid;
+    const int total = cost.step * steps + cost.front * p.B * units;
     const int begin = cta < G ? static_cast<int>(static_cast<long long>(cta) * total / G) : total;
     const int end = cta < G ? static_cast<int>((cta + 1ll) * total / G) : total;
     if (threadIdx.x == 0) {
@@ -294,12 +322,15 @@ __global__ void __launch_bounds__(384, 1)
       bars->end = end;
       bars->total = total;
       bars->grid = G;
+      bars->cost = cost;
     }
-    if (begin >= before && begin < before + mine) {  // one thread: its sequences hold the first step
+    before = cost.step * before + cost.front * lo * units;
+    mine = cost.step * mine + cost.front * (hi - lo) * units;
+    if (begin >= before && begin < before + mine) {  // one thread: its sequences hold the share's start
       int off = begin - before;
       int b = lo;
       for (; b < hi; ++b) {
-        const int s = tr_steps<WIDE>(tr_seq(p, b)) * p.Hkv * p.U;
+        const int s = (cost.step * tr_steps<WIDE>(tr_seq(p, b)) + cost.front) * units;
         if (off < s) break;
         off -= s;
       }
@@ -746,7 +777,7 @@ __global__ void __launch_bounds__(384, 1)
       const size_t out_row = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + row;
       const size_t part_row = static_cast<size_t>(slot) * (kTrTile * C::QT) + (WIDE ? t * kTrTile : 0) + r;
       if (threadIdx.x == 0 && w.from_start && !w.to_end && ok) {
-        // this CTA begins the unit: the last CTA with a share of it is the one that holds its last step
+        // this CTA begins the unit: the last one with a share of it is the one whose share holds its end
         const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
         const int first_row = w.u * C::QT * kTrTile;
         p.split[cta] = make_int4((w.b * p.Hkv + w.kvh) * p.R + first_row, min(p.R - first_row, C::QT * kTrTile),
@@ -798,6 +829,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (!write) continue;
           if (whole) {
+            // (o may start on any 16-byte border)
             __nv_bfloat16* dst = p.o + out_row * D + col0 + cc * 32;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -808,8 +840,12 @@ __global__ void __launch_bounds__(384, 1)
           } else if (live) {
             float* dst = p.part + part_row * D + col0 + cc * 32;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
+              st32(dst + 8 * q, v);
+            }
           }
         }
         if (write && (WIDE || t == 0)) {
@@ -843,19 +879,16 @@ __global__ void __launch_bounds__(384, 1)
 // of up to four partials go two rows to a warp, all of them in flight; the others one
 // row to 1, 2, 4 or 8 warps (as many as the rows leave warps for), four partials each in
 // flight.
-template <int D>
 struct TrRow {
-  static constexpr int N = D / 32;  // columns of a lane
   float m = -INFINITY, s = 0.f, l = 0.f;
-  float o[N] = {};
-  __device__ __forceinline__ void add(float m2, float s2, float l2, const float (&o2)[N]) {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
     if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
     const float mn = fmaxf(m, m2);
     const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
     s = s * fa + s2 * fb;
     l = l * fa + l2 * fb;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = o[e] * fa + o2[e] * fb;
+    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
     m = mn;
   }
 };
@@ -895,12 +928,13 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
                                                                          const int4* __restrict__ split, int grid,
                                                                          __nv_bfloat16* __restrict__ o,
                                                                          float* __restrict__ lse) {
-  constexpr int N = TrRow<D>::N;
+  constexpr int LANES = D / 4;           // lanes to a row
+  constexpr int PER = 32 / LANES;        // rows of a warp's load
   constexpr int ROWS = kTrTile * QT;
   __shared__ TrUnit unit[kTrMaxGrid];  // by CTA; those of CTAs without an entry have no items
   __shared__ int warp_sum[8];
-  __shared__ float red[8][D];
-  __shared__ float red_m[8], red_s[8], red_l[8];
+  __shared__ float4 red[8][32];
+  __shared__ float red_m[8][PER], red_s[8][PER], red_l[8][PER];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();
@@ -918,8 +952,9 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
     many_rows += sum;
   }
   int wpr = 8;  // warps to a row
-  while (wpr > 1 && many_rows * wpr > 16 * static_cast<int>(gridDim.x)) wpr >>= 1;
-  const int few_rows = 8 * 2, many_step = 8 / wpr;  // rows of an item
+  while (wpr > 1 && many_rows / PER * wpr > 8 * static_cast<int>(gridDim.x)) wpr >>= 1;
+  const int few_rows = 8 * 2 * PER, many_step = 8 / wpr * PER;  // rows of an item
+  const int my = lane / LANES, col = lane % LANES * 4;
   int total = 0;
   for (int c0 = 0; c0 < grid; c0 += 256) {
     const int c = c0 + threadIdx.x;
@@ -943,41 +978,29 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
     const TrUnit un = unit[c];
     // partial 0 is CTA c's last, the others are the later CTAs' first
     auto at = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS; };
-    auto get = [&](float4& ml, float (&v)[N], size_t row_at) {
+    auto get = [&](float4& ml, float4& v, size_t row_at) {
       ml = part_ml[row_at];
-      const float* src = part + row_at * D + lane * N;
-      if constexpr (N == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x; v[1] = x.y;
-      }
+      v = *reinterpret_cast<const float4*>(part + row_at * D + col);
     };
-    auto put = [&](const TrRow<D>& r, int row) {
+    auto put = [&](const TrRow& r, int row) {
       const float inv = r.s > 0.f ? 1.f / r.s : 0.f;
       const size_t out = static_cast<size_t>(un.row0) + row;
-      __nv_bfloat16* dst = o + out * D + lane * N;
-      if constexpr (N == 4)
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack_bf16x2(r.o[0] * inv, r.o[1] * inv), pack_bf16x2(r.o[2] * inv, r.o[3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(r.o[0] * inv, r.o[1] * inv);
-      if (lse && lane == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
+      *reinterpret_cast<uint2*>(o + out * D + col) =
+          make_uint2(pack_bf16x2(r.o.x * inv, r.o.y * inv), pack_bf16x2(r.o.z * inv, r.o.w * inv));
+      if (lse && col == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
     };
     if (un.parts <= kTrFewParts) {
       constexpr int IN = 2;
-      const int row0 = (item - un.first_item) * few_rows + warp * 2;
-      TrRow<D> acc[2];
+      const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
+      TrRow acc[2];
       for (int i0 = 0; i0 < un.parts; i0 += IN) {
-        float4 ml[IN][2];
-        float v[IN][2][N];
+        float4 ml[IN][2], v[IN][2];
 #pragma unroll
         for (int k = 0; k < IN; ++k)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             ml[k][r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            if (i0 + k < un.parts && row0 + r < un.rows) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r);
+            if (i0 + k < un.parts && row0 + r * PER < un.rows) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r * PER);
           }
 #pragma unroll
         for (int k = 0; k < IN; ++k)
@@ -986,15 +1009,14 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (row0 + r < un.rows) put(acc[r], row0 + r);
+        if (row0 + r * PER < un.rows) put(acc[r], row0 + r * PER);
     } else {
       constexpr int IN = 4;
       const int sub = warp & (wpr - 1);
-      const int row = (item - un.first_item) * many_step + warp / wpr;
-      TrRow<D> acc;
+      const int row = (item - un.first_item) * many_step + warp / wpr * PER + my;
+      TrRow acc;
       for (int i0 = sub; i0 < un.parts; i0 += wpr * IN) {
-        float4 ml[IN];
-        float v[IN][N];
+        float4 ml[IN], v[IN];
 #pragma unroll
         for (int k = 0; k < IN; ++k) {
           ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
@@ -1004,22 +1026,15 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
         for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
       }
       if (wpr > 1) {  // block-uniform
-#pragma unroll
-        for (int e = 0; e < N; ++e) red[warp][lane * N + e] = acc.o[e];
-        if (lane == 0) {
-          red_m[warp] = acc.m;
-          red_s[warp] = acc.s;
-          red_l[warp] = acc.l;
+        red[warp][lane] = acc.o;
+        if (col == 0) {
+          red_m[warp][my] = acc.m;
+          red_s[warp][my] = acc.s;
+          red_l[warp][my] = acc.l;
         }
         __syncthreads();
-        if (sub == 0) {
-          for (int k = warp + 1; k < warp + wpr; ++k) {
-            float v[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = red[k][lane * N + e];
-            acc.add(red_m[k], red_s[k], red_l[k], v);
-          }
-        }
+        if (sub == 0)
+          for (int k = warp + 1; k < warp + wpr; ++k) acc.add(red_m[k][my], red_s[k][my], red_l[k][my], red[k][lane]);
         __syncthreads();
       }
       if (sub == 0 && row < un.rows) put(acc, row);
@@ -1032,15 +1047,16 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
 // ---------------------------------------------------------------------------
 static bool tr_wide(int R) { return R > kTrTile; }
 
-// Row units of all (sequence, KV head)s and the most steps they can have, 0 from 2^31 on.
+// The most steps that a batch can have, 0 where their cost could reach 2^31.
 static long long tr_most_steps(int B, int Hkv, int R, int max_pages) {
   const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
   const long long tiles = (static_cast<long long>(max_pages) * 16 + kTrTile - 1) / kTrTile;
-  const long long steps = kTrExtra + (tr_wide(R) ? tiles : (tiles + 1) / 2);
+  const long long steps = tr_wide(R) ? tiles : (tiles + 1) / 2;
   const long long n = static_cast<long long>(B) * Hkv * U;
-  return n > ((1ll << 31) - 1) / steps ? 0 : n * steps;
+  return n > (1ll << 31) / 5 / steps ? 0 : n * steps;  // STEP + FRONT <= 5
 }
 
+// CTAs of a launch: one to an SM, none that could have no step.
 static int tr_grid(long long steps, int sms) { return static_cast<int>(steps < sms ? steps : sms); }
 
 static size_t tr_part_bytes(int grid, int R, int d) {

@@ -80,8 +80,8 @@ def test_tree_attention(L):
     _cases(L.fa_tree_decode_paged, base, wrong)
     assert L.fa_tree_workspace_bytes(0, 4, 2, 3, 4, 64, 152) == 0
     assert L.fa_tree_workspace_bytes(1, 5, 2, 3, 4, 64, 152) == 0
-    # 2 KV heads, at most 64 keys: two steps and their fronts -> 4 CTAs, two partials of 128 rows each
-    assert L.fa_tree_workspace_bytes(1, 4, 2, 3, 4, 64, 152) == 4 * (2 * 128 * (64 * 4 + 16) + 16)
+    # 2 KV heads, at most 64 keys: one step each -> 2 CTAs, two partials of 128 rows each
+    assert L.fa_tree_workspace_bytes(1, 4, 2, 3, 4, 64, 152) == 2 * (2 * 128 * (64 * 4 + 16) + 16)
     assert L.fa_tree_workspace_bytes(1, 4, 2, 300, 4096, 128, 152) == 152 * (2 * 256 * (128 * 4 + 16) + 16)
 
 
