@@ -115,10 +115,13 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
 }
 
 constexpr int kRopeWarps = 8;
+constexpr int kRopeMostRows = 4;  // of a warp
 
-template <typename E, int VEC, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams p) {
-  constexpr int U = 4;  // rows of a warp in flight
+// U: rows of a warp, all in flight at once. The sines stay in shared memory: in registers
+// they would cost a block's worth of occupancy (64 registers a thread: four blocks an SM;
+// b1 hq64 hkv8 n8192 d128 52.9 us with them there, 47.2 us without).
+template <typename E, int VEC, bool INTER, bool APPEND, int U>
+__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopeParams p) {
   __shared__ float cs[2][VEC][32];
   pdl_wait();
   pdl_launch();
@@ -132,9 +135,13 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
   const int b = there ? static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.T)) : 0;
   const int t = there ? static_cast<int>(token - static_cast<long long>(b) * p.T) : 0;
   const int half = p.rot / 2;
-  const bool turn = lane * VEC < half;  // else: the lane copies two vectors of the tail
-  const int o0 = turn ? (INTER ? 2 * lane * VEC : lane * VEC) : p.rot + (lane - half / VEC) * 2 * VEC;
-  const int o1 = turn && !INTER ? o0 + half : o0 + VEC;
+  // A lane's two vectors lie half the part's length apart (in the rotated part, and in the
+  // tail that it copies), so that neighbouring lanes' accesses are neighbours in memory.
+  const int turning = half / VEC;       // lanes of the rotated part
+  const bool turn = lane < turning;
+  constexpr bool ADJ = INTER && VEC == 1;  // a pair is two neighbours, and a vector is one of them
+  const int o0 = turn ? (ADJ ? 2 * lane : lane * VEC) : p.rot + (lane - turning) * VEC;
+  const int o1 = turn ? (ADJ ? o0 + 1 : o0 + half) : o0 + (p.lanes - turning) * VEC;
   const bool two = turn || o1 < p.d;
   const int hq = p.q.heads, hk = hq + p.k.heads;
   const int h_begin = blockIdx.y * p.head_chunk;
@@ -154,25 +161,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
   auto wanted = [&](int h) { return there && h < h_end && !(APPEND && h >= hq && slot < 0); };
 
   Raw<E, VEC> x[U], y[U];
-  auto load = [&](int h0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * kRopeWarps;
-      if (wanted(h)) {
-        const RopeSide& s = side_of_head(h);
-        const E* src = static_cast<const E*>(s.src) + b * s.sb + head_in_side(h) * s.sh + t * s.st;
-        x[u].load(src + o0);
-        if (two) y[u].load(src + o1);
-      }
+  for (int u = 0; u < U; ++u) {
+    const int h = h_begin + warp + u * kRopeWarps;
+    if (wanted(h)) {
+      const RopeSide& s = side_of_head(h);
+      const E* src = static_cast<const E*>(s.src) + b * s.sb + head_in_side(h) * s.sh + t * s.st;
+      x[u].load(src + o0);
+      if (two) y[u].load(src + o1);
     }
-  };
-  load(h_begin + warp);
+  }
 
   if (turn && there) {
     const long long pos = __ldg(p.positions + b * p.pos_sb + t);
     for (int e = warp; e < VEC; e += kRopeWarps) {
-      const unsigned long long a =
-          static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + lane * VEC + e));
+      // interleaved: half of the lane's pairs are in its first vector, half in its second
+      const int pair = !INTER || ADJ ? lane * VEC + e
+                                     : (2 * e < VEC ? o0 / 2 + e : o1 / 2 + e - VEC / 2);
+      const unsigned long long a = static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + pair));
       float s, c;  // of the signed upper half, in half turns
       sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
       cs[0][e][id] = c * p.mscale;
@@ -180,45 +186,33 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeParams 
     }
   }
   __syncthreads();
-  if (!there) return;
-  float c[VEC], s[VEC];
-  if (turn) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      c[e] = cs[0][e][id];
-      s[e] = cs[1][e][id];
-    }
-  }
-  for (int h0 = h_begin + warp; h0 < h_end; h0 += U * kRopeWarps) {
-    if (h0 != h_begin + warp) load(h0);
+  for (int u = 0; u < U; ++u) {
+    const int h = h_begin + warp + u * kRopeWarps;
+    if (!wanted(h)) continue;
+    const RopeSide& side = side_of_head(h);
+    const bool to_slot = APPEND && h >= hq;
+    if (turn && h < hk) {
+      float xv[VEC], yv[VEC];
+      x[u].get(xv);
+      y[u].get(yv);
+      // the pair's two values: element e of x and of y, or neighbours 2e, 2e + 1 of x, then y
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * kRopeWarps;
-      if (!wanted(h)) continue;
-      const RopeSide& side = side_of_head(h);
-      const bool to_slot = APPEND && h >= hq;
-      if (turn && h < hk) {
-        float xv[VEC], yv[VEC];
-        x[u].get(xv);
-        y[u].get(yv);
-        // the pair's two values: element e of x and of y, or neighbours 2e, 2e + 1 of x, then y
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float& a = !INTER ? xv[e] : (2 * e < VEC ? xv[(2 * e) % VEC] : yv[(2 * e) % VEC]);
-          float& g = !INTER ? yv[e] : (2 * e + 1 < VEC ? xv[(2 * e + 1) % VEC] : yv[(2 * e + 1) % VEC]);
-          const float a0 = a, g0 = g;
-          a = a0 * c[e] - g0 * s[e];
-          g = g0 * c[e] + a0 * s[e];
-        }
-        x[u].set(xv);
-        y[u].set(yv);
+      for (int e = 0; e < VEC; ++e) {
+        float& a = !INTER ? xv[e] : (2 * e < VEC ? xv[(2 * e) % VEC] : yv[(2 * e) % VEC]);
+        float& g = !INTER ? yv[e] : (2 * e + 1 < VEC ? xv[(2 * e + 1) % VEC] : yv[(2 * e + 1) % VEC]);
+        const float a0 = a, g0 = g, c = cs[0][e][id], s = cs[1][e][id];
+        a = a0 * c - g0 * s;
+        g = g0 * c + a0 * s;
       }
-      const long long hs = head_in_side(h);
-      E* dst = static_cast<E*>(side.dst) +
-               (to_slot ? slot * p.slot_stride + hs * p.d : b * side.db + hs * side.dh + t * side.dt);
-      x[u].store(dst + o0);
-      if (two) y[u].store(dst + o1);
+      x[u].set(xv);
+      y[u].set(yv);
     }
+    const long long hs = head_in_side(h);
+    E* dst = static_cast<E*>(side.dst) +
+             (to_slot ? slot * p.slot_stride + hs * p.d : b * side.db + hs * side.dh + t * side.dt);
+    x[u].store(dst + o0);
+    if (two) y[u].store(dst + o1);
   }
 }
 
@@ -226,6 +220,24 @@ static bool strides_ok(const RopeSide& s, int vec, bool slots) {
   auto whole = [vec](long long x) { return x % vec == 0; };
   return whole(s.sb) && whole(s.sh) && whole(s.st) && (slots || (whole(s.db) && whole(s.dh) && whole(s.dt))) &&
          (reinterpret_cast<uintptr_t>(s.src) & 15u) == 0 && (reinterpret_cast<uintptr_t>(s.dst) & 15u) == 0;
+}
+
+template <typename E, int VEC, bool APPEND>
+static int launch_rope_rows(const RopeParams& p, bool interleaved, int rows, dim3 grid, cudaStream_t stream) {
+  const dim3 block(kRopeWarps * 32);
+  auto go = [&](auto inter, auto u) {
+    return launch_dependent(rope_kernel<E, VEC, decltype(inter)::value, APPEND, decltype(u)::value>, grid, block, 0,
+                            stream, p);
+  };
+  auto with = [&](auto inter) {
+    if constexpr (VEC > 1) {
+      if (rows == 1) return go(inter, std::integral_constant<int, 1>{});
+      if (rows == 2) return go(inter, std::integral_constant<int, 2>{});
+      if (rows == 3) return go(inter, std::integral_constant<int, 3>{});
+    }
+    return go(inter, std::integral_constant<int, kRopeMostRows>{});
+  };
+  return interleaved ? with(std::true_type{}) : with(std::false_type{});
 }
 
 template <typename E, bool APPEND>
@@ -240,20 +252,17 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   const long long blocks = (p.tokens * p.lanes + 31) / 32;
   if (blocks >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   p.small = blocks * 32 < (1ll << 31);
-  // Heads of a block: a round of rows in flight for its eight warps (a warp's U heads are
-  // kRopeWarps apart), in even chunks; one row a warp where the blocks would leave SMs idle
-  // (a decode step).
-  int cuts = (heads + 4 * kRopeWarps - 1) / (4 * kRopeWarps);
+  // Heads of a block: up to four rows to each of its eight warps (a warp's heads are
+  // kRopeWarps apart), in even cuts; fewer where the blocks would leave SMs idle (a decode
+  // step).
+  int cuts = (heads + kRopeMostRows * kRopeWarps - 1) / (kRopeMostRows * kRopeWarps);
   const int most = (heads + kRopeWarps - 1) / kRopeWarps;
   while (cuts < most && blocks * cuts < 2ll * device_sm_count()) cuts = cuts * 2 < most ? cuts * 2 : most;
-  const int chunk = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps * kRopeWarps;
-  p.head_chunk = chunk;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + chunk - 1) / chunk));
-  if (vec)
-    return interleaved ? launch_dependent(rope_kernel<E, V, true, APPEND>, grid, dim3(256), 0, stream, p)
-                       : launch_dependent(rope_kernel<E, V, false, APPEND>, grid, dim3(256), 0, stream, p);
-  return interleaved ? launch_dependent(rope_kernel<E, 1, true, APPEND>, grid, dim3(256), 0, stream, p)
-                     : launch_dependent(rope_kernel<E, 1, false, APPEND>, grid, dim3(256), 0, stream, p);
+  const int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
+  p.head_chunk = rows * kRopeWarps;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.head_chunk - 1) / p.head_chunk));
+  return vec ? launch_rope_rows<E, V, APPEND>(p, interleaved, rows, grid, stream)
+             : launch_rope_rows<E, 1, APPEND>(p, interleaved, rows, grid, stream);
 }
 
 static bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
