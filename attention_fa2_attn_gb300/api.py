@@ -288,9 +288,10 @@ def fa_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bool = Tr
 
 
 # What follows is called between the layers of a decode step, where a microsecond of the
-# host counts. With no output given, a call goes through the extension module first
-# (fast(): the same tests, outputs and library call, in one step); it answers None where
-# an argument is not plainly right, and the checks below then name it.
+# host counts. A call goes through the extension module first (fast(): the same tests,
+# outputs and library call, in one step; the plan and the attention calls without given
+# outputs only); it answers None where an argument is not plainly right, and the checks
+# below then name it.
 _BF16, _I32, _F64 = torch.bfloat16, torch.int32, torch.float64
 
 
@@ -416,10 +417,9 @@ def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool) -
 
 
 def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out):
-    if q_out is None and k_out is None:
-        got = fast().rope(q, k, positions, inv_freq, interleaved, mscale, name == "fa_rope_bwd")
-        if got is not None:
-            return _answer(got, name)
+    got = fast().rope(q, k, positions, inv_freq, interleaved, mscale, name == "fa_rope_bwd", q_out, k_out)
+    if got is not None:
+        return _answer(got, name)
     if not isinstance(q, torch.Tensor) or q.dtype not in _ROPE_DTYPES:
         raise ValueError(f"{name}: q must be a bfloat16 or float32 tensor")
     dev = q.device
@@ -463,10 +463,9 @@ def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, 
                          mscale: float = 1.0, q_out=None):
     """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
     and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
-    if q_out is None:
-        got = fast().rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale)
-        if got is not None:
-            return _answer(got, "fa_rope_append_paged")
+    got = fast().rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out)
+    if got is not None:
+        return _answer(got, "fa_rope_append_paged")
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a CUDA tensor")
     dev = q.device

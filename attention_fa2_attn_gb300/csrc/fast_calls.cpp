@@ -3,9 +3,9 @@
 // Between the layers of a decode step the host's time is the call's time: the kernels of
 // fa_paged_plan or fa_rope_append_paged run for 4 us, and reading twenty attributes of
 // tensors, making the outputs and marshalling twenty arguments in Python took 15 to 20.
-// Each function here takes the arguments of the Python call of the same name (outputs not
-// given), tests them, makes the outputs on the current stream's allocator and calls the
-// library. It answers
+// Each function here takes the arguments of the Python call of the same name (without its
+// outputs, or with those of the rotary calls), tests them, makes the outputs that are not
+// given and calls the library. It answers
 //   - a tuple of the outputs, or one output,
 //   - an int, the library's status, where that is not FA_OK,
 //   - None where an argument is not plainly right: the Python call then goes through its
@@ -22,8 +22,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <array>
 #include <climits>
 #include <cmath>
+#include <utility>
 
 #include "../../include/fa_gb300.h"
 
@@ -153,13 +156,30 @@ bool angles(const Tensor& positions, const Tensor& inv_freq, int64_t B, int64_t 
          inv_freq.size(0) <= INT_MAX / 2;
 }
 
-// (q, k or None, positions, inv_freq, interleaved, mscale, backward)
+// A caller's output for rows like `like`, no two of its rows on one another.
+bool rows_out(const Tensor& t, const Tensor& like, int dev) {
+  if (!rows(t, like.scalar_type(), dev) || !same_sizes(t, like)) return false;
+  std::array<std::pair<int64_t, int64_t>, 3> dims;
+  for (int i = 0; i < 3; ++i) dims[i] = {t.size(i) > 1 ? t.stride(i) : -1, t.size(i)};
+  std::sort(dims.begin(), dims.end());
+  int64_t reach = t.size(3);  // values up to the end of the rows of the dimensions so far
+  for (const auto& d : dims) {
+    if (d.first < 0) continue;  // a dimension of one
+    if (d.first < reach) return false;
+    reach += d.first * (d.second - 1);
+  }
+  return true;
+}
+
+// (q, k or None, positions, inv_freq, interleaved, mscale, backward, q_out or None, k_out or None)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const Tensor *q, *k = nullptr, *positions, *inv_freq;
   bool inter = false, back = false, shared = false;
   float mscale = 1.f;
-  if (n != 7 || !(q = tensor_of(a[0])) || (a[1] != Py_None && !(k = tensor_of(a[1]))) ||
+  const Tensor *q_out = nullptr, *k_out = nullptr;
+  if (n != 9 || !(q = tensor_of(a[0])) || (a[1] != Py_None && !(k = tensor_of(a[1]))) ||
+      (a[7] != Py_None && !(q_out = tensor_of(a[7]))) || (a[8] != Py_None && !(k_out = tensor_of(a[8]))) ||
       !(positions = tensor_of(a[2])) || !(inv_freq = tensor_of(a[3])) || !flag_of(a[4], &inter) ||
       !float_of(a[5], &mscale) || !flag_of(a[6], &back))
     Py_RETURN_NONE;
@@ -171,8 +191,9 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!angles(*positions, *inv_freq, B, T, dev, &shared) ||
       (k && (k->size(0) != B || k->size(2) != T || k->size(3) != d || Hk < 1)))
     Py_RETURN_NONE;
-  const Tensor qo = make({B, H, T, d}, type, dev);
-  const Tensor ko = k ? make({B, Hk, T, d}, type, dev) : Tensor();
+  if ((q_out && !rows_out(*q_out, *q, dev)) || (k_out && !(k && rows_out(*k_out, *k, dev)))) Py_RETURN_NONE;
+  const Tensor qo = q_out ? *q_out : make({B, H, T, d}, type, dev);
+  const Tensor ko = k_out ? *k_out : k ? make({B, Hk, T, d}, type, dev) : Tensor();
   const long long s[12] = {q->stride(0),  q->stride(1),  q->stride(2),  qo.stride(0), qo.stride(1), qo.stride(2),
                            k ? k->stride(0) : 0, k ? k->stride(1) : 0, k ? k->stride(2) : 0,
                            k ? ko.stride(0) : 0, k ? ko.stride(1) : 0, k ? ko.stride(2) : 0};
@@ -191,13 +212,16 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale)
+// (q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out or None)
 PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const Tensor* t[8];
   bool inter = false, shared = false;
   float mscale = 1.f;
-  if (n != 10 || !flag_of(a[8], &inter) || !float_of(a[9], &mscale)) Py_RETURN_NONE;
+  const Tensor* q_out = nullptr;
+  if (n != 11 || !flag_of(a[8], &inter) || !float_of(a[9], &mscale) ||
+      (a[10] != Py_None && !(q_out = tensor_of(a[10]))))
+    Py_RETURN_NONE;
   for (int i = 0; i < 8; ++i)
     if (!(t[i] = tensor_of(a[i]))) Py_RETURN_NONE;
   const Tensor &q = *t[0], &k = *t[1], &v = *t[2], &positions = *t[3], &slots = *t[4], &inv_freq = *t[5], &kp = *t[6],
@@ -211,7 +235,8 @@ PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !same_sizes(k, v) || !same_sizes(kp, vp) || k.size(0) != B || k.size(1) != Hkv || k.size(2) != T ||
       k.size(3) != d || kp.size(3) != d || !fits(P) || !fits(kp.size(1)))
     Py_RETURN_NONE;
-  const Tensor qo = make({B, H, T, d}, at::kBFloat16, dev);
+  if (q_out && !rows_out(*q_out, q, dev)) Py_RETURN_NONE;
+  const Tensor qo = q_out ? *q_out : make({B, H, T, d}, at::kBFloat16, dev);
   const long long s[12] = {q.stride(0), q.stride(1), q.stride(2), qo.stride(0), qo.stride(1), qo.stride(2),
                            k.stride(0), k.stride(1), k.stride(2), v.stride(0),  v.stride(1),  v.stride(2)};
   const fa_status st = fa_rope_append_paged(

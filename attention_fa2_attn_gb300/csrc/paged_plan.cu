@@ -30,7 +30,8 @@ namespace fa {
 constexpr int kPage = 16;
 constexpr int kPlanSeqs = 8;          // sequences per block, one warp each
 constexpr int kPlanThreads = kPlanSeqs * 32;
-constexpr int kPlanChunk = 512;       // tokens of a sequence per block
+constexpr int kPlanRows = 4;          // tokens of a lane, their loads in flight together
+constexpr int kPlanChunk = kPlanRows * 32;  // tokens of a sequence per block
 
 struct PlanParams {
   const int* cached;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   const int b = b0 + warp;
   // needs of every sequence before this block's, then of the block's own before this warp's
   int sum = 0;
+#pragma unroll 4
   for (int i = threadIdx.x; i < b0; i += kPlanThreads) {
     const PlanSeq s = plan_seq(p, i);
     sum += pages_of(s.c + s.n) - pages_of(s.c);
@@ -105,26 +107,29 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
   }
   // rows of the step: token t sits in row t, or (align_end) in row T - n + t
   const int lead = p.align_end ? p.T - s.n : 0;
-  const int t0 = blockIdx.y * kPlanChunk;
-  const int t1 = min(p.T, t0 + kPlanChunk);
+  const int r0 = blockIdx.y * kPlanChunk + lane;
   const size_t out = static_cast<size_t>(b) * p.T;
-  for (int r = t0 + lane; r < t1; r += 32) {
-    const int t = r - lead;
-    int slot = -1, pos = 0;
+  int page[kPlanRows];
+#pragma unroll
+  for (int i = 0; i < kPlanRows; ++i) {
+    const int t = r0 + 32 * i - lead;
+    page[i] = -1;
     if (t >= 0 && t < s.n) {
-      pos = s.c + t;
-      const int pg = pos / kPage;
-      int page;
-      if (pg < have) {
-        page = row[pg];  // an entry that no block of this launch writes
-      } else {
-        const int at = before + pg - have;
-        page = at < p.num_free ? __ldg(p.free_pages + at) : -1;
-      }
-      slot = page >= 0 ? page * kPage + pos % kPage : -1;
+      const int pg = (s.c + t) / kPage;
+      const int at = before + pg - have;
+      if (pg < have)
+        page[i] = row[pg];  // an entry that no block of this launch writes
+      else if (at < p.num_free)
+        page[i] = __ldg(p.free_pages + at);
     }
-    p.slots[out + r] = slot;
-    p.positions[out + r] = pos;
+  }
+#pragma unroll
+  for (int i = 0; i < kPlanRows; ++i) {
+    const int r = r0 + 32 * i, t = r - lead;
+    if (r >= p.T) continue;
+    const bool live = t >= 0 && t < s.n;
+    p.slots[out + r] = page[i] >= 0 ? page[i] * kPage + (s.c + t) % kPage : -1;
+    p.positions[out + r] = live ? s.c + t : 0;
   }
 }
 
