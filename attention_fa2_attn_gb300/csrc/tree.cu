@@ -26,8 +26,9 @@
 //     TMEM, so that one's softmax runs under the other's MMAs; the two are joined in
 //     TMEM at the end of a share (a warp can read the other's lanes).
 //   * R > 128 (WIDE): two tiles of rows against each key tile, as the prefill kernel.
-//   * warp 8: K/V pages by TMA, 16-token boxes through the block table, into a ring of
-//     128-byte-swizzled tiles; the Q tile too (rows are dense: one plain box).
+//   * warp 8, in narrow units with warp 10: K and V pages by TMA, 16-token boxes through the
+//     block table, into rings of 128-byte-swizzled tiles; the Q tile too (rows are dense: one
+//     plain box).
 //   * warp 9: TMEM and the MMA chain. S_t(x+1) is issued right behind PV_t(x).
 //   * the mask is looked at only in tiles that reach past S - n: a thread's row has
 //     its 128 bits of the tile in four registers. Rows of padding warps are skipped.
@@ -66,7 +67,7 @@ struct TrCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
-  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, producer, MMA issuer, two idle warps
+  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, producer, MMA issuer, V producer (narrow), an idle warp
   static constexpr int SOFTMAX_REGS = 192;  // 256 * 192 + 128 * 120 = 384 * 168
   static constexpr int AUX_REGS = 120;
   static_assert(SMEM <= 232448, "shared memory of an SM");
@@ -351,12 +352,21 @@ __global__ void __launch_bounds__(384, 1)
 
   if (warp >= 8) {
     warpgroup_reg_dealloc<C::AUX_REGS>();
-    if (warp == 8) {
-      // ======================= producer =======================
+    if (warp == 8 || (!WIDE && warp == 10)) {
+      // ======================= producers: K (and Q), V =======================
+      // Narrow: a warp each. A tile is 8 or 16 boxes of 16 rows per operand, and one warp
+      // issuing both spent 650 cycles a tile and 57 a box on it, more than the tile's HBM time
+      // at d = 64 (b19 hkv8 s16384 125 -> 107 us; d = 128 the same). Wide: one warp for both,
+      // there is time, and a second one's waits take issue slots from two softmax warps (b19
+      // hq64 t64 d64 319 us, 339 us with two).
+      const bool is_k = warp == 8;
+      const int op_first = is_k ? 0 : 1, op_end = WIDE || !is_k ? 2 : 1;  // 0: K, 1: V
       if (lane == 0) {
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
+        if (is_k) {
+          tma_prefetch_desc(&tmQ);
+          tma_prefetch_desc(&tmK);
+        }
+        if (op_end == 2) tma_prefetch_desc(&tmV);
       }
       TrWalk<WIDE> walk(bars);
       TrSeg w;
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(384, 1)
         int ent = -1, ent_next = fetch(0);
         // The last segment's Q is in use until its last S: this one's first tiles go ahead
         // of its Q (all but one stage of the ring, which that segment's own end frees).
-        bool q_due = true;
+        bool q_due = is_k;
         auto load_q = [&]() {
           if (lane == 0) {
             mbar_arrive_expect_tx(&bars->q_full, C::QT * C::Q_BYTES);
@@ -404,38 +414,31 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           const int s = g % ST;
-          const uint32_t u = g / ST;
           if ((x & 3) == 0) {
             ent = ent_next;
             ent_next = fetch(x + 4);
           }
           const int npg = min(8, n_pages - (w.x0 + x) * 8);  // pages past the end are not loaded
-          const uint32_t bytes = static_cast<uint32_t>(npg) * 16 * 128 * C::KCH;
           int pe = __shfl_sync(0xffffffffu, ent, (x & 3) * 8 + (pi & 7));
           if (pi < npg && (pe < 0 || pe >= p.num_pages)) {
             // never dereferenced: page 0 is loaded in its place, the output is undefined
             record_error(p.err, FA_ERR_BOUNDS, SITE_TR_TABLE);
             pe = 0;
           }
-          if (g >= ST && !mbar_wait(&bars->k_empty[s], (u - 1) & 1, tmo, abort_flag)) {
-            ok = false;
-            break;
+          for (int op = op_first; op < op_end; ++op) {
+            if (g >= ST && !mbar_wait(op ? &bars->v_empty[s] : &bars->k_empty[s], (g / ST - 1) & 1, tmo, abort_flag)) {
+              ok = false;
+              if (op > op_first) mbar_wait(&bars->k_full[s], (g / ST) & 1, tmo_unwind);  // issued: let it land
+              break;
+            }
+            uint64_t* full = op ? &bars->v_full[s] : &bars->k_full[s];
+            if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(npg) * 16 * 128 * C::KCH);
+            __syncwarp();
+            if (pi < npg)
+              tma_load_3d((op ? sV : sK) + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, op ? &tmV : &tmK, full,
+                          pc * 64, w.kvh, pe * 16);
           }
-          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[s], bytes);
-          __syncwarp();
-          if (pi < npg)
-            tma_load_3d(sK + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, &tmK, &bars->k_full[s], pc * 64,
-                        w.kvh, pe * 16);
-          if (g >= ST && !mbar_wait(&bars->v_empty[s], (u - 1) & 1, tmo, abort_flag)) {
-            ok = false;
-            mbar_wait(&bars->k_full[s], u & 1, tmo_unwind);  // K was issued: let it land
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&bars->v_full[s], bytes);
-          __syncwarp();
-          if (pi < npg)
-            tma_load_3d(sV + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, &tmV, &bars->v_full[s], pc * 64,
-                        w.kvh, pe * 16);
+          if (!ok) break;
         }
         if (ok && q_due) {
           if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
@@ -447,10 +450,9 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) fail(SITE_TR_PRODUCER);
       if (*abort_flag) {  // copies in flight must land before the CTA exits
         if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) {
-          mbar_wait(&bars->k_full[x % ST], (x / ST) & 1, tmo_unwind);
-          mbar_wait(&bars->v_full[x % ST], (x / ST) & 1, tmo_unwind);
-        }
+        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x)
+          for (int op = op_first; op < op_end; ++op)
+            mbar_wait(op ? &bars->v_full[x % ST] : &bars->k_full[x % ST], (x / ST) & 1, tmo_unwind);
       }
     } else if (warp == 9) {
       // ======================= MMA issuer =======================
