@@ -82,12 +82,13 @@ struct TrParams {
   const int* mask;
   long long mask_sb;  // words from a sequence's mask to the next's; 0: one for all
   int B, Hkv, T, R, U;  // U: row units of a (sequence, KV head)
+  int V;                // CTAs that go over the same keys side by side, a row unit each: U, or 1
   int words;            // of a mask row
   int max_pages, num_pages;
   float c;  // scale * log2(e)
   float* part;     // [2 * grid][128 * QT][D]: unnormalised O of partial shares
   float4* part_ml; // [2 * grid][128 * QT]: (max in log2 units, sum as P V saw it, sum, -)
-  int4* split;     // [grid]: (first row, rows, last CTA, -) of the unit that CTA c begins and does not end; z < 0: none
+  int4* split;     // [grid]: (first row, rows, partials, -) of the unit that CTA c begins and does not end; z == 0: none
   unsigned* err;
   unsigned long long timeout_ns;
 };
@@ -166,8 +167,13 @@ struct TrWalk {
     } while (j0 == j1);
     constexpr int PER = WIDE ? 1 : 2;
     g.b = b;
-    g.kvh = hu / p.U;
-    g.u = hu - g.kvh * p.U;
+    if (p.V > 1) {  // the CTA's row unit is its place in its group
+      g.kvh = hu;
+      g.u = static_cast<int>(blockIdx.x) % p.V;
+    } else {
+      g.kvh = hu / p.U;
+      g.u = hu - g.kvh * p.U;
+    }
     g.S = q.S;
     g.n = q.n;
     g.x0 = j0 * PER;
@@ -177,7 +183,7 @@ struct TrWalk {
     g.unit_end = at - from + cost;
     off += to - from;
     at += to - from;
-    if (off == cost * p.Hkv * p.U) {
+    if (off == cost * p.Hkv * (p.U / p.V)) {
       ++b;
       off = 0;
     }
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(384, 1)
     pdl_wait();
     if (threadIdx.x == 0) {
       record_error(p.err, FA_ERR_TIMEOUT, SITE_TR_SMEM);
-      p.split[cta] = make_int4(0, 0, -1, 0);
+      p.split[cta] = make_int4(0, 0, 0, 0);
     }
     return;
   }
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(384, 1)
     const int lo = min(p.B, static_cast<int>(threadIdx.x) * per), hi = min(p.B, lo + per);
     int mine = 0;  // a batch's whole cost is below 2^31
     for (int b = lo; b < hi; ++b) mine += tr_steps<WIDE>(tr_seq(p, b));
-    const int units = p.Hkv * p.U;  // of a sequence
+    const int units = p.Hkv * (p.U / p.V);  // of a sequence, for each CTA of a group
     mine *= units;
     int inc = mine;
 #pragma unroll
@@ -311,13 +317,13 @@ __global__ void __launch_bounds__(384, 1)
     // for 256 rows costs as much as some tiles: a CTA gets LEAST steps at least, but no two
     // units while others get none. A share is a step's cost or more either way, so that every
     // CTA between a unit's first and last has a step of it.
-    const int grid = static_cast<int>(gridDim.x);
+    const int grid = static_cast<int>(gridDim.x) / p.V, me = cta / p.V;  // groups, and this CTA's
     const bool few = steps <= 2 * C::LEAST * grid;
     const TrCost cost = few ? TrCost{1, 0} : TrCost{C::STEP, C::FRONT};
     const int G = few ? min(grid, max(steps / C::LEAST, p.B * units)) : grid;
     const int total = cost.step * steps + cost.front * p.B * units;
-    const int begin = cta < G ? static_cast<int>(static_cast<long long>(cta) * total / G) : total;
-    const int end = cta < G ? static_cast<int>((cta + 1ll) * total / G) : total;
+    const int begin = me < G ? static_cast<int>(static_cast<long long>(me) * total / G) : total;
+    const int end = me < G ? static_cast<int>((me + 1ll) * total / G) : total;
     if (threadIdx.x == 0) {
       bars->begin = begin;
       bars->end = end;
@@ -360,13 +366,14 @@ __global__ void __launch_bounds__(384, 1)
       // there is time, and a second one's waits take issue slots from two softmax warps (b19
       // hq64 t64 d64 319 us, 339 us with two).
       const bool is_k = warp == 8;
-      const int op_first = is_k ? 0 : 1, op_end = WIDE || !is_k ? 2 : 1;  // 0: K, 1: V
+      const CUtensorMap* my_map = is_k ? &tmK : &tmV;
+      uint8_t* my_ring = is_k ? sK : sV;
+      uint64_t* my_full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* my_empty = is_k ? bars->k_empty : bars->v_empty;
       if (lane == 0) {
-        if (is_k) {
-          tma_prefetch_desc(&tmQ);
-          tma_prefetch_desc(&tmK);
-        }
-        if (op_end == 2) tma_prefetch_desc(&tmV);
+        if (is_k) tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(my_map);
+        if (WIDE) tma_prefetch_desc(&tmV);
       }
       TrWalk<WIDE> walk(bars);
       TrSeg w;
@@ -425,18 +432,24 @@ __global__ void __launch_bounds__(384, 1)
             record_error(p.err, FA_ERR_BOUNDS, SITE_TR_TABLE);
             pe = 0;
           }
-          for (int op = op_first; op < op_end; ++op) {
-            if (g >= ST && !mbar_wait(op ? &bars->v_empty[s] : &bars->k_empty[s], (g / ST - 1) & 1, tmo, abort_flag)) {
-              ok = false;
-              if (op > op_first) mbar_wait(&bars->k_full[s], (g / ST) & 1, tmo_unwind);  // issued: let it land
-              break;
-            }
-            uint64_t* full = op ? &bars->v_full[s] : &bars->k_full[s];
-            if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(npg) * 16 * 128 * C::KCH);
+          const uint32_t bytes = static_cast<uint32_t>(npg) * 16 * 128 * C::KCH;
+          auto load = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty) -> bool {
+            if (g >= ST && !mbar_wait(&empty[s], (g / ST - 1) & 1, tmo, abort_flag)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
             __syncwarp();
             if (pi < npg)
-              tma_load_3d((op ? sV : sK) + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, op ? &tmV : &tmK, full,
-                          pc * 64, w.kvh, pe * 16);
+              tma_load_3d(ring + s * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, map, &full[s], pc * 64, w.kvh,
+                          pe * 16);
+            return true;
+          };
+          if constexpr (WIDE) {
+            ok = load(&tmK, sK, bars->k_full, bars->k_empty);
+            if (ok && !load(&tmV, sV, bars->v_full, bars->v_empty)) {
+              ok = false;
+              mbar_wait(&bars->k_full[s], (g / ST) & 1, tmo_unwind);  // K was issued: let it land
+            }
+          } else {
+            ok = load(my_map, my_ring, my_full, my_empty);
           }
           if (!ok) break;
         }
@@ -450,9 +463,10 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) fail(SITE_TR_PRODUCER);
       if (*abort_flag) {  // copies in flight must land before the CTA exits
         if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x)
-          for (int op = op_first; op < op_end; ++op)
-            mbar_wait(op ? &bars->v_full[x % ST] : &bars->k_full[x % ST], (x / ST) & 1, tmo_unwind);
+        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) {
+          mbar_wait(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
+          if (WIDE) mbar_wait(&bars->v_full[x % ST], (x / ST) & 1, tmo_unwind);
+        }
       }
     } else if (warp == 9) {
       // ======================= MMA issuer =======================
@@ -779,11 +793,11 @@ __global__ void __launch_bounds__(384, 1)
       const size_t out_row = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + row;
       const size_t part_row = static_cast<size_t>(slot) * (kTrTile * C::QT) + (WIDE ? t * kTrTile : 0) + r;
       if (threadIdx.x == 0 && w.from_start && !w.to_end && ok) {
-        // this CTA begins the unit: the last one with a share of it is the one whose share holds its end
+        // this CTA begins the unit: the last group with a share of it is the one whose share holds its end
         const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
         const int first_row = w.u * C::QT * kTrTile;
         p.split[cta] = make_int4((w.b * p.Hkv + w.kvh) * p.R + first_row, min(p.R - first_row, C::QT * kTrTile),
-                                 static_cast<int>(last), 0);
+                                 static_cast<int>(last) - cta / p.V + 1, 0);
         listed = true;
       }
       float m_all = m, sum = l + lc, lsum = l;
@@ -863,7 +877,7 @@ __global__ void __launch_bounds__(384, 1)
       // exchange area before the next segment fills it
       if constexpr (!WIDE) named_bar_sync(2, 256);
     }
-    if (threadIdx.x == 0 && !listed) p.split[cta] = make_int4(0, 0, -1, 0);
+    if (threadIdx.x == 0 && !listed) p.split[cta] = make_int4(0, 0, 0, 0);
   }
 
   tc_fence_before();
@@ -928,6 +942,7 @@ template <int D, int QT>
 __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const float* __restrict__ part,
                                                                          const float4* __restrict__ part_ml,
                                                                          const int4* __restrict__ split, int grid,
+                                                                         int V,
                                                                          __nv_bfloat16* __restrict__ o,
                                                                          float* __restrict__ lse) {
   constexpr int LANES = D / 4;           // lanes to a row
@@ -946,7 +961,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
     TrUnit u = {0, 0, 0, 0};
     if (c < grid) {
       const int4 un = split[c];
-      if (un.z >= 0) u = {0, un.x, un.y, un.z - c + 1};
+      u = {0, un.x, un.z > 0 ? un.y : 0, un.z};
       unit[c] = u;
     }
     int sum;
@@ -978,8 +993,8 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       if (unit[mid].first_item <= item) c = mid; else hi = mid;
     }
     const TrUnit un = unit[c];
-    // partial 0 is CTA c's last, the others are the later CTAs' first
-    auto at = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * ROWS; };
+    // partial 0 is CTA c's last, the others are the first of the later groups' CTAs
+    auto at = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i * V)) * ROWS; };
     auto get = [&](float4& ml, float4& v, size_t row_at) {
       ml = part_ml[row_at];
       v = *reinterpret_cast<const float4*>(part + row_at * D + col);
@@ -1087,7 +1102,7 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   const int merge_grid = kTrMergeBlocks * grid;
   return launch_dependent(tree_merge_kernel<D, C::QT>, dim3(merge_grid), dim3(256), 0, stream,
                           static_cast<const float*>(p.part), static_cast<const float4*>(p.part_ml),
-                          static_cast<const int4*>(p.split), grid, p.o, p.lse);
+                          static_cast<const int4*>(p.split), grid, p.V, p.o, p.lse);
 }
 
 }  // namespace fa
@@ -1172,6 +1187,10 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
   p.T = T;
   p.R = R;
   p.U = tr_wide(R) ? (R + 2 * kTrTile - 1) / (2 * kTrTile) : 1;
+  // The row units of a KV head read the same keys: side by side they take them from L2 (b19
+  // hq64 hkv8 t64 s16384 d128: 420 us, one after the other 455 us). Groups leave up to U - 1 SMs
+  // over, so only where that is little; a head of more rows than these is compute-bound anyway.
+  p.V = p.U <= 8 && p.U <= grid ? p.U : 1;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.c = scale * kLog2e;
