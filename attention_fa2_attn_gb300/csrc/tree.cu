@@ -147,12 +147,14 @@ struct TrSeg {
 // Walks a share segment by segment; each role walks by itself.
 template <bool WIDE>
 struct TrWalk {
-  int b, off, at, end;  // sequence, cost into it; cost into the batch; the share's end
-  TrCost c;
-  __device__ __forceinline__ TrWalk(const TrBars* s) : b(s->b0), off(s->off0), at(s->begin), end(s->end), c(s->cost) {}
+  int b, off, at;  // sequence, cost into it; cost into the batch
+  const volatile TrBars* s;  // the rest is read again each time: few registers over the tile loops
+  __device__ __forceinline__ TrWalk(const TrBars* bars) : b(bars->b0), off(bars->off0), at(bars->begin), s(bars) {}
   __device__ __forceinline__ bool next(const TrParams& p, TrSeg& g) {
     TrSeq q;
     int cost, hu, from, to, j0, j1;
+    const TrCost c = {s->cost.step, s->cost.front};
+    const int end = s->end;
     do {
       if (at >= end) return false;
       q = tr_seq(p, b);
@@ -656,10 +658,15 @@ __global__ void __launch_bounds__(384, 1)
       const int row = WIDE ? (w.u * 2 + t) * kTrTile + r : r;  // of the R rows
       const bool has_rows = row - lane < p.R;                  // some row of this warp exists (warp-uniform)
       const bool tile_exists = !WIDE || (w.u * 2 + t) * kTrTile < p.R;
-      const int node = row % p.T;
-      const bool live = row < p.R && node < w.n;
+      // The row's node, -1 if it has none. Formed anew where it is needed, in masked tiles and
+      // at the segment's end: kept over the loop below, it and the mask's address are spilled.
+      auto node_of = [&]() {
+        int x = row;
+        asm volatile("" : "+r"(x));
+        const int node = x % p.T;
+        return x < p.R && node < w.n ? node : -1;
+      };
       const int base = w.S - w.n;  // first node's key
-      const int* mrow = p.mask + w.b * p.mask_sb + static_cast<size_t>(node) * p.words;
       const int step = WIDE ? 1 : 2;
       const int x_first = WIDE ? 0 : t;
       const int mine = !tile_exists || w.nt <= x_first ? 0 : (w.nt - x_first + step - 1) / step;  // tiles of this slot
@@ -673,8 +680,10 @@ __global__ void __launch_bounds__(384, 1)
         const bool masked = key0 + kTrTile > base;
         uint32_t bits[4];  // fetched while S is being computed
         if (masked) {
+          const int node = node_of();
+          const int* mrow = p.mask + w.b * p.mask_sb + static_cast<size_t>(max(node, 0)) * p.words;
 #pragma unroll
-          for (int wd = 0; wd < 4; ++wd) bits[wd] = live ? tr_bits(mrow, p.words, w.n, key0 + 32 * wd - base) : 0u;
+          for (int wd = 0; wd < 4; ++wd) bits[wd] = node >= 0 ? tr_bits(mrow, p.words, w.n, key0 + 32 * wd - base) : 0u;
         }
         if (!wwait(&bars->s_full[t], cnt & 1)) {
           ok = false;
@@ -784,6 +793,7 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) fail(SITE_TR_SOFTMAX);
 
       // ---- the segment's end: final rows, or a partial
+      const bool live = node_of() >= 0;
       if (!live) {
         m = -INFINITY;
         l = lc = 0.f;
