@@ -311,7 +311,7 @@ def fa_paged_plan(cached_lens, new_lens, free_pages, block_table, T: int, align_
                   slots=None, positions=None, pages_used=None):
     """Block tables, slot maps and positions of a step: cached_lens, new_lens [B], free_pages [F],
     block_table [B][max_pages] (extended in place), all int32 on one device
-    -> (seqlens [B], slots [B][T], positions [B][T], pages_used [1])."""
+    -> (seqlens [B], slots [B][T], positions [B][T], pages_used [1]), new ones in one allocation."""
     if seqlens is None and slots is None and positions is None and pages_used is None:
         got = fast().paged_plan(cached_lens, new_lens, free_pages, block_table, T, align_end)
         if got is not None:
@@ -341,7 +341,8 @@ def fa_paged_plan(cached_lens, new_lens, free_pages, block_table, T: int, align_
 
 def fa_tree_mask(parents, seqlens, tree_lens=None, mask=None, positions=None):
     """Visibility mask and positions of drafted trees: parents [B][T], seqlens [B], tree_lens [B] or
-    None (T nodes each), int32 -> (mask [B][T][ceil(T/32)] int32, positions [B][T] int32)."""
+    None (T nodes each), int32 -> (mask [B][T][ceil(T/32)] int32, positions [B][T] int32), new ones in
+    one allocation."""
     if mask is None and positions is None:
         got = fast().tree_mask(parents, seqlens, tree_lens)
         if got is not None:

@@ -60,6 +60,29 @@ Tensor make(at::IntArrayRef sizes, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(sizes, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
 }
 
+// Dense int tensors as parts of one allocation, each at a 16-byte border: an allocation costs
+// more than all else that a step call does on the host but the launch.
+template <size_t N>
+std::array<Tensor, N> make_ints(const std::array<std::array<int64_t, 3>, N>& sizes, const std::array<int, N>& dims,
+                                int dev) {
+  std::array<int64_t, N> at;
+  int64_t total = 0;
+  for (size_t i = 0; i < N; ++i) {
+    int64_t n = 1;
+    for (int k = 0; k < dims[i]; ++k) n *= sizes[i][k];
+    at[i] = total;
+    total += (n + 3) & ~int64_t(3);
+  }
+  const Tensor all = make({total}, at::kInt, dev);
+  std::array<Tensor, N> out;
+  for (size_t i = 0; i < N; ++i) {
+    out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+    out[i].unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(sizes[i].data(), dims[i]));
+    out[i].unsafeGetTensorImpl()->set_storage_offset(at[i]);
+  }
+  return out;
+}
+
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
 bool int_of(PyObject* o, int* out) {
@@ -119,8 +142,8 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t B = table->size(0), pages = table->size(1), F = free_pages->size(0);
   if (cached->size(0) != B || fresh->size(0) != B || !fits(B) || !fits(pages) || !fits(F) || !fits(B * T))
     Py_RETURN_NONE;
-  const Tensor seqlens = make({B}, at::kInt, dev), slots = make({B, T}, at::kInt, dev),
-               positions = make({B, T}, at::kInt, dev), used = make({1}, at::kInt, dev);
+  const auto [seqlens, slots, positions, used] =
+      make_ints<4>({{{B, 0, 0}, {B, T, 0}, {B, T, 0}, {1, 0, 0}}}, {1, 2, 2, 1}, dev);
   const fa_status st =
       fa_paged_plan(ints(*cached), ints(*fresh), ints(*free_pages), static_cast<int>(F), ints_out(*table),
                     ints_out(seqlens), ints_out(slots), ints_out(positions), ints_out(used), static_cast<int>(B), T,
@@ -142,7 +165,7 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int64_t B = parents->size(0), T = parents->size(1);
   if (seqlens->size(0) != B || (lens && lens->size(0) != B) || !fits(B) || !fits(T)) Py_RETURN_NONE;
-  const Tensor mask = make({B, T, (T + 31) / 32}, at::kInt, dev), positions = make({B, T}, at::kInt, dev);
+  const auto [mask, positions] = make_ints<2>({{{B, T, (T + 31) / 32}, {B, T, 0}}}, {3, 2}, dev);
   const fa_status st = fa_tree_mask(ints(*parents), ints(*seqlens), lens ? ints(*lens) : nullptr, ints_out(mask),
                                     ints_out(positions), static_cast<int>(B), static_cast<int>(T), stream_of(dev));
   return answer(st, {mask, positions});

@@ -63,7 +63,7 @@ struct TrCfg {
   static constexpr int OFF_EX = OFF_BAR + 384;
   static constexpr int SMEM = OFF_EX + kTrTile * 5 * 4;  // at most 227 KB; the base is 1024-byte aligned
   static constexpr int LEAST = WIDE ? 4 : 1;  // steps of a share
-  static constexpr int STEP = WIDE ? 2 : 3, FRONT = WIDE ? 3 : 1;  // TrCost
+  static constexpr int STEP = WIDE ? 2 : 3, FRONT = WIDE ? 6 : 4;  // TrCost
   static constexpr int TMEM_COLS = 512;
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
@@ -82,7 +82,9 @@ struct TrParams {
   const int* mask;
   long long mask_sb;  // words from a sequence's mask to the next's; 0: one for all
   int B, Hkv, T, R, U;  // U: row units of a (sequence, KV head)
-  int V;                // CTAs that go over the same keys side by side, a row unit each: U, or 1
+  int V, Hv;            // CTAs of a group, which go over the same keys side by side: the row units of
+                        // Hv KV heads (V = U * Hv), or 1
+  int units;            // of a sequence, for each CTA of a group
   int words;            // of a mask row
   int max_pages, num_pages;
   float c;  // scale * log2(e)
@@ -169,9 +171,10 @@ struct TrWalk {
     } while (j0 == j1);
     constexpr int PER = WIDE ? 1 : 2;
     g.b = b;
-    if (p.V > 1) {  // the CTA's row unit is its place in its group
-      g.kvh = hu;
-      g.u = static_cast<int>(blockIdx.x) % p.V;
+    if (p.V > 1) {  // the CTA's head (of Hv) and row unit are its place in its group
+      const int place = static_cast<int>(blockIdx.x) % p.V;
+      g.kvh = hu * p.Hv + place / p.U;
+      g.u = place % p.U;
     } else {
       g.kvh = hu / p.U;
       g.u = hu - g.kvh * p.U;
@@ -185,7 +188,7 @@ struct TrWalk {
     g.unit_end = at - from + cost;
     off += to - from;
     at += to - from;
-    if (off == cost * p.Hkv * (p.U / p.V)) {
+    if (off == cost * p.units) {
       ++b;
       off = 0;
     }
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(384, 1)
     const int lo = min(p.B, static_cast<int>(threadIdx.x) * per), hi = min(p.B, lo + per);
     int mine = 0;  // a batch's whole cost is below 2^31
     for (int b = lo; b < hi; ++b) mine += tr_steps<WIDE>(tr_seq(p, b));
-    const int units = p.Hkv * (p.U / p.V);  // of a sequence, for each CTA of a group
+    const int units = p.units;
     mine *= units;
     int inc = mine;
 #pragma unroll
@@ -1173,14 +1176,15 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
       return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
   }
   for (int i = 0; i < 2; ++i) {
-    // one 16-token page of one KV head per box
+    // one 16-token page of one KV head per box; L2 fetches what a row is, no neighbour's
+    const CUtensorMapL2promotion fetch = d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)num_pages * 16};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2};
     cuuint32_t box[3] = {64, 1, 16};
     cuuint32_t es[3] = {1, 1, 1};
     if (enc(i == 0 ? &tk : &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(i == 0 ? k_pages : v_pages),
             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
   }
   TrParams p;
@@ -1197,10 +1201,21 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
   p.T = T;
   p.R = R;
   p.U = tr_wide(R) ? (R + 2 * kTrTile - 1) / (2 * kTrTile) : 1;
-  // The row units of a KV head read the same keys: side by side they take them from L2 (b19
-  // hq64 hkv8 t64 s16384 d128: 420 us, one after the other 455 us). Groups leave up to U - 1 SMs
-  // over, so only where that is little; a head of more rows than these is compute-bound anyway.
-  p.V = p.U <= 8 && p.U <= grid ? p.U : 1;
+  // Side by side: the row units of a KV head, which read the same keys (from L2 all but once:
+  // b19 hq64 hkv8 t64 s16384 d128 420 us, 455 us one after the other), and as many KV heads
+  // as fit, whose keys lie beside one another in a page (b38 hq64 hkv8 t8 s8192 d64 104 us,
+  // 112 us one after the other). Up to 16 CTAs, and groups that leave few SMs over.
+  p.V = p.Hv = 1;
+  if (p.U <= 8)
+    for (int h = Hkv; h >= 1; --h) {
+      const int v = h * p.U;
+      if (Hkv % h == 0 && v <= 16 && v <= grid && grid % v <= grid / 24) {
+        p.V = v;
+        p.Hv = h;
+        break;
+      }
+    }
+  p.units = p.V > 1 ? Hkv / p.Hv : Hkv * p.U;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.c = scale * kLog2e;

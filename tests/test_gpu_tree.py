@@ -188,6 +188,15 @@ def test_many_ragged_sequences(T, Hq, Hkv):
     _check(_case(B, Hq, Hkv, T, 64, seqlens, 17, max_pages=90))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [(5, 16, 16), (9, 22, 11), (3, 24, 3), (20, 21, 3), (40, 24, 6), (70, 40, 5), (300, 8, 1), (90, 26, 2)])
+def test_heads_and_row_units_side_by_side(T, Hq, Hkv, d):
+    # KV heads and row units that do and do not fill groups of CTAs, up to more units than a group takes
+    rng = np.random.default_rng(Hkv)
+    seqlens = np.concatenate([[T, 0, 1], rng.integers(T, 2500, 4)])
+    _check(_case(7, Hq, Hkv, T, d, seqlens, 30 + Hkv))
+
+
 def test_many_sequences():
     # more sequences than threads of a block: the share's scan goes over several each
     rng = np.random.default_rng(18)
