@@ -905,8 +905,8 @@ __global__ void __launch_bounds__(384, 1)
 // + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Every block makes the list of split
 // units from the CTAs' entries (in their order, so that all agree), keeps it in shared
 // memory and takes items of it in turn. What a row costs is round trips to L2, so: units
-// of up to four partials go two rows to a warp, all of them in flight; the others one
-// row to 1, 2, 4 or 8 warps (as many as the rows leave warps for), four partials each in
+// of two partials go two rows to a lane group, all of them in flight; the others one row
+// to 1, 2, 4 or 8 warps (as many as the rows leave warps for), four partials of each in
 // flight.
 struct TrRow {
   float m = -INFINITY, s = 0.f, l = 0.f;
@@ -923,7 +923,7 @@ struct TrRow {
 };
 
 constexpr int kTrMaxGrid = 1024;  // CTAs the list has room for
-constexpr int kTrFewParts = 4;
+constexpr int kTrFewParts = 2;
 constexpr int kTrMergeBlocks = 3;  // per SM
 
 struct TrUnit {
@@ -1020,23 +1020,20 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       if (lse && col == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
     };
     if (un.parts <= kTrFewParts) {
-      constexpr int IN = 2;
       const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
       TrRow acc[2];
-      for (int i0 = 0; i0 < un.parts; i0 += IN) {
-        float4 ml[IN][2], v[IN][2];
+      float4 ml[kTrFewParts][2], v[kTrFewParts][2];
 #pragma unroll
-        for (int k = 0; k < IN; ++k)
+      for (int k = 0; k < kTrFewParts; ++k)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            ml[k][r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            if (i0 + k < un.parts && row0 + r * PER < un.rows) get(ml[k][r], v[k][r], at(i0 + k) + row0 + r * PER);
-          }
+        for (int r = 0; r < 2; ++r) {
+          ml[k][r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+          if (k < un.parts && row0 + r * PER < un.rows) get(ml[k][r], v[k][r], at(k) + row0 + r * PER);
+        }
 #pragma unroll
-        for (int k = 0; k < IN; ++k)
+      for (int k = 0; k < kTrFewParts; ++k)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
-      }
+        for (int r = 0; r < 2; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if (row0 + r * PER < un.rows) put(acc[r], row0 + r * PER);
