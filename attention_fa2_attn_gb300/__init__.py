@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) fused attention forward: prefill, split-KV decode, paged decode.
+"""GB300 (sm_103a) fused attention: prefill, backward, split-KV and paged decode, and the
+calls around the paged cache (plans, rotary positions, trees of drafted tokens).
 
 The computation runs in the CUDA library ``libfa_gb300.so`` (C ABI in
 ``include/fa_gb300.h``); ``api`` holds thin PyTorch-facing wrappers with the

@@ -30,6 +30,12 @@ inline int launch_dependent(void (*kfn)(KArgs...), dim3 grid, dim3 block, size_t
   return launch_status();
 }
 
+// Whether two byte ranges share a byte (a null pointer: no).
+inline bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x && y && x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Only after pdl_wait(): a dependent launched early must not see the grid before this
 // one as complete while it still runs.

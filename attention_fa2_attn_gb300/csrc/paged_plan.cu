@@ -23,11 +23,14 @@
 // fit in registers): a thread walks up the parents in shared memory; as parent(i) < i the
 // visited bits fall, so it keeps one 32-bit word and stores it (and the empty ones it
 // skips) when the walk leaves it.
+#include <initializer_list>
+
 #include "launch.cuh"
 
 namespace fa {
 
 constexpr int kPage = 16;
+constexpr int kMostPages = (1 << 27) - 1;  // a pool's: its slots are 32-bit numbers
 constexpr int kPlanSeqs = 8;          // sequences per block, one warp each
 constexpr int kPlanThreads = kPlanSeqs * 32;
 constexpr int kPlanRows = 4;          // tokens of a lane, their loads in flight together
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     const int r = r0 + 32 * i, t = r - lead;
     if (r >= p.T) continue;
     const bool live = t >= 0 && t < s.n;
-    p.slots[out + r] = page[i] >= 0 ? page[i] * kPage + (s.c + t) % kPage : -1;
+    p.slots[out + r] = page[i] >= 0 && page[i] < kMostPages ? page[i] * kPage + (s.c + t) % kPage : -1;
     p.positions[out + r] = live ? s.c + t : 0;
   }
 }
@@ -247,6 +250,18 @@ fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_
   if (static_cast<long long>(B) * T >= (1ll << 31) || static_cast<long long>(B) * max_pages >= (1ll << 31) ||
       static_cast<long long>(max_pages) * kPage >= (1ll << 31) || T > 65535ll * kPlanChunk)
     return FA_ERR_UNSUPPORTED;
+  {
+    // blocks read the lengths and the free list of all sequences while others write theirs
+    const long long b4 = 4ll * B, bt4 = b4 * T;
+    const struct { const void* p; long long n; } in[] = {{cached, b4}, {new_lens, b4}, {free_pages, 4ll * num_free}},
+        out[] = {{block_table, b4 * max_pages}, {seqlens, b4}, {slots, bt4}, {positions, bt4}, {pages_used, 4}};
+    for (int i = 0; i < 5; ++i) {
+      for (const auto& x : in)
+        if (overlap(out[i].p, out[i].n, x.p, x.n)) return FA_ERR_INVALID_ARG;
+      for (int k = 0; k < i; ++k)
+        if (overlap(out[i].p, out[i].n, out[k].p, out[k].n)) return FA_ERR_INVALID_ARG;
+    }
+  }
   PlanParams p;
   p.cached = cached;
   p.new_lens = new_lens;
@@ -275,6 +290,15 @@ fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_l
     return FA_ERR_INVALID_ARG;
   if (B < 1 || T < 1) return FA_ERR_INVALID_ARG;
   if (B > 65535 || T > kTreeMaxNodes) return FA_ERR_UNSUPPORTED;
+  {
+    const long long b4 = 4ll * B, bt4 = b4 * T, m4 = bt4 * ((T + 31) / 32);
+    for (const void* x : {static_cast<const void*>(mask), static_cast<const void*>(positions)}) {
+      const long long n = x == mask ? m4 : bt4;
+      if (overlap(x, n, parents, bt4) || overlap(x, n, seqlens, b4) || overlap(x, n, tree_lens, b4))
+        return FA_ERR_INVALID_ARG;
+    }
+    if (overlap(mask, m4, positions, bt4)) return FA_ERR_INVALID_ARG;
+  }
   unsigned* err = device_error_word();
   if (!err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);

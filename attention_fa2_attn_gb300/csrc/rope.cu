@@ -393,6 +393,8 @@ fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void
       misaligned(v_pages, 16))
     return FA_ERR_INVALID_ARG;
   if (page_size != 16 || static_cast<long long>(num_pages) * 16 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  const long long pool = 32ll * num_pages * Hkv * d;
+  if (overlap(k_pages, pool, v_pages, pool)) return FA_ERR_INVALID_ARG;
   RopeParams p = {};
   p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
   p.k = side_of(k, k_pages, strides + 6, nullptr, B, Hkv, T);

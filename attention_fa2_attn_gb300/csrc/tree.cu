@@ -14,13 +14,15 @@
 // gets such a K/V tile (64 KB at d = 128) every 1.5 us.
 //
 // How.
-//   * Work is cut into equal shares of key tiles, not of sequences: every CTA of the
-//     one-per-SM grid sums the batch's key tiles for itself and takes the share
-//     [c N / G, (c+1) N / G) of them. Lengths live on the device and may differ by any
+//   * Work is cut into equal shares of key tiles, not of sequences: every group of CTAs of
+//     the one-per-SM grid sums the batch's cost for itself and takes the share
+//     [c N / G, (c+1) N / G) of it. Lengths live on the device and may differ by any
 //     factor; every SM has the same number of tiles within one. A share that does not
 //     cover its (sequence, KV head) whole leaves fp32 partials (O, max, sums) in the
 //     workspace, at most two per CTA, and the merge kernel joins them. A list of the
 //     split ones, one entry per CTA, tells it which; what is whole is written at once.
+//   * The CTAs of a group go over the same keys side by side: KV heads whose rows lie beside
+//     one another in a page, and the row units of a head, which share its keys in L2.
 //   * R <= 128 (NARROW): two key tiles at a time for the one tile of rows. Softmax
 //     warps 0-3 take the even tiles, 4-7 the odd ones, each with its own S/P and O in
 //     TMEM, so that one's softmax runs under the other's MMAs; the two are joined in
@@ -1146,9 +1148,18 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
       !(scale < INFINITY))
     return FA_ERR_INVALID_ARG;
   if (page_size != 16 || (d != 64 && d != 128)) return FA_ERR_UNSUPPORTED;
-  if (static_cast<long long>(num_pages) * 16 >= (1ll << 31) || static_cast<long long>(max_pages) * 16 >= (1ll << 31) ||
-      static_cast<long long>(B) * Hq * T >= (1ll << 31))
-    return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * 16 >= (1ll << 31) ||
+      static_cast<long long>(max_pages) * 16 > (1ll << 31) - 256 || static_cast<long long>(B) * Hq * T >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;  // (a key's index, rounded up to whole tiles, is a 32-bit number)
+  {
+    // o, lse and the workspace are written while q is still read by other CTAs
+    const long long rows = static_cast<long long>(B) * Hq * T, q_bytes = rows * d * 2;
+    if (overlap(o, q_bytes, q, q_bytes) || overlap(lse, rows * 4, q, q_bytes) || overlap(lse, rows * 4, o, q_bytes) ||
+        overlap(workspace, static_cast<long long>(ws_bytes), q, q_bytes) ||
+        overlap(workspace, static_cast<long long>(ws_bytes), o, q_bytes) ||
+        overlap(workspace, static_cast<long long>(ws_bytes), lse, rows * 4))
+      return FA_ERR_INVALID_ARG;
+  }
   const int R = Hq / Hkv * T;
   const long long steps = tr_most_steps(B, Hkv, R, max_pages);
   if (steps == 0) return FA_ERR_UNSUPPORTED;

@@ -339,7 +339,8 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
  *   row)] (new) are clamped and FA_ERR_BOUNDS is recorded. When the free list is too
  *   short, FA_ERR_BOUNDS is recorded, the pages past its end are -1 in the table and
  *   their tokens' slots -1; pages_used says how many were needed.
- *   block_table must not overlap any other argument.
+ *   Table entries outside [0, 2^27 - 1) give their tokens no slot (-1).
+ *   No output, block_table among them, may overlap another argument (FA_ERR_INVALID_ARG).
  */
 FA_API fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_pages, int num_free,
                                int* block_table, int* seqlens, int* slots, int* positions, int* pages_used,
@@ -354,6 +355,7 @@ FA_API fa_status fa_paged_plan(const int* cached, const int* new_lens, const int
  *     node j (itself or an ancestor). Rows from n_b on are 0.
  *   positions [B][T] int32 out: seqlens[b] - n_b + depth (0 at a root); 0 from n_b on.
  *   A parent outside [-1, i) records FA_ERR_BOUNDS and counts as -1. T <= 8192, B <= 65535.
+ *   No output may overlap another argument (FA_ERR_INVALID_ARG).
  */
 FA_API fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_lens, int* mask,
                               int* positions, int B, int T, void* stream);
@@ -406,7 +408,7 @@ FA_API fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, v
  *   A slot of -1 writes nothing (q is rotated all the same); any other slot outside
  *   [0, num_pages * 16) records FA_ERR_BOUNDS and writes nothing. Slots of one call must
  *   differ: which of two rows for one slot stays is undefined.
- *   page_size == 16.
+ *   The pools may not overlap (FA_ERR_INVALID_ARG). page_size == 16.
  */
 FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
                                       const long long* strides, const int* positions, const int* slots,
@@ -429,7 +431,8 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
  *   d in {64, 128}, page_size == 16, any Hq / Hkv and T with B * Hq * T < 2^31.
  *   workspace: at least fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count)
  *   bytes, 256-byte aligned; its contents need no initialisation, and calls that may
- *   overlap on the GPU need one each.
+ *   overlap on the GPU need one each. q, o, lse and the workspace may not overlap
+ *   (FA_ERR_INVALID_ARG).
  *   Keys and values inside a sequence must be finite, as for every call here: a row's weight
  *   of 0 does not cancel a NaN value that the mask hides from it. Pool rows past a
  *   sequence's end are never used, whatever they hold.

@@ -10,7 +10,18 @@ import torch
 import attention_fa2_attn_gb300 as fa
 from attention_fa2_attn_gb300 import _lib
 
-P = ctypes.c_void_p(256)
+class _Fresh:
+    """A fake address of its own each time it is taken, 2^44 bytes from the others."""
+
+    def __init__(self):
+        self.at = 0
+
+    def __call__(self):
+        self.at += 1 << 44
+        return ctypes.c_void_p(self.at)
+
+
+P = "an address"  # replaced by a fresh one in every call
 ODD = ctypes.c_void_p(258)  # 2-byte aligned only
 INV, UNS = _lib.FA_ERR_INVALID_ARG, _lib.FA_ERR_UNSUPPORTED
 STRIDES = (ctypes.c_longlong * 12)(*range(12))
@@ -23,8 +34,9 @@ def L():
 
 def _cases(call, base, wrong):
     for change, status in wrong:
-        args = dict(base, **change)
-        assert call(*args.values()) == status, (change, status)
+        fresh = _Fresh()
+        args = [fresh() if v is P else v for v in dict(base, **change).values()]
+        assert call(*args) == status, (change, status)
 
 
 def test_plan(L):
@@ -35,6 +47,33 @@ def test_plan(L):
     wrong += [({"num_free": -1}, INV), ({"B": 0}, INV), ({"T": 0}, INV), ({"max_pages": 0}, INV), ({"page_size": 32}, UNS),
               ({"B": 1 << 16, "T": 1 << 15}, UNS), ({"max_pages": 1 << 27}, UNS), ({"B": 1 << 20, "max_pages": 1 << 11}, UNS)]
     _cases(L.fa_paged_plan, base, wrong)
+
+
+def test_overlapping_outputs(L):
+    at = [ctypes.c_void_p(4096 * (i + 1)) for i in range(9)]
+    plan = lambda a: L.fa_paged_plan(a[0], a[1], a[2], 4, a[3], a[4], a[5], a[6], a[7], 2, 3, 4, 16, 0, None)  # noqa: E731
+    for out in range(3, 8):
+        for other in range(out):
+            for shift in (0, 4):
+                a = list(at)
+                a[out] = ctypes.c_void_p(a[other].value + shift)
+                if shift < (8 if other in (0, 1, 4) else 16):  # the shortest are two lengths long
+                    assert plan(a) == INV, (out, other, shift)
+    mask = lambda a: L.fa_tree_mask(a[0], a[1], a[2], a[3], a[4], 2, 3, None)  # noqa: E731
+    for out in (3, 4):
+        for other in range(out):
+            a = list(at)
+            a[out] = ctypes.c_void_p(a[other].value + 4)
+            assert mask(a) == INV, (out, other)
+    append = dict(q=P, k=P, v=P, qo=P, strides=STRIDES, positions=P, slots=P, inv_freq=P, kp=ctypes.c_void_p(1 << 20),
+                  vp=ctypes.c_void_p((1 << 20) + 4096), B=1, Hq=2, Hkv=1, T=3, page_size=16, num_pages=4, d=64, rot=32, inter=0,
+                  mscale=1.0, stream=None)
+    _cases(L.fa_rope_append_paged, append, [({}, INV)])
+    tree = dict(q=ctypes.c_void_p(1 << 20), kp=P, vp=P, table=P, seqlens=P, mask=P, shared=0, lens=None, o=P, lse=None, B=1, Hq=4,
+                Hkv=2, T=3, max_pages=4, page_size=16, num_pages=9, d=64, scale=0.125, ws=P, ws_bytes=1 << 20, stream=None)
+    near = ctypes.c_void_p((1 << 20) + 256)
+    _cases(L.fa_tree_decode_paged, tree, [({"o": near}, INV), ({"lse": near}, INV), ({"ws": near}, INV),
+                                          ({"ws": ctypes.c_void_p((1 << 19) + 256)}, INV)])
 
 
 def test_tree_mask(L):
@@ -76,7 +115,7 @@ def test_tree_attention(L):
     wrong += [({n: 0}, INV) for n in ("B", "Hq", "Hkv", "T", "max_pages", "num_pages")]
     wrong += [({"Hq": 5}, INV), ({"scale": 0.0}, INV), ({"scale": math.nan}, INV), ({"scale": math.inf}, INV), ({"d": 96}, UNS),
               ({"page_size": 32}, UNS), ({"num_pages": 1 << 27}, UNS), ({"max_pages": 1 << 27}, UNS),
-              ({"B": 1 << 20, "T": 1 << 10}, UNS)]
+              ({"max_pages": (1 << 27) - 1}, UNS), ({"B": 1 << 20, "T": 1 << 10}, UNS)]
     _cases(L.fa_tree_decode_paged, base, wrong)
     assert L.fa_tree_workspace_bytes(0, 4, 2, 3, 4, 64, 152) == 0
     assert L.fa_tree_workspace_bytes(1, 5, 2, 3, 4, 64, 152) == 0
