@@ -20,7 +20,8 @@
 // already on their way. A row's d * 2 bytes are whole 128-byte lines for the layouts
 // that matter, whatever the strides between rows, so no transpose through shared memory
 // is needed to go between [B][T][heads][d] and [B][heads][T][d].
-// Inputs whose rows are not whole aligned vectors take VEC = 1 (one pair, plain loads).
+// Rows that are not whole aligned 16-byte vectors take the widest that they are (b4 h32
+// n4096 d72, 20 of them rotated, bf16: pairs of values, 45 us; single ones 79 us).
 #include <math.h>
 
 #include <type_traits>
@@ -64,32 +65,48 @@ struct Vec16<float> {
   static constexpr int N = 4;
 };
 
-// VEC values as they lie in memory, and as floats
+// VEC values as they lie in memory (2 to 16 bytes, one access), and as floats
 template <typename E, int VEC>
 struct Raw {
-  using T = typename std::conditional<VEC == 1, E, uint4>::type;
+  static constexpr int BYTES = VEC * sizeof(E);
+  using T = typename std::conditional<
+      BYTES == 16, uint4,
+      typename std::conditional<BYTES == 8, uint2, typename std::conditional<BYTES == 4, uint32_t, E>::type>::type>::type;
   T r;
   __device__ __forceinline__ void load(const E* p) { r = *reinterpret_cast<const T*>(p); }
   __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<T*>(p) = r; }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    if constexpr (BYTES == 16)
+      return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    else if constexpr (BYTES == 8)
+      return i == 0 ? r.x : r.y;
+    else
+      return r;
+  }
   __device__ __forceinline__ void get(float (&v)[VEC]) const {
-    if constexpr (VEC == 1) {
+    if constexpr (BYTES == 2) {
       v[0] = static_cast<float>(r);
     } else {
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        v[i] = sizeof(E) == 4 ? __uint_as_float(w[i % 4])
-                              : __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        v[i] = sizeof(E) == 4 ? __uint_as_float(word(i % (BYTES / 4)))
+                              : __uint_as_float(i % 2 ? word(i / 2) & 0xffff0000u : word(i / 2) << 16);
     }
   }
   __device__ __forceinline__ void set(const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
+    if constexpr (BYTES == 2) {
       r = static_cast<E>(v[0]);
-    } else if constexpr (sizeof(E) == 2) {
-      r = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7]));
     } else {
-      r = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      uint32_t w[BYTES / 4];
+#pragma unroll
+      for (int i = 0; i < BYTES / 4; ++i)
+        w[i] = sizeof(E) == 4 ? __float_as_uint(v[i % VEC]) : pack_bf16x2(v[2 * i % VEC], v[(2 * i + 1) % VEC]);
+      if constexpr (BYTES == 16)
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (BYTES == 8)
+        r = make_uint2(w[0], w[1]);
+      else
+        r = w[0];
     }
   }
 };
@@ -216,10 +233,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopePara
   }
 }
 
-static bool strides_ok(const RopeSide& s, int vec, bool slots) {
+// Whether every row of the operand starts on a border of `vec` values of `elem` bytes.
+static bool rows_on(const RopeSide& s, int vec, unsigned elem, bool slots) {
   auto whole = [vec](long long x) { return x % vec == 0; };
   return whole(s.sb) && whole(s.sh) && whole(s.st) && (slots || (whole(s.db) && whole(s.dh) && whole(s.dt))) &&
-         (reinterpret_cast<uintptr_t>(s.src) & 15u) == 0 && (reinterpret_cast<uintptr_t>(s.dst) & 15u) == 0;
+         ((reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) & (vec * elem - 1)) == 0;
 }
 
 template <typename E, int VEC, bool APPEND>
@@ -230,7 +248,7 @@ static int launch_rope_rows(const RopeParams& p, bool interleaved, int rows, dim
                             stream, p);
   };
   auto with = [&](auto inter) {
-    if constexpr (VEC > 1) {
+    if constexpr (VEC == Vec16<E>::N) {
       if (rows == 1) return go(inter, std::integral_constant<int, 1>{});
       if (rows == 2) return go(inter, std::integral_constant<int, 2>{});
       if (rows == 3) return go(inter, std::integral_constant<int, 3>{});
@@ -243,10 +261,12 @@ static int launch_rope_rows(const RopeParams& p, bool interleaved, int rows, dim
 template <typename E, bool APPEND>
 static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   constexpr int V = Vec16<E>::N;
-  // whole vectors on both sides of every pair, in the tail and in every row's start
-  const bool vec = (p.rot / 2) % V == 0 && p.d % V == 0 && strides_ok(p.q, V, false) &&
-                   (p.k.heads == 0 || strides_ok(p.k, V, APPEND)) && (p.v.heads == 0 || strides_ok(p.v, V, true));
-  const int w = vec ? V : 1;
+  // the widest vectors that are whole on both sides of every pair, in the tail and at every row's start
+  int w = V;
+  while (w > 1 && !((p.rot / 2) % w == 0 && p.d % w == 0 && rows_on(p.q, w, sizeof(E), false) &&
+                    (p.k.heads == 0 || rows_on(p.k, w, sizeof(E), APPEND)) &&
+                    (p.v.heads == 0 || rows_on(p.v, w, sizeof(E), true))))
+    w /= 2;
   p.lanes = p.rot / 2 / w + ((p.d - p.rot) / w + 1) / 2;
   const int heads = p.q.heads + p.k.heads + p.v.heads;
   const long long blocks = (p.tokens * p.lanes + 31) / 32;
@@ -261,8 +281,10 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   const int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
   p.head_chunk = rows * kRopeWarps;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.head_chunk - 1) / p.head_chunk));
-  return vec ? launch_rope_rows<E, V, APPEND>(p, interleaved, rows, grid, stream)
-             : launch_rope_rows<E, 1, APPEND>(p, interleaved, rows, grid, stream);
+  if (w == V) return launch_rope_rows<E, V, APPEND>(p, interleaved, rows, grid, stream);
+  if (V > 4 && w == 4) return launch_rope_rows<E, 4, APPEND>(p, interleaved, rows, grid, stream);
+  if (w == 2) return launch_rope_rows<E, 2, APPEND>(p, interleaved, rows, grid, stream);
+  return launch_rope_rows<E, 1, APPEND>(p, interleaved, rows, grid, stream);
 }
 
 static bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }

@@ -380,7 +380,7 @@ FA_API fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, 
  *   fa_dtype). Rows of d are dense; strides (HOST memory, 12 values, in elements) are those
  *   of (batch, head, position) for q, q_out, k, k_out, so the rows may lie in a fused
  *   projection [B][T][heads][d]. Pointers need the element's alignment only; rows that are
- *   whole 16-byte vectors (and rot_dim / 2 a multiple of one) take the wider kernel.
+ *   whole 16-byte vectors (and rot_dim / 2 a multiple of one) take the widest kernel.
  *   q_out and k_out may be q and k with the same strides; otherwise no output may overlap
  *   an input or another output. Inputs may have strides of 0.
  *   positions [B][T] int32, or [T] with positions_shared; any int32 value.

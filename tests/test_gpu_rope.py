@@ -122,6 +122,27 @@ def test_strides_in_place_and_shared_positions(interleaved):
     assert torch.equal(wide, qo[:, :1].expand(B, Hq, T, d))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows_on_every_border_give_the_same_bits(interleaved, dtype):
+    # inputs and outputs that start 0 .. 8 values past a 16-byte border, rows that keep or break it
+    B, H, T, d = 2, 3, 5, 64
+    x, pos = _rand((B, H, T, d), 60, dtype), _positions(B, T, 61)
+    for rot in (64, 48, 40, 36, 34):
+        inv_freq, _ = fa.fa_rope_inv_freq(rot)
+        want = fa.fa_rope(x, None, pos, inv_freq, interleaved=interleaved)[0]
+        _check(want, x, pos, inv_freq, interleaved)
+        for off in (0, 1, 2, 4, 8):
+            for pitch in (d, d + 1, d + 2, d + 4, d + 8):
+                def at():
+                    flat = torch.zeros(off + B * H * T * pitch, dtype=dtype, device=DEV)
+                    return flat[off:].view(B, H, T, pitch)[..., :d]
+                src, dst = at(), at()
+                src.copy_(x)
+                fa.fa_rope(src, None, pos, inv_freq, interleaved=interleaved, q_out=dst)
+                assert torch.equal(dst, want), (rot, off, pitch)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_backward_is_the_transpose_and_matches_differences(interleaved):
     inv_freq, _ = fa.fa_rope_inv_freq(48)

@@ -210,6 +210,29 @@ def test_one_long_sequence_is_split_and_joined(T, d):
     _check(c)
 
 
+@pytest.mark.parametrize("T", [2, 70])
+def test_a_million_keys(T):
+    # one KV head over 2^20 + 37 keys: every CTA has a share of the one unit (or of each row unit)
+    c = _case(1, 4, 1, T, 64, [2**20 + 37], 40, lens=[T])
+    o, lse = _call(c)
+    rows = [0, T - 1]  # of the first and the last head
+    part = dict(c, q=c["q"][:, [0, 3]][:, :, rows].contiguous())
+    words = c["mask"][0].cpu().numpy().view(np.uint32)
+    k = c["kp"][c["table"][0].long()].reshape(-1, 64)[: 2**20 + 37].double().cpu().numpy()
+    v = c["vp"][c["table"][0].long()].reshape(-1, 64)[: 2**20 + 37].double().cpu().numpy()
+    q = part["q"][0].double().cpu().numpy()
+    for h in range(2):
+        for i, r in enumerate(rows):
+            s = k @ q[h, i] / 8.0
+            for j in range(T):
+                if not (int(words[r, j // 32]) >> (j % 32)) & 1:
+                    s[2**20 + 37 - T + j] = -np.inf
+            w = np.exp(s - s.max())
+            got, l = o[0, (0, 3)[h], r].double().cpu().numpy(), float(lse[0, (0, 3)[h], r])
+            assert np.abs(got - w @ v / w.sum()).max() <= 1e-3  # |O| is below 1e-2 here
+            assert abs(l - (s.max() + np.log(w.sum()))) <= 1e-3
+
+
 def test_past_32_bit_offsets():
     # a pool of 2^31 + elements whose last pages are in use
     Hkv, d, T = 8, 128, 4
