@@ -10,24 +10,33 @@ unsigned* device_error_word();
 int device_sm_count();
 unsigned long long wait_timeout_ns();
 
-// Launches `kfn` as a programmatic dependent of the launch before it on `stream`:
-// the kernel executes griddepcontrol.wait before its first global access.
+// Launches `kfn` as a programmatic dependent of the launch before it on `stream`, in
+// clusters of `cluster` blocks: the kernel executes griddepcontrol.wait before its first
+// global access.
 template <typename... KArgs, typename... Args>
-inline int launch_dependent(void (*kfn)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                            const Args&... args) {
+inline int launch_dependent_cluster(void (*kfn)(KArgs...), dim3 grid, int cluster, dim3 block, size_t smem,
+                                    cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, args...);
   if (e != cudaSuccess) return record_cuda_failure(e);
   return launch_status();
+}
+template <typename... KArgs, typename... Args>
+inline int launch_dependent(void (*kfn)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                            const Args&... args) {
+  return launch_dependent_cluster(kfn, grid, 1, block, smem, stream, args...);
 }
 
 // Whether two byte ranges share a byte (a null pointer: no).

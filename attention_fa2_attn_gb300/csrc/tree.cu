@@ -28,6 +28,8 @@
 //     TMEM, so that one's softmax runs under the other's MMAs; the two are joined in
 //     TMEM at the end of a share (a warp can read the other's lanes).
 //   * R > 128 (WIDE): two tiles of rows against each key tile, as the prefill kernel.
+//   * Small problems: a unit to a cluster, whose CTAs join their partials through shared
+//     memory (one launch, no workspace).
 //   * warp 8, in narrow units with warp 10: K and V pages by TMA, 16-token boxes through the
 //     block table, into rings of 128-byte-swizzled tiles; the Q tile too (rows are dense: one
 //     plain box).
@@ -37,6 +39,7 @@
 // Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the
 // CTA unwinds. The softmax warps leave together by a vote at the barrier they share.
 #include <atomic>
+#include <type_traits>
 
 #include "launch.cuh"
 
@@ -64,6 +67,12 @@ struct TrCfg {
   static constexpr int OFF_BAR = OFF_V + STAGES * KV_BYTES;
   static constexpr int OFF_EX = OFF_BAR + 384;
   static constexpr int SMEM = OFF_EX + kTrTile * 5 * 4;  // at most 227 KB; the base is 1024-byte aligned
+  // clustered: partials of all rows over Q and the rings, 16 bytes of padding a row against
+  // bank conflicts, then their maxima and sums (behind Q, which may still be on its way
+  // where a share is empty)
+  static constexpr int PART_PITCH = D * 4 + 16;
+  static constexpr int OFF_ML = QT * kTrTile * PART_PITCH;
+  static_assert(OFF_ML >= OFF_K && OFF_ML + QT * kTrTile * 16 <= OFF_BAR, "partials");
   static constexpr int LEAST = WIDE ? 4 : 1;  // steps of a share
   static constexpr int STEP = WIDE ? 2 : 3, FRONT = WIDE ? 6 : 4;  // TrCost
   static constexpr int TMEM_COLS = 512;
@@ -88,6 +97,7 @@ struct TrParams {
                         // Hv KV heads (V = U * Hv), or 1
   int units;            // of a sequence, for each CTA of a group
   int words;            // of a mask row
+  int C;                // CTAs of a cluster (the clustered form)
   int max_pages, num_pages;
   float c;  // scale * log2(e)
   float* part;     // [2 * grid][128 * QT][D]: unnormalised O of partial shares
@@ -98,9 +108,10 @@ struct TrParams {
 };
 
 // What shares are cut in: `step` for a step and, ahead of a unit's first, `front` for what
-// a unit costs beside its tiles (Q, the first S, writing O). Measured: a narrow unit about
-// a third of its pair of tiles, a wide one 1.5 tiles. Batches of so few steps that a CTA
-// has hardly more than one are cut by steps alone.
+// a unit costs beside its tiles (Q, the first S, writing O): 4/3 of a pair of tiles in
+// narrow units, 3 tiles in wide ones (64 sequences of up to 2100 keys, d = 128: 92 us with
+// starts uncounted, 63 us; 16 of up to 16384, 512 rows, d = 64: 174 us at 1.5 tiles, 166 us
+// at 3). Batches of so few steps that a CTA has hardly more than one are cut by steps alone.
 struct TrCost {
   int step, front;
   // the steps whose cost ends within the first `at` of a unit
@@ -114,6 +125,7 @@ struct TrBars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  int finished;  // the clustered form: this CTA's partial is there
   // where this CTA's share begins
   int b0, off0, begin, end, total, grid;
   TrCost cost;
@@ -146,6 +158,32 @@ struct TrSeg {
   int x0, nt;    // first key tile and how many
   bool from_start, to_end;
   int unit_end;  // where the unit ends in the whole batch's cost
+};
+
+// The clustered form: a unit to a cluster, an even run of its steps to each CTA.
+template <bool WIDE>
+struct TrOne {
+  bool done = false;
+  __device__ __forceinline__ TrOne(const TrBars*) {}
+  __device__ __forceinline__ bool next(const TrParams& p, TrSeg& g) {
+    if (done) return false;
+    done = true;
+    constexpr int PER = WIDE ? 1 : 2;
+    const int unit = static_cast<int>(blockIdx.x) / p.C, rank = static_cast<int>(blockIdx.x) - unit * p.C;
+    const int bh = unit / p.U;
+    g.b = bh / p.Hkv;
+    g.kvh = bh - g.b * p.Hkv;
+    g.u = unit - bh * p.U;
+    const TrSeq q = tr_seq(p, g.b);
+    g.S = q.S;
+    g.n = q.n;
+    const int steps = tr_steps<WIDE>(q), per = (steps + p.C - 1) / p.C;
+    g.x0 = min(steps, rank * per) * PER;
+    g.nt = max(0, min(q.tiles, min(steps, (rank + 1) * per) * PER) - g.x0);
+    g.from_start = g.to_end = p.C == 1;
+    g.unit_end = 0;
+    return true;
+  }
 };
 
 // Walks a share segment by segment; each role walks by itself.
@@ -219,6 +257,27 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// The other CTAs of the cluster: a barrier for all their threads, and reads of their shared
+// memory at the place that `p` has in this CTA's.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ int ld_cluster_int(uint32_t a) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
 __device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
   uint32_t r;
   asm volatile(
@@ -250,11 +309,27 @@ __device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, in
   return left < 32 ? v & ((1u << left) - 1u) : v;
 }
 
-template <int D, bool WIDE>
+// A row's partials joined: maximum, sums, and a lane's four columns of O.
+struct TrRow {
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
+    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
+    m = mn;
+  }
+};
+
+template <int D, bool WIDE, bool CL>
 __global__ void __launch_bounds__(384, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const TrParams p) {
   using C = TrCfg<D, WIDE>;
+  using Walk = typename std::conditional<CL, TrOne<WIDE>, TrWalk<WIDE>>::type;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
@@ -271,7 +346,7 @@ __global__ void __launch_bounds__(384, 1)
     pdl_wait();
     if (threadIdx.x == 0) {
       record_error(p.err, FA_ERR_TIMEOUT, SITE_TR_SMEM);
-      p.split[cta] = make_int4(0, 0, 0, 0);
+      if (!CL) p.split[cta] = make_int4(0, 0, 0, 0);
     }
     return;
   }
@@ -291,13 +366,14 @@ __global__ void __launch_bounds__(384, 1)
     }
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
+    bars->finished = 0;
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
   pdl_wait();
 
   // ---- this CTA's share of the batch's cost: a block-wide scan over the sequences
-  {
+  if constexpr (!CL) {
     const int per = (p.B + C::THREADS - 1) / C::THREADS;
     const int lo = min(p.B, static_cast<int>(threadIdx.x) * per), hi = min(p.B, lo + per);
     int mine = 0;  // a batch's whole cost is below 2^31
@@ -382,7 +458,7 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(my_map);
         if (WIDE) tma_prefetch_desc(&tmV);
       }
-      TrWalk<WIDE> walk(bars);
+      Walk walk(bars);
       TrSeg w;
       uint32_t g = 0;  // key tiles loaded so far (ring position)
       uint32_t q_loads = 0;
@@ -528,7 +604,7 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         return r;
       };
-      TrWalk<WIDE> walk(bars);
+      Walk walk(bars);
       TrSeg w;
       uint32_t g = 0;      // key tiles of earlier segments (ring position)
       uint32_t seg_i = 0;
@@ -636,6 +712,10 @@ __global__ void __launch_bounds__(384, 1)
       commit(&bars->drain);  // every MMA must finish before TMEM is released
       mbar_wait(&bars->drain, 0, tmo_unwind);
     }
+    if (CL && p.C > 1) {  // the partials are there; they have been read
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     // ======================= softmax: warps 0-3 (slot 0), 4-7 (slot 1) =======================
     warpgroup_reg_alloc<C::SOFTMAX_REGS>();
@@ -653,7 +733,7 @@ __global__ void __launch_bounds__(384, 1)
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
     };
-    TrWalk<WIDE> walk(bars);
+    Walk walk(bars);
     TrSeg w;
     uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
     uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
@@ -807,7 +887,7 @@ __global__ void __launch_bounds__(384, 1)
       const int slot = 2 * cta + (w.from_start ? 1 : 0);
       const size_t out_row = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + row;
       const size_t part_row = static_cast<size_t>(slot) * (kTrTile * C::QT) + (WIDE ? t * kTrTile : 0) + r;
-      if (threadIdx.x == 0 && w.from_start && !w.to_end && ok) {
+      if (!CL && threadIdx.x == 0 && w.from_start && !w.to_end && ok) {
         // this CTA begins the unit: the last group with a share of it is the one whose share holds its end
         const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
         const int first_row = w.u * C::QT * kTrTile;
@@ -829,6 +909,9 @@ __global__ void __launch_bounds__(384, 1)
         f1 = ex2_approx(m1 - m_use);
         sum = f0 * ex[256 + r] + f1 * ex[384 + r];
         if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
+      } else if (CL) {
+        // (a partial goes where the other slot's MMAs read their operands)
+        if (!vote_all(1, 256, ok)) break;
       } else if (!ok) {
         break;
       }
@@ -868,6 +951,13 @@ __global__ void __launch_bounds__(384, 1)
                   live ? make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
                                     pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]))
                        : make_uint4(0u, 0u, 0u, 0u);
+          } else if (CL) {
+            if (m_all != -INFINITY) {  // else its weight is 0 and nobody reads it (nor has Q necessarily come)
+              float* dst = reinterpret_cast<float*>(smem + (WIDE ? t * kTrTile + r : r) * C::PART_PITCH) + col0 + cc * 32;
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            }
           } else if (live) {
             float* dst = p.part + part_row * D + col0 + cc * 32;
 #pragma unroll
@@ -883,7 +973,8 @@ __global__ void __launch_bounds__(384, 1)
           if (whole) {
             if (p.lse) p.lse[out_row] = lsum > 0.f ? (m_all + log2f(lsum)) * kLn2 : -INFINITY;
           } else {
-            p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
+            float4* ml = CL ? reinterpret_cast<float4*>(smem + C::OFF_ML) + (WIDE ? t * kTrTile + r : r) : p.part_ml + part_row;
+            *ml = make_float4(m_all, sum, lsum, 0.f);
           }
         }
       }
@@ -892,7 +983,41 @@ __global__ void __launch_bounds__(384, 1)
       // exchange area before the next segment fills it
       if constexpr (!WIDE) named_bar_sync(2, 256);
     }
-    if (threadIdx.x == 0 && !listed) p.split[cta] = make_int4(0, 0, 0, 0);
+    if (!CL && threadIdx.x == 0 && !listed) p.split[cta] = make_int4(0, 0, 0, 0);
+    if (CL && p.C > 1) {
+      // Joined inside the cluster: each CTA reads its part of the rows out of all CTAs' shared
+      // memory. (These warps: the others have given their registers away.)
+      if (threadIdx.x == 0) bars->finished = ok;
+      cluster_sync();
+      constexpr int LANES = D / 4, PER = 32 / LANES;  // lanes to a row, rows of a warp's load
+      const int rank = cta % p.C;
+      const int unit_rows = min(p.R - w.u * C::QT * kTrTile, C::QT * kTrTile);
+      const int per = (unit_rows + p.C - 1) / p.C, last = min(unit_rows, (rank + 1) * per);
+      const int my = lane / LANES, col = lane % LANES * 4;
+      bool all = true;
+      for (int c = 0; c < p.C; ++c) all &= ld_cluster_int(in_cta(&bars->finished, c)) != 0;
+      for (int row = rank * per + warp * PER + my; all && row < last; row += 8 * PER) {
+        TrRow acc;
+        for (int c0 = 0; c0 < p.C; c0 += 4) {  // four CTAs' loads in flight
+          float4 ml[4], o[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c0 + c >= p.C) continue;
+            ml[c] = ld_cluster(in_cta(smem + C::OFF_ML + row * 16, c0 + c));
+            o[c] = ld_cluster(in_cta(smem + row * C::PART_PITCH + col * 4, c0 + c));
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < p.C) acc.add(ml[c].x, ml[c].y, ml[c].z, o[c]);
+        }
+        const float inv = acc.s > 0.f ? 1.f / acc.s : 0.f;
+        const size_t out = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + w.u * C::QT * kTrTile + row;
+        *reinterpret_cast<uint2*>(p.o + out * D + col) =
+            make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
+        if (p.lse && col == 0) p.lse[out] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * kLn2 : -INFINITY;
+      }
+      cluster_sync();  // nobody leaves while others read its shared memory
+    }
   }
 
   tc_fence_before();
@@ -910,20 +1035,6 @@ __global__ void __launch_bounds__(384, 1)
 // of two partials go two rows to a lane group, all of them in flight; the others one row
 // to 1, 2, 4 or 8 warps (as many as the rows leave warps for), four partials of each in
 // flight.
-struct TrRow {
-  float m = -INFINITY, s = 0.f, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
-  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
-    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
-    const float mn = fmaxf(m, m2);
-    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
-    s = s * fa + s2 * fb;
-    l = l * fa + l2 * fb;
-    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
-    m = mn;
-  }
-};
-
 constexpr int kTrMaxGrid = 1024;  // CTAs the list has room for
 constexpr int kTrFewParts = 2;
 constexpr int kTrMergeBlocks = 3;  // per SM
@@ -1088,16 +1199,33 @@ static long long tr_most_steps(int B, int Hkv, int R, int max_pages) {
 // CTAs of a launch: one to an SM, none that could have no step.
 static int tr_grid(long long steps, int sms) { return static_cast<int>(steps < sms ? steps : sms); }
 
+// The clustered form for small problems: a unit to a cluster of C CTAs, which join their
+// partials through shared memory. It saves the share scan, the second launch and the
+// partials' way through L2 (b1 hkv8 t8 s1000 d128 8.2 us, 11.0 us), but takes no more
+// than C of the SMs for a unit and counts with the longest context the table allows: taken
+// where that leaves a CTA about as many steps as equal shares over all SMs would. Returns C,
+// 0 for the general form.
+static int tr_cluster(long long steps, int B, int Hkv, int R, int max_pages, int sms) {
+  const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
+  const long long units = static_cast<long long>(B) * Hkv * U, of_unit = steps / units;
+  if (units > sms) return 0;
+  int c = 1;
+  // (an 8-CTA cluster needs 8 free SMs of one GPC: 15 of them fit on 152 SMs, 36 of 4)
+  while (c < 8 && units <= sms / (2 * c + c / 2) && c < of_unit) c *= 2;
+  const long long per = (of_unit + c - 1) / c, shared = (steps + sms - 1) / sms;
+  return per <= shared + (tr_wide(R) ? 3 : 1) ? c : 0;
+}
+
 static size_t tr_part_bytes(int grid, int R, int d) {
   return static_cast<size_t>(2) * grid * (tr_wide(R) ? 256 : 128) * d * 4;
 }
 static size_t tr_ml_bytes(int grid, int R) { return static_cast<size_t>(2) * grid * (tr_wide(R) ? 256 : 128) * 16; }
 
-template <int D, bool WIDE>
+template <int D, bool WIDE, bool CL>
 static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TrParams& p,
                        int grid, cudaStream_t stream) {
   using C = TrCfg<D, WIDE>;
-  auto kfn = tree_kernel<D, WIDE>;
+  auto kfn = tree_kernel<D, WIDE, CL>;
   // the attribute holds for the life of the device's context: asked for once per device
   static std::atomic<unsigned long long> asked{0};
   int dev = 0;
@@ -1109,6 +1237,7 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
     if (e != cudaSuccess) return record_cuda_failure(e);
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
+  if (CL) return launch_dependent_cluster(kfn, dim3(grid), p.C, dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (rc != FA_OK) return rc;
   const int merge_grid = kTrMergeBlocks * grid;
@@ -1129,6 +1258,7 @@ size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int
   if (R >= (1ll << 31)) return 0;
   const long long steps = tr_most_steps(B, Hkv, static_cast<int>(R), max_pages);
   if (steps == 0) return 0;
+  if (tr_cluster(steps, B, Hkv, static_cast<int>(R), max_pages, num_sms)) return 0;
   const int grid = tr_grid(steps, num_sms);
   return tr_part_bytes(grid, static_cast<int>(R), d) + tr_ml_bytes(grid, static_cast<int>(R)) +
          static_cast<size_t>(grid) * 16;
@@ -1139,8 +1269,7 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
                                void* o, float* lse, int B, int Hq, int Hkv, int T, int max_pages, int page_size,
                                int num_pages, int d, float scale, void* workspace, size_t ws_bytes, void* stream) {
   auto mis = [](const void* x, uintptr_t m) { return (reinterpret_cast<uintptr_t>(x) & (m - 1)) != 0; };
-  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !tree_mask || !o || !workspace)
-    return FA_ERR_INVALID_ARG;
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !tree_mask || !o) return FA_ERR_INVALID_ARG;
   if (mis(q, 16) || mis(k_pages, 16) || mis(v_pages, 16) || mis(o, 16) || mis(block_table, 4) || mis(seqlens, 4) ||
       mis(tree_mask, 4) || (tree_lens && mis(tree_lens, 4)) || (lse && mis(lse, 4)) || mis(workspace, 256))
     return FA_ERR_INVALID_ARG;
@@ -1166,8 +1295,10 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
   const int sms = device_sm_count();
   if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
   if (sms > kTrMaxGrid) return FA_ERR_UNSUPPORTED;
-  if (ws_bytes < fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, sms)) return FA_ERR_INVALID_ARG;
-  const int grid = tr_grid(steps, sms);
+  const size_t need = fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, sms);
+  if (ws_bytes < need || (need && !workspace)) return FA_ERR_INVALID_ARG;
+  const int cluster = tr_cluster(steps, B, Hkv, R, max_pages, sms);
+  const int grid = cluster ? B * Hkv * (tr_wide(R) ? (R + 2 * kTrTile - 1) / (2 * kTrTile) : 1) * cluster : tr_grid(steps, sms);
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;
 
@@ -1224,22 +1355,30 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
       }
     }
   p.units = p.V > 1 ? Hkv / p.Hv : Hkv * p.U;
+  p.C = cluster;
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.c = scale * kLog2e;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.part = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float4*>(ws + tr_part_bytes(grid, R, d));
-  p.split = reinterpret_cast<int4*>(ws + tr_part_bytes(grid, R, d) + tr_ml_bytes(grid, R));
+  p.part = nullptr;
+  p.part_ml = nullptr;
+  p.split = nullptr;
+  if (!cluster) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float4*>(ws + tr_part_bytes(grid, R, d));
+    p.split = reinterpret_cast<int4*>(ws + tr_part_bytes(grid, R, d) + tr_ml_bytes(grid, R));
+  }
   p.err = device_error_word();
   if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
   p.timeout_ns = wait_timeout_ns();
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  int rc;
-  if (tr_wide(R))
-    rc = d == 128 ? launch_tree<128, true>(tq, tk, tv, p, grid, cs) : launch_tree<64, true>(tq, tk, tv, p, grid, cs);
-  else
-    rc = d == 128 ? launch_tree<128, false>(tq, tk, tv, p, grid, cs) : launch_tree<64, false>(tq, tk, tv, p, grid, cs);
+  auto go = [&](auto wide, auto cl) {
+    constexpr bool W = decltype(wide)::value, CL = decltype(cl)::value;
+    return d == 128 ? launch_tree<128, W, CL>(tq, tk, tv, p, grid, cs) : launch_tree<64, W, CL>(tq, tk, tv, p, grid, cs);
+  };
+  const std::true_type yes{};
+  const std::false_type no{};
+  const int rc = tr_wide(R) ? (cluster ? go(yes, yes) : go(yes, no)) : (cluster ? go(no, yes) : go(no, no));
   return static_cast<fa_status>(rc);
 }
 

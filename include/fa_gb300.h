@@ -430,7 +430,7 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
  *   batch with mask_shared; o, lse as fa_decode_paged (lse may be NULL).
  *   d in {64, 128}, page_size == 16, any Hq / Hkv and T with B * Hq * T < 2^31.
  *   workspace: at least fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count)
- *   bytes, 256-byte aligned; its contents need no initialisation, and calls that may
+ *   bytes, 256-byte aligned (may be NULL where that is 0); its contents need no initialisation, and calls that may
  *   overlap on the GPU need one each. q, o, lse and the workspace may not overlap
  *   (FA_ERR_INVALID_ARG).
  *   Keys and values inside a sequence must be finite, as for every call here: a row's weight
@@ -446,7 +446,8 @@ FA_API fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const 
                                       float scale, void* workspace, size_t ws_bytes, void* stream);
 
 /* fa_tree_workspace_bytes -- two fp32 partials (O, max, sums) of a row tile for each CTA that
- * the call launches on num_sms SMs, and its list of split work; 0 for invalid sizes. */
+ * the call launches on num_sms SMs, and its list of split work; 0 for problems that are small
+ * under the longest contexts the table allows (joined in shared memory), and for invalid sizes. */
 FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
 
 /*

@@ -157,7 +157,8 @@ def _wrong(s):
                    {"seqlens": i64}, {"seqlens": seqlens[:2]}, {"tree_mask": mask[:2]}, {"tree_mask": mask.long()},
                    {"tree_mask": _i32(np.zeros((T, 2)))}, {"tree_lens": i64}, {"tree_lens": s["new"][:1]}, {"seqlens": seqlens.cpu()},
                    {"out": q.float()}, {"lse": torch.empty(B, 6, T, dtype=torch.float64, device=DEV)},
-                   {"workspace": torch.empty(16, dtype=torch.uint8, device=DEV)}):
+                   {"block_table": torch.zeros(B, 65536, dtype=torch.int32, device=DEV),
+                    "workspace": torch.empty(16, dtype=torch.uint8, device=DEV)}):
         yield lambda c=change: fa.fa_tree_decode_paged(**dict(tree, **c)), change
 
 

@@ -51,9 +51,18 @@ def _ref(c, lens=True, **kw):
     return oracle.tree_attention(c["q"], c["kp"], c["vp"], c["table"], c["seqlens"], c["mask"], c["lens"] if lens else None, **kw)
 
 
+def _wide_table(c):
+    """The same problem under a table for contexts of 320 000 keys: the call counts with the longest that the
+    table allows, and takes the form for large problems."""
+    t = c["table"]
+    return dict(c, table=torch.cat([t, t.new_full((t.shape[0], 20000 - t.shape[1]), -1)], 1).contiguous())
+
+
 def _check(c, what="", lens=True, **kw):
     o, lse = _call(c, lens, **kw)
-    compare(o, lse, *_ref(c, lens, **kw), what=what)
+    want = _ref(c, lens, **kw)
+    compare(o, lse, *want, what=what)
+    compare(*_call(_wide_table(c), lens, **kw), *want, what=what + ", wide table")
     assert fa.fa_get_last_device_error()[0] == 0
     return o, lse
 
@@ -124,9 +133,12 @@ def test_a_chain_is_causal_decode():
         compare(o, lse, o_ref, lse_ref)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("T", [2, 40])
-def test_pool_rows_behind_a_sequence_do_not_matter(T):
+def test_pool_rows_behind_a_sequence_do_not_matter(T, wide):
     c = _case(2, 8, 2, T, 128, [T + 3, 211], 11, lens=[T, 1], max_pages=20)
+    if wide:
+        c = _wide_table(c)
     o, lse = _check(c)
     kp, vp = c["kp"].clone(), c["vp"].clone()
     used = torch.zeros(kp.shape[0] * 16, dtype=torch.bool, device=DEV)
@@ -142,8 +154,12 @@ def test_pool_rows_behind_a_sequence_do_not_matter(T):
     assert fa.fa_get_last_device_error()[0] == 0
 
 
-def test_rows_that_the_call_does_not_own_are_left_as_they_were():
-    c = _case(2, 8, 2, 5, 64, [50, 300], 12)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("T", [5, 50])
+def test_rows_that_the_call_does_not_own_are_left_as_they_were(T, wide):
+    c = _case(2, 8, 2, T, 64, [50, 300], 12)
+    if wide:
+        c = _wide_table(c)
     B, Hq, T, d = c["q"].shape
     o = torch.full((B + 1, Hq, T, d), 7.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((B + 1, Hq, T), 7.0, device=DEV)
@@ -254,12 +270,13 @@ def test_bad_table_entries_are_reported():
     for lens in (None, [4]):
         c = _case(1, 8, 2, 4, 64, [300], 24, lens=lens)
         nodes = int(c["lens"][0])  # the first has none: no key is needed, so no entry is read
-        t = c["table"].clone()
-        for entry in (c["kp"].shape[0], -1):
-            t[0, 3] = entry
-            o, _ = _call(dict(c, table=t))
-            assert fa.fa_get_last_device_error()[0] == (5 if nodes else 0)
-            assert nodes or not o.any()
+        for form in (c, _wide_table(c)):
+            t = form["table"].clone()
+            for entry in (c["kp"].shape[0], -1):
+                t[0, 3] = entry
+                o, _ = _call(dict(c, table=t))
+                assert fa.fa_get_last_device_error()[0] == (5 if nodes else 0)
+                assert nodes or not o.any()
         _check(c)
 
 
@@ -272,15 +289,19 @@ def test_lengths_out_of_range_are_clamped():
     assert not o3.any() and torch.isinf(lse3).all()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("T", [4, 60])
-def test_graph_streams_and_workspaces(T):
+def test_graph_streams_and_workspaces(T, wide):
     c = _case(3, 8, 2, T, 128, [700, 90, 1300], 26)
+    if wide:
+        c = _wide_table(c)
     want = _call(c)
     for _ in range(3):
         got = _call(c)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     B, Hq, _, d = c["q"].shape
     nbytes = fa.fa_tree_workspace_bytes(B, Hq, 2, T, c["table"].shape[1], d)
+    assert (nbytes > 0) == wide
     ws = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)  # NaNs: nothing of it is taken for a partial
     outs = (torch.empty_like(want[0]), torch.empty_like(want[1]))
     torch.cuda.synchronize()

@@ -70,7 +70,7 @@ def test_overlapping_outputs(L):
                   mscale=1.0, stream=None)
     _cases(L.fa_rope_append_paged, append, [({}, INV)])
     tree = dict(q=ctypes.c_void_p(1 << 20), kp=P, vp=P, table=P, seqlens=P, mask=P, shared=0, lens=None, o=P, lse=None, B=1, Hq=4,
-                Hkv=2, T=3, max_pages=4, page_size=16, num_pages=9, d=64, scale=0.125, ws=P, ws_bytes=1 << 20, stream=None)
+                Hkv=2, T=3, max_pages=65536, page_size=16, num_pages=9, d=64, scale=0.125, ws=P, ws_bytes=1 << 20, stream=None)
     near = ctypes.c_void_p((1 << 20) + 256)
     _cases(L.fa_tree_decode_paged, tree, [({"o": near}, INV), ({"lse": near}, INV), ({"ws": near}, INV),
                                           ({"ws": ctypes.c_void_p((1 << 19) + 256)}, INV)])
@@ -109,8 +109,8 @@ def test_append(L):
 
 def test_tree_attention(L):
     base = dict(q=P, kp=P, vp=P, table=P, seqlens=P, mask=P, shared=0, lens=None, o=P, lse=None, B=1, Hq=4, Hkv=2, T=3,
-                max_pages=4, page_size=16, num_pages=9, d=64, scale=0.125, ws=P, ws_bytes=1 << 40, stream=None)
-    wrong = [({n: None}, INV) for n in ("q", "kp", "vp", "table", "seqlens", "mask", "o", "ws")]
+                max_pages=65536, page_size=16, num_pages=9, d=64, scale=0.125, ws=P, ws_bytes=1 << 40, stream=None)
+    wrong = [({n: None}, INV) for n in ("q", "kp", "vp", "table", "seqlens", "mask", "o")]
     wrong += [({n: ODD}, INV) for n in ("q", "kp", "vp", "table", "seqlens", "mask", "lens", "o", "lse", "ws")]
     wrong += [({n: 0}, INV) for n in ("B", "Hq", "Hkv", "T", "max_pages", "num_pages")]
     wrong += [({"Hq": 5}, INV), ({"scale": 0.0}, INV), ({"scale": math.nan}, INV), ({"scale": math.inf}, INV), ({"d": 96}, UNS),
@@ -119,8 +119,9 @@ def test_tree_attention(L):
     _cases(L.fa_tree_decode_paged, base, wrong)
     assert L.fa_tree_workspace_bytes(0, 4, 2, 3, 4, 64, 152) == 0
     assert L.fa_tree_workspace_bytes(1, 5, 2, 3, 4, 64, 152) == 0
-    # 2 KV heads, at most 64 keys: one step each -> 2 CTAs, two partials of 128 rows each
-    assert L.fa_tree_workspace_bytes(1, 4, 2, 3, 4, 64, 152) == 2 * (2 * 128 * (64 * 4 + 16) + 16)
+    # small problems are joined inside clusters and need none: 8 KV heads, up to 1000 keys
+    assert L.fa_tree_workspace_bytes(1, 32, 8, 8, 63, 128, 152) == 0
+    assert L.fa_tree_workspace_bytes(1, 4, 2, 3, 65536, 64, 152) == 152 * (2 * 128 * (64 * 4 + 16) + 16)
     assert L.fa_tree_workspace_bytes(1, 4, 2, 300, 4096, 128, 152) == 152 * (2 * 256 * (128 * 4 + 16) + 16)
 
 
