@@ -24,6 +24,7 @@
 // n4096 d72, 20 of them rotated, bf16: pairs of values, 45 us; single ones 79 us).
 #include <math.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "launch.cuh"
@@ -306,6 +307,23 @@ static RopeSide side_of(const void* src, void* dst, const long long* s, const lo
   return r;
 }
 
+// Outputs that start where another operand does: in place with the same strides is fine, all
+// else would have rows written that others still read. (Rows that only meet further on, in
+// two views of one buffer, are the caller's to keep apart.)
+static bool starts_on_another(const RopeSide& q, const RopeSide& k) {
+  auto moved = [](const RopeSide& s) { return s.src == s.dst && (s.sb != s.db || s.sh != s.dh || s.st != s.dt); };
+  return moved(q) || (k.heads > 0 && (moved(k) || q.dst == k.dst || q.dst == k.src || q.src == k.dst));
+}
+
+// Whether the rows of a source or of a destination meet `bytes` bytes at `at`, by the range that
+// they span.
+static bool rows_meet(const void* rows, long long sb, long long sh, long long st, int B, int heads, int T, int d,
+                      unsigned elem, const void* at, long long bytes) {
+  long long lo = 0, hi = d;
+  for (const long long reach : {sb * (B - 1), sh * (heads - 1), st * (T - 1)}) (reach < 0 ? lo : hi) += reach;
+  return overlap(static_cast<const char*>(rows) + lo * elem, (hi - lo) * elem, at, bytes);
+}
+
 static fa_status check_rope(const void* q, const void* q_out, const int* positions, const double* inv_freq, int B,
                             int Hq, int Hk, int T, int d, int rot_dim, float mscale, unsigned elem) {
   if (!q || !q_out || !positions || !inv_freq) return FA_ERR_INVALID_ARG;
@@ -331,6 +349,7 @@ static fa_status rope_any(const void* q, const void* k, void* q_out, void* k_out
   RopeParams p = {};
   p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
   if (Hk > 0) p.k = side_of(k, k_out, strides + 6, strides + 9, B, Hk, T);
+  if (starts_on_another(p.q, p.k)) return FA_ERR_INVALID_ARG;
   p.positions = positions;
   p.pos_sb = positions_shared ? 0 : T;
   p.inv_freq = inv_freq;
@@ -421,6 +440,19 @@ fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void
   p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
   p.k = side_of(k, k_pages, strides + 6, nullptr, B, Hkv, T);
   p.v = side_of(v, v_pages, strides + 9, nullptr, B, Hkv, T);
+  {
+    // rows go to any slot while others are still read; q_out may be q and nothing else
+    if (starts_on_another(p.q, RopeSide{}) || q_out == k || q_out == v) return FA_ERR_INVALID_ARG;
+    const long long bt4 = 4ll * B * T;
+    for (const void* pages : {k_pages, v_pages}) {
+      if (rows_meet(q, p.q.sb, p.q.sh, p.q.st, B, Hq, T, d, 2, pages, pool) ||
+          rows_meet(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2, pages, pool) ||
+          rows_meet(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2, pages, pool) ||
+          rows_meet(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2, pages, pool) || overlap(positions, bt4, pages, pool) ||
+          overlap(slots, bt4, pages, pool) || overlap(inv_freq, 4ll * rot_dim, pages, pool))
+        return FA_ERR_INVALID_ARG;
+    }
+  }
   p.positions = positions;
   p.pos_sb = T;
   p.inv_freq = inv_freq;

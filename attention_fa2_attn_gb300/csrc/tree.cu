@@ -1281,13 +1281,18 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
       static_cast<long long>(max_pages) * 16 > (1ll << 31) - 256 || static_cast<long long>(B) * Hq * T >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;  // (a key's index, rounded up to whole tiles, is a 32-bit number)
   {
-    // o, lse and the workspace are written while q is still read by other CTAs
+    // o, lse and the workspace are written while other CTAs still read the rest
     const long long rows = static_cast<long long>(B) * Hq * T, q_bytes = rows * d * 2;
-    if (overlap(o, q_bytes, q, q_bytes) || overlap(lse, rows * 4, q, q_bytes) || overlap(lse, rows * 4, o, q_bytes) ||
-        overlap(workspace, static_cast<long long>(ws_bytes), q, q_bytes) ||
-        overlap(workspace, static_cast<long long>(ws_bytes), o, q_bytes) ||
-        overlap(workspace, static_cast<long long>(ws_bytes), lse, rows * 4))
-      return FA_ERR_INVALID_ARG;
+    const long long pool = 32ll * num_pages * Hkv * d, b4 = 4ll * B;
+    const struct { const void* p; long long n; } out[] = {{o, q_bytes}, {lse, rows * 4}, {workspace, static_cast<long long>(ws_bytes)}},
+        in[] = {{q, q_bytes}, {k_pages, pool}, {v_pages, pool}, {block_table, b4 * max_pages}, {seqlens, b4},
+                {tree_lens, b4}, {tree_mask, 4ll * (mask_shared ? 1 : B) * T * ((T + 31ll) / 32)}};
+    for (int i = 0; i < 3; ++i) {
+      for (const auto& x : in)
+        if (overlap(out[i].p, out[i].n, x.p, x.n)) return FA_ERR_INVALID_ARG;
+      for (int k = 0; k < i; ++k)
+        if (overlap(out[i].p, out[i].n, out[k].p, out[k].n)) return FA_ERR_INVALID_ARG;
+    }
   }
   const int R = Hq / Hkv * T;
   const long long steps = tr_most_steps(B, Hkv, R, max_pages);

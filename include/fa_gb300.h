@@ -382,7 +382,8 @@ FA_API fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, 
  *   projection [B][T][heads][d]. Pointers need the element's alignment only; rows that are
  *   whole 16-byte vectors (and rot_dim / 2 a multiple of one) take the widest kernel.
  *   q_out and k_out may be q and k with the same strides; otherwise no output may overlap
- *   an input or another output. Inputs may have strides of 0.
+ *   an input or another output (FA_ERR_INVALID_ARG where they start at one address; views of
+ *   one buffer that meet further on are not found). Inputs may have strides of 0.
  *   positions [B][T] int32, or [T] with positions_shared; any int32 value.
  *   inv_freq [rot_dim / 2] fp64 (device). The angle is exact to 2^-33 turns at any position.
  *   2 <= rot_dim <= d <= 1024, rot_dim even. mscale > 0.
@@ -408,7 +409,8 @@ FA_API fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, v
  *   A slot of -1 writes nothing (q is rotated all the same); any other slot outside
  *   [0, num_pages * 16) records FA_ERR_BOUNDS and writes nothing. Slots of one call must
  *   differ: which of two rows for one slot stays is undefined.
- *   The pools may not overlap (FA_ERR_INVALID_ARG). page_size == 16.
+ *   The pools may overlap neither each other nor another argument (by the range that its
+ *   rows span), and q_out starts neither on k nor on v (FA_ERR_INVALID_ARG). page_size == 16.
  */
 FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
                                       const long long* strides, const int* positions, const int* slots,
@@ -431,8 +433,8 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
  *   d in {64, 128}, page_size == 16, any Hq / Hkv and T with B * Hq * T < 2^31.
  *   workspace: at least fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count)
  *   bytes, 256-byte aligned (may be NULL where that is 0); its contents need no initialisation, and calls that may
- *   overlap on the GPU need one each. q, o, lse and the workspace may not overlap
- *   (FA_ERR_INVALID_ARG).
+ *   overlap on the GPU need one each. o, lse and the workspace may overlap no
+ *   other argument (FA_ERR_INVALID_ARG).
  *   Keys and values inside a sequence must be finite, as for every call here: a row's weight
  *   of 0 does not cancel a NaN value that the mask hides from it. Pool rows past a
  *   sequence's end are never used, whatever they hold.

@@ -76,6 +76,43 @@ def test_overlapping_outputs(L):
                                           ({"ws": ctypes.c_void_p((1 << 19) + 256)}, INV)])
 
 
+def test_tree_outputs_on_inputs(L):
+    """o, lse and the workspace on the pools, the table, the lengths or the mask."""
+    at = ctypes.c_void_p(1 << 20)
+    base = dict(q=P, kp=P, vp=P, table=P, seqlens=P, mask=P, shared=0, lens=P, o=P, lse=P, B=1, Hq=4, Hkv=2, T=3, max_pages=65536,
+                page_size=16, num_pages=9, d=64, scale=0.125, ws=None, ws_bytes=0, stream=None)  # (no workspace: nothing runs)
+    for out in ("o", "lse", "ws"):
+        for other in ("kp", "vp", "table", "seqlens", "mask", "lens"):
+            _cases(L.fa_tree_decode_paged, base, [({out: at, other: at, "ws_bytes": 256}, INV)])
+
+
+def test_rope_operands_on_one_another(L):
+    at = ctypes.c_void_p(1 << 20)
+    st = lambda q, qo, k, ko: (ctypes.c_longlong * 12)(*q, *qo, *k, *ko)  # noqa: E731
+    dense, other = (384, 192, 64), (384, 64, 128)  # [b][h][t] and [b][t][h] of 2 heads, 3 positions
+    base = dict(q=P, k=P, qo=P, ko=P, strides=st(dense, dense, dense, dense), positions=P, shared=0, inv_freq=P, B=2, Hq=2, Hk=2, T=3,
+                d=64, rot=32, inter=0, mscale=1.0, dtype=0, stream=None)
+    wrong = [({"q": at, "qo": at, "strides": st(dense, other, dense, dense)}, INV),
+             ({"k": at, "ko": at, "strides": st(dense, dense, dense, other)}, INV),
+             ({"qo": at, "ko": at}, INV), ({"qo": at, "k": at}, INV), ({"q": at, "ko": at}, INV)]
+    _cases(L.fa_rope, base, wrong)
+    _cases(L.fa_rope_bwd, base, wrong)
+
+
+def test_append_operands_on_one_another(L):
+    at, near = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 64)
+    dense, other = (384, 192, 64), (384, 64, 128)
+    strides = (ctypes.c_longlong * 12)(*dense, *dense, *dense, *dense)
+    base = dict(q=P, k=P, v=P, qo=P, strides=strides, positions=P, slots=P, inv_freq=P, kp=P, vp=P, B=2, Hq=2, Hkv=2, T=3,
+                page_size=16, num_pages=4, d=64, rot=32, inter=0, mscale=1.0, stream=None)
+    wrong = [({"qo": at, n: at}, INV) for n in ("k", "v")]
+    wrong += [({"q": at, "qo": at, "strides": (ctypes.c_longlong * 12)(*dense, *other, *dense, *dense)}, INV)]
+    wrong += [({pool: at, n: near}, INV) for pool in ("kp", "vp") for n in ("q", "k", "v", "qo", "positions", "slots", "inv_freq")]
+    # rows that end in the pool: 2 batches span 384 + 192 + 128 + 64 values
+    wrong += [({pool: at, n: ctypes.c_void_p((1 << 20) - 2 * 768 + 2)}, INV) for pool in ("kp", "vp") for n in ("q", "k", "v", "qo")]
+    _cases(L.fa_rope_append_paged, base, wrong)
+
+
 def test_tree_mask(L):
     base = dict(parents=P, seqlens=P, lens=None, mask=P, positions=P, B=2, T=3, stream=None)
     wrong = [({n: None}, INV) for n in ("parents", "seqlens", "mask", "positions")]
