@@ -75,6 +75,7 @@ struct TrCfg {
   static_assert(OFF_ML >= OFF_K && OFF_ML + QT * kTrTile * 16 <= OFF_BAR, "partials");
   static constexpr int LEAST = WIDE ? 4 : 1;  // steps of a share
   static constexpr int STEP = WIDE ? 2 : 3, FRONT = WIDE ? 6 : 4;  // TrCost
+  static_assert(STEP + FRONT <= 8, "a batch's cost (tr_most_steps)");
   static constexpr int TMEM_COLS = 512;
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
@@ -1193,7 +1194,7 @@ static long long tr_most_steps(int B, int Hkv, int R, int max_pages) {
   const long long tiles = (static_cast<long long>(max_pages) * 16 + kTrTile - 1) / kTrTile;
   const long long steps = tr_wide(R) ? tiles : (tiles + 1) / 2;
   const long long n = static_cast<long long>(B) * Hkv * U;
-  return n > (1ll << 31) / 5 / steps ? 0 : n * steps;  // STEP + FRONT <= 5
+  return n > (1ll << 31) / 8 / steps ? 0 : n * steps;  // STEP + FRONT <= 8
 }
 
 // CTAs of a launch: one to an SM, none that could have no step.

@@ -76,6 +76,15 @@ def test_overlapping_outputs(L):
                                           ({"ws": ctypes.c_void_p((1 << 19) + 256)}, INV)])
 
 
+def test_tree_batches_whose_cost_is_no_int(L):
+    # a step costs up to 3 and a unit's start 4: 350 million sequences of one page would pass 2^31
+    B = 350_000_000
+    assert L.fa_tree_workspace_bytes(B, 1, 1, 1, 1, 64, 152) == 0 and L.fa_tree_workspace_bytes(B // 2, 1, 1, 1, 1, 64, 152) > 0
+    base = dict(q=P, kp=P, vp=P, table=P, seqlens=P, mask=P, shared=0, lens=None, o=P, lse=P, B=B, Hq=1, Hkv=1, T=1, max_pages=1,
+                page_size=16, num_pages=9, d=64, scale=0.125, ws=None, ws_bytes=0, stream=None)
+    _cases(L.fa_tree_decode_paged, base, [({}, UNS)])
+
+
 def test_tree_outputs_on_inputs(L):
     """o, lse and the workspace on the pools, the table, the lengths or the mask."""
     at = ctypes.c_void_p(1 << 20)
