@@ -1202,19 +1202,26 @@ static int tr_grid(long long steps, int sms) { return static_cast<int>(steps < s
 
 // The clustered form for small problems: a unit to a cluster of C CTAs, which join their
 // partials through shared memory. It saves the share scan, the second launch and the
-// partials' way through L2 (b1 hkv8 t8 s1000 d128 8.2 us, 11.0 us), but takes no more
-// than C of the SMs for a unit and counts with the longest context the table allows: taken
-// where that leaves a CTA about as many steps as equal shares over all SMs would. Returns C,
-// 0 for the general form.
-static int tr_cluster(long long steps, int B, int Hkv, int R, int max_pages, int sms) {
+// partials' way through L2 (b1 hkv8 t8 d128, s1000 8.4 us against 11.3, s8000 12.8 against
+// 15.0; b4 s2000 10.8 against 16.4), but takes no more than C of the SMs for a unit and counts with the longest context
+// the table allows: taken where that leaves a CTA about as many steps as equal shares over
+// all SMs would. One sequence, whose units are all of one length, may take a few more
+// (t8 hkv8 s24000, 8 steps for 5: d128 22.0 against 22.4 us, d64 16.2 against 18.0; hkv4
+// s16000, 6 for 2: 18.3 against 15.9 us). Returns C, 0 for the general form.
+constexpr int kTrMaxCluster = 12;
+static int tr_cluster(long long steps, int B, int Hkv, int R, int sms) {
+  // clusters of 1, 2, .. 12 of these CTAs that run at once on 152 SMs, by the driver's
+  // occupancy query: a cluster needs SMs of one GPC, and those have 16 to 20
+  static const int fit[kTrMaxCluster] = {152, 76, 46, 36, 28, 23, 15, 15, 15, 13, 8, 8};
   const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
   const long long units = static_cast<long long>(B) * Hkv * U, of_unit = steps / units;
-  if (units > sms) return 0;
-  int c = 1;
-  // (an 8-CTA cluster needs 8 free SMs of one GPC: 15 of them fit on 152 SMs, 36 of 4)
-  while (c < 8 && units <= sms / (2 * c + c / 2) && c < of_unit) c *= 2;
-  const long long per = (of_unit + c - 1) / c, shared = (steps + sms - 1) / sms;
-  return per <= shared + (tr_wide(R) ? 3 : 1) ? c : 0;
+  int most = 0;
+  while (most < kTrMaxCluster && units * 152 <= static_cast<long long>(fit[most]) * sms) ++most;
+  if (most == 0) return 0;
+  const long long per = (of_unit + most - 1) / most, shared = (steps + sms - 1) / sms;
+  long long most_steps = shared + (tr_wide(R) ? 3 : B == 1 ? 2 : 1);
+  if (B == 1 && shared >= 4) ++most_steps;
+  return per <= most_steps ? static_cast<int>((of_unit + per - 1) / per) : 0;  // no more CTAs than the steps need
 }
 
 static size_t tr_part_bytes(int grid, int R, int d) {
@@ -1227,7 +1234,7 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
                        int grid, cudaStream_t stream) {
   using C = TrCfg<D, WIDE>;
   auto kfn = tree_kernel<D, WIDE, CL>;
-  // the attribute holds for the life of the device's context: asked for once per device
+  // the attributes hold for the life of the device's context: asked for once per device
   static std::atomic<unsigned long long> asked{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1235,6 +1242,7 @@ static int launch_tree(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(asked.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess && CL) e = cudaFuncSetAttribute(kfn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return record_cuda_failure(e);
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -1259,7 +1267,7 @@ size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int
   if (R >= (1ll << 31)) return 0;
   const long long steps = tr_most_steps(B, Hkv, static_cast<int>(R), max_pages);
   if (steps == 0) return 0;
-  if (tr_cluster(steps, B, Hkv, static_cast<int>(R), max_pages, num_sms)) return 0;
+  if (tr_cluster(steps, B, Hkv, static_cast<int>(R), num_sms)) return 0;
   const int grid = tr_grid(steps, num_sms);
   return tr_part_bytes(grid, static_cast<int>(R), d) + tr_ml_bytes(grid, static_cast<int>(R)) +
          static_cast<size_t>(grid) * 16;
@@ -1303,7 +1311,7 @@ fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const void* v
   if (sms > kTrMaxGrid) return FA_ERR_UNSUPPORTED;
   const size_t need = fa_tree_workspace_bytes(B, Hq, Hkv, T, max_pages, d, sms);
   if (ws_bytes < need || (need && !workspace)) return FA_ERR_INVALID_ARG;
-  const int cluster = tr_cluster(steps, B, Hkv, R, max_pages, sms);
+  const int cluster = tr_cluster(steps, B, Hkv, R, sms);
   const int grid = cluster ? B * Hkv * (tr_wide(R) ? (R + 2 * kTrTile - 1) / (2 * kTrTile) : 1) * cluster : tr_grid(steps, sms);
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;

@@ -80,6 +80,21 @@ def test_parity(B, Hq, Hkv, T, seqlens, d):
     _check(c, "T nodes each", lens=False)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hkv,S,wide", [
+    (152, 250, False), (76, 511, False), (46, 760, False), (36, 1000, False), (28, 1270, False), (23, 1533, False), (15, 1790, False),
+    (15, 2048, False), (15, 2300, False), (13, 5100, False), (8, 5600, False), (8, 6100, False), (8, 3030, True), (15, 1100, True),
+])
+def test_clusters_of_every_size(Hkv, S, wide, d):
+    # one sequence whose heads leave room for 1, 2, 3, .. 12 CTAs each
+    T, G = (33, 4) if wide else (3, 2)
+    c = _case(1, G * Hkv, Hkv, T, d, [S], S + d)
+    assert fa.fa_tree_workspace_bytes(1, G * Hkv, Hkv, T, c["table"].shape[1], d) == 0
+    if Hkv < 76:  # (76 and 152 heads share out evenly at any length)
+        assert fa.fa_tree_workspace_bytes(1, G * Hkv, Hkv, T, 20000, d) > 0
+    _check(c)
+
+
 @pytest.mark.parametrize("n", range(0, 20))
 def test_every_border_of_the_last_tiles(n):
     # the first node crosses a tile border, and the last key moves through a page
