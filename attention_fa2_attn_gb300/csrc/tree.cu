@@ -4,7 +4,7 @@
 // drafted nodes. Query row i < n is node i: it sees key j if j < S - n (the committed
 // text) or bit j - (S - n) of its mask row is set. O = softmax(scale * q K^T) V over
 // the keys it sees, lse = ln sum exp; a row that sees none, and rows from n on, get
-// O = 0 and lse = -inf. A KV head's g = Hq / Hkv query heads times T nodes are R = g * T
+// O = 0 and lse = -inf; a row whose query is not finite gets NaN for both. A KV head's g = Hq / Hkv query heads times T nodes are R = g * T
 // rows, dense in q, o and lse: row r is node r % T of head r / T.
 //
 // What bounds it. K and V are read once for R rows: R FLOP per byte. Up to some 256
@@ -310,7 +310,8 @@ __device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, in
   return left < 32 ? v & ((1u << left) - 1u) : v;
 }
 
-// A row's partials joined: maximum, sums, and a lane's four columns of O.
+// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
+// maximum is +inf (its scores were NaN) makes all of them NaN.
 struct TrRow {
   float m = -INFINITY, s = 0.f, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
@@ -884,6 +885,9 @@ __global__ void __launch_bounds__(384, 1)
         m = -INFINITY;
         l = lc = 0.f;
       }
+      // A score that is NaN (a query that is not finite) may have left m at -inf, which would
+      // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
+      if (l != l) m = INFINITY;
       const bool whole = w.from_start && w.to_end;
       const int slot = 2 * cta + (w.from_start ? 1 : 0);
       const size_t out_row = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + row;
@@ -917,7 +921,7 @@ __global__ void __launch_bounds__(384, 1)
         break;
       }
       if (whole) {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
         f0 *= inv;
         f1 *= inv;
       }
@@ -972,7 +976,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (write && (WIDE || t == 0)) {
           if (whole) {
-            if (p.lse) p.lse[out_row] = lsum > 0.f ? (m_all + log2f(lsum)) * kLn2 : -INFINITY;
+            if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
           } else {
             float4* ml = CL ? reinterpret_cast<float4*>(smem + C::OFF_ML) + (WIDE ? t * kTrTile + r : r) : p.part_ml + part_row;
             *ml = make_float4(m_all, sum, lsum, 0.f);
@@ -1011,11 +1015,11 @@ __global__ void __launch_bounds__(384, 1)
           for (int c = 0; c < 4; ++c)
             if (c0 + c < p.C) acc.add(ml[c].x, ml[c].y, ml[c].z, o[c]);
         }
-        const float inv = acc.s > 0.f ? 1.f / acc.s : 0.f;
+        const float inv = acc.s == 0.f ? 0.f : 1.f / acc.s;
         const size_t out = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + w.u * C::QT * kTrTile + row;
         *reinterpret_cast<uint2*>(p.o + out * D + col) =
             make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
-        if (p.lse && col == 0) p.lse[out] = acc.l > 0.f ? (acc.m + log2f(acc.l)) * kLn2 : -INFINITY;
+        if (p.lse && col == 0) p.lse[out] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * kLn2;
       }
       cluster_sync();  // nobody leaves while others read its shared memory
     }
@@ -1127,11 +1131,11 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       v = *reinterpret_cast<const float4*>(part + row_at * D + col);
     };
     auto put = [&](const TrRow& r, int row) {
-      const float inv = r.s > 0.f ? 1.f / r.s : 0.f;
+      const float inv = r.s == 0.f ? 0.f : 1.f / r.s;
       const size_t out = static_cast<size_t>(un.row0) + row;
       *reinterpret_cast<uint2*>(o + out * D + col) =
           make_uint2(pack_bf16x2(r.o.x * inv, r.o.y * inv), pack_bf16x2(r.o.z * inv, r.o.w * inv));
-      if (lse && col == 0) lse[out] = r.l > 0.f ? (r.m + log2f(r.l)) * kLn2 : -INFINITY;
+      if (lse && col == 0) lse[out] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
     };
     if (un.parts <= kTrFewParts) {
       const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
