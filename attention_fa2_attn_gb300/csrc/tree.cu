@@ -546,12 +546,12 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (!ok) fail(SITE_TR_PRODUCER);
-      if (*abort_flag) {  // copies in flight must land before the CTA exits
-        if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-        for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) {
-          mbar_wait(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
-          if (WIDE) mbar_wait(&bars->v_full[x % ST], (x / ST) & 1, tmo_unwind);
-        }
+      // Copies in flight must land before the CTA exits. Waited for whether or not a wait has
+      // run out so far: another role's may after this warp has issued its last copy.
+      if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+      for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) {
+        mbar_wait(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
+        if (WIDE) mbar_wait(&bars->v_full[x % ST], (x / ST) & 1, tmo_unwind);
       }
     } else if (warp == 9) {
       // ======================= MMA issuer =======================
