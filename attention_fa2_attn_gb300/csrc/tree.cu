@@ -906,7 +906,8 @@ __global__ void __launch_bounds__(384, 1)
         ex[t * 128 + r] = m;
         ex[(2 + t) * 128 + r] = l + lc;
         if (t == 1) ex[4 * 128 + r] = l;
-        if (!vote_all(1, 256, ok)) break;  // all eight warps leave in the same segment
+        ok = vote_all(1, 256, ok);
+        if (!ok) break;  // all eight warps leave in the same segment
         const float m0 = ex[r], m1 = ex[128 + r];
         m_all = fmaxf(m0, m1);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
@@ -916,7 +917,8 @@ __global__ void __launch_bounds__(384, 1)
         if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
       } else if (CL) {
         // (a partial goes where the other slot's MMAs read their operands)
-        if (!vote_all(1, 256, ok)) break;
+        ok = vote_all(1, 256, ok);
+        if (!ok) break;
       } else if (!ok) {
         break;
       }
@@ -992,7 +994,7 @@ __global__ void __launch_bounds__(384, 1)
     if (CL && p.C > 1) {
       // Joined inside the cluster: each CTA reads its part of the rows out of all CTAs' shared
       // memory. (These warps: the others have given their registers away.)
-      if (threadIdx.x == 0) bars->finished = ok;
+      if (threadIdx.x == 0) bars->finished = ok;  // as all eight warps voted
       cluster_sync();
       constexpr int LANES = D / 4, PER = 32 / LANES;  // lanes to a row, rows of a warp's load
       const int rank = cta % p.C;

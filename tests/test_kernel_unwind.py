@@ -40,3 +40,13 @@ def test_tree_producers_wait_for_their_copies_whatever_happens():
     for at in waits:
         heads = _enclosing(code, at)
         assert not any("abort_flag" in h and h.startswith("if") for h in heads), heads[:3]
+
+
+def test_tree_softmax_warps_keep_what_they_voted():
+    # in a cluster the other CTAs join what is `finished`: all eight warps' partials, not those of the voter's own slot
+    code = _code("tree.cu")
+    votes = [m.start() for m in re.finditer(r"\bvote_all\(1, 256, ok\)", code)]
+    assert len(votes) == 2
+    for at in votes:
+        assert re.search(r"[;{}]\s*ok = $", code[:at]), code[at - 40:at + 30]
+    assert "bars->finished = ok;" in code
