@@ -10,7 +10,8 @@
 // Angles. A far position needs t to a small part of 2 pi, which p * inv_freq in 32
 // bits has not (at p = 10^6 it is off by 0.06). Here inv_freq / (2 pi) is a 64-bit
 // fraction of a turn, so the integer product p * that, modulo 2^64, IS the angle
-// modulo a turn, off by at most |p| * 2^-64 turns; its upper 32 bits go to sincospif.
+// modulo a turn, off by less than |p| * 2^-63 turns; its upper 32 bits go to sincospif.
+// An inv_freq that is NaN, infinite or 2^53 and more makes its pairs NaN.
 // No table of cosines, no largest position, no FP64 pipe (which is narrow here).
 //
 // How: bound by reading and writing each value once. A lane owns VEC pairs of a token
@@ -112,24 +113,24 @@ struct Raw {
   }
 };
 
-// f / (2 pi) modulo 1 as a 64-bit fraction, from the double's bits: its 53-bit mantissa
-// times floor(2^64 / (2 pi)), shifted by its exponent.
-__device__ __forceinline__ unsigned long long turns_of(double f) {
+// f / (2 pi) modulo 1 as a 64-bit fraction, off by less than 2^-63 turns, from the double's bits:
+// f = m * 2^-s with a 53-bit m, so the fraction is m * floor(2^128 / (2 pi)) shifted right by
+// s + 64, modulo 2^64 (the constant loses less than |f| * 2^-128 turns, the shift 2^-64). False:
+// f is NaN, infinite or not below 2^53.
+__device__ __forceinline__ bool turns_of(double f, unsigned long long& turns) {
   const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(f));
   const int e = static_cast<int>((bits >> 52) & 0x7ff);
-  if (e == 0) return 0;  // zero (a denormal's turn is far below 2^-64)
+  const int s = 1075 - e;
+  turns = 0;
+  if (s < 0) return false;
+  if (e == 0 || s >= 128) return true;  // zero, or far below 2^-64 turns
   const unsigned long long m = (bits & 0xfffffffffffffull) | (1ull << 52);
-  constexpr unsigned long long kInv2Pi = 0x28BE60DB9391054Aull;
-  const unsigned long long lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-  const int s = 1075 - e;  // f = m * 2^-s
-  unsigned long long r;
-  if (s <= 0)
-    r = s > -64 ? lo << -s : 0;
-  else if (s < 64)
-    r = (lo >> s) | (hi << (64 - s));
-  else
-    r = s < 128 ? hi >> (s - 64) : 0;
-  return (bits >> 63) ? 0ull - r : r;
+  constexpr unsigned long long kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;  // 1 / (2 pi), 128 bits
+  const unsigned long long low = __umul64hi(m, kLo), mid = m * kHi + low;  // the product but its last 64 bits
+  const unsigned long long top = __umul64hi(m, kHi) + (mid < low);
+  const unsigned long long r = s < 64 ? (mid >> s) | (top << 1 << (63 - s)) : top >> (s - 64);
+  turns = (bits >> 63) ? 0ull - r : r;
+  return true;
 }
 
 constexpr int kRopeWarps = 8;
@@ -196,9 +197,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopePara
       // interleaved: half of the lane's pairs are in its first vector, half in its second
       const int pair = !INTER || ADJ ? lane * VEC + e
                                      : (2 * e < VEC ? o0 / 2 + e : o1 / 2 + e - VEC / 2);
-      const unsigned long long a = static_cast<unsigned long long>(pos) * turns_of(__ldg(p.inv_freq + pair));
+      unsigned long long a;
+      const bool angle = turns_of(__ldg(p.inv_freq + pair), a);
+      a *= static_cast<unsigned long long>(pos);
       float s, c;  // of the signed upper half, in half turns
       sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
+      if (!angle) s = c = NAN;
       cs[0][e][id] = c * p.mscale;
       cs[1][e][id] = s * p.mscale * p.sign;
     }
