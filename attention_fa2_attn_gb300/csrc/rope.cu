@@ -10,7 +10,8 @@
 // Angles. A far position needs t to a small part of 2 pi, which p * inv_freq in 32
 // bits has not (at p = 10^6 it is off by 0.06). Here inv_freq / (2 pi) is a 64-bit
 // fraction of a turn, so the integer product p * that, modulo 2^64, IS the angle
-// modulo a turn, off by less than |p| * 2^-63 turns; its upper 32 bits go to sincospif.
+// modulo a turn, off by less than |p| * 2^-63 turns. What it is past the nearest quarter
+// turn goes to sincospif.
 // An inv_freq that is NaN, infinite or 2^53 and more makes its pairs NaN.
 // No table of cosines, no largest position, no FP64 pipe (which is narrow here).
 //
@@ -200,8 +201,21 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopePara
       unsigned long long a;
       const bool angle = turns_of(__ldg(p.inv_freq + pair), a);
       a *= static_cast<unsigned long long>(pos);
-      float s, c;  // of the signed upper half, in half turns
-      sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &s, &c);
+      // The nearest quarter turn comes off the whole number, so that rounding to 24 bits is
+      // by 2^-24 of at most an eighth of a turn, as the sine and cosine of it need.
+      const unsigned quarter = static_cast<unsigned>((a + (1ull << 61)) >> 62);
+      const long long rest = static_cast<long long>(a - (static_cast<unsigned long long>(quarter) << 62));
+      float s, c;
+      sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);  // (in half turns)
+      if (quarter & 1) {
+        const float was = s;
+        s = c;
+        c = -was;
+      }
+      if (quarter & 2) {
+        s = -s;
+        c = -c;
+      }
       if (!angle) s = c = NAN;
       cs[0][e][id] = c * p.mscale;
       cs[1][e][id] = s * p.mscale * p.sign;

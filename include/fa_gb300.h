@@ -386,7 +386,10 @@ FA_API fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, 
  *   one buffer that meet further on are not found). Inputs may have strides of 0.
  *   positions [B][T] int32, or [T] with positions_shared; any int32 value.
  *   inv_freq [rot_dim / 2] fp64 (device), below 2^53 in magnitude; the pairs of others, NaN
- *   and infinity among them, become NaN. The angle is exact to 2^-33 turns at any position.
+ *   and infinity among them, become NaN. The angle p * inv_freq is
+ *   formed in whole numbers (off by less than |p| * 2^-63 turns, 2^-32 at the farthest
+ *   position), brought within an eighth of a turn of a multiple of a quarter, and rounded to
+ *   24 bits there.
  *   2 <= rot_dim <= d <= 1024, rot_dim even. mscale > 0.
  */
 FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
