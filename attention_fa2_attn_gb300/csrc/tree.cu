@@ -17,7 +17,7 @@
 //   * Work is cut into equal shares of key tiles, not of sequences: every group of CTAs of
 //     the one-per-SM grid sums the batch's cost for itself and takes the share
 //     [c N / G, (c+1) N / G) of it. Lengths live on the device and may differ by any
-//     factor; every SM has the same number of tiles within one. A share that does not
+//     factor; every share costs the same within a step. A share that does not
 //     cover its (sequence, KV head) whole leaves fp32 partials (O, max, sums) in the
 //     workspace, at most two per CTA, and the merge kernel joins them. A list of the
 //     split ones, one entry per CTA, tells it which; what is whole is written at once.
@@ -28,8 +28,9 @@
 //     TMEM, so that one's softmax runs under the other's MMAs; the two are joined in
 //     TMEM at the end of a share (a warp can read the other's lanes).
 //   * R > 128 (WIDE): two tiles of rows against each key tile, as the prefill kernel.
-//   * Small problems: a unit to a cluster, whose CTAs join their partials through shared
-//     memory (one launch, no workspace).
+//   * Small problems (tr_cluster): a unit to a cluster, whose CTAs join their partials
+//     through shared memory (one launch, no workspace). Units are not shared out there, so
+//     it is for few steps.
 //   * warp 8, in narrow units with warp 10: K and V pages by TMA, 16-token boxes through the
 //     block table, into rings of 128-byte-swizzled tiles; the Q tile too (rows are dense: one
 //     plain box).
@@ -1209,25 +1210,39 @@ static int tr_grid(long long steps, int sms) { return static_cast<int>(steps < s
 // The clustered form for small problems: a unit to a cluster of C CTAs, which join their
 // partials through shared memory. It saves the share scan, the second launch and the
 // partials' way through L2 (b1 hkv8 t8 d128, s1000 8.4 us against 11.3, s8000 12.8 against
-// 15.0; b4 s2000 10.8 against 16.4), but takes no more than C of the SMs for a unit and counts with the longest context
-// the table allows: taken where that leaves a CTA about as many steps as equal shares over
-// all SMs would. One sequence, whose units are all of one length, may take a few more
-// (t8 hkv8 s24000, 8 steps for 5: d128 22.0 against 22.4 us, d64 16.2 against 18.0; hkv4
-// s16000, 6 for 2: 18.3 against 15.9 us). Returns C, 0 for the general form.
+// 15.0; b4 s2000 10.8 against 16.4), but takes no more than C of the SMs for a unit and
+// counts with the longest context the table allows: taken where that leaves a CTA about as
+// many steps as equal shares over all SMs would. One sequence, whose units are all of one
+// length, may take a few more (t8 hkv8 s24000, 8 steps for 5: d128 22.0 against 22.4 us, d64
+// 16.2 against 18.0; hkv4 s16000, 6 for 2: 18.3 against 15.9 us).
+//   In a batch one sequence may fill its row of the table and the others be short; their SMs
+// are idle while its clusters go through it, so a CTA gets few steps there. At the most that
+// the rule takes, one long sequence among short ones costs up to a quarter more than equal
+// shares, and a batch of long ones a tenth to a third less (d128, us, clusters / shares, one
+// long and all long: narrow b19 hkv8 s2048, 8 steps, 17.6 / 15.9 and 28.9 / 32.6; b19 hkv4
+// s2560, 5 steps, 14.9 / 12.3 and 17.0 / 21.4; wide b19 hkv8 s1280, 10 steps, 21.1 / 21.3 and
+// 27.3 / 31.3; b19 hkv4 s2048, 8 steps, 25.9 / 20.7 and 27.6 / 34.1; b4 hkv8 s4096, 8 steps,
+// 23.1 / 29.6 and 23.9 / 35.8). Past it: narrow b19 hkv8 s8192 57.7 / 20.9 and 95.9 / 99.5.
+// Returns C, 0 for the general form.
 constexpr int kTrMaxCluster = 12;
 static int tr_cluster(long long steps, int B, int Hkv, int R, int sms) {
   // clusters of 1, 2, .. 12 of these CTAs that run at once on 152 SMs, by the driver's
-  // occupancy query: a cluster needs SMs of one GPC, and those have 16 to 20
+  // occupancy query on one GPU: a cluster needs SMs of one GPC, and its GPCs had 16 to 20.
+  // Where another GPU's are cut otherwise, clusters too many wait for a second wave.
   static const int fit[kTrMaxCluster] = {152, 76, 46, 36, 28, 23, 15, 15, 15, 13, 8, 8};
-  const long long U = tr_wide(R) ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
+  const bool wide = tr_wide(R);
+  const long long U = wide ? (R + 2ll * kTrTile - 1) / (2 * kTrTile) : 1;
   const long long units = static_cast<long long>(B) * Hkv * U, of_unit = steps / units;
   int most = 0;
   while (most < kTrMaxCluster && units * 152 <= static_cast<long long>(fit[most]) * sms) ++most;
   if (most == 0) return 0;
   const long long per = (of_unit + most - 1) / most, shared = (steps + sms - 1) / sms;
-  long long most_steps = shared + (tr_wide(R) ? 3 : B == 1 ? 2 : 1);
+  const int C = static_cast<int>((of_unit + per - 1) / per);  // no more CTAs than the steps need
+  long long most_steps = shared + (wide ? 3 : B == 1 ? 2 : 1);
   if (B == 1 && shared >= 4) ++most_steps;
-  return per <= most_steps ? static_cast<int>((of_unit + per - 1) / per) : 0;  // no more CTAs than the steps need
+  const long long ragged = C == 1 ? (wide ? 10 : 8) : (wide ? 8 : 5);
+  if (B > 1 && most_steps > ragged) most_steps = ragged;
+  return per <= most_steps ? C : 0;
 }
 
 static size_t tr_part_bytes(int grid, int R, int d) {
