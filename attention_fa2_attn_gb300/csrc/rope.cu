@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "launch.cuh"
+#include "rows.h"
 
 namespace fa {
 
@@ -325,17 +326,30 @@ static RopeSide side_of(const void* src, void* dst, const long long* s, const lo
   return r;
 }
 
-// Outputs that start where another operand does: in place with the same strides is fine, all
-// else would have rows written that others still read. (Rows that only meet further on, in
-// two views of one buffer, are the caller's to keep apart.)
-static bool starts_on_another(const RopeSide& q, const RopeSide& k) {
-  auto moved = [](const RopeSide& s) { return s.src == s.dst && (s.sb != s.db || s.sh != s.dh || s.st != s.dt); };
-  return moved(q) || (k.heads > 0 && (moved(k) || q.dst == k.dst || q.dst == k.src || q.src == k.dst));
+static Rows rows_of(const void* at, long long sb, long long sh, long long st, int B, int heads, int T, int d,
+                    unsigned elem) {
+  return Rows{at, {sb * elem, sh * elem, st * elem}, {B, heads, T}, static_cast<long long>(d) * elem};
+}
+
+// Whether a row of an output lies on one of another operand, or on another of its own: rows
+// would be written that others still read. In place (a destination that is its source, stride
+// for stride) is fine.
+static bool outputs_meet(const RopeSide& q, const RopeSide& k, int B, int T, int d, unsigned elem,
+                         const int* positions, long long pos_bytes, const double* inv_freq, long long freq_bytes) {
+  auto src = [&](const RopeSide& s) { return rows_of(s.src, s.sb, s.sh, s.st, B, s.heads, T, d, elem); };
+  auto dst = [&](const RopeSide& s) { return rows_of(s.dst, s.db, s.dh, s.dt, B, s.heads, T, d, elem); };
+  auto in_place = [](const RopeSide& s) { return s.src == s.dst && s.sb == s.db && s.sh == s.dh && s.st == s.dt; };
+  auto bad = [&](const RopeSide& s) {
+    return (!in_place(s) && rows_meet(src(s), dst(s))) || rows_meet_themselves(dst(s)) ||
+           rows_meet(dst(s), dense_rows(positions, pos_bytes)) || rows_meet(dst(s), dense_rows(inv_freq, freq_bytes));
+  };
+  return bad(q) || (k.heads > 0 && (bad(k) || rows_meet(dst(q), dst(k)) || rows_meet(dst(q), src(k)) ||
+                                    rows_meet(src(q), dst(k))));
 }
 
 // Whether the rows of a source or of a destination meet `bytes` bytes at `at`, by the range that
 // they span.
-static bool rows_meet(const void* rows, long long sb, long long sh, long long st, int B, int heads, int T, int d,
+static bool span_meets(const void* rows, long long sb, long long sh, long long st, int B, int heads, int T, int d,
                       unsigned elem, const void* at, long long bytes) {
   long long lo = 0, hi = d;
   for (const long long reach : {sb * (B - 1), sh * (heads - 1), st * (T - 1)}) (reach < 0 ? lo : hi) += reach;
@@ -367,7 +381,8 @@ static fa_status rope_any(const void* q, const void* k, void* q_out, void* k_out
   RopeParams p = {};
   p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
   if (Hk > 0) p.k = side_of(k, k_out, strides + 6, strides + 9, B, Hk, T);
-  if (starts_on_another(p.q, p.k)) return FA_ERR_INVALID_ARG;
+  if (outputs_meet(p.q, p.k, B, T, d, elem, positions, 4ll * T * (positions_shared ? 1 : B), inv_freq, 4ll * rot_dim))
+    return FA_ERR_INVALID_ARG;
   p.positions = positions;
   p.pos_sb = positions_shared ? 0 : T;
   p.inv_freq = inv_freq;
@@ -460,13 +475,17 @@ fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void
   p.v = side_of(v, v_pages, strides + 9, nullptr, B, Hkv, T);
   {
     // rows go to any slot while others are still read; q_out may be q and nothing else
-    if (starts_on_another(p.q, RopeSide{}) || q_out == k || q_out == v) return FA_ERR_INVALID_ARG;
     const long long bt4 = 4ll * B * T;
+    const Rows out = rows_of(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2);
+    if (outputs_meet(p.q, RopeSide{}, B, T, d, 2, positions, bt4, inv_freq, 4ll * rot_dim) ||
+        rows_meet(out, rows_of(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2)) ||
+        rows_meet(out, rows_of(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2)) || rows_meet(out, dense_rows(slots, bt4)))
+      return FA_ERR_INVALID_ARG;
     for (const void* pages : {k_pages, v_pages}) {
-      if (rows_meet(q, p.q.sb, p.q.sh, p.q.st, B, Hq, T, d, 2, pages, pool) ||
-          rows_meet(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2, pages, pool) ||
-          rows_meet(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2, pages, pool) ||
-          rows_meet(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2, pages, pool) || overlap(positions, bt4, pages, pool) ||
+      if (span_meets(q, p.q.sb, p.q.sh, p.q.st, B, Hq, T, d, 2, pages, pool) ||
+          span_meets(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2, pages, pool) ||
+          span_meets(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2, pages, pool) ||
+          span_meets(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2, pages, pool) || overlap(positions, bt4, pages, pool) ||
           overlap(slots, bt4, pages, pool) || overlap(inv_freq, 4ll * rot_dim, pages, pool))
         return FA_ERR_INVALID_ARG;
     }

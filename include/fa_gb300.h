@@ -381,9 +381,10 @@ FA_API fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, 
  *   of (batch, head, position) for q, q_out, k, k_out, so the rows may lie in a fused
  *   projection [B][T][heads][d]. Pointers need the element's alignment only; rows that are
  *   whole 16-byte vectors (and rot_dim / 2 a multiple of one) take the widest kernel.
- *   q_out and k_out may be q and k with the same strides; otherwise no output may overlap
- *   an input or another output (FA_ERR_INVALID_ARG where they start at one address; views of
- *   one buffer that meet further on are not found). Inputs may have strides of 0.
+ *   q_out and k_out may be q and k with the same strides; otherwise no row of an output may
+ *   overlap an input or another row of an output (FA_ERR_INVALID_ARG; found for all strides
+ *   whose dimensions nest, as those of a projection do, and most others). Rows of several
+ *   operands may alternate in one buffer. Inputs may have strides of 0.
  *   positions [B][T] int32, or [T] with positions_shared; any int32 value.
  *   inv_freq [rot_dim / 2] fp64 (device), below 2^53 in magnitude; the pairs of others, NaN
  *   and infinity among them, become NaN. The angle p * inv_freq is
@@ -414,7 +415,8 @@ FA_API fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, v
  *   [0, num_pages * 16) records FA_ERR_BOUNDS and writes nothing. Slots of one call must
  *   differ: which of two rows for one slot stays is undefined.
  *   The pools may overlap neither each other nor another argument (by the range that its
- *   rows span), and q_out starts neither on k nor on v (FA_ERR_INVALID_ARG). page_size == 16.
+ *   rows span), nor rows of q_out another argument but for q_out being q (FA_ERR_INVALID_ARG).
+ *   page_size == 16.
  */
 FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void* q_out,
                                       const long long* strides, const int* positions, const int* slots,
