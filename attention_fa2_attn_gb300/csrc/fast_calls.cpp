@@ -83,6 +83,14 @@ std::array<Tensor, N> make_ints(const std::array<std::array<int64_t, 3>, N>& siz
   return out;
 }
 
+// The interpreter is released from here to the end of the scope: an allocation may wait for
+// the driver, and a launch for room in the stream's queue. Tensors of the arguments are kept by
+// the caller's frame.
+struct NoInterpreter {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoInterpreter() { PyEval_RestoreThread(state); }
+};
+
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream(); }
 
 bool int_of(PyObject* o, int* out) {
@@ -142,13 +150,16 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t B = table->size(0), pages = table->size(1), F = free_pages->size(0);
   if (cached->size(0) != B || fresh->size(0) != B || !fits(B) || !fits(pages) || !fits(F) || !fits(B * T))
     Py_RETURN_NONE;
-  const auto [seqlens, slots, positions, used] =
-      make_ints<4>({{{B, 0, 0}, {B, T, 0}, {B, T, 0}, {1, 0, 0}}}, {1, 2, 2, 1}, dev);
-  const fa_status st =
-      fa_paged_plan(ints(*cached), ints(*fresh), ints(*free_pages), static_cast<int>(F), ints_out(*table),
-                    ints_out(seqlens), ints_out(slots), ints_out(positions), ints_out(used), static_cast<int>(B), T,
-                    static_cast<int>(pages), 16, end, stream_of(dev));
-  return answer(st, {seqlens, slots, positions, used});
+  std::array<Tensor, 4> out;  // seqlens, slots, positions, pages used
+  fa_status st;
+  {
+    NoInterpreter released;
+    out = make_ints<4>({{{B, 0, 0}, {B, T, 0}, {B, T, 0}, {1, 0, 0}}}, {1, 2, 2, 1}, dev);
+    st = fa_paged_plan(ints(*cached), ints(*fresh), ints(*free_pages), static_cast<int>(F), ints_out(*table),
+                       ints_out(out[0]), ints_out(out[1]), ints_out(out[2]), ints_out(out[3]), static_cast<int>(B), T,
+                       static_cast<int>(pages), 16, end, stream_of(dev));
+  }
+  return answer(st, {out[0], out[1], out[2], out[3]});
   END_HANDLE_TH_ERRORS
 }
 
@@ -165,10 +176,15 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int64_t B = parents->size(0), T = parents->size(1);
   if (seqlens->size(0) != B || (lens && lens->size(0) != B) || !fits(B) || !fits(T)) Py_RETURN_NONE;
-  const auto [mask, positions] = make_ints<2>({{{B, T, (T + 31) / 32}, {B, T, 0}}}, {3, 2}, dev);
-  const fa_status st = fa_tree_mask(ints(*parents), ints(*seqlens), lens ? ints(*lens) : nullptr, ints_out(mask),
-                                    ints_out(positions), static_cast<int>(B), static_cast<int>(T), stream_of(dev));
-  return answer(st, {mask, positions});
+  std::array<Tensor, 2> out;  // mask, positions
+  fa_status st;
+  {
+    NoInterpreter released;
+    out = make_ints<2>({{{B, T, (T + 31) / 32}, {B, T, 0}}}, {3, 2}, dev);
+    st = fa_tree_mask(ints(*parents), ints(*seqlens), lens ? ints(*lens) : nullptr, ints_out(out[0]), ints_out(out[1]),
+                      static_cast<int>(B), static_cast<int>(T), stream_of(dev));
+  }
+  return answer(st, {out[0], out[1]});
   END_HANDLE_TH_ERRORS
 }
 
@@ -215,17 +231,22 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (k && (k->size(0) != B || k->size(2) != T || k->size(3) != d || Hk < 1)))
     Py_RETURN_NONE;
   if ((q_out && !rows_out(*q_out, *q, dev)) || (k_out && !(k && rows_out(*k_out, *k, dev)))) Py_RETURN_NONE;
-  const Tensor qo = q_out ? *q_out : make({B, H, T, d}, type, dev);
-  const Tensor ko = k_out ? *k_out : k ? make({B, Hk, T, d}, type, dev) : Tensor();
-  const long long s[12] = {q->stride(0),  q->stride(1),  q->stride(2),  qo.stride(0), qo.stride(1), qo.stride(2),
-                           k ? k->stride(0) : 0, k ? k->stride(1) : 0, k ? k->stride(2) : 0,
-                           k ? ko.stride(0) : 0, k ? ko.stride(1) : 0, k ? ko.stride(2) : 0};
-  const fa_status st = (back ? fa_rope_bwd : fa_rope)(
-      q->const_data_ptr(), k ? k->const_data_ptr() : nullptr, qo.mutable_data_ptr(),
-      k ? ko.mutable_data_ptr() : nullptr, s, ints(*positions), shared,
-      static_cast<const double*>(inv_freq->const_data_ptr()), static_cast<int>(B), static_cast<int>(H),
-      static_cast<int>(Hk), static_cast<int>(T), static_cast<int>(d), static_cast<int>(2 * inv_freq->size(0)), inter,
-      mscale, type == at::kFloat ? FA_DTYPE_F32 : FA_DTYPE_BF16, stream_of(dev));
+  Tensor qo, ko;
+  fa_status st;
+  {
+    NoInterpreter released;
+    qo = q_out ? *q_out : make({B, H, T, d}, type, dev);
+    if (k) ko = k_out ? *k_out : make({B, Hk, T, d}, type, dev);
+    const long long s[12] = {q->stride(0),  q->stride(1),  q->stride(2),  qo.stride(0), qo.stride(1), qo.stride(2),
+                             k ? k->stride(0) : 0, k ? k->stride(1) : 0, k ? k->stride(2) : 0,
+                             k ? ko.stride(0) : 0, k ? ko.stride(1) : 0, k ? ko.stride(2) : 0};
+    st = (back ? fa_rope_bwd : fa_rope)(
+        q->const_data_ptr(), k ? k->const_data_ptr() : nullptr, qo.mutable_data_ptr(),
+        k ? ko.mutable_data_ptr() : nullptr, s, ints(*positions), shared,
+        static_cast<const double*>(inv_freq->const_data_ptr()), static_cast<int>(B), static_cast<int>(H),
+        static_cast<int>(Hk), static_cast<int>(T), static_cast<int>(d), static_cast<int>(2 * inv_freq->size(0)), inter,
+        mscale, type == at::kFloat ? FA_DTYPE_F32 : FA_DTYPE_BF16, stream_of(dev));
+  }
   if (k || st != FA_OK) return answer(st, {qo, ko});
   PyObject* w = THPVariable_Wrap(qo);
   if (!w) return nullptr;
@@ -259,15 +280,20 @@ PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       k.size(3) != d || kp.size(3) != d || !fits(P) || !fits(kp.size(1)))
     Py_RETURN_NONE;
   if (q_out && !rows_out(*q_out, q, dev)) Py_RETURN_NONE;
-  const Tensor qo = q_out ? *q_out : make({B, H, T, d}, at::kBFloat16, dev);
-  const long long s[12] = {q.stride(0), q.stride(1), q.stride(2), qo.stride(0), qo.stride(1), qo.stride(2),
-                           k.stride(0), k.stride(1), k.stride(2), v.stride(0),  v.stride(1),  v.stride(2)};
-  const fa_status st = fa_rope_append_paged(
-      q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.mutable_data_ptr(), s, ints(positions),
-      ints(slots), static_cast<const double*>(inv_freq.const_data_ptr()), kp.mutable_data_ptr(), vp.mutable_data_ptr(),
-      static_cast<int>(B), static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(T),
-      static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), static_cast<int>(2 * inv_freq.size(0)),
-      inter, mscale, stream_of(dev));
+  Tensor qo;
+  fa_status st;
+  {
+    NoInterpreter released;
+    qo = q_out ? *q_out : make({B, H, T, d}, at::kBFloat16, dev);
+    const long long s[12] = {q.stride(0), q.stride(1), q.stride(2), qo.stride(0), qo.stride(1), qo.stride(2),
+                             k.stride(0), k.stride(1), k.stride(2), v.stride(0),  v.stride(1),  v.stride(2)};
+    st = fa_rope_append_paged(
+        q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.mutable_data_ptr(), s, ints(positions),
+        ints(slots), static_cast<const double*>(inv_freq.const_data_ptr()), kp.mutable_data_ptr(),
+        vp.mutable_data_ptr(), static_cast<int>(B), static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(T),
+        static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), static_cast<int>(2 * inv_freq.size(0)),
+        inter, mscale, stream_of(dev));
+  }
   return answer(st, {qo});
   END_HANDLE_TH_ERRORS
 }
@@ -297,18 +323,24 @@ PyObject* tree_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !fits(Hkv) || !fits(pages) || !fits(kp.size(1)))
     Py_RETURN_NONE;
   if (a[7] == Py_None) scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
-  const int sms = at::cuda::getCurrentDeviceProperties()->multiProcessorCount;
-  const size_t bytes =
-      fa_tree_workspace_bytes(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T),
-                              static_cast<int>(pages), static_cast<int>(d), sms);
-  const Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev), o = make({B, Hq, T, d}, at::kBFloat16, dev),
-               lse = make({B, Hq, T}, at::kFloat, dev);
-  const fa_status st = fa_tree_decode_paged(
-      q.const_data_ptr(), kp.const_data_ptr(), vp.const_data_ptr(), ints(table), ints(seqlens), ints(mask), shared,
-      lens ? ints(*lens) : nullptr, o.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()),
-      static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T), static_cast<int>(pages),
-      static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), scale, ws.mutable_data_ptr(), bytes,
-      stream_of(dev));
+  Tensor o, lse;
+  fa_status st;
+  {
+    NoInterpreter released;
+    const int sms = at::cuda::getCurrentDeviceProperties()->multiProcessorCount;
+    const size_t bytes =
+        fa_tree_workspace_bytes(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T),
+                                static_cast<int>(pages), static_cast<int>(d), sms);
+    const Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    o = make({B, Hq, T, d}, at::kBFloat16, dev);
+    lse = make({B, Hq, T}, at::kFloat, dev);
+    st = fa_tree_decode_paged(
+        q.const_data_ptr(), kp.const_data_ptr(), vp.const_data_ptr(), ints(table), ints(seqlens), ints(mask), shared,
+        lens ? ints(*lens) : nullptr, o.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()),
+        static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T), static_cast<int>(pages),
+        static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), scale, ws.mutable_data_ptr(), bytes,
+        stream_of(dev));
+  }
   return answer(st, {o, lse});
   END_HANDLE_TH_ERRORS
 }
