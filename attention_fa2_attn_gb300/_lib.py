@@ -11,6 +11,7 @@ import ctypes
 import importlib.util
 import os
 import re
+import warnings
 
 from . import build as _build
 
@@ -107,15 +108,28 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
 _fast_calls = None
 
 
+class _NoFastCalls:
+    """In the place of an extension module that is not there: every call is left to the checks in Python."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def fast():
     """The extension module ``_fast`` (the step calls from Python objects to the library),
     loaded after the library it is linked to."""
     global _fast_calls
     if _fast_calls is None:
         lib()
-        spec = importlib.util.spec_from_file_location("_fast", _build.FAST_PATH)
-        _fast_calls = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_fast_calls)
+        try:
+            spec = importlib.util.spec_from_file_location("_fast", _build.fast_path())
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+        except (ImportError, OSError) as e:
+            warnings.warn(f"no extension module, step calls cost about 15 us more on the host: {e}", RuntimeWarning,
+                          stacklevel=3)
+            module = _NoFastCalls()
+        _fast_calls = module
     return _fast_calls
 
 

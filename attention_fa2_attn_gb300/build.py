@@ -5,8 +5,9 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel with
 into one shared library next to this file. ``csrc/fast_calls.cpp`` (the step
 calls' way from Python objects to that library) is compiled beside them with
 the host compiler against the installed torch and becomes the extension module
-``_fast``. A rebuild happens only when a source or header is newer than what
-was built from it (or ``force=True``).
+``_fast``; the library needs neither, and where the module cannot be built the
+calls go through their checks in Python. A rebuild happens only when a source or
+header is newer than what was built from it (or ``force=True``).
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,7 +27,6 @@ BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 LIB_NAME = "libfa_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 FAST_SRC = os.path.join(CSRC, "fast_calls.cpp")
-FAST_PATH = os.path.join(HERE, "_fast.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [
@@ -51,19 +52,42 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps() -> list[str]:
-    files = [*sources(), FAST_SRC]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    return files
+def _headers() -> list[str]:
+    return [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+
+
+def _older(built: str, deps: list[str]) -> bool:
+    return not os.path.exists(built) or any(os.path.getmtime(f) > os.path.getmtime(built) for f in deps)
+
+
+def _lib_stale() -> bool:
+    deps = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + _headers()
+    return _older(LIB_PATH, deps)
+
+
+def fast_path() -> str:
+    return os.path.join(HERE, "_fast.so")
+
+
+def _fast_sources() -> list[str]:
+    return [FAST_SRC, *_headers()]
+
+
+def _failed_mark() -> tuple[str, str]:
+    """A file that says which extension could not be built, and what it says then."""
+    return (os.path.join(BUILD_DIR, "fast.failed"),
+            f"{fast_path()} {max(os.path.getmtime(f) for f in _fast_sources())}")
+
+
+def _fast_stale() -> bool:
+    path, text = _failed_mark()
+    if os.path.exists(path) and open(path).read() == text:
+        return False  # once is enough: the calls go without it
+    return _older(fast_path(), _fast_sources())
 
 
 def needs_build() -> bool:
-    built = (LIB_PATH, FAST_PATH)
-    if not all(os.path.exists(f) for f in built):
-        return True
-    t = min(os.path.getmtime(f) for f in built)
-    return any(os.path.getmtime(f) > t for f in _deps())
+    return _lib_stale() or _fast_stale()
 
 
 def _run(cmd: list[str], what: str) -> str:
@@ -97,19 +121,15 @@ def _link_fast(obj: str) -> None:
     import torch
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = FAST_PATH + ".tmp"
+    tmp = fast_path() + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{HERE}", f"-l:{LIB_NAME}", f"-L{lib}",
           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
           f"-Wl,-rpath,{lib}"], "linking _fast")
-    os.replace(tmp, FAST_PATH)
+    os.replace(tmp, fast_path())
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link; returns the library path. Raises on any compiler error."""
-    if not force and not needs_build():
-        return LIB_PATH
+def _compile_lib(ex: ThreadPoolExecutor, verbose: bool) -> list[str]:
     nvcc = _nvcc()
-    os.makedirs(BUILD_DIR, exist_ok=True)
 
     def compile_one(src: str) -> tuple[str, str]:
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
@@ -119,15 +139,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 4)) as ex:
-        fast = ex.submit(_compile_fast)
-        results = list(ex.map(compile_one, sources()))
-        fast_obj = fast.result()
+    results = list(ex.map(compile_one, sources()))
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
+    return [o for o, _ in results]
+
+
+def _link_lib(objs: list[str]) -> None:
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc, ARCH, "-shared", f"-Xlinker=-soname={LIB_NAME}", "-o", tmp, *[o for o, _ in results], "-lcuda"]
+    cmd = [_nvcc(), ARCH, "-shared", f"-Xlinker=-soname={LIB_NAME}", "-o", tmp, *objs, "-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         # libcuda is only needed at run time through the runtime's entry-point
@@ -137,7 +158,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_fast(fast_obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link what is stale; returns the library's path. Raises where the library does not
+    compile, warns where the extension does not (the calls then go through their checks in Python)."""
+    lib_due, fast_due = force or _lib_stale(), force or _fast_stale()
+    if not lib_due and not fast_due:
+        return LIB_PATH
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    mark, text = _failed_mark()
+    with ThreadPoolExecutor(max_workers=min(9, os.cpu_count() or 4)) as ex:
+        fast = ex.submit(_compile_fast) if fast_due else None
+        if lib_due:
+            _link_lib(_compile_lib(ex, verbose))
+        if fast:
+            try:
+                _link_fast(fast.result())
+                if os.path.exists(mark):
+                    os.remove(mark)
+            except Exception as e:  # whatever a host without compiler or headers answers
+                with open(mark, "w") as f:
+                    f.write(text)
+                warnings.warn(f"the step calls' extension module was not built, they take their slower way: {e}",
+                              RuntimeWarning, stacklevel=2)
     return LIB_PATH
 
 
