@@ -7,12 +7,14 @@ calls' way from Python objects to that library) is compiled beside them with
 the host compiler against the installed torch and becomes the extension module
 ``_fast``; the library needs neither, and where the module cannot be built the
 calls go through their checks in Python. A rebuild happens only when a source or
-header is newer than what was built from it (or ``force=True``).
+header is newer than what was built from it (or ``force=True``), and of the module
+when there is none for this Python and this torch.
 """
 
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -66,7 +68,12 @@ def _lib_stale() -> bool:
 
 
 def fast_path() -> str:
-    return os.path.join(HERE, "_fast.so")
+    """The extension module's file, named after the Python and the torch whose layouts it was compiled to: one built
+    for others is not found, and a new one is built."""
+    import torch
+
+    abi = f"{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.cxx11-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_fast.{re.sub(r'[^A-Za-z0-9._+-]', '_', abi)}.so")
 
 
 def _fast_sources() -> list[str]:

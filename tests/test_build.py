@@ -5,6 +5,7 @@ import subprocess
 import warnings
 
 import pytest
+import torch
 
 from attention_fa2_attn_gb300 import _lib, build
 
@@ -62,6 +63,18 @@ def test_the_library_is_what_a_build_is_for(tree):
     with pytest.raises(RuntimeError, match="rope.cu"):
         build.build()
     assert not os.path.exists(build.LIB_PATH)
+
+
+def test_another_torch_makes_the_extension_stale(tree, monkeypatch):
+    build.build()
+    n = len(tree["ran"])
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert build.needs_build()
+    build.build()
+    new = tree["ran"][n:]
+    assert new and not any(".cu" in c for cmd in new for c in cmd), "the library was not stale"
+    assert not build.needs_build()
+    assert len(_extensions()) == 2  # each torch loads its own
 
 
 def test_sources_make_their_own_part_stale(tree):
