@@ -33,6 +33,9 @@ _D = ctypes.c_double
 
 FA_DTYPE_BF16 = 0
 FA_DTYPE_F32 = 1
+FA_PLAN_MAX_T = 8388480
+FA_TREE_MASK_MAX_T = 8192
+FA_TREE_MASK_MAX_B = 65535
 FA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # name -> (restype, argtypes); mirrors include/fa_gb300.h

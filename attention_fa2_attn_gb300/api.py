@@ -13,7 +13,19 @@ import math
 
 import torch
 
-from ._lib import FA_DTYPE_BF16, FA_DTYPE_F32, FA_ROPE_SCALINGS, FAError, check, fast, lib
+from ._lib import (
+    FA_DTYPE_BF16,
+    FA_DTYPE_F32,
+    FA_ERR_UNSUPPORTED,
+    FA_PLAN_MAX_T,
+    FA_ROPE_SCALINGS,
+    FA_TREE_MASK_MAX_B,
+    FA_TREE_MASK_MAX_T,
+    FAError,
+    check,
+    fast,
+    lib,
+)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -328,6 +340,8 @@ def fa_paged_plan(cached_lens, new_lens, free_pages, block_table, T: int, align_
     T = int(T)
     if T < 1:
         raise ValueError(f"T must be at least 1, got {T}")
+    if T > FA_PLAN_MAX_T or B * T >= 2**31:  # before outputs of that size are made
+        check(FA_ERR_UNSUPPORTED, "fa_paged_plan")
     seqlens = _out(seqlens, "seqlens", (B,), _I32, block_table)
     slots = _out(slots, "slots", (B, T), _I32, block_table)
     positions = _out(positions, "positions", (B, T), _I32, block_table)
@@ -353,6 +367,8 @@ def fa_tree_mask(parents, seqlens, tree_lens=None, mask=None, positions=None):
     if tree_lens is not None:
         _need_ints("tree_lens", tree_lens, (B,), parents.device)
     _on_current_device(parents)
+    if B > FA_TREE_MASK_MAX_B or T > FA_TREE_MASK_MAX_T:
+        check(FA_ERR_UNSUPPORTED, "fa_tree_mask")
     mask = _out(mask, "mask", (B, T, (T + 31) // 32), _I32, parents)
     positions = _out(positions, "positions", (B, T), _I32, parents)
     st = lib().fa_tree_mask(_ptr(parents), _ptr(seqlens), _ptr(tree_lens), _ptr(mask), _ptr(positions), B, T,

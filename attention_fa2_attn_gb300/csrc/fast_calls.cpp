@@ -148,7 +148,8 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !dense(*free_pages, at::kInt, 1, dev))
     Py_RETURN_NONE;
   const int64_t B = table->size(0), pages = table->size(1), F = free_pages->size(0);
-  if (cached->size(0) != B || fresh->size(0) != B || !fits(B) || !fits(pages) || !fits(F) || !fits(B * T))
+  if (cached->size(0) != B || fresh->size(0) != B || !fits(B) || !fits(pages) || !fits(F) || !fits(B * T) ||
+      T > FA_PLAN_MAX_T)  // refused before its outputs are made
     Py_RETURN_NONE;
   std::array<Tensor, 4> out;  // seqlens, slots, positions, pages used
   fa_status st;
@@ -175,7 +176,8 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (lens && !dense(*lens, at::kInt, 1, dev)))
     Py_RETURN_NONE;
   const int64_t B = parents->size(0), T = parents->size(1);
-  if (seqlens->size(0) != B || (lens && lens->size(0) != B) || !fits(B) || !fits(T)) Py_RETURN_NONE;
+  if (seqlens->size(0) != B || (lens && lens->size(0) != B) || B > FA_TREE_MASK_MAX_B || T > FA_TREE_MASK_MAX_T)
+    Py_RETURN_NONE;
   std::array<Tensor, 2> out;  // mask, positions
   fa_status st;
   {

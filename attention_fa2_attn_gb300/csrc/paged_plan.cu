@@ -35,6 +35,7 @@ constexpr int kPlanSeqs = 8;          // sequences per block, one warp each
 constexpr int kPlanThreads = kPlanSeqs * 32;
 constexpr int kPlanRows = 4;          // tokens of a lane, their loads in flight together
 constexpr int kPlanChunk = kPlanRows * 32;  // tokens of a sequence per block
+static_assert(FA_PLAN_MAX_T == 65535 * kPlanChunk, "blockIdx.y counts a sequence's chunks");
 
 struct PlanParams {
   const int* cached;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(128) tree_mask_small_kernel(const int* __restr
   positions[row] = i < l.n ? l.S - l.n + seen - 1 : 0;
 }
 
-constexpr int kTreeMaxNodes = 8192;  // parents of one sequence in shared memory
+constexpr int kTreeMaxNodes = FA_TREE_MASK_MAX_T;  // parents of one sequence in shared memory
 
 __global__ void __launch_bounds__(128) tree_mask_kernel(const int* __restrict__ parents,
                                                         const int* __restrict__ seqlens,
@@ -248,7 +249,7 @@ fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_
   if (B < 1 || T < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
   if (page_size != kPage) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * T >= (1ll << 31) || static_cast<long long>(B) * max_pages >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * kPage >= (1ll << 31) || T > 65535ll * kPlanChunk)
+      static_cast<long long>(max_pages) * kPage >= (1ll << 31) || T > FA_PLAN_MAX_T)
     return FA_ERR_UNSUPPORTED;
   {
     // blocks read the lengths and the free list of all sequences while others write theirs
@@ -289,7 +290,7 @@ fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_l
   if (bad(parents) || bad(seqlens) || bad(mask) || bad(positions) || (tree_lens && bad(tree_lens)))
     return FA_ERR_INVALID_ARG;
   if (B < 1 || T < 1) return FA_ERR_INVALID_ARG;
-  if (B > 65535 || T > kTreeMaxNodes) return FA_ERR_UNSUPPORTED;
+  if (B > FA_TREE_MASK_MAX_B || T > kTreeMaxNodes) return FA_ERR_UNSUPPORTED;
   {
     const long long b4 = 4ll * B, bt4 = b4 * T, m4 = bt4 * ((T + 31) / 32);
     for (const void* x : {static_cast<const void*>(mask), static_cast<const void*>(positions)}) {

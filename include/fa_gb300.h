@@ -82,6 +82,12 @@ typedef enum {
   FA_ROPE_YARN = 3    /* slow pairs / factor, fast pairs kept, a linear ramp between; mscale 0.1 ln factor + 1 */
 } fa_rope_scaling;
 
+/* Limits of the plan and mask calls' outputs, which are much larger than their inputs: a caller that
+ * allocates them can ask first. */
+#define FA_PLAN_MAX_T 8388480      /* rows of a sequence in fa_paged_plan; B * T < 2^31 as well */
+#define FA_TREE_MASK_MAX_T 8192    /* nodes of a tree in fa_tree_mask */
+#define FA_TREE_MASK_MAX_B 65535   /* trees of a call */
+
 /* Library version, major*10000 + minor*100 + patch. */
 FA_API int fa_version(void);
 
@@ -341,6 +347,7 @@ FA_API fa_status fa_decode_paged(const void* q, const void* k_pages, const void*
  *   their tokens' slots -1; pages_used says how many were needed.
  *   Table entries outside [0, 2^27 - 1) give their tokens no slot (-1).
  *   No output, block_table among them, may overlap another argument (FA_ERR_INVALID_ARG).
+ *   B * T < 2^31, T <= FA_PLAN_MAX_T.
  */
 FA_API fa_status fa_paged_plan(const int* cached, const int* new_lens, const int* free_pages, int num_free,
                                int* block_table, int* seqlens, int* slots, int* positions, int* pages_used,
@@ -354,7 +361,7 @@ FA_API fa_status fa_paged_plan(const int* cached, const int* new_lens, const int
  *   mask [B][T][ceil(T / 32)] int32 out: bit j % 32 of word j / 32 of row i: node i sees
  *     node j (itself or an ancestor). Rows from n_b on are 0.
  *   positions [B][T] int32 out: seqlens[b] - n_b + depth (0 at a root); 0 from n_b on.
- *   A parent outside [-1, i) records FA_ERR_BOUNDS and counts as -1. T <= 8192, B <= 65535.
+ *   A parent outside [-1, i) records FA_ERR_BOUNDS and counts as -1. T <= FA_TREE_MASK_MAX_T, B <= FA_TREE_MASK_MAX_B.
  *   No output may overlap another argument (FA_ERR_INVALID_ARG).
  */
 FA_API fa_status fa_tree_mask(const int* parents, const int* seqlens, const int* tree_lens, int* mask,
