@@ -510,7 +510,9 @@ def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, 
 
 def fa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, max_pages: int, d: int,
                             num_sms: int | None = None, device=None) -> int:
-    """Bytes of workspace fa_tree_decode_paged needs on a device with num_sms SMs (None: this one)."""
+    """Bytes of workspace fa_tree_decode_paged needs on a device with num_sms SMs (None: this one), for this shape: a
+    smaller batch or a narrower table may need more. num_sms * (2 * rows * (4 * d + 16) + 16) holds for every batch and
+    table, rows = 128 where Hq / Hkv * T <= 128, else 256."""
     if num_sms is None:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         num_sms = torch.cuda.get_device_properties(dev).multi_processor_count

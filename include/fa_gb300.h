@@ -463,7 +463,10 @@ FA_API fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const 
 
 /* fa_tree_workspace_bytes -- two fp32 partials (O, max, sums) of a row tile for each CTA that
  * the call launches on num_sms SMs, and its list of split work; 0 for problems that are small
- * under the longest contexts the table allows (joined in shared memory), and for invalid sizes. */
+ * under the longest contexts the table allows (joined in shared memory), and for invalid sizes.
+ * It is the need of this shape and of no other: a smaller batch or table may take the other
+ * form and need more. What holds for every B, Hkv and max_pages is
+ *   num_sms * (2 * rows * (4 * d + 16) + 16),  rows = 128 where Hq / Hkv * T <= 128, else 256. */
 FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
 
 /*

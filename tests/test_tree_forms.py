@@ -30,6 +30,45 @@ def test_small_batches_stay_in_clusters():
     assert _clustered(1, 8, 1000, NARROW) and _clustered(1, 8, 8000, NARROW) and _clustered(16, 8, 1000, WIDE)
 
 
+def _largest(rows, d, sms):
+    """What the header gives for every batch and table."""
+    tile = 128 if rows["Hq"] * rows["T"] <= 128 else 256
+    return sms * (2 * tile * (4 * d + 16) + 16)
+
+
+@pytest.mark.parametrize("rows", [NARROW, WIDE, dict(Hq=1, T=1), dict(Hq=16, T=8), dict(Hq=1, T=129), dict(Hq=16, T=128)])
+def test_one_workspace_for_all_batches_and_tables(rows):
+    L = _lib.lib()
+    need = lambda B, Hkv, mp, d, sms: L.fa_tree_workspace_bytes(B, rows["Hq"] * Hkv, Hkv, rows["T"], mp, d, sms)  # noqa: E731
+    for d in (64, 128):
+        for sms in (1, 132, 148, 152):
+            most = _largest(rows, d, sms)
+            sizes = {need(B, Hkv, mp, d, sms) for B in (1, 2, 3, 7, 10, 13, 16, 19, 38, 64, 500) for Hkv in (1, 2, 3, 8, 32)
+                     for mp in (1, 7, 32, 96, 192, 1000, 8192, 65536)}
+            assert max(sizes) <= most and (sms == 1 or 0 in sizes)
+            assert need(64, 8, 8192, d, sms) == most  # and no more than a large call needs
+    # the need of one shape is no bound for smaller ones: fewer sequences, more bytes
+    if rows is NARROW:
+        assert need(19, 8, 96, 128, 152) == 0 < need(12, 8, 96, 128, 152)
+
+
+@pytest.mark.gpu
+def test_a_workspace_made_once_serves_every_batch():
+    from test_gpu_tree import _call, _case
+
+    d, Hkv = 64, 8
+    ws = torch.full((_largest(NARROW, d, torch.cuda.get_device_properties(0).multi_processor_count),), 255, dtype=torch.uint8,
+                    device="cuda:0")
+    c = _case(20, 4 * Hkv, Hkv, 8, d, [1500 - 70 * b for b in range(20)], 80, lens=[8] * 20)
+    forms = set()
+    for B in range(20, 0, -1):
+        part = {k: (v[:B].contiguous() if k in ("q", "table", "seqlens", "mask", "lens") else v) for k, v in c.items()}
+        forms.add(fa.fa_tree_workspace_bytes(B, 4 * Hkv, Hkv, 8, c["table"].shape[1], d) > 0)
+        got, want = _call(part, workspace=ws), _call(part)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), B
+    assert forms == {False, True}
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [NARROW, WIDE], ids=["narrow", "wide"])
