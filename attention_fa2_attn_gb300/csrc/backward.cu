@@ -269,15 +269,14 @@ __device__ __forceinline__ void bwd_dq_cta(const CUtensorMap& tmQ, const CUtenso
         k_only = -1;
         issued = j + 1;
       }
-      if (*abort_flag) {
-        // copies in flight must land before the CTA exits
-        mbar_wait(&bars->fix_full, 0, tmo_unwind);
-        for (int x = max(0, issued - 2); x < issued; ++x) {
-          mbar_wait(&bars->slot_full[slot_late(x)], (x >> 1) & 1, tmo_unwind);
-          mbar_wait(&bars->slot_full[slot_early(x)], (x >> 1) & 1, tmo_unwind);
-        }
-        if (k_only >= 0) mbar_wait(&bars->slot_full[slot_late(k_only)], (k_only >> 1) & 1, tmo_unwind);
+      // copies in flight must land before the CTA exits, whether or not a wait has run out so
+      // far: another role's may yet
+      mbar_wait(&bars->fix_full, 0, tmo_unwind);
+      for (int x = max(0, issued - 2); x < issued; ++x) {
+        mbar_wait(&bars->slot_full[slot_late(x)], (x >> 1) & 1, tmo_unwind);
+        mbar_wait(&bars->slot_full[slot_early(x)], (x >> 1) & 1, tmo_unwind);
       }
+      if (k_only >= 0) mbar_wait(&bars->slot_full[slot_late(k_only)], (k_only >> 1) & 1, tmo_unwind);
     }
   } else if (warp == C::MMA_WARP) {
     const bool leader = elect_one();
@@ -618,14 +617,13 @@ __device__ __forceinline__ void bwd_dkdv_cta(const CUtensorMap& tmQ, const CUten
         q_only = -1;
         issued = i + 1;
       }
-      if (*abort_flag) {
-        mbar_wait(&bars->fix_full, 0, tmo_unwind);
-        for (int x = max(0, issued - 2); x < issued; ++x) {
-          mbar_wait(&bars->slot_full[slot_late(x)], (x >> 1) & 1, tmo_unwind);
-          mbar_wait(&bars->slot_full[slot_early(x)], (x >> 1) & 1, tmo_unwind);
-        }
-        if (q_only >= 0) mbar_wait(&bars->slot_full[slot_late(q_only)], (q_only >> 1) & 1, tmo_unwind);
+      // as in the other half: the copies land first
+      mbar_wait(&bars->fix_full, 0, tmo_unwind);
+      for (int x = max(0, issued - 2); x < issued; ++x) {
+        mbar_wait(&bars->slot_full[slot_late(x)], (x >> 1) & 1, tmo_unwind);
+        mbar_wait(&bars->slot_full[slot_early(x)], (x >> 1) & 1, tmo_unwind);
       }
+      if (q_only >= 0) mbar_wait(&bars->slot_full[slot_late(q_only)], (q_only >> 1) & 1, tmo_unwind);
     }
   } else if (warp == C::MMA_WARP) {
     const bool leader = elect_one();

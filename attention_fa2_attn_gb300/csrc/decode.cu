@@ -204,13 +204,15 @@ __global__ void __launch_bounds__(160, PAGED ? 2 : 1)
       }
       issued = it + 1;
     }
-    if (!ok) {
-      if (lane == 0) {
+    if (lane == 0) {
+      if (!ok) {
         record_error(p.err, FA_ERR_TIMEOUT, SITE_DEC_PRODUCER);
         *abort_flag = 1;
-        for (int it = max(0, issued - STAGES); it < issued; ++it)
-          mbar_wait(&full[it % STAGES], (it / STAGES) & 1, tmo_unwind);
       }
+      // copies in flight must land before the CTA exits, whether or not a wait has run out so
+      // far: a consumer's may yet
+      for (int it = max(0, issued - STAGES); it < issued; ++it)
+        mbar_wait(&full[it % STAGES], (it / STAGES) & 1, tmo_unwind);
     }
   } else {
     // ======================= consumer warps 0-3 =======================

@@ -276,13 +276,12 @@ __global__ void __launch_bounds__(KoCfg<D>::THREADS, 1)
         if (!retire(t)) ok = false;
       bulk_wait_all();
       if (!ok) fail(SITE_KO_PRODUCER);
-      if (*abort_flag) {
-        // loads still in flight must land before the CTA exits: at most the last
-        // phase of kv_full and q_full, and the last step of each O' buffer
-        if (kv_loads > 0) mbar_wait(&bars->kv_full, (kv_loads - 1) & 1, tmo_unwind);
-        if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-        for (int t = max(0, o_steps - 2); t < o_steps; ++t) mbar_wait(&bars->o_full[t & 1], (t >> 1) & 1, tmo_unwind);
-      }
+      // loads still in flight must land before the CTA exits (whether or not a wait has run
+      // out so far: another role's may yet): at most the last phase of kv_full and q_full,
+      // and the last step of each O' buffer
+      if (kv_loads > 0) mbar_wait(&bars->kv_full, (kv_loads - 1) & 1, tmo_unwind);
+      if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+      for (int t = max(0, o_steps - 2); t < o_steps; ++t) mbar_wait(&bars->o_full[t & 1], (t >> 1) & 1, tmo_unwind);
     }
   } else if (warp == C::MMA_WARP) {
     // ======================= MMA issuer =======================

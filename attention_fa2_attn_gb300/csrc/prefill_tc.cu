@@ -371,13 +371,12 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
       }
-      if (*abort_flag) {
-        // copies still in flight must complete before the CTA exits
-        if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-        for (uint32_t x = g > C::STAGES ? g - C::STAGES : 0; x < g; ++x) {
-          mbar_wait(&bars->k_full[x % C::STAGES], (x / C::STAGES) & 1, tmo_unwind);
-          mbar_wait(&bars->v_full[x % C::STAGES], (x / C::STAGES) & 1, tmo_unwind);
-        }
+      // Copies still in flight must complete before the CTA exits. Waited for whether or not a
+      // wait has run out so far: another role's may after the last copy was issued here.
+      if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+      for (uint32_t x = g > C::STAGES ? g - C::STAGES : 0; x < g; ++x) {
+        mbar_wait(&bars->k_full[x % C::STAGES], (x / C::STAGES) & 1, tmo_unwind);
+        mbar_wait(&bars->v_full[x % C::STAGES], (x / C::STAGES) & 1, tmo_unwind);
       }
     }
   } else if (warp == C::MMA_WARP) {

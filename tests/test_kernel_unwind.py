@@ -50,3 +50,11 @@ def test_tree_softmax_warps_keep_what_they_voted():
     for at in votes:
         assert re.search(r"[;{}]\s*ok = $", code[:at]), code[at - 40:at + 30]
     assert "bars->finished = ok;" in code
+
+
+def test_every_producer_waits_for_its_copies_whatever_happens():
+    for name, least in (("prefill_tc.cu", 3), ("decode.cu", 1), ("kv_outer.cu", 3), ("backward.cu", 8), ("tree.cu", 3)):
+        code = _code(name)
+        kept = [at for at in _landing_waits(code)
+                if not any(re.fullmatch(r"if \((?:\*abort_flag|!ok)\)", h) for h in _enclosing(code, at))]
+        assert len(kept) >= least and len(kept) == len(_landing_waits(code)), name
