@@ -22,7 +22,9 @@
 // rounds are the logarithm of the depth and not the depth. Larger ones (their sets do not
 // fit in registers): a thread walks up the parents in shared memory; as parent(i) < i the
 // visited bits fall, so it keeps one 32-bit word and stores it (and the empty ones it
-// skips) when the walk leaves it.
+// skips) when the walk leaves it. Bound by the deepest walk, 0.15 us an ancestor (a chain of
+// 1024 nodes 156 us, of 8192 1.25 ms), or by its stores, a row apart from lane to lane (random
+// trees of 8192 nodes: one 34 us, sixteen 186 us, 0.72 TB/s).
 #include <initializer_list>
 
 #include "launch.cuh"

@@ -19,7 +19,9 @@
  *
  * Conventions shared by every call
  *   - Every tensor argument is a DEVICE pointer owned by the caller, dense
- *     row-major, 16-byte aligned. The library never frees or keeps them.
+ *     row-major, 16-byte aligned (but where a call says otherwise: the rotary
+ *     calls take strides and the element's alignment, int32 arguments 4 bytes).
+ *     The library never frees or keeps them.
  *   - Layouts: q, o are [B][Hq][T][d]; k, v are [B][Hkv][S][d]; lse is
  *     [B][Hq][T] fp32 (natural log of the sum of exp of the scaled scores).
  *   - GQA: Hq % Hkv == 0; query head h reads KV head h / (Hq / Hkv).
@@ -30,17 +32,18 @@
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream). Argument errors are returned synchronously, before
  *     anything is launched; FA_ERR_CUDA reports a failed launch.
- *   - The prefill, decode and backward kernels launch as programmatic
- *     dependents of the launch before them on `stream` and may start while
- *     it finishes; each waits (griddepcontrol.wait) before its first access
- *     to global memory, so stream order holds for every input and output.
- *     The unsplit prefill, the decode kernel, the LSE merge and the backward's
- *     main grid also let the next launch on the stream start early; a kernel of
- *     the caller's launched that way after them must likewise wait before
- *     reading their outputs.
+ *   - The prefill, decode, backward, plan, mask, rotary and tree kernels launch
+ *     as programmatic dependents of the launch before them on `stream` and may
+ *     start while it finishes; each waits (griddepcontrol.wait) before its
+ *     first access to global memory, so stream order holds for every input and
+ *     output. The unsplit prefill, the decode kernel, the merges, the backward's
+ *     main grid and the plan, mask and rotary kernels also let the next launch
+ *     on the stream start early; a kernel of the caller's launched that way
+ *     after them must likewise wait before reading their outputs.
  *   - Kernels never trap. Every wait inside a kernel is bounded; a wait that
  *     runs out, or a bounds check that fails (paged block-table entries),
- *     records a code in a device-side error word and the kernel returns.
+ *     records a code in a device-side error word and the kernel returns, its
+ *     own copies landed and its MMAs drained.
  *     fa_get_last_device_error() reads and clears that word.
  *   - The library allocates no device memory. Scratch space (split-KV
  *     partials, the backward's per-row values, the running state of the
