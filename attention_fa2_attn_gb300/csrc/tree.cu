@@ -4,7 +4,8 @@
 // drafted nodes. Query row i < n is node i: it sees key j if j < S - n (the committed
 // text) or bit j - (S - n) of its mask row is set. O = softmax(scale * q K^T) V over
 // the keys it sees, lse = ln sum exp; a row that sees none, and rows from n on, get
-// O = 0 and lse = -inf; a row whose query is not finite gets NaN for both. A KV head's g = Hq / Hkv query heads times T nodes are R = g * T
+// O = 0 and lse = -inf; a row with a score of NaN or +inf (a query that is not finite) gets NaN
+// for both. A KV head's g = Hq / Hkv query heads times T nodes are R = g * T
 // rows, dense in q, o and lse: row r is node r % T of head r / T.
 //
 // What bounds it. K and V are read once for R rows: R FLOP per byte. Up to some 256

@@ -453,8 +453,9 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
  *   other argument (FA_ERR_INVALID_ARG).
  *   Keys and values inside a sequence must be finite, as for every call here: a row's weight
  *   of 0 does not cancel a NaN value that the mask hides from it. Pool rows past a
- *   sequence's end are never used, whatever they hold. A query row that is not finite and
- *   sees a key gets NaN in O and lse where its softmax is one (its scores NaN or +inf).
+ *   sequence's end are never used, whatever they hold. A query row with a score that is NaN
+ *   or +inf (one that is not finite itself) gets NaN in O and lse; scores of -inf weigh
+ *   nothing, and a row that has no other gets what one without keys gets.
  *   A table entry outside [0, num_pages) is not dereferenced: FA_ERR_BOUNDS is recorded and
  *   that sequence's output is undefined.
  */

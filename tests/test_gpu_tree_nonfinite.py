@@ -58,3 +58,21 @@ def test_rows_that_see_nothing_stay_empty(T, wide):
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert not o[0, :, 1].any() and (lse[0, :, 1] == -np.inf).all()
     assert not o[1, :, T - 1].any() and (lse[1, :, T - 1] == -np.inf).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_of_minus_infinity_weigh_nothing(wide):
+    # an infinite query against keys of one sign there: all scores are -inf (an empty row), or all +inf (NaN)
+    c = _case(2, 4, 1, 3, 64, [300, 2], 72, lens=[3, 2])
+    c["kp"][..., 5] = c["kp"][..., 5].abs() + 0.5
+    if wide:
+        c = _wide_table(c)
+    want = _call(c)
+    q = c["q"].clone()
+    q[:, 0, 1, 5], q[:, 2, 0, 5] = -float("inf"), float("inf")
+    o, lse = _call(dict(c, q=q))
+    assert not o[:, 0, 1].any() and (lse[:, 0, 1] == -np.inf).all()
+    assert torch.isnan(o[:, 2, 0]).all() and torch.isnan(lse[:, 2, 0]).all()
+    keep = torch.ones(2, 4, 3, dtype=torch.bool, device=q.device)
+    keep[:, 0, 1] = keep[:, 2, 0] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
