@@ -25,10 +25,18 @@ from .api import (  # noqa: F401
     fa_num_splits_heuristic,
     fa_num_splits_prefill,
     fa_paged_plan,
+    fa_pages_compact,
+    fa_pages_copy,
+    fa_pages_fork,
+    fa_pages_free,
     fa_rope,
     fa_rope_append_paged,
+    fa_rope_axes,
+    fa_rope_axes_append_paged,
+    fa_rope_axes_bwd,
     fa_rope_bwd,
     fa_rope_inv_freq,
+    fa_rope_pair_axis,
     fa_selftest_wait_timeout,
     fa_set_wait_timeout_ns,
     fa_tree_decode_paged,

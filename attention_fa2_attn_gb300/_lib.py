@@ -36,6 +36,8 @@ FA_DTYPE_F32 = 1
 FA_PLAN_MAX_T = 8388480
 FA_TREE_MASK_MAX_T = 8192
 FA_TREE_MASK_MAX_B = 65535
+FA_PAGES_MAX = 4194304
+FA_ROPE_MAX_AXES = 8
 FA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 # name -> (restype, argtypes); mirrors include/fa_gb300.h
@@ -69,6 +71,16 @@ SIGNATURES = {
         _I,
         [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
     ),
+    "fa_rope_axes": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_rope_axes_bwd": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_rope_axes_append_paged": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P],
+    ),
+    "fa_pages_fork": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "fa_pages_copy": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
+    "fa_pages_free": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "fa_pages_compact": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "fa_tree_decode_paged": (
         _I,
         [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P],

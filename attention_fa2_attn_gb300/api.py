@@ -17,7 +17,9 @@ from ._lib import (
     FA_DTYPE_BF16,
     FA_DTYPE_F32,
     FA_ERR_UNSUPPORTED,
+    FA_PAGES_MAX,
     FA_PLAN_MAX_T,
+    FA_ROPE_MAX_AXES,
     FA_ROPE_SCALINGS,
     FA_TREE_MASK_MAX_B,
     FA_TREE_MASK_MAX_T,
@@ -420,21 +422,29 @@ def _rows_out(t, name: str, like: torch.Tensor):
     return t
 
 
-def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool) -> bool:
+def _need_angles(positions, inv_freq, B: int, T: int, device, shared_ok: bool, pair_axis=None) -> bool:
+    """Whether the positions are one row for the whole batch; with pair_axis they have an axis in front."""
     if not isinstance(positions, torch.Tensor) or positions.dtype != _I32 or positions.device != device \
             or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous int32 tensor on {device}")
     shape = tuple(positions.shape)
+    if pair_axis is not None:
+        if len(shape) < 2 or not 1 <= shape[0] <= FA_ROPE_MAX_AXES:
+            raise ValueError(f"positions must have 1 to {FA_ROPE_MAX_AXES} axes in front, got {shape}")
+        shape = shape[1:]
     if shape != (B, T) and not (shared_ok and shape == (T,)):
-        raise ValueError(f"positions must be [{B}][{T}]{f' or [{T}]' if shared_ok else ''}, got {shape}")
+        front = "" if pair_axis is None else "[axes]"
+        raise ValueError(f"positions must be {front}[{B}][{T}]{f' or {front}[{T}]' if shared_ok else ''}, got {tuple(positions.shape)}")
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != _F64 or inv_freq.device != device \
             or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a contiguous 1-D float64 tensor on {device} (fa_rope_inv_freq)")
+    if pair_axis is not None:
+        _need_ints("pair_axis", pair_axis, tuple(inv_freq.shape), device)
     return len(shape) == 1
 
 
-def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out):
-    got = fast().rope(q, k, positions, inv_freq, interleaved, mscale, name == "fa_rope_bwd", q_out, k_out)
+def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_out, *pair_axis):
+    got = fast().rope(q, k, positions, inv_freq, interleaved, mscale, name.endswith("_bwd"), q_out, k_out, *pair_axis)
     if got is not None:
         return _answer(got, name)
     if not isinstance(q, torch.Tensor) or q.dtype not in _ROPE_DTYPES:
@@ -443,7 +453,9 @@ def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_ou
     _need_rows(q, "q", q.dtype, dev)
     _on_current_device(q)
     B, Hq, T, d = q.shape
-    shared = _need_angles(positions, inv_freq, B, T, dev, True)
+    if pair_axis and pair_axis[0] is None:
+        raise ValueError(f"{name}: pair_axis must be an int32 tensor (fa_rope_pair_axis)")
+    shared = _need_angles(positions, inv_freq, B, T, dev, True, *pair_axis)
     q_out = _rows_out(q_out, "q_out", q)
     Hk, sk, sko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
@@ -456,9 +468,10 @@ def _rope(name: str, q, k, positions, inv_freq, interleaved, mscale, q_out, k_ou
     elif k_out is not None:
         raise ValueError("k_out without k")
     strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *sk, *sko)
+    axes = (_ptr(pair_axis[0]), positions.shape[0]) if pair_axis else ()
     st = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), strides, _ptr(positions), int(shared),
-                              _ptr(inv_freq), B, Hq, Hk, T, d, 2 * inv_freq.shape[0], int(interleaved), float(mscale),
-                              _ROPE_DTYPES[q.dtype], _stream(q))
+                              _ptr(inv_freq), *axes, B, Hq, Hk, T, d, 2 * inv_freq.shape[0], int(interleaved),
+                              float(mscale), _ROPE_DTYPES[q.dtype], _stream(q))
     check(st, name)
     return q_out, k_out
 
@@ -476,13 +489,39 @@ def fa_rope_bwd(dq_out, dk_out, positions, inv_freq, interleaved: bool = False, 
     return _rope("fa_rope_bwd", dq_out, dk_out, positions, inv_freq, interleaved, mscale, q_out, k_out)
 
 
-def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved: bool = False,
-                         mscale: float = 1.0, q_out=None):
-    """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
-    and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
-    got = fast().rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out)
+def fa_rope_pair_axis(sections, cyclic: bool = False, device="cuda"):
+    """The axis of each rotary pair, sections[a] pairs on axis a: in blocks, or (cyclic) pair i on axis i % len(sections)
+    while that has pairs left and on axis 0 else -> int32 [sum(sections)] on device."""
+    n = [int(s) for s in sections]
+    if not 1 <= len(n) <= FA_ROPE_MAX_AXES or min(n) < 0 or sum(n) < 1:
+        raise ValueError(f"sections must be 1 to {FA_ROPE_MAX_AXES} counts of pairs, got {sections!r}")
+    A, total = len(n), sum(n)
+    if cyclic:
+        axis = [i % A if i // A < n[i % A] else 0 for i in range(total)]
+    else:
+        axis = [a for a in range(A) for _ in range(n[a])]
+    if [axis.count(a) for a in range(A)] != n:
+        raise ValueError(f"pairs in turn do not come to the sections {sections!r}: no axis may have more than axis 0")
+    return torch.tensor(axis, dtype=_I32).to(device)
+
+
+def fa_rope_axes(q, k, positions, inv_freq, pair_axis, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None):
+    """fa_rope for positions with several axes, [axes][B][T] or [axes][T] int32: pair i turns by the position on axis
+    pair_axis[i] (int32 [rot/2], fa_rope_pair_axis) -> (q_out, k_out)."""
+    return _rope("fa_rope_axes", q, k, positions, inv_freq, interleaved, mscale, q_out, k_out, pair_axis)
+
+
+def fa_rope_axes_bwd(dq_out, dk_out, positions, inv_freq, pair_axis, interleaved: bool = False, mscale: float = 1.0,
+                     q_out=None, k_out=None):
+    """Gradients of fa_rope_axes: those of its outputs -> (dq, dk), into q_out and k_out where given."""
+    return _rope("fa_rope_axes_bwd", dq_out, dk_out, positions, inv_freq, interleaved, mscale, q_out, k_out, pair_axis)
+
+
+def _append(name: str, q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out, *pair_axis):
+    got = fast().rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out,
+                                   *pair_axis)
     if got is not None:
-        return _answer(got, "fa_rope_append_paged")
+        return _answer(got, name)
     if not isinstance(q, torch.Tensor):
         raise ValueError("q must be a CUDA tensor")
     dev = q.device
@@ -497,15 +536,161 @@ def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, 
     _need_rows(k, "k", _BF16, dev, (B, Hkv, T, d))
     _need_rows(v, "v", _BF16, dev, (B, Hkv, T, d))
     _on_current_device(q)
-    _need_angles(positions, inv_freq, B, T, dev, False)
+    if pair_axis and pair_axis[0] is None:
+        raise ValueError(f"{name}: pair_axis must be an int32 tensor (fa_rope_pair_axis)")
+    _need_angles(positions, inv_freq, B, T, dev, False, *pair_axis)
     _need_ints("slots", slots, (B, T), dev)
     q_out = _rows_out(q_out, "q_out", q)
     strides = _Strides(*q.stride()[:3], *q_out.stride()[:3], *k.stride()[:3], *v.stride()[:3])
-    st = lib().fa_rope_append_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), strides, _ptr(positions), _ptr(slots),
-                                    _ptr(inv_freq), _ptr(k_pages), _ptr(v_pages), B, Hq, Hkv, T, page_size, P, d,
-                                    2 * inv_freq.shape[0], int(interleaved), float(mscale), _stream(q))
-    check(st, "fa_rope_append_paged")
+    axes = (_ptr(pair_axis[0]), positions.shape[0]) if pair_axis else ()
+    st = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), strides, _ptr(positions), _ptr(slots),
+                              _ptr(inv_freq), *axes, _ptr(k_pages), _ptr(v_pages), B, Hq, Hkv, T, page_size, P, d,
+                              2 * inv_freq.shape[0], int(interleaved), float(mscale), _stream(q))
+    check(st, name)
     return q_out
+
+
+def fa_rope_append_paged(q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved: bool = False,
+                         mscale: float = 1.0, q_out=None):
+    """New rows of a step over the paged cache: q [B][Hq][T][d] rotated -> q_out; k [B][Hkv][T][d] rotated
+    and v written to rows slots [B][T] of the pools [P][16][Hkv][d] (-1: not written). bf16."""
+    return _append("fa_rope_append_paged", q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out)
+
+
+def fa_rope_axes_append_paged(q, k, v, positions, slots, inv_freq, pair_axis, k_pages, v_pages, interleaved: bool = False,
+                              mscale: float = 1.0, q_out=None):
+    """fa_rope_append_paged for positions [axes][B][T] with several axes; pair_axis as fa_rope_axes."""
+    return _append("fa_rope_axes_append_paged", q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale,
+                   q_out, pair_axis)
+
+
+def _need_table(block_table, seqlens, shares=None):
+    """-> (B, max_pages, device) of a block table with its lengths, and the shares of the pool's pages."""
+    _need(block_table, "block_table", _I32, 2)
+    _on_current_device(block_table)
+    B, max_pages = block_table.shape
+    dev = block_table.device
+    _need_ints("seqlens", seqlens, (B,), dev)
+    if shares is not None:
+        _need(shares, "shares", _I32, 1)
+        if shares.device != dev:
+            raise ValueError(f"shares must be on {dev}")
+    return B, max_pages, dev
+
+
+def fa_pages_fork(block_table, seqlens, parents, free_pages, shares, table_out=None, lens_out=None, copy_src=None,
+                  copy_dst=None, pages_used=None):
+    """Sequences that go on from rows parents [n] of the table (-1: an empty one): they share its whole pages (shares [P],
+    one more each, in place) and get a page from free_pages for the tokens behind them
+    -> (table [n][max_pages], lens [n], copy_src [n], copy_dst [n], pages_used [1]), int32, new ones in one allocation."""
+    if table_out is None and lens_out is None and copy_src is None and copy_dst is None and pages_used is None:
+        got = fast().pages_fork(block_table, seqlens, parents, free_pages, shares)
+        if got is not None:
+            return _answer(got, "fa_pages_fork")
+    _need(shares, "shares", _I32, 1)
+    B, max_pages, dev = _need_table(block_table, seqlens, shares)
+    for t, name in ((parents, "parents"), (free_pages, "free_pages")):
+        _need(t, name, _I32, 1)
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    n, P = parents.shape[0], shares.shape[0]
+    if n * max_pages >= 2**31:  # before outputs of that size are made
+        check(FA_ERR_UNSUPPORTED, "fa_pages_fork")
+    table_out = _out(table_out, "table_out", (n, max_pages), _I32, block_table)
+    lens_out = _out(lens_out, "lens_out", (n,), _I32, block_table)
+    copy_src = _out(copy_src, "copy_src", (n,), _I32, block_table)
+    copy_dst = _out(copy_dst, "copy_dst", (n,), _I32, block_table)
+    pages_used = _out(pages_used, "pages_used", (1,), _I32, block_table)
+    st = lib().fa_pages_fork(_ptr(block_table), _ptr(seqlens), _ptr(parents), _ptr(free_pages), free_pages.shape[0],
+                             _ptr(shares), _ptr(table_out), _ptr(lens_out), _ptr(copy_src), _ptr(copy_dst),
+                             _ptr(pages_used), B, n, max_pages, 16, P, _stream(block_table))
+    check(st, "fa_pages_fork")
+    return table_out, lens_out, copy_src, copy_dst, pages_used
+
+
+def fa_pages_copy(k_pages, v_pages, src, dst, count=None):
+    """Pages dst [n] of the pools [P][16][Hkv][d] or [layers][P][16][Hkv][d] get what pages src [n] hold, bf16; pairs with
+    a -1, and those from count [1] on where it is given, are passed over. In place."""
+    got = fast().pages_copy(k_pages, v_pages, src, dst, count)
+    if got is not None:
+        if got is not True:
+            _answer(got, "fa_pages_copy")
+        return
+    ndim = k_pages.dim() if isinstance(k_pages, torch.Tensor) else 4
+    _need(k_pages, "k_pages", _BF16, 5 if ndim == 5 else 4)
+    _need(v_pages, "v_pages", _BF16, ndim)
+    dev = k_pages.device
+    _on_current_device(k_pages)
+    if tuple(v_pages.shape) != tuple(k_pages.shape) or v_pages.device != dev:
+        raise ValueError(f"k_pages and v_pages must have one shape on {dev}")
+    _need(src, "src", _I32, 1)
+    _need_ints("src", src, tuple(src.shape), dev)
+    _need_ints("dst", dst, tuple(src.shape), dev)
+    if count is not None and (not isinstance(count, torch.Tensor) or count.dtype != _I32 or count.device != dev
+                              or count.numel() < 1 or not count.is_contiguous()):
+        raise ValueError(f"count must be a contiguous int32 tensor on {dev}, its first value the number of pairs")
+    if src.shape[0] == 0:
+        return
+    layers = k_pages.shape[0] if ndim == 5 else 1
+    P, page_size, Hkv, d = k_pages.shape[-4:]
+    st = lib().fa_pages_copy(_ptr(k_pages), _ptr(v_pages), _ptr(src), _ptr(dst), _ptr(count), src.shape[0], layers, P,
+                             page_size, Hkv, d, _stream(k_pages))
+    check(st, "fa_pages_copy")
+
+
+def fa_pages_free(block_table, seqlens, shares, rows=None, shares_out=None, freed=None, num_freed=None):
+    """The pages of rows [n] of the table (None: all) that no other row holds: shares [P] counted down, in place or into
+    shares_out -> (freed [min(P, n * max_pages)] ascending, -1 behind them, num_freed [1]), int32."""
+    if freed is None and num_freed is None:
+        got = fast().pages_free(block_table, seqlens, shares, rows, shares_out)
+        if got is not None:
+            return _answer(got, "fa_pages_free")
+    _need(shares, "shares", _I32, 1)
+    B, max_pages, dev = _need_table(block_table, seqlens, shares)
+    n, P = B, shares.shape[0]
+    if rows is not None:
+        _need(rows, "rows", _I32, 1)
+        n = rows.shape[0]
+        if rows.device != dev:
+            raise ValueError(f"rows must be on {dev}")
+    if P > FA_PAGES_MAX:
+        check(FA_ERR_UNSUPPORTED, "fa_pages_free")
+    shares_out = shares if shares_out is None else _out(shares_out, "shares_out", (P,), _I32, block_table)
+    freed = _out(freed, "freed", (min(P, n * max_pages),), _I32, block_table)
+    num_freed = _out(num_freed, "num_freed", (1,), _I32, block_table)
+    st = lib().fa_pages_free(_ptr(block_table), _ptr(seqlens), _ptr(rows), _ptr(shares), _ptr(shares_out), _ptr(freed),
+                             _ptr(num_freed), B, n, max_pages, 16, P, _stream(block_table))
+    check(st, "fa_pages_free")
+    return freed, num_freed
+
+
+def fa_pages_compact(block_table, seqlens, shares, first: int = 0, table_out=None, shares_out=None, copy_src=None,
+                     copy_dst=None, counts=None):
+    """The live pages of a pool from page first on moved to first, first + 1, ..: the table and shares [P] are rewritten, in
+    place or into table_out and shares_out -> (copy_src, copy_dst [min((P - first) // 2, B * max_pages)] for fa_pages_copy,
+    -1 behind the moves, counts [2]: moves, live pages), int32."""
+    if copy_src is None and copy_dst is None and counts is None:
+        got = fast().pages_compact(block_table, seqlens, shares, first, table_out, shares_out)
+        if got is not None:
+            return _answer(got, "fa_pages_compact")
+    _need(shares, "shares", _I32, 1)
+    B, max_pages, dev = _need_table(block_table, seqlens, shares)
+    P, first = shares.shape[0], int(first)
+    if P > FA_PAGES_MAX:
+        check(FA_ERR_UNSUPPORTED, "fa_pages_compact")
+    if not 0 <= first < max(P, 1):
+        raise ValueError(f"first must be in [0, {P}), got {first}")
+    table_out = block_table if table_out is None else _out(table_out, "table_out", (B, max_pages), _I32, block_table)
+    shares_out = shares if shares_out is None else _out(shares_out, "shares_out", (P,), _I32, block_table)
+    cap = min((P - first) // 2, B * max_pages)
+    copy_src = _out(copy_src, "copy_src", (cap,), _I32, block_table)
+    copy_dst = _out(copy_dst, "copy_dst", (cap,), _I32, block_table)
+    counts = _out(counts, "counts", (2,), _I32, block_table)
+    st = lib().fa_pages_compact(_ptr(block_table), _ptr(seqlens), _ptr(shares), _ptr(table_out), _ptr(shares_out),
+                                _ptr(copy_src), _ptr(copy_dst), _ptr(counts), B, max_pages, 16, P, first,
+                                _stream(block_table))
+    check(st, "fa_pages_compact")
+    return copy_src, copy_dst, counts
 
 
 def fa_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, max_pages: int, d: int,
@@ -608,6 +793,14 @@ __all__ = [
     "fa_rope",
     "fa_rope_bwd",
     "fa_rope_append_paged",
+    "fa_rope_pair_axis",
+    "fa_rope_axes",
+    "fa_rope_axes_bwd",
+    "fa_rope_axes_append_paged",
+    "fa_pages_fork",
+    "fa_pages_copy",
+    "fa_pages_free",
+    "fa_pages_compact",
     "fa_tree_decode_paged",
     "fa_tree_workspace_bytes",
     "fa_get_last_device_error",

@@ -41,6 +41,17 @@ enum ErrSite : unsigned {
   SITE_TR_SOFTMAX = 21,
   SITE_TR_TABLE = 22,
   SITE_TR_SMEM = 23,
+  SITE_PAGES_FORK = 24,
+  SITE_PAGES_COPY = 25,
+  SITE_PAGES_FREE = 26,
+  SITE_PAGES_COMPACT = 27,
+  SITE_ROPE_AXIS = 28,
+  SITE_PX_PRODUCER = 29,
+  SITE_PX_MMA = 30,
+  SITE_PX_SOFTMAX = 31,
+  SITE_PX_TABLE = 32,
+  SITE_PX_GROUPS = 33,
+  SITE_PX_SMEM = 34,
 };
 
 __device__ __forceinline__ void record_error(unsigned* err, unsigned code, unsigned site) {

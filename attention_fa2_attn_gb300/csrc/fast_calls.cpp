@@ -190,11 +190,16 @@ PyObject* tree_mask(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-bool angles(const Tensor& positions, const Tensor& inv_freq, int64_t B, int64_t T, int dev, bool* shared) {
-  *shared = positions.dim() == 1;
-  return dense(positions, at::kInt, *shared ? 1 : 2, dev) && dense(inv_freq, at::kDouble, 1, dev) &&
-         (*shared || positions.size(0) == B) && positions.size(positions.dim() - 1) == T &&
-         inv_freq.size(0) <= INT_MAX / 2;
+// Positions [B][T] or [T], with the pairs' axes [axes][B][T] or [axes][T].
+bool angles(const Tensor& positions, const Tensor& inv_freq, const Tensor* axis, int64_t B, int64_t T, int dev,
+            bool* shared) {
+  const int front = axis ? 1 : 0;
+  *shared = positions.dim() == 1 + front;
+  return dense(positions, at::kInt, (*shared ? 1 : 2) + front, dev) && dense(inv_freq, at::kDouble, 1, dev) &&
+         (*shared || positions.size(front) == B) && positions.size(positions.dim() - 1) == T &&
+         inv_freq.size(0) <= INT_MAX / 2 &&
+         (!axis || (dense(*axis, at::kInt, 1, dev) && axis->size(0) == inv_freq.size(0) && positions.size(0) >= 1 &&
+                    positions.size(0) <= FA_ROPE_MAX_AXES));
 }
 
 // A caller's output for rows like `like`, no two of its rows on one another.
@@ -212,14 +217,14 @@ bool rows_out(const Tensor& t, const Tensor& like, int dev) {
   return true;
 }
 
-// (q, k or None, positions, inv_freq, interleaved, mscale, backward, q_out or None, k_out or None)
+// (q, k or None, positions, inv_freq, interleaved, mscale, backward, q_out or None, k_out or None[, pair_axis])
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const Tensor *q, *k = nullptr, *positions, *inv_freq;
   bool inter = false, back = false, shared = false;
   float mscale = 1.f;
-  const Tensor *q_out = nullptr, *k_out = nullptr;
-  if (n != 9 || !(q = tensor_of(a[0])) || (a[1] != Py_None && !(k = tensor_of(a[1]))) ||
+  const Tensor *q_out = nullptr, *k_out = nullptr, *axis = nullptr;
+  if ((n != 9 && n != 10) || (n == 10 && !(axis = tensor_of(a[9]))) || !(q = tensor_of(a[0])) || (a[1] != Py_None && !(k = tensor_of(a[1]))) ||
       (a[7] != Py_None && !(q_out = tensor_of(a[7]))) || (a[8] != Py_None && !(k_out = tensor_of(a[8]))) ||
       !(positions = tensor_of(a[2])) || !(inv_freq = tensor_of(a[3])) || !flag_of(a[4], &inter) ||
       !float_of(a[5], &mscale) || !flag_of(a[6], &back))
@@ -229,7 +234,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if ((type != at::kBFloat16 && type != at::kFloat) || !rows(*q, type, dev) || (k && !rows(*k, type, dev)))
     Py_RETURN_NONE;
   const int64_t B = q->size(0), H = q->size(1), T = q->size(2), d = q->size(3), Hk = k ? k->size(1) : 0;
-  if (!angles(*positions, *inv_freq, B, T, dev, &shared) ||
+  if (!angles(*positions, *inv_freq, axis, B, T, dev, &shared) ||
       (k && (k->size(0) != B || k->size(2) != T || k->size(3) != d || Hk < 1)))
     Py_RETURN_NONE;
   if ((q_out && !rows_out(*q_out, *q, dev)) || (k_out && !(k && rows_out(*k_out, *k, dev)))) Py_RETURN_NONE;
@@ -242,12 +247,17 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long s[12] = {q->stride(0),  q->stride(1),  q->stride(2),  qo.stride(0), qo.stride(1), qo.stride(2),
                              k ? k->stride(0) : 0, k ? k->stride(1) : 0, k ? k->stride(2) : 0,
                              k ? ko.stride(0) : 0, k ? ko.stride(1) : 0, k ? ko.stride(2) : 0};
-    st = (back ? fa_rope_bwd : fa_rope)(
-        q->const_data_ptr(), k ? k->const_data_ptr() : nullptr, qo.mutable_data_ptr(),
-        k ? ko.mutable_data_ptr() : nullptr, s, ints(*positions), shared,
-        static_cast<const double*>(inv_freq->const_data_ptr()), static_cast<int>(B), static_cast<int>(H),
-        static_cast<int>(Hk), static_cast<int>(T), static_cast<int>(d), static_cast<int>(2 * inv_freq->size(0)), inter,
-        mscale, type == at::kFloat ? FA_DTYPE_F32 : FA_DTYPE_BF16, stream_of(dev));
+    const void *from_q = q->const_data_ptr(), *from_k = k ? k->const_data_ptr() : nullptr;
+    void *to_q = qo.mutable_data_ptr(), *to_k = k ? ko.mutable_data_ptr() : nullptr;
+    const double* freq = static_cast<const double*>(inv_freq->const_data_ptr());
+    const int b = static_cast<int>(B), h = static_cast<int>(H), hk = static_cast<int>(Hk), t = static_cast<int>(T),
+              dim = static_cast<int>(d), rot = static_cast<int>(2 * inv_freq->size(0)),
+              dtype = type == at::kFloat ? FA_DTYPE_F32 : FA_DTYPE_BF16;
+    st = axis ? (back ? fa_rope_axes_bwd : fa_rope_axes)(from_q, from_k, to_q, to_k, s, ints(*positions), shared, freq,
+                                                         ints(*axis), static_cast<int>(positions->size(0)), b, h, hk, t,
+                                                         dim, rot, inter, mscale, dtype, stream_of(dev))
+              : (back ? fa_rope_bwd : fa_rope)(from_q, from_k, to_q, to_k, s, ints(*positions), shared, freq, b, h, hk,
+                                               t, dim, rot, inter, mscale, dtype, stream_of(dev));
   }
   if (k || st != FA_OK) return answer(st, {qo, ko});
   PyObject* w = THPVariable_Wrap(qo);
@@ -258,14 +268,14 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out or None)
+// (q, k, v, positions, slots, inv_freq, k_pages, v_pages, interleaved, mscale, q_out or None[, pair_axis])
 PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   const Tensor* t[8];
   bool inter = false, shared = false;
   float mscale = 1.f;
-  const Tensor* q_out = nullptr;
-  if (n != 11 || !flag_of(a[8], &inter) || !float_of(a[9], &mscale) ||
+  const Tensor *q_out = nullptr, *axis = nullptr;
+  if ((n != 11 && n != 12) || (n == 12 && !(axis = tensor_of(a[11]))) || !flag_of(a[8], &inter) || !float_of(a[9], &mscale) ||
       (a[10] != Py_None && !(q_out = tensor_of(a[10]))))
     Py_RETURN_NONE;
   for (int i = 0; i < 8; ++i)
@@ -277,7 +287,7 @@ PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !dense(kp, at::kBFloat16, 4, dev) || !dense(vp, at::kBFloat16, 4, dev) || !dense(slots, at::kInt, 2, dev))
     Py_RETURN_NONE;
   const int64_t B = q.size(0), H = q.size(1), T = q.size(2), d = q.size(3), P = kp.size(0), Hkv = kp.size(2);
-  if (!angles(positions, inv_freq, B, T, dev, &shared) || shared || !same_sizes(slots, positions) ||
+  if (!angles(positions, inv_freq, axis, B, T, dev, &shared) || shared || slots.size(0) != B || slots.size(1) != T ||
       !same_sizes(k, v) || !same_sizes(kp, vp) || k.size(0) != B || k.size(1) != Hkv || k.size(2) != T ||
       k.size(3) != d || kp.size(3) != d || !fits(P) || !fits(kp.size(1)))
     Py_RETURN_NONE;
@@ -289,12 +299,19 @@ PyObject* rope_append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     qo = q_out ? *q_out : make({B, H, T, d}, at::kBFloat16, dev);
     const long long s[12] = {q.stride(0), q.stride(1), q.stride(2), qo.stride(0), qo.stride(1), qo.stride(2),
                              k.stride(0), k.stride(1), k.stride(2), v.stride(0),  v.stride(1),  v.stride(2)};
-    st = fa_rope_append_paged(
-        q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.mutable_data_ptr(), s, ints(positions),
-        ints(slots), static_cast<const double*>(inv_freq.const_data_ptr()), kp.mutable_data_ptr(),
-        vp.mutable_data_ptr(), static_cast<int>(B), static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(T),
-        static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), static_cast<int>(2 * inv_freq.size(0)),
-        inter, mscale, stream_of(dev));
+    const double* freq = static_cast<const double*>(inv_freq.const_data_ptr());
+    const int b = static_cast<int>(B), h = static_cast<int>(H), hkv = static_cast<int>(Hkv), t = static_cast<int>(T),
+              page = static_cast<int>(kp.size(1)), pages = static_cast<int>(P), dim = static_cast<int>(d),
+              rot = static_cast<int>(2 * inv_freq.size(0));
+    st = axis ? fa_rope_axes_append_paged(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(),
+                                          qo.mutable_data_ptr(), s, ints(positions), ints(slots), freq, ints(*axis),
+                                          static_cast<int>(positions.size(0)), kp.mutable_data_ptr(),
+                                          vp.mutable_data_ptr(), b, h, hkv, t, page, pages, dim, rot, inter, mscale,
+                                          stream_of(dev))
+              : fa_rope_append_paged(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qo.mutable_data_ptr(),
+                                     s, ints(positions), ints(slots), freq, kp.mutable_data_ptr(),
+                                     vp.mutable_data_ptr(), b, h, hkv, t, page, pages, dim, rot, inter, mscale,
+                                     stream_of(dev));
   }
   return answer(st, {qo});
   END_HANDLE_TH_ERRORS
@@ -347,9 +364,131 @@ PyObject* tree_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A block table with its lengths, and the shares of the pool's pages.
+bool shared_table(const Tensor& table, const Tensor& seqlens, const Tensor& shares, int dev) {
+  return dense(table, at::kInt, 2, dev) && dense(seqlens, at::kInt, 1, dev) && dense(shares, at::kInt, 1, dev) &&
+         seqlens.size(0) == table.size(0) && fits(table.size(0)) && fits(table.size(1)) && fits(shares.size(0));
+}
+
+// (block_table, seqlens, parents, free_pages, shares)
+PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const Tensor* t[5];
+  if (n != 5) Py_RETURN_NONE;
+  for (int i = 0; i < 5; ++i)
+    if (!(t[i] = tensor_of(a[i]))) Py_RETURN_NONE;
+  const Tensor &table = *t[0], &seqlens = *t[1], &parents = *t[2], &free_pages = *t[3], &shares = *t[4];
+  const int dev = device_for(table);
+  if (!shared_table(table, seqlens, shares, dev) || !dense(parents, at::kInt, 1, dev) ||
+      !dense(free_pages, at::kInt, 1, dev))
+    Py_RETURN_NONE;
+  const int64_t B = table.size(0), pages = table.size(1), N = parents.size(0), F = free_pages.size(0);
+  if (!fits(N) || !fits(F) || !fits(N * pages)) Py_RETURN_NONE;  // refused before its outputs are made
+  std::array<Tensor, 5> out;  // table, lengths, sources, destinations, pages used
+  fa_status st;
+  {
+    NoInterpreter released;
+    out = make_ints<5>({{{N, pages, 0}, {N, 0, 0}, {N, 0, 0}, {N, 0, 0}, {1, 0, 0}}}, {2, 1, 1, 1, 1}, dev);
+    st = fa_pages_fork(ints(table), ints(seqlens), ints(parents), ints(free_pages), static_cast<int>(F),
+                       ints_out(shares), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]), ints_out(out[3]),
+                       ints_out(out[4]), static_cast<int>(B), static_cast<int>(N), static_cast<int>(pages), 16,
+                       static_cast<int>(shares.size(0)), stream_of(dev));
+  }
+  return answer(st, {out[0], out[1], out[2], out[3], out[4]});
+  END_HANDLE_TH_ERRORS
+}
+
+// (k_pages, v_pages, src, dst, count or None) -> True
+PyObject* pages_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const Tensor* t[4];
+  const Tensor* count = nullptr;
+  if (n != 5 || (a[4] != Py_None && !(count = tensor_of(a[4])))) Py_RETURN_NONE;
+  for (int i = 0; i < 4; ++i)
+    if (!(t[i] = tensor_of(a[i]))) Py_RETURN_NONE;
+  const Tensor &kp = *t[0], &vp = *t[1], &src = *t[2], &dst = *t[3];
+  const int dev = device_for(kp);
+  const int dim = static_cast<int>(kp.dim());
+  if ((dim != 4 && dim != 5) || !dense(kp, at::kBFloat16, dim, dev) || !dense(vp, at::kBFloat16, dim, dev) ||
+      !same_sizes(kp, vp) || !dense(src, at::kInt, 1, dev) || !dense(dst, at::kInt, 1, dev) || !same_sizes(src, dst) ||
+      (count && (count->dim() < 1 || !dense(*count, at::kInt, static_cast<int>(count->dim()), dev) || count->numel() < 1)))
+    Py_RETURN_NONE;
+  for (int i = 0; i < dim; ++i)
+    if (!fits(kp.size(i))) Py_RETURN_NONE;
+  if (src.size(0) < 1 || !fits(src.size(0))) Py_RETURN_NONE;
+  fa_status st;
+  {
+    NoInterpreter released;
+    st = fa_pages_copy(kp.mutable_data_ptr(), vp.mutable_data_ptr(), ints(src), ints(dst), count ? ints(*count) : nullptr,
+                       static_cast<int>(src.size(0)), dim == 5 ? static_cast<int>(kp.size(0)) : 1,
+                       static_cast<int>(kp.size(dim - 4)), static_cast<int>(kp.size(dim - 3)),
+                       static_cast<int>(kp.size(dim - 2)), static_cast<int>(kp.size(dim - 1)), stream_of(dev));
+  }
+  if (st != FA_OK) return PyLong_FromLong(st);
+  Py_RETURN_TRUE;
+  END_HANDLE_TH_ERRORS
+}
+
+// (block_table, seqlens, shares, rows or None, shares_out or None)
+PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const Tensor *table, *seqlens, *shares, *rows_in = nullptr, *after = nullptr;
+  if (n != 5 || !(table = tensor_of(a[0])) || !(seqlens = tensor_of(a[1])) || !(shares = tensor_of(a[2])) ||
+      (a[3] != Py_None && !(rows_in = tensor_of(a[3]))) || (a[4] != Py_None && !(after = tensor_of(a[4]))))
+    Py_RETURN_NONE;
+  const int dev = device_for(*table);
+  if (!shared_table(*table, *seqlens, *shares, dev) || (rows_in && !dense(*rows_in, at::kInt, 1, dev)) ||
+      (after && (!dense(*after, at::kInt, 1, dev) || !same_sizes(*after, *shares))))
+    Py_RETURN_NONE;
+  const int64_t B = table->size(0), pages = table->size(1), P = shares->size(0), N = rows_in ? rows_in->size(0) : B;
+  if (!fits(N) || P > FA_PAGES_MAX) Py_RETURN_NONE;
+  std::array<Tensor, 2> out;  // freed pages, their number
+  fa_status st;
+  {
+    NoInterpreter released;
+    out = make_ints<2>({{{std::min(P, N * pages), 0, 0}, {1, 0, 0}}}, {1, 1}, dev);
+    st = fa_pages_free(ints(*table), ints(*seqlens), rows_in ? ints(*rows_in) : nullptr, ints(*shares),
+                       ints_out(after ? *after : *shares), ints_out(out[0]), ints_out(out[1]), static_cast<int>(B),
+                       static_cast<int>(N), static_cast<int>(pages), 16, static_cast<int>(P), stream_of(dev));
+  }
+  return answer(st, {out[0], out[1]});
+  END_HANDLE_TH_ERRORS
+}
+
+// (block_table, seqlens, shares, first, table_out or None, shares_out or None)
+PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const Tensor *table, *seqlens, *shares, *table_out = nullptr, *after = nullptr;
+  int first = 0;
+  if (n != 6 || !(table = tensor_of(a[0])) || !(seqlens = tensor_of(a[1])) || !(shares = tensor_of(a[2])) ||
+      !int_of(a[3], &first) || (a[4] != Py_None && !(table_out = tensor_of(a[4]))) ||
+      (a[5] != Py_None && !(after = tensor_of(a[5]))))
+    Py_RETURN_NONE;
+  const int dev = device_for(*table);
+  if (!shared_table(*table, *seqlens, *shares, dev) ||
+      (table_out && (!dense(*table_out, at::kInt, 2, dev) || !same_sizes(*table_out, *table))) ||
+      (after && (!dense(*after, at::kInt, 1, dev) || !same_sizes(*after, *shares))))
+    Py_RETURN_NONE;
+  const int64_t B = table->size(0), pages = table->size(1), P = shares->size(0);
+  if (P > FA_PAGES_MAX || first < 0 || first >= P) Py_RETURN_NONE;
+  std::array<Tensor, 3> out;  // sources, destinations, counts
+  fa_status st;
+  {
+    NoInterpreter released;
+    const int64_t cap = std::min((P - first) / 2, B * pages);
+    out = make_ints<3>({{{cap, 0, 0}, {cap, 0, 0}, {2, 0, 0}}}, {1, 1, 1}, dev);
+    st = fa_pages_compact(ints(*table), ints(*seqlens), ints(*shares), ints_out(table_out ? *table_out : *table),
+                          ints_out(after ? *after : *shares), ints_out(out[0]), ints_out(out[1]), ints_out(out[2]),
+                          static_cast<int>(B), static_cast<int>(pages), 16, static_cast<int>(P), first, stream_of(dev));
+  }
+  return answer(st, {out[0], out[1], out[2]});
+  END_HANDLE_TH_ERRORS
+}
+
 #define FA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FA_METHOD(paged_plan), FA_METHOD(tree_mask), FA_METHOD(rope), FA_METHOD(rope_append_paged),
-                         FA_METHOD(tree_decode_paged), {nullptr, nullptr, 0, nullptr}};
+                         FA_METHOD(tree_decode_paged), FA_METHOD(pages_fork), FA_METHOD(pages_copy),
+                         FA_METHOD(pages_free), FA_METHOD(pages_compact), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "Step calls from Python objects to the C ABI.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

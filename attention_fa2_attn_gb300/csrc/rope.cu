@@ -5,7 +5,8 @@
 //   (a cos t - b sin t, b cos t + a sin t) * mscale,  t = p * inv_freq[i];
 // the gradient is the transpose, the same with -t. Pairs are (x[i], x[i + rot/2])
 // ("half") or (x[2i], x[2i+1]) ("interleaved"), i < rot/2; values from rot on pass
-// through.
+// through. With several axes (time, height, width) a token has a position on each, and
+// p is the one on pair i's axis: the same kernel, with one more load for each angle.
 //
 // Angles. A far position needs t to a small part of 2 pi, which p * inv_freq in 32
 // bits has not (at p = 10^6 it is off by 0.06). Here inv_freq / (2 pi) is a 64-bit
@@ -49,6 +50,9 @@ struct RopeParams {
   RopeSide q, k, v;         // v.heads = 0 but for appends
   const int* positions;
   long long pos_sb;         // 0: one row of positions for the whole batch
+  const int* axis;          // of each pair; null: one axis
+  long long axis_stride;    // from an axis' positions to the next's
+  int axes;
   const double* inv_freq;
   const int* slots;         // appends: k and v rows go to slot * slot_stride + head * d
   long long slot_stride;
@@ -196,11 +200,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopePara
   }
 
   if (turn && there) {
-    const long long pos = __ldg(p.positions + b * p.pos_sb + t);
+    const int* at_token = p.positions + b * p.pos_sb + t;
+    const long long only = p.axis ? 0 : __ldg(at_token);
     for (int e = warp; e < VEC; e += kRopeWarps) {
       // interleaved: half of the lane's pairs are in its first vector, half in its second
       const int pair = !INTER || ADJ ? lane * VEC + e
                                      : (2 * e < VEC ? o0 / 2 + e : o1 / 2 + e - VEC / 2);
+      long long pos = only;
+      if (p.axis) {
+        const int ax = __ldg(p.axis + pair);
+        if (ax >= 0 && ax < p.axes)
+          pos = __ldg(at_token + ax * p.axis_stride);
+        else
+          record_error(p.err, FA_ERR_BOUNDS, SITE_ROPE_AXIS);  // such a pair stays at position 0
+      }
       unsigned long long a;
       const bool angle = turns_of(__ldg(p.inv_freq + pair), a);
       a *= static_cast<unsigned long long>(pos);
@@ -333,17 +346,43 @@ static Rows rows_of(const void* at, long long sb, long long sh, long long st, in
   return Rows{at, {sb * elem, sh * elem, st * elem}, {B, heads, T}, static_cast<long long>(d) * elem};
 }
 
+// What turns the rows: positions and angles, and the pairs' axes where there are several.
+struct RopeTurn {
+  const int* positions;
+  int shared;
+  const double* inv_freq;
+  const int* axis;  // null: one axis
+  int axes;
+  int B, T, rot;
+  long long axis_stride() const { return shared ? T : static_cast<long long>(B) * T; }
+  Rows pos_rows() const { return dense_rows(positions, 4 * axis_stride() * (axis ? axes : 1)); }
+  Rows freq_rows() const { return dense_rows(inv_freq, 4ll * rot); }
+  Rows axis_rows() const { return dense_rows(axis, 2ll * rot); }
+  bool met_by(const Rows& rows) const {
+    return rows_meet(rows, pos_rows()) || rows_meet(rows, freq_rows()) || rows_meet(rows, axis_rows());
+  }
+  void give(RopeParams& p) const {
+    p.positions = positions;
+    p.pos_sb = shared ? 0 : T;
+    p.inv_freq = inv_freq;
+    p.axis = axis;
+    p.axes = axes;
+    p.axis_stride = axis_stride();
+    p.tokens = static_cast<long long>(B) * T;
+    p.T = T;
+    p.rot = rot;
+  }
+};
+
 // Whether a row of an output lies on one of another operand, or on another of its own: rows
 // would be written that others still read. In place (a destination that is its source, stride
 // for stride) is fine.
-static bool outputs_meet(const RopeSide& q, const RopeSide& k, int B, int T, int d, unsigned elem,
-                         const int* positions, long long pos_bytes, const double* inv_freq, long long freq_bytes) {
+static bool outputs_meet(const RopeSide& q, const RopeSide& k, int B, int T, int d, unsigned elem, const RopeTurn& turn) {
   auto src = [&](const RopeSide& s) { return rows_of(s.src, s.sb, s.sh, s.st, B, s.heads, T, d, elem); };
   auto dst = [&](const RopeSide& s) { return rows_of(s.dst, s.db, s.dh, s.dt, B, s.heads, T, d, elem); };
   auto in_place = [](const RopeSide& s) { return s.src == s.dst && s.sb == s.db && s.sh == s.dh && s.st == s.dt; };
   auto bad = [&](const RopeSide& s) {
-    return (!in_place(s) && rows_meet(src(s), dst(s))) || rows_meet_themselves(dst(s)) ||
-           rows_meet(dst(s), dense_rows(positions, pos_bytes)) || rows_meet(dst(s), dense_rows(inv_freq, freq_bytes));
+    return (!in_place(s) && rows_meet(src(s), dst(s))) || rows_meet_themselves(dst(s)) || turn.met_by(dst(s));
   };
   return bad(q) || (k.heads > 0 && (bad(k) || rows_meet(dst(q), dst(k)) || rows_meet(dst(q), src(k)) ||
                                     rows_meet(src(q), dst(k))));
@@ -358,46 +397,93 @@ static bool span_meets(const void* rows, long long sb, long long sh, long long s
   return overlap(static_cast<const char*>(rows) + lo * elem, (hi - lo) * elem, at, bytes);
 }
 
-static fa_status check_rope(const void* q, const void* q_out, const int* positions, const double* inv_freq, int B,
-                            int Hq, int Hk, int T, int d, int rot_dim, float mscale, unsigned elem) {
-  if (!q || !q_out || !positions || !inv_freq) return FA_ERR_INVALID_ARG;
-  if (misaligned(q, elem) || misaligned(q_out, elem) || misaligned(positions, 4) || misaligned(inv_freq, 8))
+static fa_status check_rope(const void* q, const void* q_out, const RopeTurn& turn, int B, int Hq, int Hk, int T, int d,
+                            int rot_dim, float mscale, unsigned elem) {
+  if (!q || !q_out || !turn.positions || !turn.inv_freq) return FA_ERR_INVALID_ARG;
+  if (misaligned(q, elem) || misaligned(q_out, elem) || misaligned(turn.positions, 4) || misaligned(turn.inv_freq, 8) ||
+      misaligned(turn.axis, 4))
     return FA_ERR_INVALID_ARG;
+  if (turn.axes < 1) return FA_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hk < 0 || T < 1 || d < 2 || rot_dim < 2 || (rot_dim & 1) || rot_dim > d)
     return FA_ERR_INVALID_ARG;
   if (!isfinite(mscale) || mscale <= 0.f) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * T >= (1ll << 31) || d > 1024 || Hq > 65535 || Hk > 65535) return FA_ERR_UNSUPPORTED;
+  if (turn.axes > FA_ROPE_MAX_AXES) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
 static fa_status rope_any(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
-                          const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk,
-                          int T, int d, int rot_dim, int interleaved, float mscale, int dtype, float sign,
-                          void* stream) {
+                          const RopeTurn& turn, int B, int Hq, int Hk, int T, int d, int rot_dim, int interleaved,
+                          float mscale, int dtype, float sign, void* stream) {
   if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_F32) return FA_ERR_UNSUPPORTED;
   const unsigned elem = dtype == FA_DTYPE_F32 ? 4 : 2;
-  const fa_status st = check_rope(q, q_out, positions, inv_freq, B, Hq, Hk, T, d, rot_dim, mscale, elem);
+  const fa_status st = check_rope(q, q_out, turn, B, Hq, Hk, T, d, rot_dim, mscale, elem);
   if (st != FA_OK) return st;
   if (!strides || (Hk > 0 && (!k || !k_out || misaligned(k, elem) || misaligned(k_out, elem))))
     return FA_ERR_INVALID_ARG;
   RopeParams p = {};
   p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
   if (Hk > 0) p.k = side_of(k, k_out, strides + 6, strides + 9, B, Hk, T);
-  if (outputs_meet(p.q, p.k, B, T, d, elem, positions, 4ll * T * (positions_shared ? 1 : B), inv_freq, 4ll * rot_dim))
-    return FA_ERR_INVALID_ARG;
-  p.positions = positions;
-  p.pos_sb = positions_shared ? 0 : T;
-  p.inv_freq = inv_freq;
-  p.tokens = static_cast<long long>(B) * T;
-  p.T = T;
+  if (outputs_meet(p.q, p.k, B, T, d, elem, turn)) return FA_ERR_INVALID_ARG;
+  turn.give(p);
   p.d = d;
-  p.rot = rot_dim;
   p.mscale = mscale;
   p.sign = sign;
+  if (turn.axis) {
+    p.err = device_error_word();
+    if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  }
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int rc = dtype == FA_DTYPE_F32 ? launch_rope<float, false>(p, interleaved != 0, cs)
                                        : launch_rope<__nv_bfloat16, false>(p, interleaved != 0, cs);
   return static_cast<fa_status>(rc);
+}
+
+static fa_status append_any(const void* q, const void* k, const void* v, void* q_out, const long long* strides,
+                            const RopeTurn& turn, const int* slots, void* k_pages, void* v_pages, int B, int Hq, int Hkv,
+                            int T, int page_size, int num_pages, int d, int rot_dim, int interleaved, float mscale,
+                            void* stream) {
+  const fa_status st = check_rope(q, q_out, turn, B, Hq, Hkv, T, d, rot_dim, mscale, 2);
+  if (st != FA_OK) return st;
+  if (!strides || !k || !v || !slots || !k_pages || !v_pages || Hkv < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(k_pages, 16) ||
+      misaligned(v_pages, 16))
+    return FA_ERR_INVALID_ARG;
+  if (page_size != 16 || static_cast<long long>(num_pages) * 16 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  const long long pool = 32ll * num_pages * Hkv * d;
+  if (overlap(k_pages, pool, v_pages, pool)) return FA_ERR_INVALID_ARG;
+  RopeParams p = {};
+  p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
+  p.k = side_of(k, k_pages, strides + 6, nullptr, B, Hkv, T);
+  p.v = side_of(v, v_pages, strides + 9, nullptr, B, Hkv, T);
+  {
+    // rows go to any slot while others are still read; q_out may be q and nothing else
+    const Rows of_slots = dense_rows(slots, 4ll * B * T);
+    const Rows out = rows_of(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2);
+    if (outputs_meet(p.q, RopeSide{}, B, T, d, 2, turn) ||
+        rows_meet(out, rows_of(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2)) ||
+        rows_meet(out, rows_of(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2)) || rows_meet(out, of_slots))
+      return FA_ERR_INVALID_ARG;
+    for (const void* pages : {k_pages, v_pages}) {
+      const Rows pool_rows = dense_rows(pages, pool);
+      if (span_meets(q, p.q.sb, p.q.sh, p.q.st, B, Hq, T, d, 2, pages, pool) ||
+          span_meets(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2, pages, pool) ||
+          span_meets(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2, pages, pool) ||
+          span_meets(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2, pages, pool) || turn.met_by(pool_rows) ||
+          rows_meet(of_slots, pool_rows))
+        return FA_ERR_INVALID_ARG;
+    }
+  }
+  turn.give(p);
+  p.slots = slots;
+  p.slot_stride = static_cast<long long>(Hkv) * d;
+  p.num_slots = num_pages * 16;
+  p.d = d;
+  p.mscale = mscale;
+  p.sign = 1.f;
+  p.err = device_error_word();
+  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  return static_cast<fa_status>(launch_rope<__nv_bfloat16, true>(p, interleaved != 0, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace fa
@@ -447,14 +533,33 @@ fa_status fa_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, double 
 fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
                   const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk, int T,
                   int d, int rot_dim, int interleaved, float mscale, int dtype, void* stream) {
-  return rope_any(q, k, q_out, k_out, strides, positions, positions_shared, inv_freq, B, Hq, Hk, T, d, rot_dim,
-                  interleaved, mscale, dtype, 1.f, stream);
+  return rope_any(q, k, q_out, k_out, strides, {positions, positions_shared, inv_freq, nullptr, 1, B, T, rot_dim}, B, Hq,
+                  Hk, T, d, rot_dim, interleaved, mscale, dtype, 1.f, stream);
 }
 
 fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const long long* strides,
                       const int* positions, int positions_shared, const double* inv_freq, int B, int Hq, int Hk,
                       int T, int d, int rot_dim, int interleaved, float mscale, int dtype, void* stream) {
-  return rope_any(dq_out, dk_out, dq, dk, strides, positions, positions_shared, inv_freq, B, Hq, Hk, T, d, rot_dim,
+  return rope_any(dq_out, dk_out, dq, dk, strides, {positions, positions_shared, inv_freq, nullptr, 1, B, T, rot_dim}, B,
+                  Hq, Hk, T, d, rot_dim, interleaved, mscale, dtype, -1.f, stream);
+}
+
+fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                       const int* positions, int positions_shared, const double* inv_freq, const int* pair_axis,
+                       int axes, int B, int Hq, int Hk, int T, int d, int rot_dim, int interleaved, float mscale,
+                       int dtype, void* stream) {
+  if (!pair_axis) return FA_ERR_INVALID_ARG;
+  return rope_any(q, k, q_out, k_out, strides, {positions, positions_shared, inv_freq, pair_axis, axes, B, T, rot_dim}, B,
+                  Hq, Hk, T, d, rot_dim, interleaved, mscale, dtype, 1.f, stream);
+}
+
+fa_status fa_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const long long* strides,
+                           const int* positions, int positions_shared, const double* inv_freq, const int* pair_axis,
+                           int axes, int B, int Hq, int Hk, int T, int d, int rot_dim, int interleaved, float mscale,
+                           int dtype, void* stream) {
+  if (!pair_axis) return FA_ERR_INVALID_ARG;
+  return rope_any(dq_out, dk_out, dq, dk, strides,
+                  {positions, positions_shared, inv_freq, pair_axis, axes, B, T, rot_dim}, B, Hq, Hk, T, d, rot_dim,
                   interleaved, mscale, dtype, -1.f, stream);
 }
 
@@ -462,51 +567,18 @@ fa_status fa_rope_append_paged(const void* q, const void* k, const void* v, void
                                const int* positions, const int* slots, const double* inv_freq, void* k_pages,
                                void* v_pages, int B, int Hq, int Hkv, int T, int page_size, int num_pages, int d,
                                int rot_dim, int interleaved, float mscale, void* stream) {
-  const fa_status st = check_rope(q, q_out, positions, inv_freq, B, Hq, Hkv, T, d, rot_dim, mscale, 2);
-  if (st != FA_OK) return st;
-  if (!strides || !k || !v || !slots || !k_pages || !v_pages || Hkv < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
-  if (misaligned(k, 2) || misaligned(v, 2) || misaligned(slots, 4) || misaligned(k_pages, 16) ||
-      misaligned(v_pages, 16))
-    return FA_ERR_INVALID_ARG;
-  if (page_size != 16 || static_cast<long long>(num_pages) * 16 >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  const long long pool = 32ll * num_pages * Hkv * d;
-  if (overlap(k_pages, pool, v_pages, pool)) return FA_ERR_INVALID_ARG;
-  RopeParams p = {};
-  p.q = side_of(q, q_out, strides, strides + 3, B, Hq, T);
-  p.k = side_of(k, k_pages, strides + 6, nullptr, B, Hkv, T);
-  p.v = side_of(v, v_pages, strides + 9, nullptr, B, Hkv, T);
-  {
-    // rows go to any slot while others are still read; q_out may be q and nothing else
-    const long long bt4 = 4ll * B * T;
-    const Rows out = rows_of(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2);
-    if (outputs_meet(p.q, RopeSide{}, B, T, d, 2, positions, bt4, inv_freq, 4ll * rot_dim) ||
-        rows_meet(out, rows_of(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2)) ||
-        rows_meet(out, rows_of(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2)) || rows_meet(out, dense_rows(slots, bt4)))
-      return FA_ERR_INVALID_ARG;
-    for (const void* pages : {k_pages, v_pages}) {
-      if (span_meets(q, p.q.sb, p.q.sh, p.q.st, B, Hq, T, d, 2, pages, pool) ||
-          span_meets(q_out, p.q.db, p.q.dh, p.q.dt, B, Hq, T, d, 2, pages, pool) ||
-          span_meets(k, p.k.sb, p.k.sh, p.k.st, B, Hkv, T, d, 2, pages, pool) ||
-          span_meets(v, p.v.sb, p.v.sh, p.v.st, B, Hkv, T, d, 2, pages, pool) || overlap(positions, bt4, pages, pool) ||
-          overlap(slots, bt4, pages, pool) || overlap(inv_freq, 4ll * rot_dim, pages, pool))
-        return FA_ERR_INVALID_ARG;
-    }
-  }
-  p.positions = positions;
-  p.pos_sb = T;
-  p.inv_freq = inv_freq;
-  p.slots = slots;
-  p.slot_stride = static_cast<long long>(Hkv) * d;
-  p.num_slots = num_pages * 16;
-  p.tokens = static_cast<long long>(B) * T;
-  p.T = T;
-  p.d = d;
-  p.rot = rot_dim;
-  p.mscale = mscale;
-  p.sign = 1.f;
-  p.err = device_error_word();
-  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
-  return static_cast<fa_status>(launch_rope<__nv_bfloat16, true>(p, interleaved != 0, static_cast<cudaStream_t>(stream)));
+  return append_any(q, k, v, q_out, strides, {positions, 0, inv_freq, nullptr, 1, B, T, rot_dim}, slots, k_pages, v_pages,
+                    B, Hq, Hkv, T, page_size, num_pages, d, rot_dim, interleaved, mscale, stream);
+}
+
+fa_status fa_rope_axes_append_paged(const void* q, const void* k, const void* v, void* q_out, const long long* strides,
+                                    const int* positions, const int* slots, const double* inv_freq,
+                                    const int* pair_axis, int axes, void* k_pages, void* v_pages, int B, int Hq,
+                                    int Hkv, int T, int page_size, int num_pages, int d, int rot_dim, int interleaved,
+                                    float mscale, void* stream) {
+  if (!pair_axis) return FA_ERR_INVALID_ARG;
+  return append_any(q, k, v, q_out, strides, {positions, 0, inv_freq, pair_axis, axes, B, T, rot_dim}, slots, k_pages,
+                    v_pages, B, Hq, Hkv, T, page_size, num_pages, d, rot_dim, interleaved, mscale, stream);
 }
 
 }  // extern "C"

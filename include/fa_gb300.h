@@ -90,6 +90,8 @@ typedef enum {
 #define FA_PLAN_MAX_T 8388480      /* rows of a sequence in fa_paged_plan; B * T < 2^31 as well */
 #define FA_TREE_MASK_MAX_T 8192    /* nodes of a tree in fa_tree_mask */
 #define FA_TREE_MASK_MAX_B 65535   /* trees of a call */
+#define FA_PAGES_MAX 4194304       /* pages of a pool in fa_pages_free and fa_pages_compact */
+#define FA_ROPE_MAX_AXES 8         /* axes of the positions in the fa_rope_axes calls */
 
 /* Library version, major*10000 + minor*100 + patch. */
 FA_API int fa_version(void);
@@ -416,6 +418,26 @@ FA_API fa_status fa_rope_bwd(const void* dq_out, const void* dk_out, void* dq, v
                              void* stream);
 
 /*
+ * fa_rope_axes, fa_rope_axes_bwd -- fa_rope and fa_rope_bwd for positions with several axes (time, height and
+ * width of a token of an image or a video): pair i turns by the position on its own axis.
+ *   positions [axes][B][T] int32, or [axes][T] with positions_shared; any int32 value.
+ *   pair_axis [rot_dim / 2] int32 (device): the axis of each pair, in [0, axes); a pair with another one records
+ *   FA_ERR_BOUNDS and turns as at position 0. 1 <= axes <= FA_ROPE_MAX_AXES. Blocks of pairs, axes in turn, or any
+ *   other way to share the pairs out; angles that begin anew on each axis are a matter of inv_freq.
+ *   All else as fa_rope; no output may overlap pair_axis either. Where every pair's axis has the same positions the
+ *   result is fa_rope's, bit for bit.
+ */
+FA_API fa_status fa_rope_axes(const void* q, const void* k, void* q_out, void* k_out, const long long* strides,
+                              const int* positions, int positions_shared, const double* inv_freq,
+                              const int* pair_axis, int axes, int B, int Hq, int Hk, int T, int d, int rot_dim,
+                              int interleaved, float mscale, int dtype, void* stream);
+FA_API fa_status fa_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                  const long long* strides, const int* positions, int positions_shared,
+                                  const double* inv_freq, const int* pair_axis, int axes, int B, int Hq, int Hk,
+                                  int T, int d, int rot_dim, int interleaved, float mscale, int dtype,
+                                  void* stream);
+
+/*
  * fa_rope_append_paged -- the new rows of a step over the paged cache: q rotated, k rotated
  * into its pages, v into its pages, in one launch.
  *   q [B][Hq][T][d], k, v [B][Hkv][T][d] bf16 with strides (HOST, 12 values: q, q_out, k, v)
@@ -433,6 +455,87 @@ FA_API fa_status fa_rope_append_paged(const void* q, const void* k, const void* 
                                       const double* inv_freq, void* k_pages, void* v_pages, int B, int Hq,
                                       int Hkv, int T, int page_size, int num_pages, int d, int rot_dim,
                                       int interleaved, float mscale, void* stream);
+
+/* fa_rope_axes_append_paged -- fa_rope_append_paged for positions [axes][B][T] with several axes: pair_axis and
+ * axes as fa_rope_axes, all else as fa_rope_append_paged. */
+FA_API fa_status fa_rope_axes_append_paged(const void* q, const void* k, const void* v, void* q_out,
+                                           const long long* strides, const int* positions, const int* slots,
+                                           const double* inv_freq, const int* pair_axis, int axes, void* k_pages,
+                                           void* v_pages, int B, int Hq, int Hkv, int T, int page_size,
+                                           int num_pages, int d, int rot_dim, int interleaved, float mscale,
+                                           void* stream);
+
+/*
+ * The pages of a cache that several sequences share. Row b of the block table holds the ceil(seqlens[b] / 16)
+ * pages of sequence b; shares [num_pages] int32 says of each page how many sequences hold it beside its first
+ * owner. It begins as zeros, and a page that fa_paged_plan hands out keeps its 0: only the calls here change it.
+ * Lengths outside [0, max_pages * 16] are clamped and FA_ERR_BOUNDS is recorded; so it is for table entries in use
+ * outside [0, num_pages), which are passed over. page_size == 16; B * max_pages and n * max_pages < 2^31.
+ * No output may overlap another argument but where a call says so (FA_ERR_INVALID_ARG).
+ */
+
+/*
+ * fa_pages_fork -- sequences that go on from others: beams, or several samples of one prompt. Child i shares the
+ * whole pages of row parents[i] and gets a page of its own for the tokens behind them, if there are any. These
+ * pages come from the front of the free list, in the order of i.
+ *   block_table [B][max_pages], seqlens [B]; parents [n] int32 in [0, B), or -1: a child of length 0 (any other
+ *   records FA_ERR_BOUNDS and counts as -1); free_pages [num_free] (may be NULL when 0).
+ *   shares: one more for each child on a whole page of its parent, in place.
+ *   table_out [n][max_pages] out: the child's pages, 0 behind them; lens_out [n] out: its length;
+ *   copy_src, copy_dst [n] out: the parent's last page and the child's where it needs a copy (for fa_pages_copy),
+ *   -1 both where it needs none; pages_used [1] out: pages needed.
+ *   Where the free list is too short, or names a page outside the pool, FA_ERR_BOUNDS is recorded and the child's
+ *   last page is -1, in the table and among the copies.
+ *   The parents' rows go on to hold their pages; fa_pages_free gives them back. A row may be forked any number of
+ *   times in one call.
+ */
+FA_API fa_status fa_pages_fork(const int* block_table, const int* seqlens, const int* parents,
+                               const int* free_pages, int num_free, int* shares, int* table_out, int* lens_out,
+                               int* copy_src, int* copy_dst, int* pages_used, int B, int n, int max_pages,
+                               int page_size, int num_pages, void* stream);
+
+/*
+ * fa_pages_copy -- page dst[i] gets what page src[i] holds, in both pools of every layer.
+ *   k_pages, v_pages [layers][num_pages][16][Hkv][d] bf16; src, dst [n] int32; count [1] int32 (device, may be
+ *   NULL): only the first min(n, count) pairs.
+ *   A pair with a -1 is passed over; one with a page outside [0, num_pages) as well, and FA_ERR_BOUNDS is recorded.
+ *   Destinations must differ, and none may be another pair's source: what such a page gets is undefined.
+ *   The pools may not overlap. Any Hkv and d <= 1024.
+ */
+FA_API fa_status fa_pages_copy(void* k_pages, void* v_pages, const int* src, const int* dst, const int* count, int n,
+                               int layers, int num_pages, int page_size, int Hkv, int d, void* stream);
+
+/*
+ * fa_pages_free -- the pages of sequences that end, but for those that others still hold.
+ *   rows [n] int32: rows of the table, each in [0, B), -1: none (any other records FA_ERR_BOUNDS and counts as
+ *   -1); NULL: all, n == B. A row that is named twice is given back twice.
+ *   shares_out [num_pages] out: one less for each row that held the page, 0 where nobody does any more. It may be
+ *   shares.
+ *   freed [min(num_pages, n * max_pages)] int32 out: the pages that nobody holds any more, ascending, -1 behind
+ *   them; num_freed [1] out: how many.
+ *   A page that is given back more often than it is held is freed once, and FA_ERR_BOUNDS is recorded.
+ *   The rows and their lengths are left as they are: a caller takes them out of its batch.
+ *   num_pages <= FA_PAGES_MAX.
+ */
+FA_API fa_status fa_pages_free(const int* block_table, const int* seqlens, const int* rows, const int* shares,
+                               int* shares_out, int* freed, int* num_freed, int B, int n, int max_pages,
+                               int page_size, int num_pages, void* stream);
+
+/*
+ * fa_pages_compact -- the live pages of a pool moved to its front. A page from `first` on is live if a row of the
+ * table holds it; the L live ones end up as pages first .. first + L - 1. Those among them that are there already
+ * stay; the i-th of the others, ascending, goes to the i-th page there that is not live.
+ *   table_out [B][max_pages] out: the rows with the new pages, entries behind a sequence's pages as they were;
+ *   shares_out [num_pages] out: the shares at the pages' new places, 0 at pages that nobody holds, those below
+ *   first as they were. Either may be its input.
+ *   copy_src, copy_dst [min((num_pages - first) / 2, B * max_pages)] int32 out: the moves (for fa_pages_copy, with
+ *   counts as its count), -1 behind them; no source is a destination. NULL where that is 0.
+ *   counts [2] int32 out: moves, L.
+ *   0 <= first < num_pages <= FA_PAGES_MAX: pages below first are not moved nor given away.
+ */
+FA_API fa_status fa_pages_compact(const int* block_table, const int* seqlens, const int* shares, int* table_out,
+                                  int* shares_out, int* copy_src, int* copy_dst, int* counts, int B, int max_pages,
+                                  int page_size, int num_pages, int first, void* stream);
 
 /*
  * fa_tree_decode_paged -- attention of a tree of drafted tokens over the paged cache, the

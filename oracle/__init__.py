@@ -32,7 +32,11 @@ from .attention import (  # noqa: F401
 from .serving import (  # noqa: F401
     pack_words,
     paged_plan,
+    pages_compact,
+    pages_fork,
+    pages_free,
     rope,
+    rope_axes,
     tree_attention,
     tree_sees,
 )

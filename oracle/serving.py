@@ -1,5 +1,5 @@
-"""Oracles of the paged-cache and position calls: plans, tree masks, rotary positions
-and tree attention. Plain loops and fp64 (angles in long double), written from the
+"""Oracles of the paged-cache and position calls: plans, tree masks, rotary positions,
+shared pages and tree attention. Plain loops and fp64 (angles in long double), written from the
 definitions; nothing here is shared with the CUDA library."""
 
 from __future__ import annotations
@@ -85,6 +85,101 @@ def rope(x, positions, inv_freq, interleaved=False, mscale=1.0, transposed=False
     y[..., first] = a * cos - b * sin
     y[..., second] = b * cos + a * sin
     return y
+
+
+def rope_axes(x, positions, inv_freq, axis, interleaved=False, mscale=1.0, transposed=False):
+    """x [B][H][T][d], positions [axes][B][T]; pair i turned by the position on axis[i], one pair at a time; fp64 result."""
+    x, positions = _np(x).astype(np.float64), _np(positions).astype(np.int64)
+    y, n = x.copy(), len(inv_freq)
+    for i, (f, a) in enumerate(zip(_np(inv_freq), _np(axis))):
+        one, two = (2 * i, 2 * i + 1) if interleaved else (i, n + i)
+        turn = np.fmod(positions[a].astype(np.longdouble) * np.longdouble(f), TWO_PI)
+        c, s = (fn(turn).astype(np.float64)[:, None] * mscale for fn in (np.cos, np.sin))
+        s = -s if transposed else s
+        y[..., one], y[..., two] = x[..., one] * c - x[..., two] * s, x[..., two] * c + x[..., one] * s
+    return y
+
+
+def _held(table, seqlens, b):
+    """Pages of row b, its length clamped to what the row holds."""
+    n = min(max(int(seqlens[b]), 0), table.shape[1] * PAGE)
+    return [int(x) for x in table[b, : -(-n // PAGE)]], n
+
+
+def pages_fork(table, seqlens, parents, free, shares):
+    """-> (table [n][max_pages], lens, copy_src, copy_dst, pages used, shares, in_bounds)."""
+    table, seqlens, parents, free = (_np(x).astype(np.int64) for x in (table, seqlens, parents, free))
+    shares = _np(shares).astype(np.int64).copy()
+    P, rows, lens, src, dst, used, ok = len(shares), [], [], [], [], 0, True
+    for p in parents:
+        ok &= -1 <= p < len(table)
+        held, n = _held(table, seqlens, p) if 0 <= p < len(table) else ([], 0)
+        ok &= not 0 <= p < len(table) or n == seqlens[p]
+        row, a, b = np.zeros(table.shape[1], np.int64), -1, -1
+        for j, page in enumerate(held):
+            if (j + 1) * PAGE <= n:
+                row[j] = page
+                if 0 <= page < P:
+                    shares[page] += 1
+                else:
+                    ok = False
+            else:
+                fresh = int(free[used]) if used < len(free) else -1
+                used += 1
+                good = 0 <= fresh < P
+                row[j] = fresh if good else -1
+                ok &= good and 0 <= page < P
+                if 0 <= page < P:
+                    a, b = (page, fresh) if good else (-1, -1)
+        rows.append(row), lens.append(n), src.append(a), dst.append(b)
+    return np.array(rows), np.array(lens), np.array(src), np.array(dst), used, shares, ok
+
+
+def pages_free(table, seqlens, shares, rows=None):
+    """-> (pages that nobody holds any more, ascending; shares; in_bounds)."""
+    table, seqlens = _np(table).astype(np.int64), _np(seqlens).astype(np.int64)
+    shares = _np(shares).astype(np.int64).copy()
+    holders, ok, gone = shares + 1, True, set()
+    for r in range(len(table)) if rows is None else _np(rows):
+        if not 0 <= r < len(table):
+            ok &= r == -1
+            continue
+        held, n = _held(table, seqlens, r)
+        ok &= n == seqlens[r]
+        for page in held:
+            if not 0 <= page < len(shares):
+                ok = False
+                continue
+            holders[page] -= 1
+            ok &= holders[page] >= 0
+            if holders[page] == 0:
+                gone.add(page)
+    for page in range(len(shares)):
+        shares[page] = 0 if page in gone else holders[page] - 1
+    return sorted(gone), shares, ok
+
+
+def pages_compact(table, seqlens, shares, first=0):
+    """-> (table, shares, sources, destinations, live pages, in_bounds)."""
+    table, seqlens = _np(table).astype(np.int64).copy(), _np(seqlens).astype(np.int64)
+    was, ok, P = _np(shares).astype(np.int64), True, len(shares)
+    live = set()
+    for b in range(len(table)):
+        held, n = _held(table, seqlens, b)
+        ok &= n == seqlens[b] and all(0 <= x < P for x in held)
+        live |= {x for x in held if first <= x < P}
+    end = first + len(live)
+    src = sorted(x for x in live if x >= end)
+    dst = [x for x in range(first, end) if x not in live]
+    to = dict(zip(src, dst))
+    for b in range(len(table)):
+        for j in range(len(_held(table, seqlens, b)[0])):
+            table[b, j] = to.get(int(table[b, j]), table[b, j])
+    after = np.zeros(P, np.int64)
+    after[:first] = was[:first]
+    for x in live:
+        after[to.get(x, x)] = was[x]
+    return table, after, src, dst, len(live), ok
 
 
 def tree_attention(q, k_pages, v_pages, table, seqlens, mask, tree_lens=None, scale=None):
