@@ -29,6 +29,8 @@ from .api import (  # noqa: F401
     fa_pages_copy,
     fa_pages_fork,
     fa_pages_free,
+    fa_prefix_decode_paged,
+    fa_prefix_workspace_bytes,
     fa_rope,
     fa_rope_append_paged,
     fa_rope_axes,

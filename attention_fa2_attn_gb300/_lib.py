@@ -37,6 +37,7 @@ FA_PLAN_MAX_T = 8388480
 FA_TREE_MASK_MAX_T = 8192
 FA_TREE_MASK_MAX_B = 65535
 FA_PAGES_MAX = 4194304
+FA_PREFIX_MAX_GROUPS = 4096
 FA_ROPE_MAX_AXES = 8
 FA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -86,6 +87,11 @@ SIGNATURES = {
         [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P],
     ),
     "fa_tree_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "fa_prefix_decode_paged": (
+        _I,
+        [_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P],
+    ),
+    "fa_prefix_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_get_last_device_error": (_I, [_P, ctypes.POINTER(_I)]),
     "fa_set_wait_timeout_ns": (None, [_ULL]),
     "fa_get_wait_timeouts": (None, [ctypes.POINTER(_ULL), ctypes.POINTER(_ULL)]),

@@ -748,6 +748,60 @@ def fa_tree_decode_paged(q, k_pages, v_pages, block_table, seqlens, tree_mask, t
     return o, lse
 
 
+def fa_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, max_pages: int, d: int, num_sms: int | None = None,
+                              device=None) -> int:
+    """Bytes of workspace fa_prefix_decode_paged needs on a device with num_sms SMs (None: this one); 0 for sizes that it
+    does not take."""
+    if num_sms is None:
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        num_sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    return int(lib().fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, int(num_sms)))
+
+
+def fa_prefix_decode_paged(q, k_pages, v_pages, block_table, seqlens, group_starts, prefix_lens, causal: bool = True,
+                           scale: float | None = None, workspace=None, out=None, lse=None):
+    """fa_decode_paged for a batch whose sequences share prefixes: sequences group_starts[g] .. group_starts[g + 1] - 1
+    (int32 [groups + 1]) have their first prefix_lens[g] keys (int32 [groups]) on the same pages, which are read once
+    -> (o, lse)."""
+    if workspace is None and out is None and lse is None:
+        got = fast().prefix_decode_paged(q, k_pages, v_pages, block_table, seqlens, group_starts, prefix_lens, causal, scale)
+        if got is not None:
+            return _answer(got, "fa_prefix_decode_paged")
+    _need(q, "q", _BF16, 4)
+    _need(k_pages, "k_pages", _BF16, 4)
+    _need(v_pages, "v_pages", _BF16, 4)
+    _need(block_table, "block_table", _I32, 2)
+    B, Hq, T, d = q.shape
+    P, page_size, Hkv, _ = k_pages.shape
+    max_pages = block_table.shape[1]
+    dev = q.device
+    if not (dev == k_pages.device == v_pages.device == block_table.device):
+        raise ValueError("q, the pools and block_table must be on one device")
+    _on_current_device(q)
+    if tuple(k_pages.shape) != tuple(v_pages.shape) or k_pages.shape[3] != d:
+        raise ValueError(f"k_pages and v_pages must both be [P][page_size][Hkv][{d}]")
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}][max_pages]")
+    _need_ints("seqlens", seqlens, (B,), dev)
+    _need(prefix_lens, "prefix_lens", _I32, 1)
+    groups = prefix_lens.shape[0]
+    _need_ints("prefix_lens", prefix_lens, (groups,), dev)
+    _need_ints("group_starts", group_starts, (groups + 1,), dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, device=dev)
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws_bytes = _ws_bytes(workspace, nbytes, dev)
+    o = _out(out, "out", q.shape, _BF16, q)
+    lse = _out(lse, "lse", (B, Hq, T), torch.float32, q)
+    st = lib().fa_prefix_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seqlens),
+                                      _ptr(group_starts), _ptr(prefix_lens), groups, _ptr(o), _ptr(lse), B, Hq, Hkv, T,
+                                      max_pages, page_size, P, d, scale, int(causal), _ptr(workspace), ws_bytes,
+                                      _stream(q))
+    check(st, "fa_prefix_decode_paged")
+    return o, lse
+
+
 def fa_get_last_device_error(device=None) -> tuple[int, int]:
     """Synchronise the current stream and read/clear the device error word -> (status, raw word)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
@@ -803,6 +857,8 @@ __all__ = [
     "fa_pages_compact",
     "fa_tree_decode_paged",
     "fa_tree_workspace_bytes",
+    "fa_prefix_decode_paged",
+    "fa_prefix_workspace_bytes",
     "fa_get_last_device_error",
     "fa_set_wait_timeout_ns",
     "fa_get_wait_timeouts",

@@ -364,6 +364,50 @@ PyObject* tree_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (q, k_pages, v_pages, block_table, seqlens, group_starts, prefix_lens, causal, scale or None)
+PyObject* prefix_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const Tensor* t[7];
+  bool causal = false;
+  float scale = 0.f;
+  if (n != 9 || !flag_of(a[7], &causal) || (a[8] != Py_None && !float_of(a[8], &scale))) Py_RETURN_NONE;
+  for (int i = 0; i < 7; ++i)
+    if (!(t[i] = tensor_of(a[i]))) Py_RETURN_NONE;
+  const Tensor &q = *t[0], &kp = *t[1], &vp = *t[2], &table = *t[3], &seqlens = *t[4], &starts = *t[5], &lens = *t[6];
+  const int dev = device_for(q);
+  if (!dense(q, at::kBFloat16, 4, dev) || !dense(kp, at::kBFloat16, 4, dev) || !dense(vp, at::kBFloat16, 4, dev) ||
+      !dense(table, at::kInt, 2, dev) || !dense(seqlens, at::kInt, 1, dev) || !dense(starts, at::kInt, 1, dev) ||
+      !dense(lens, at::kInt, 1, dev))
+    Py_RETURN_NONE;
+  const int64_t B = q.size(0), Hq = q.size(1), T = q.size(2), d = q.size(3), P = kp.size(0), Hkv = kp.size(2),
+                pages = table.size(1), G = lens.size(0);
+  if (!same_sizes(kp, vp) || kp.size(3) != d || table.size(0) != B || seqlens.size(0) != B || starts.size(0) != G + 1 ||
+      !fits(B) || !fits(Hq) || !fits(T) || !fits(d) || !fits(P) || !fits(Hkv) || !fits(pages) || !fits(kp.size(1)) ||
+      !fits(G))
+    Py_RETURN_NONE;
+  if (a[8] == Py_None) scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  Tensor o, lse;
+  fa_status st;
+  {
+    NoInterpreter released;
+    const int sms = at::cuda::getCurrentDeviceProperties()->multiProcessorCount;
+    const size_t bytes =
+        fa_prefix_workspace_bytes(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T),
+                                  static_cast<int>(pages), static_cast<int>(d), sms);
+    const Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    o = make({B, Hq, T, d}, at::kBFloat16, dev);
+    lse = make({B, Hq, T}, at::kFloat, dev);
+    st = fa_prefix_decode_paged(
+        q.const_data_ptr(), kp.const_data_ptr(), vp.const_data_ptr(), ints(table), ints(seqlens), ints(starts), ints(lens),
+        static_cast<int>(G), o.mutable_data_ptr(), static_cast<float*>(lse.mutable_data_ptr()), static_cast<int>(B),
+        static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T), static_cast<int>(pages),
+        static_cast<int>(kp.size(1)), static_cast<int>(P), static_cast<int>(d), scale, causal, ws.mutable_data_ptr(),
+        bytes, stream_of(dev));
+  }
+  return answer(st, {o, lse});
+  END_HANDLE_TH_ERRORS
+}
+
 // A block table with its lengths, and the shares of the pool's pages.
 bool shared_table(const Tensor& table, const Tensor& seqlens, const Tensor& shares, int dev) {
   return dense(table, at::kInt, 2, dev) && dense(seqlens, at::kInt, 1, dev) && dense(shares, at::kInt, 1, dev) &&
@@ -487,7 +531,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FA_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FA_METHOD(paged_plan), FA_METHOD(tree_mask), FA_METHOD(rope), FA_METHOD(rope_append_paged),
-                         FA_METHOD(tree_decode_paged), FA_METHOD(pages_fork), FA_METHOD(pages_copy),
+                         FA_METHOD(tree_decode_paged), FA_METHOD(prefix_decode_paged), FA_METHOD(pages_fork), FA_METHOD(pages_copy),
                          FA_METHOD(pages_free), FA_METHOD(pages_compact), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", "Step calls from Python objects to the C ABI.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,60 @@
+// join.cuh -- what the kernels share that cut a row's keys over several CTAs and join the
+// partial results.
+#pragma once
+
+#include "common.cuh"
+
+namespace fa {
+
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// 32 bytes in one store: a warp whose threads each write a row of their own spends a
+// wavefront per row and store, so half as many as with 16 bytes.
+__device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Whether all `nthreads` threads at the barrier say yes; it is their barrier as well.
+__device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
+// maximum is +inf (its scores were NaN) makes all of them NaN.
+struct RowJoin {
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
+    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
+    m = mn;
+  }
+};
+
+}  // namespace fa

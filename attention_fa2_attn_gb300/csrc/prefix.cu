@@ -1,0 +1,1162 @@
+// prefix.cu -- attention of a batch over the paged cache whose sequences share a prefix, with
+// the shared keys read once for all of a group.
+//
+// What it computes. Row i of sequence b sees keys j <= S - T + i (causal; else j < S), S =
+// seqlens[b], exactly as fa_decode_paged. A group is a run of sequences whose first P keys lie
+// on the same pages. The softmax over [0, S) is joined from one over [0, P), whose keys are
+// read through the group's first row of the table for all of its rows at once, and one over
+// [P, S), read through the sequence's own row:
+//   m = max(m1, m2), l = 2^(m1 - m) l1 + 2^(m2 - m) l2, O = (2^(m1 - m) O1 + 2^(m2 - m) O2) / l.
+//
+// What bounds it. A KV head's Hq / Hkv heads and T positions of n sequences are n g T rows
+// against each shared key: 64 sequences of 8 heads each make 512 FLOP per byte, where one alone
+// has 8. So the prefix costs tensor-core and softmax time, what a sequence has of its own HBM
+// time.
+//
+// How. As the tree kernel: 128 rows a tile on the tensor cores, one CTA to an SM, equal shares
+// of the batch's cost whatever the lengths, partials joined by a second kernel.
+//   * An item is a group (its prefix) or a sequence (its own keys). Its row tiles hold the
+//     rows of as many whole sequences as fit, in q's order, so one 4-D box brings a tile of Q:
+//     [sequences][R rows] behind one another. With R > 128 a sequence is several tiles.
+//   * Two row tiles make a wide unit, which goes over the keys with one tile of keys against
+//     both. A last tile alone is a narrow unit: two tiles of keys at a time, each with its own
+//     S, P and O. A CTA takes units of both kinds as its share has them: most rows of a batch's
+//     prefix are wide, every sequence's own are narrow (R <= 128).
+//   * The CTAs that are neighbours take the KV heads of one cost line side by side.
+//   * A share of a unit leaves fp32 partials at (the rows before the unit + 256 times the
+//     CTA's number): no two shares meet there, since along the line either the unit or the CTA
+//     goes up. A sequence without a prefix whose keys lie in one share is written at once.
+// P is rounded to bf16 for the tensor cores (by at most 2^-8 of a weight; fp32 would take twice
+// the MMAs), O once at the end; sums and maxima are fp32.
+// Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the CTA
+// unwinds. The softmax warps leave together, by a vote in every unit.
+#include <atomic>
+
+#include "join.cuh"
+#include "launch.cuh"
+
+namespace fa {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_tiled();  // defined in api.cu
+
+constexpr int kPxTile = 128;  // rows of a tile, keys of a tile
+constexpr int kPxUnit = 2 * kPxTile;  // rows of a unit, at most
+
+template <int D>
+struct PxCfg {
+  static constexpr int KCH = D / 64;
+  static constexpr int CHUNK_BYTES = 128 * 128;
+  static constexpr int Q_BYTES = kPxTile * D * 2;
+  static constexpr int KV_BYTES = kPxTile * D * 2;
+  // what the SM's shared memory holds beside two Q tiles; K runs ahead of V by a step anyway
+  static constexpr int K_STAGES = D == 64 ? 6 : 3, V_STAGES = D == 64 ? 6 : 2;
+  static constexpr int OFF_K = 2 * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + K_STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + V_STAGES * KV_BYTES;
+  static constexpr int OFF_EX = OFF_BAR + 384;
+  static constexpr int SMEM = OFF_EX + kPxTile * 5 * 4;
+  static_assert(SMEM <= 232448, "shared memory of an SM");
+  static_assert(OFF_BAR - OFF_K >= (2 * FA_PREFIX_MAX_GROUPS + 1) * 4, "the groups, before the rings are in use");
+  static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
+  static constexpr int O_OFF = 128;
+  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, K producer, MMA issuer, V producer, an idle warp
+  static constexpr int SOFTMAX_REGS = 192;  // 256 * 192 + 128 * 120 = 384 * 168
+  static constexpr int AUX_REGS = 120;
+};
+
+// What shares are cut in: `step` for a step of a unit and, ahead of its first, `front` for what
+// it costs beside its keys.
+struct PxCost {
+  int narrow_step, narrow_front, wide_step, wide_front;
+};
+constexpr int kPxMostCost = 10;  // of a step with its unit's start
+
+struct PxParams {
+  __nv_bfloat16* o;
+  float* lse;  // may be null
+  const int* block_table;
+  const int* seqlens;
+  const int* starts;       // [G + 1]
+  const int* prefix_lens;  // [G]
+  int B, G, Hkv, T, R, causal;
+  int spt;    // sequences of a row tile (1 where R > 128)
+  int TS;     // row tiles of a sequence (1 where R <= 128)
+  int V;      // KV heads side by side
+  int units;  // KV heads of each of these places
+  int max_pages, num_pages;
+  float c;  // scale * log2(e)
+  PxCost cost;
+  long long area;   // rows of partials of one place and kind
+  float* part;      // [2 kinds][V][area][D]: unnormalised O
+  float4* part_ml;  // (max in log2 units, sum as P V saw it, sum, -)
+  int2* desc;       // [2 kinds][B][Hkv][TS]: (first CTA << 16 | CTAs, first row), or kPxDone
+  unsigned* err;
+  unsigned long long timeout_ns;
+};
+constexpr int kPxDone = -1;  // the rows are written
+
+struct PxBars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  // where this CTA's share begins
+  int it0, off0, group0, begin, end, total, grid;
+  int no_groups;  // the groups are not what they should be: every sequence by itself
+  PxCost cost;
+};
+static_assert(sizeof(PxBars) <= 384, "barrier area");
+
+__device__ __forceinline__ int px_len(const PxParams& p, int b) {
+  return max(0, min(__ldg(p.seqlens + b), p.max_pages * 16));
+}
+// Keys that a group reads once: whole pages, of two sequences or more, which its first one has.
+__device__ __forceinline__ int px_prefix(const PxParams& p, int s0, int s1, int asked) {
+  return s1 - s0 < 2 ? 0 : max(0, min(asked, px_len(p, s0))) & ~15;
+}
+
+// A group's prefix or a sequence's own keys.
+struct PxItem {
+  int s0, s1;  // its sequences
+  int k0, k1;  // its keys
+  int tiles;   // row tiles
+  __device__ __forceinline__ int key_tiles() const { return k1 > k0 ? (k1 - k0 + kPxTile - 1) / kPxTile : 0; }
+  // cost of a wide and of a narrow unit, and of a KV head's units together
+  __device__ __forceinline__ int wide(const PxCost& c) const { return c.wide_front + c.wide_step * key_tiles(); }
+  __device__ __forceinline__ int narrow(const PxCost& c) const {
+    return c.narrow_front + c.narrow_step * ((key_tiles() + 1) / 2);
+  }
+  __device__ __forceinline__ int head(const PxCost& c) const {
+    return k1 > k0 ? tiles / 2 * wide(c) + (tiles & 1) * narrow(c) : 0;
+  }
+};
+__device__ __forceinline__ PxItem px_group(const PxParams& p, int s0, int s1, int prefix) {
+  const int n = max(0, s1 - s0);
+  return PxItem{s0, s1, 0, prefix, p.R <= kPxTile ? (n + p.spt - 1) / p.spt : n * p.TS};
+}
+__device__ __forceinline__ PxItem px_sequence(const PxParams& p, int b, int prefix) {
+  return PxItem{b, b + 1, prefix, px_len(p, b), p.TS};
+}
+
+// A run of steps of one unit inside a CTA's share.
+struct PxSeg {
+  PxItem item;
+  int hu, kvh;   // KV head of the place, and of all
+  int tile;      // first row tile
+  bool wide, own;  // own: a sequence's own keys
+  int x0, nt;    // first key tile and how many
+  bool from_start, to_end;
+  int unit_end;  // where the unit ends on the cost line
+};
+
+// Walks a share segment by segment; each role walks by itself. Items: the groups, then the
+// sequences.
+struct PxWalk {
+  int it, off, at, g;  // item, cost into it, cost into the line, the group that is looked at
+  const volatile PxBars* s;
+  __device__ __forceinline__ PxWalk(const PxBars* bars)
+      : it(bars->it0), off(bars->off0), at(bars->begin), g(bars->group0), s(bars) {}
+  __device__ __forceinline__ PxItem item(const PxParams& p, int i) {
+    const bool none = s->no_groups;
+    if (i < p.G) {
+      const int s0 = __ldg(p.starts + i), s1 = __ldg(p.starts + i + 1);
+      return none ? PxItem{0, 0, 0, 0, 0} : px_group(p, s0, s1, px_prefix(p, s0, s1, __ldg(p.prefix_lens + i)));
+    }
+    const int b = i - p.G;
+    int prefix = 0;
+    if (!none) {
+      while (g + 1 < p.G && __ldg(p.starts + g + 1) <= b) ++g;
+      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
+      if (b >= s0 && b < s1) prefix = px_prefix(p, s0, s1, __ldg(p.prefix_lens + g));
+    }
+    return px_sequence(p, b, prefix);
+  }
+  __device__ __forceinline__ bool next(const PxParams& p, PxSeg& w) {
+    const PxCost c = {s->cost.narrow_step, s->cost.narrow_front, s->cost.wide_step, s->cost.wide_front};
+    const int end = s->end;
+    int from, to, j0, j1, cost;
+    do {
+      if (at >= end) return false;
+      w.item = item(p, it);
+      const int head = w.item.head(c);
+      if (head == 0) {  // nothing to do (its cost is 0)
+        ++it;
+        off = 0;
+        j0 = j1 = 0;
+        continue;
+      }
+      w.own = it >= p.G;
+      w.hu = off / head;
+      const int rest = off - w.hu * head, pair = w.item.wide(c), u = min(w.item.tiles / 2, rest / pair);
+      w.tile = 2 * u;
+      w.wide = u < w.item.tiles / 2;
+      from = rest - u * pair;
+      cost = w.wide ? pair : w.item.narrow(c);
+      to = min(cost, from + end - at);
+      const int step = w.wide ? c.wide_step : c.narrow_step, front = w.wide ? c.wide_front : c.narrow_front;
+      j0 = from < front ? 0 : (from - front) / step;
+      j1 = to < front ? 0 : (to - front) / step;
+      w.unit_end = at - from + cost;
+      off += to - from;
+      at += to - from;
+      if (off == head * p.units) {
+        ++it;
+        off = 0;
+      }
+      // a share that ends inside a unit's first step leaves all of it to the next CTA
+    } while (j0 == j1);
+    const int per = w.wide ? 1 : 2;
+    w.kvh = w.hu * p.V + static_cast<int>(blockIdx.x) % p.V;
+    w.x0 = j0 * per;
+    w.nt = min(w.item.key_tiles(), j1 * per) - w.x0;
+    w.from_start = j0 == 0;
+    w.to_end = to == cost;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PxParams p) {
+  using C = PxCfg<D>;
+  constexpr int KST = C::K_STAGES, VST = C::V_STAGES;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  PxBars* bars = reinterpret_cast<PxBars*>(smem + C::OFF_BAR);
+  float* ex = reinterpret_cast<float*>(smem + C::OFF_EX);  // [5][128]: max and sum of both slots, lse sum of slot 1
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  const int me = cta / p.V;  // this CTA's number on its line
+
+  if (smem_u32(smem) & 1023u) {  // the swizzle atoms' alignment; the block's only shared memory starts at a multiple
+    pdl_wait();
+    if (threadIdx.x == 0) record_error(p.err, FA_ERR_TIMEOUT, SITE_PX_SMEM);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < 6; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
+      mbar_init(&bars->v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t], 128);
+      mbar_init(&bars->pv_done[t], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&bars->tmem_base, 512);
+  pdl_wait();
+
+  // ---- this CTA's share of its line's cost: a block-wide scan over the items. The groups go
+  // through shared memory that the rings use later.
+  {
+    int* gs = reinterpret_cast<int*>(sK);  // [G + 1]: starts
+    int* gp = gs + p.G + 1;                // [G]: prefixes
+    bool bad = false;
+    for (int g = threadIdx.x; g < p.G; g += C::THREADS) {
+      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
+      gs[g] = s0;
+      if (g == p.G - 1) gs[p.G] = s1;
+      const bool fine = 0 <= s0 && s0 <= s1 && s1 <= p.B;
+      bad |= !fine;
+      gp[g] = fine ? px_prefix(p, s0, s1, __ldg(p.prefix_lens + g)) : 0;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
+    auto group_of = [&](int b) {  // the last that begins at or before b
+      int g = 0, hi = p.G;
+      while (hi - g > 1) {
+        const int mid = (g + hi) / 2;
+        if (gs[mid] <= b) g = mid; else hi = mid;
+      }
+      return g;
+    };
+    auto item = [&](int i, int& g) {
+      if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0} : px_group(p, gs[i], gs[i + 1], gp[i]);
+      const int b = i - p.G;
+      if (bad) return px_sequence(p, b, 0);
+      if (g < 0) g = group_of(b);
+      while (g + 1 < p.G && gs[g + 1] <= b) ++g;
+      return px_sequence(p, b, b >= gs[g] && b < gs[g + 1] ? gp[g] : 0);
+    };
+    const int items = p.G + p.B;
+    const int per = (items + C::THREADS - 1) / C::THREADS;
+    const int lo = min(items, static_cast<int>(threadIdx.x) * per), hi = min(items, lo + per);
+    int steps = 0, mine = 0, g = -1;  // a line's whole cost is below 2^31
+    for (int i = lo; i < hi; ++i) {
+      const PxItem x = item(i, g);
+      steps += x.head(PxCost{1, 0, 1, 0});
+      mine += x.head(p.cost);
+    }
+    // block-wide sums through the exchange area, which nothing uses yet
+    int* wsum = reinterpret_cast<int*>(ex);
+    auto scan = [&](int v, int& total) {
+      int inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      int before = inc - v;
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < 12; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+      }
+      __syncthreads();
+      return before;
+    };
+    int all_steps, total;
+    scan(steps * p.units, all_steps);
+    const int grid = static_cast<int>(gridDim.x) / p.V;
+    // lines of so few steps that a CTA has hardly more than one are cut by steps alone; a
+    // share is a step's cost or more either way, so that every CTA between a unit's first and
+    // last has a step of it
+    const bool few = all_steps <= 2 * grid;
+    const PxCost cost = few ? PxCost{1, 0, 1, 0} : p.cost;
+    mine = (few ? steps : mine) * p.units;
+    const int before = scan(mine, total);
+    const int shares = few ? min(grid, max(1, all_steps)) : grid;
+    const int begin = me < shares ? static_cast<int>(static_cast<long long>(me) * total / shares) : total;
+    const int end = me < shares ? static_cast<int>((me + 1ll) * total / shares) : total;
+    if (threadIdx.x == 0) {
+      bars->begin = begin;
+      bars->end = end;
+      bars->total = total;
+      bars->grid = shares;
+      bars->cost = cost;
+      bars->no_groups = bad;
+      if (begin >= end) bars->it0 = bars->off0 = bars->group0 = 0;
+    }
+    if (begin < end && begin >= before && begin < before + mine) {  // one thread: its items hold the share's start
+      int off = begin - before, i = lo;
+      g = -1;
+      for (; i < hi; ++i) {
+        const int s = item(i, g).head(cost) * p.units;
+        if (off < s) break;
+        off -= s;
+      }
+      bars->it0 = i;
+      bars->off0 = off;
+      bars->group0 = max(g, 0);
+    }
+    // rows that a kind has no partials of: somebody has to say so
+    for (int b = cta; b < p.B; b += gridDim.x) {
+      int gb = -1;
+      const PxItem x = item(p.G + b, gb);
+      const int n = p.Hkv * p.TS;
+      const size_t at = static_cast<size_t>(b) * n;
+      if (x.k0 == 0)
+        for (int i = threadIdx.x; i < n; i += C::THREADS) p.desc[at + i] = make_int2(0, 0);
+      if (x.k1 <= x.k0)
+        for (int i = threadIdx.x; i < n; i += C::THREADS) p.desc[static_cast<size_t>(p.B) * n + at + i] = make_int2(0, 0);
+    }
+  }
+  fence_async_smem();  // the rings' memory was read and written by plain accesses
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort_flag = &bars->abort_flag;
+  const uint64_t tmo = p.timeout_ns;
+  const uint64_t tmo_unwind = unwind_timeout(tmo);
+  auto fail = [&](unsigned site) {
+    record_error(p.err, FA_ERR_TIMEOUT, site);
+    *abort_flag = 1;
+  };
+
+  if (warp >= 8) {
+    warpgroup_reg_dealloc<C::AUX_REGS>();
+    if (warp == 8 || warp == 10) {
+      // ======================= producers: K (and Q), V =======================
+      const bool is_k = warp == 8;
+      const CUtensorMap* my_map = is_k ? &tmK : &tmV;
+      uint8_t* my_ring = is_k ? sK : sV;
+      uint64_t* my_full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* my_empty = is_k ? bars->k_empty : bars->v_empty;
+      const uint32_t ST = is_k ? KST : VST;
+      if (lane == 0) {
+        if (is_k) tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(my_map);
+      }
+      PxWalk walk(bars);
+      PxSeg w;
+      uint32_t g = 0;  // key tiles loaded so far (ring position)
+      uint32_t stage = 0, lap = 0;
+      uint32_t q_loads = 0;
+      const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
+      bool ok = true;
+      while (ok && !*abort_flag && walk.next(p, w)) {
+        const int* trow = p.block_table + static_cast<size_t>(w.item.s0) * p.max_pages;
+        const int page0 = w.item.k0 >> 4;  // (k0 is a page's start)
+        const int n_pages = (w.item.k1 + 15) >> 4;
+        // a lane holds one of 32 entries, four tiles' worth; the next 32 are fetched meanwhile
+        auto fetch = [&](int x) -> int {
+          const int pg = page0 + (w.x0 + x) * 8 + lane;
+          return pg < n_pages && x * 8 + lane < w.nt * 8 ? __ldg(trow + pg) : -1;
+        };
+        int ent = -1, ent_next = fetch(0);
+        // The last segment's Q is in use until its last S: this one's first tiles go ahead of
+        // its Q (all but one stage of the ring, which that segment's own end frees).
+        bool q_due = is_k;
+        auto load_q = [&]() {
+          if (lane == 0) {
+            const int rows = min(p.R, kPxTile) * p.spt;  // of a box; those behind the batch's end are zeros
+            const int tiles = w.wide ? 2 : 1;
+            mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(tiles * C::KCH * rows * 128));
+            for (int t = 0; t < tiles; ++t) {
+              const int tile = w.tile + t, seq = tile / p.TS;
+              for (int c = 0; c < C::KCH; ++c)
+                tma_load_4d(sQ + t * C::Q_BYTES + c * C::CHUNK_BYTES, &tmQ, &bars->q_full, c * 64,
+                            (tile - seq * p.TS) * kPxTile, w.kvh, w.item.s0 + seq * p.spt);
+            }
+          }
+          ++q_loads;
+          q_due = false;
+        };
+        auto q_free = [&]() {  // uniform: every lane asks, and one answer counts
+          return q_loads == 0 || __all_sync(0xffffffffu, mbar_test(&bars->q_empty, (q_loads - 1) & 1));
+        };
+        for (int x = 0; x < w.nt; ++x, ++g) {
+          if (q_due) {
+            if (q_free()) {
+              load_q();
+            } else if (x == KST - 1) {
+              if (!mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
+                ok = false;
+                break;
+              }
+              load_q();
+            }
+          }
+          if ((x & 3) == 0) {
+            ent = ent_next;
+            ent_next = fetch(x + 4);
+          }
+          const int npg = min(8, n_pages - page0 - (w.x0 + x) * 8);  // pages past the end are not loaded
+          int pe = __shfl_sync(0xffffffffu, ent, (x & 3) * 8 + (pi & 7));
+          if (pi < npg && (pe < 0 || pe >= p.num_pages)) {
+            // never dereferenced: page 0 is loaded in its place, the output is undefined
+            record_error(p.err, FA_ERR_BOUNDS, SITE_PX_TABLE);
+            pe = 0;
+          }
+          if (g >= ST && !mbar_wait(&my_empty[stage], (lap & 1) ^ 1, tmo, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&my_full[stage], static_cast<uint32_t>(npg) * 16 * 128 * C::KCH);
+          __syncwarp();
+          if (pi < npg)
+            tma_load_3d(my_ring + stage * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, my_map, &my_full[stage], pc * 64,
+                        w.kvh, pe * 16);
+          if (++stage == ST) {
+            stage = 0;
+            ++lap;
+          }
+        }
+        if (ok && q_due) {
+          if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
+            ok = false;
+          else
+            load_q();
+        }
+      }
+      if (!ok) fail(SITE_PX_PRODUCER);
+      // Copies in flight must land before the CTA exits. Waited for whether or not a wait has
+      // run out so far: another role's may after this warp has issued its last copy.
+      if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+      for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) mbar_wait(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
+    } else if (warp == 9) {
+      // ======================= MMA issuer =======================
+      const bool leader = elect_one();
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kPxTile, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sV), C::CHUNK_BYTES, 1024);
+      // S of slot t = Q (row tile q) K^T, K in ring stage st
+      auto qk = [=](int t, int q, uint32_t st) {
+        const uint64_t a0 = dQ + static_cast<uint64_t>((q * C::Q_BYTES) >> 4);
+        const uint64_t b0 = dK + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+        const uint32_t dS = tmem + t * C::SLOT_COLS;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4);
+            tc_mma_ss(dS, a0 + off, b0 + off, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+        }
+      };
+      auto pv = [=](int t, uint32_t st, bool first) {
+        const uint64_t b0 = dV + static_cast<uint64_t>((st * C::KV_BYTES) >> 4);
+        const uint32_t dO = tmem + t * C::SLOT_COLS + C::O_OFF;
+        const uint32_t aP = tmem + t * C::SLOT_COLS;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < kPxTile / 16; ++kk)
+            tc_mma_ts(dO, aP + kk * 8, b0 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      auto commit = [=](uint64_t* bar) {
+        if (leader) tc_commit(bar);
+      };
+      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, tmo, abort_flag); };
+      auto wait_k = [&](uint32_t x) -> bool {
+        const bool r = wwait(&bars->k_full[x % KST], (x / KST) & 1);
+        tc_fence_after();
+        return r;
+      };
+      auto wait_v = [&](uint32_t x) -> bool {
+        const bool r = wwait(&bars->v_full[x % VST], (x / VST) & 1);
+        tc_fence_after();
+        return r;
+      };
+      uint32_t pph[2] = {0, 0};  // p_full phase parities
+      auto wait_p = [&](int t) -> bool {
+        const bool r = wwait(&bars->p_full[t], t ? pph[1] : pph[0]);
+        if (t) pph[1] ^= 1; else pph[0] ^= 1;
+        tc_fence_after();
+        return r;
+      };
+      PxWalk walk(bars);
+      PxSeg w;
+      uint32_t g = 0;  // key tiles of earlier segments (ring position)
+      uint32_t seg_i = 0;
+      bool ok = true;
+      for (; ok && walk.next(p, w); ++seg_i, g += w.nt) {
+        const int nt = w.nt;  // (one at least)
+        if (!wwait(&bars->q_full, seg_i & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (!w.wide) {
+          // slots take the tiles in turn: tile x in slot x & 1
+          for (int x = 0; x < 2 && x < nt; ++x) {
+            if (!wait_k(g + x)) {
+              ok = false;
+              break;
+            }
+            qk(x, 0, (g + x) % KST);
+            commit(&bars->s_full[x]);
+            commit(&bars->k_empty[(g + x) % KST]);
+            if (x + 1 == nt) commit(&bars->q_empty);
+          }
+          for (int x = 0; ok && x < nt; ++x) {
+            const int t = x & 1;
+            if (!wait_p(t) || !wait_v(g + x)) {
+              ok = false;
+              break;
+            }
+            pv(t, (g + x) % VST, x < 2);
+            commit(&bars->v_empty[(g + x) % VST]);
+            if (x + 2 >= nt) {
+              commit(&bars->pv_done[t]);
+            } else {
+              // S of this slot overwrites the columns P was read from; one thread's MMAs run in order
+              if (!wait_k(g + x + 2)) {
+                ok = false;
+                break;
+              }
+              qk(t, 0, (g + x + 2) % KST);
+              commit(&bars->s_full[t]);
+              commit(&bars->k_empty[(g + x + 2) % KST]);
+              if (x + 3 == nt) commit(&bars->q_empty);  // the segment's last S
+            }
+          }
+        } else {
+          if (!wait_k(g)) {
+            ok = false;
+            break;
+          }
+          qk(0, 0, g % KST);
+          commit(&bars->s_full[0]);
+          qk(1, 1, g % KST);
+          commit(&bars->s_full[1]);
+          commit(&bars->k_empty[g % KST]);
+          if (nt == 1) commit(&bars->q_empty);
+          for (int x = 0; ok && x < nt; ++x) {
+            const uint32_t sv = (g + x) % VST, sk = (g + x + 1) % KST;
+            const bool more = x + 1 < nt;
+            for (int t = 0; t < 2; ++t) {
+              if (!wait_p(t) || (t == 0 && !wait_v(g + x))) {
+                ok = false;
+                break;
+              }
+              pv(t, sv, x == 0);
+              if (t == 1) commit(&bars->v_empty[sv]);
+              if (more) {
+                if (t == 0 && !wait_k(g + x + 1)) {
+                  ok = false;
+                  break;
+                }
+                qk(t, t, sk);
+                commit(&bars->s_full[t]);
+              } else {
+                commit(&bars->pv_done[t]);
+              }
+            }
+            if (ok && more) {
+              commit(&bars->k_empty[sk]);
+              if (x + 2 == nt) commit(&bars->q_empty);
+            }
+          }
+        }
+      }
+      if (!ok && leader) fail(SITE_PX_MMA);
+      commit(&bars->drain);  // every MMA must finish before TMEM is released
+      mbar_wait(&bars->drain, 0, tmo_unwind);
+    }
+  } else {
+    // ======================= softmax: warps 0-3 (slot 0), 4-7 (slot 1) =======================
+    warpgroup_reg_alloc<C::SOFTMAX_REGS>();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * C::SLOT_COLS;
+    const uint32_t tO = tS + C::O_OFF;
+    const float2 c2 = make_float2(p.c, p.c);
+    // The reference maximum m is raised only when a row's maximum climbs more than this above
+    // it; until then the exponentials stay below 2^8 and carry one constant factor that O / l
+    // cancels.
+    constexpr float kRescaleSlack = 8.f;
+    bool ok = true;
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+    };
+    PxWalk walk(bars);
+    PxSeg w;
+    uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
+    uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
+    uint32_t gkv = 0;   // ring position at the segment's start
+    while (walk.next(p, w)) {
+      // this thread's row: sequence, and row of its R; -1: none
+      const int tile = w.tile + (w.wide ? t : 0);
+      int seq, rr;
+      if (p.R <= kPxTile) {
+        const int q = r / p.R;
+        seq = w.item.s0 + tile * p.spt + q;
+        rr = r - q * p.R;
+        if (q >= p.spt || seq >= w.item.s1) rr = -1;
+      } else {
+        const int q = tile / p.TS;
+        seq = w.item.s0 + q;
+        rr = (tile - q * p.TS) * kPxTile + r;
+        if (rr >= p.R) rr = -1;
+      }
+      const bool valid = rr >= 0;
+      const bool has_rows = __any_sync(0xffffffffu, valid);
+      // keys of the item that the row sees; rows of nobody are not masked
+      int sees = 0x7fffffff;
+      if (valid) {
+        const int S = px_len(p, seq);
+        sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w.item.k1) - w.item.k0;
+      }
+      const int step = w.wide ? 1 : 2;
+      const int x_first = w.wide ? 0 : t;
+      const int mine = w.nt <= x_first ? 0 : (w.nt - x_first + step - 1) / step;  // tiles of this slot
+      float m = -INFINITY;
+      float l = 0.f;   // sum of the unrounded p: the lse's
+      float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
+
+      for (int i = 0; i < mine; ++i, ++cnt) {
+        const int x = x_first + i * step;  // tile of the segment
+        const int key0 = (w.x0 + x) * kPxTile;  // from k0
+        if (!wwait(&bars->s_full[t], cnt & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (has_rows) {
+          uint32_t raw[4][32];
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, raw[cc]);
+          tmem_ld_wait();
+          float s[128];
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(raw[k >> 5][k & 31]);
+          if (__any_sync(0xffffffffu, sees < key0 + kPxTile)) {
+            const int left = sees - key0;
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (k >= left) s[k] = -INFINITY;
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float a = fmax3(s[16 * k], s[16 * k + 1], s[16 * k + 2]);
+#pragma unroll
+            for (int e = 3; e < 15; e += 2) a = fmax3(a, s[16 * k + e], s[16 * k + e + 1]);
+            mx8[k] = fmaxf(a, s[16 * k + 15]);
+          }
+          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+          const float m_tile = mx * p.c;
+          const float m_new = (m_tile > m + kRescaleSlack) ? m_tile : m;
+          const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+          const float alpha = valid ? ex2_approx(m - m_use) : 1.f;
+          // the largest p is not 1 against a stale reference: O's normaliser counts it as the
+          // bf16 product sees it, so that a nearly one-hot row is not off by its rounding
+          const float p_top = ex2_approx(fmaf(mx, p.c, -m_use));
+          const float p_top_err = __bfloat162float(__float2bfloat16_rn(p_top)) - p_top;
+          const float2 nm2 = make_float2(-m_use, -m_use);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int e = cc * 32 + 2 * k;
+              const float2 v = ffma2(make_float2(s[e], s[e + 1]), c2, nm2);
+              const float2 ev = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              acc[k & 3] = fadd2(acc[k & 3], ev);
+              pk[k] = pack_bf16x2(ev.x, ev.y);
+            }
+            tmem_st16(tS + cc * 16, pk);
+          }
+          const float2 at = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+          l = fmaf(l, alpha, at.x + at.y);
+          lc = fmaf(lc, alpha, p_top_err);
+          m = m_new;
+          // PV of this slot's previous tile is complete: S of this one was issued behind it
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int cc = 0; cc < D / 32; cc += 2) {
+              uint32_t o0[32], o1[32];
+              tmem_ld32(tO + cc * 32, o0);
+              tmem_ld32(tO + cc * 32 + 32, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 v0 = fmul2(make_float2(__uint_as_float(o0[k]), __uint_as_float(o0[k + 1])), al2);
+                const float2 v1 = fmul2(make_float2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), al2);
+                o0[k] = __float_as_uint(v0.x);
+                o0[k + 1] = __float_as_uint(v0.y);
+                o1[k] = __float_as_uint(v1.x);
+                o1[k + 1] = __float_as_uint(v1.y);
+              }
+              tmem_st32(tO + cc * 32, o0);
+              tmem_st32(tO + cc * 32 + 32, o1);
+            }
+          }
+        }
+        // V rows past the item's end hold whatever the pool or an earlier tile left there, and
+        // 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
+        const int rows_there = w.item.k1 - w.item.k0 - key0;
+        if (rows_there < kPxTile && (!w.wide || t == 0)) {
+          const uint32_t xg = gkv + x;
+          if (!wwait(&bars->v_full[xg % VST], (xg / VST) & 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* vt = sV + (xg % VST) * C::KV_BYTES;
+          for (int idx = r; idx < (kPxTile - rows_there) * C::KCH * 8; idx += 128) {
+            const int vr = rows_there + idx / (C::KCH * 8);
+            const int rem = idx % (C::KCH * 8);
+            *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::CHUNK_BYTES + vr * 128 + (rem & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
+      }
+      gkv += w.nt;
+      if (ok && mine > 0) {
+        if (!wwait(&bars->pv_done[t], ecnt & 1)) ok = false;
+        ++ecnt;
+        tc_fence_after();
+      }
+      if (!ok) fail(SITE_PX_SOFTMAX);
+
+      // ---- the segment's end: final rows, or a partial
+      if (!valid) {
+        m = -INFINITY;
+        l = lc = 0.f;
+      }
+      // A score that is NaN (a query that is not finite) may have left m at -inf, which would
+      // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
+      if (l != l) m = INFINITY;
+      const bool whole = w.own && w.item.k0 == 0 && w.from_start && w.to_end;
+      float m_all = m, sum = l + lc, lsum = l;
+      float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
+      if (!w.wide) {
+        ex[t * 128 + r] = m;
+        ex[(2 + t) * 128 + r] = l + lc;
+        if (t == 1) ex[4 * 128 + r] = l;
+      }
+      ok = vote_all(1, 256, ok);
+      if (!ok) break;  // all eight warps leave in the same segment
+      if (!w.wide) {
+        const float m0 = ex[r], m1 = ex[128 + r];
+        m_all = fmaxf(m0, m1);
+        const float m_use = m_all == -INFINITY ? 0.f : m_all;
+        f0 = ex2_approx(m0 - m_use);
+        f1 = ex2_approx(m1 - m_use);
+        sum = f0 * ex[256 + r] + f1 * ex[384 + r];
+        if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
+        f0 *= inv;
+        f1 *= inv;
+      }
+      if (has_rows) {
+        // the row's place in its item's partials, and in the output
+        const int at_row = p.units * p.R * w.item.s0 + (w.hu * (w.item.s1 - w.item.s0) + seq - w.item.s0) * p.R + rr;
+        const long long base = (static_cast<long long>(w.own) * p.V + cta % p.V) * p.area;
+        const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
+        const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + w.kvh) * p.R + rr;
+        // narrow: each slot's warps write half the columns of the joined O
+        const bool take0 = f0 != 0.f;
+        const bool take1 = !w.wide && w.nt > 1 && f1 != 0.f;
+        const uint32_t o_base = tmem + lane_base + (w.wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
+        const int c_lo = w.wide ? 0 : t * (D / 64), c_hi = w.wide ? D / 32 : c_lo + D / 64;
+#pragma unroll 1
+        for (int cc = c_lo; cc < c_hi; ++cc) {
+          uint32_t a[32], b[32];
+          tmem_ld32(o_base + cc * 32, a);
+          if (!w.wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
+          tmem_ld_wait();
+          float o[32];
+          // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
+            o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
+          }
+          if (!valid) continue;
+          if (whole) {
+            // (o may start on any 16-byte border)
+            __nv_bfloat16* dst = p.o + out_row * D + cc * 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(dst + 8 * q) =
+                  make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                             pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+          } else {
+            float* dst = p.part + part_row * D + cc * 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
+              st32(dst + 8 * q, v);
+            }
+          }
+        }
+        if (valid && (w.wide || t == 0)) {
+          if (whole) {
+            if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
+          } else {
+            p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
+          }
+          if (w.from_start && rr % kPxTile == 0) {
+            // this CTA begins the unit: the last with a share of it is the one whose share holds its end
+            const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
+            const size_t at = ((static_cast<size_t>(w.own) * p.B + seq) * p.Hkv + w.kvh) * p.TS + rr / kPxTile;
+            p.desc[at] = whole ? make_int2(kPxDone, 0)
+                               : make_int2(me << 16 | (static_cast<int>(last) - me + 1), static_cast<int>(base + at_row));
+          }
+        }
+      }
+      tc_fence_before();
+      // narrow: both slots' O have been read by all before either is overwritten, and the
+      // exchange area before the next segment fills it
+      if (!w.wide) named_bar_sync(2, 256);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of each row that is not written yet, of its prefix and of its own keys:
+// lse = log2 sum 2^(m_s - m) l_s + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. A row has
+// D / 4 lanes; 1, 2, 4 or 8 warps take its partials in turn, four of each in flight.
+struct PxJoin {
+  const float* part;
+  const float4* part_ml;
+  const int2* desc;
+  __nv_bfloat16* o;
+  float* lse;
+  long long rows;  // B * Hkv * R
+  int R, TS, per_kind;  // descriptors of a kind
+  int grid;        // CTAs of a line
+  long long part_rows;
+};
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
+  constexpr int LANES = D / 4, PER = 32 / LANES, IN = 4;
+  __shared__ float4 red[8][32];
+  __shared__ float red_m[8][PER], red_s[8][PER], red_l[8][PER];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_launch();
+  const int sub = warp % WPR, my = lane / LANES, col = lane % LANES * 4;
+  const long long row = (static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR) * PER + my;
+  int2 d[2] = {make_int2(kPxDone, 0), make_int2(kPxDone, 0)};
+  long long r_in_tile = 0;
+  if (row < p.rows) {
+    const unsigned head = static_cast<unsigned>(row) / static_cast<unsigned>(p.R);
+    const int rr = static_cast<int>(row - static_cast<long long>(head) * p.R);
+    const size_t at = static_cast<size_t>(head) * p.TS + rr / kPxTile;
+    d[0] = p.desc[at];
+    d[1] = p.desc[static_cast<size_t>(p.per_kind) + at];
+    r_in_tile = rr % kPxTile;
+  }
+  const bool todo = d[1].x != kPxDone;
+  int first[2], count[2];
+  long long at[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    first[k] = d[k].x >> 16;
+    count[k] = d[k].x & 0xffff;
+    at[k] = d[k].y + r_in_tile + static_cast<long long>(kPxUnit) * first[k];
+    // (after a wait that ran out a descriptor may be anything)
+    if (!todo || first[k] < 0 || first[k] + count[k] > p.grid || at[k] < 0 ||
+        at[k] + static_cast<long long>(kPxUnit) * count[k] >= p.part_rows + kPxUnit)
+      count[k] = 0;
+  }
+  const int n = count[0] + count[1];
+  RowJoin acc;
+  for (int i0 = sub; i0 < n; i0 += WPR * IN) {
+    float4 ml[IN], v[IN];
+#pragma unroll
+    for (int k = 0; k < IN; ++k) {
+      const int i = i0 + WPR * k;
+      ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const long long x = i < count[0] ? at[0] + static_cast<long long>(kPxUnit) * i
+                                         : at[1] + static_cast<long long>(kPxUnit) * (i - count[0]);
+        ml[k] = p.part_ml[x];
+        v[k] = *reinterpret_cast<const float4*>(p.part + x * D + col);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
+  }
+  if constexpr (WPR > 1) {
+    red[warp][lane] = acc.o;
+    if (col == 0) {
+      red_m[warp][my] = acc.m;
+      red_s[warp][my] = acc.s;
+      red_l[warp][my] = acc.l;
+    }
+    __syncthreads();
+    if (sub == 0)
+      for (int k = warp + 1; k < warp + WPR; ++k) acc.add(red_m[k][my], red_s[k][my], red_l[k][my], red[k][lane]);
+  }
+  if (todo && sub == 0) {
+    const float inv = acc.s == 0.f ? 0.f : 1.f / acc.s;
+    *reinterpret_cast<uint2*>(p.o + row * D + col) =
+        make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
+    if (p.lse && col == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+struct PxShape {
+  int R, spt, TS, V, grid;  // grid: CTAs of a line
+  long long area, desc;     // rows of partials of a place and kind, descriptors of a kind
+  size_t part, ml, all;     // bytes
+};
+
+// How the problem is laid out on `sms` SMs; false: its cost could reach 2^31.
+static bool px_shape(int B, int Hq, int Hkv, int T, int max_pages, int d, int sms, PxShape& s) {
+  const long long R = static_cast<long long>(Hq / Hkv) * T;
+  if (R >= (1ll << 30) || B * R * Hkv > (1ll << 30)) return false;
+  s.R = static_cast<int>(R);
+  s.spt = R <= kPxTile ? static_cast<int>(kPxTile / R) : 1;
+  s.TS = static_cast<int>((R + kPxTile - 1) / kPxTile);
+  // KV heads side by side, as many as fit: their keys lie beside one another in a page. Up to
+  // 16, and groups that leave few SMs over.
+  s.V = 1;
+  for (int h = Hkv < 16 ? Hkv : 16; h >= 1; --h)
+    if (Hkv % h == 0 && h <= sms && sms % h <= sms / 24) {
+      s.V = h;
+      break;
+    }
+  const long long units = Hkv / s.V, tiles = (static_cast<long long>(max_pages) * 16 + kPxTile - 1) / kPxTile;
+  // steps of a line: a row tile of every sequence over all keys, of its prefix and of its own
+  const long long rows = 2ll * B * s.TS * units;
+  if (rows > (1ll << 31) / kPxMostCost / tiles) return false;
+  s.grid = static_cast<int>(rows * tiles < sms / s.V ? rows * tiles : sms / s.V);
+  s.area = units * R * B + static_cast<long long>(kPxUnit) * s.grid;
+  s.desc = static_cast<long long>(B) * Hkv * s.TS;
+  s.part = static_cast<size_t>(2 * s.V * s.area) * d * 4;
+  s.ml = static_cast<size_t>(2 * s.V * s.area) * 16;
+  s.all = s.part + s.ml + static_cast<size_t>(2 * s.desc) * 8;
+  return true;
+}
+
+template <int D>
+static int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PxParams& p,
+                         const PxJoin& j, int grid, int sms, cudaStream_t stream) {
+  using C = PxCfg<D>;
+  auto kfn = prefix_kernel<D>;
+  // the attribute holds for the life of the device's context: asked for once per device
+  static std::atomic<unsigned long long> asked{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return record_cuda_failure(e);
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return record_cuda_failure(e);
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
+  if (rc != FA_OK) return rc;
+  // warps to a row: as many as rows leave of some 24 an SM
+  constexpr int PER = 128 / D;
+  const long long warps = (j.rows + PER - 1) / PER;
+  int wpr = 8;
+  while (wpr > 1 && warps * wpr > 24ll * sms) wpr >>= 1;
+  const dim3 blocks(static_cast<unsigned>((warps * wpr + 7) / 8));
+  if (wpr == 8) return launch_dependent(prefix_join_kernel<D, 8>, blocks, dim3(256), 0, stream, j);
+  if (wpr == 4) return launch_dependent(prefix_join_kernel<D, 4>, blocks, dim3(256), 0, stream, j);
+  if (wpr == 2) return launch_dependent(prefix_join_kernel<D, 2>, blocks, dim3(256), 0, stream, j);
+  return launch_dependent(prefix_join_kernel<D, 1>, blocks, dim3(256), 0, stream, j);
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || d < 1 || num_sms < 1 || Hq % Hkv != 0) return 0;
+  PxShape s;
+  return px_shape(B, Hq, Hkv, T, max_pages, d, num_sms, s) ? s.all : 0;
+}
+
+fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                                 const int* seqlens, const int* group_starts, const int* prefix_lens, int groups,
+                                 void* o, float* lse, int B, int Hq, int Hkv, int T, int max_pages, int page_size,
+                                 int num_pages, int d, float scale, int causal, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  auto mis = [](const void* x, uintptr_t m) { return (reinterpret_cast<uintptr_t>(x) & (m - 1)) != 0; };
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !group_starts || !prefix_lens || !o || !workspace)
+    return FA_ERR_INVALID_ARG;
+  if (mis(q, 16) || mis(k_pages, 16) || mis(v_pages, 16) || mis(o, 16) || mis(block_table, 4) || mis(seqlens, 4) ||
+      mis(group_starts, 4) || mis(prefix_lens, 4) || (lse && mis(lse, 4)) || mis(workspace, 256))
+    return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || max_pages < 1 || num_pages < 1 || groups < 1 || Hq % Hkv != 0 ||
+      !(scale > 0.f) || !(scale < INFINITY))
+    return FA_ERR_INVALID_ARG;
+  if (page_size != 16 || (d != 64 && d != 128) || groups > FA_PREFIX_MAX_GROUPS) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * 16 >= (1ll << 31) ||
+      static_cast<long long>(max_pages) * 16 > (1ll << 31) - 256 || static_cast<long long>(B) * Hq * T >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;  // (a key's index, rounded up to whole tiles, is a 32-bit number)
+  {
+    // o, lse and the workspace are written while other CTAs still read the rest
+    const long long rows = static_cast<long long>(B) * Hq * T, q_bytes = rows * d * 2;
+    const long long pool = 32ll * num_pages * Hkv * d, b4 = 4ll * B;
+    const struct { const void* p; long long n; } out[] = {{o, q_bytes}, {lse, rows * 4}, {workspace, static_cast<long long>(ws_bytes)}},
+        in[] = {{q, q_bytes}, {k_pages, pool}, {v_pages, pool}, {block_table, b4 * max_pages}, {seqlens, b4},
+                {group_starts, 4ll * groups + 4}, {prefix_lens, 4ll * groups}};
+    for (int i = 0; i < 3; ++i) {
+      for (const auto& x : in)
+        if (overlap(out[i].p, out[i].n, x.p, x.n)) return FA_ERR_INVALID_ARG;
+      for (int k = 0; k < i; ++k)
+        if (overlap(out[i].p, out[i].n, out[k].p, out[k].n)) return FA_ERR_INVALID_ARG;
+    }
+  }
+  const int sms = device_sm_count();
+  if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  PxShape s;
+  if (sms > 32767 || !px_shape(B, Hq, Hkv, T, max_pages, d, sms, s)) return FA_ERR_UNSUPPORTED;
+  if (ws_bytes < s.all) return FA_ERR_INVALID_ARG;
+  if (2 * s.V * s.area >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return FA_ERR_CUDA;
+  CUtensorMap tq, tk, tv;
+  {
+    // a KV head's R rows are dense; a box is the rows of a tile, of several sequences or of one
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.R, (cuuint64_t)Hkv, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)s.R * d * 2, (cuuint64_t)Hkv * s.R * d * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)(s.R < kPxTile ? s.R : kPxTile), 1, (cuuint32_t)s.spt};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    if (enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
+  }
+  for (int i = 0; i < 2; ++i) {
+    // one 16-token page of one KV head per box; L2 fetches what a row is, no neighbour's
+    const CUtensorMapL2promotion fetch = d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)num_pages * 16};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2};
+    cuuint32_t box[3] = {64, 1, 16};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (enc(i == 0 ? &tk : &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(i == 0 ? k_pages : v_pages),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PxParams p = {};
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.block_table = block_table;
+  p.seqlens = seqlens;
+  p.starts = group_starts;
+  p.prefix_lens = prefix_lens;
+  p.B = B;
+  p.G = groups;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.R = s.R;
+  p.causal = causal ? 1 : 0;
+  p.spt = s.spt;
+  p.TS = s.TS;
+  p.V = s.V;
+  p.units = Hkv / s.V;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.c = scale * kLog2e;
+  p.cost = d == 128 ? PxCost{4, 5, 3, 6} : PxCost{3, 4, 3, 6};
+  p.area = s.area;
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float4*>(ws + s.part);
+  p.desc = reinterpret_cast<int2*>(ws + s.part + s.ml);
+  p.err = device_error_word();
+  if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  p.timeout_ns = wait_timeout_ns();
+  const PxJoin j = {p.part, p.part_ml, p.desc, p.o, lse, static_cast<long long>(B) * Hkv * s.R, s.R, s.TS,
+                    static_cast<int>(s.desc), s.grid, 2 * s.V * s.area};
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return static_cast<fa_status>(d == 128 ? launch_prefix<128>(tq, tk, tv, p, j, s.V * s.grid, sms, cs)
+                                         : launch_prefix<64>(tq, tk, tv, p, j, s.V * s.grid, sms, cs));
+}
+
+}  // extern "C"

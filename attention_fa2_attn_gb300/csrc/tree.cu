@@ -47,6 +47,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "join.cuh"
 #include "launch.cuh"
 
 namespace fa {
@@ -243,27 +244,6 @@ struct TrWalk {
   }
 };
 
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// 32 bytes in one store: a warp whose threads each write a row of their own spends a
-// wavefront per row and store, so half as many as with 16 bytes.
-__device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // The other CTAs of the cluster: a barrier for all their threads, and reads of their shared
 // memory at the place that `p` has in this CTA's.
 __device__ __forceinline__ void cluster_sync() {
@@ -285,19 +265,6 @@ __device__ __forceinline__ int ld_cluster_int(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(nthreads), "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 // 32 visibility bits of a row for keys off .. off + 31, counted from the first node
 // (negative: committed text). `row`: the row's mask words, n nodes.
 __device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, int off) {
@@ -315,22 +282,6 @@ __device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, in
   const int left = n - off;  // nodes from here on
   return left < 32 ? v & ((1u << left) - 1u) : v;
 }
-
-// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
-// maximum is +inf (its scores were NaN) makes all of them NaN.
-struct TrRow {
-  float m = -INFINITY, s = 0.f, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
-  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
-    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
-    const float mn = fmaxf(m, m2);
-    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
-    s = s * fa + s2 * fb;
-    l = l * fa + l2 * fb;
-    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
-    m = mn;
-  }
-};
 
 template <int D, bool WIDE, bool CL>
 __global__ void __launch_bounds__(384, 1)
@@ -1010,7 +961,7 @@ __global__ void __launch_bounds__(384, 1)
       bool all = true;
       for (int c = 0; c < p.C; ++c) all &= ld_cluster_int(in_cta(&bars->finished, c)) != 0;
       for (int row = rank * per + warp * PER + my; all && row < last; row += 8 * PER) {
-        TrRow acc;
+        RowJoin acc;
         for (int c0 = 0; c0 < p.C; c0 += 4) {  // four CTAs' loads in flight
           float4 ml[4], o[4];
 #pragma unroll
@@ -1138,7 +1089,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       ml = part_ml[row_at];
       v = *reinterpret_cast<const float4*>(part + row_at * D + col);
     };
-    auto put = [&](const TrRow& r, int row) {
+    auto put = [&](const RowJoin& r, int row) {
       const float inv = r.s == 0.f ? 0.f : 1.f / r.s;
       const size_t out = static_cast<size_t>(un.row0) + row;
       *reinterpret_cast<uint2*>(o + out * D + col) =
@@ -1147,7 +1098,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
     };
     if (un.parts <= kTrFewParts) {
       const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
-      TrRow acc[2];
+      RowJoin acc[2];
       float4 ml[kTrFewParts][2], v[kTrFewParts][2];
 #pragma unroll
       for (int k = 0; k < kTrFewParts; ++k)
@@ -1167,7 +1118,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       constexpr int IN = 4;
       const int sub = warp & (wpr - 1);
       const int row = (item - un.first_item) * many_step + warp / wpr * PER + my;
-      TrRow acc;
+      RowJoin acc;
       for (int i0 = sub; i0 < un.parts; i0 += wpr * IN) {
         float4 ml[IN], v[IN];
 #pragma unroll

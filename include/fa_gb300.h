@@ -91,6 +91,7 @@ typedef enum {
 #define FA_TREE_MASK_MAX_T 8192    /* nodes of a tree in fa_tree_mask */
 #define FA_TREE_MASK_MAX_B 65535   /* trees of a call */
 #define FA_PAGES_MAX 4194304       /* pages of a pool in fa_pages_free and fa_pages_compact */
+#define FA_PREFIX_MAX_GROUPS 4096  /* groups of a call of fa_prefix_decode_paged */
 #define FA_ROPE_MAX_AXES 8         /* axes of the positions in the fa_rope_axes calls */
 
 /* Library version, major*10000 + minor*100 + patch. */
@@ -575,6 +576,38 @@ FA_API fa_status fa_tree_decode_paged(const void* q, const void* k_pages, const 
  * form and need more. What holds for every B, Hkv and max_pages is
  *   num_sms * (2 * rows * (4 * d + 16) + 16),  rows = 128 where Hq / Hkv * T <= 128, else 256. */
 FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
+
+/*
+ * fa_prefix_decode_paged -- fa_decode_paged for a batch whose sequences share prefixes (forked ones, or requests
+ * behind one prompt): the shared keys are read once for all of a group.
+ *   Group g is sequences group_starts[g] .. group_starts[g + 1] - 1. Their first prefix_lens[g] keys are the same:
+ *   their rows of block_table begin with the same pages, as many as these keys fill. Those whole pages (of what the
+ *   first of them has) are read through its row, for all of the group's queries at once; what follows through each
+ *   sequence's own. A group of one sequence, and sequences in no group, are read by themselves.
+ *   group_starts [groups + 1] int32 (device), not falling, in [0, B]: where they are not, FA_ERR_BOUNDS is recorded and
+ *   every sequence is read by itself, so that the result is the same. prefix_lens [groups] int32 (device): any value,
+ *   0 and less for none. 1 <= groups <= FA_PREFIX_MAX_GROUPS.
+ *   q, pools, block_table, seqlens, o, lse (may be NULL), scale, causal: as fa_decode_paged, and the same result, for
+ *   any Hq / Hkv and T with B * Hq * T <= 2^30. d in {64, 128}, page_size == 16.
+ *   workspace: at least fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count) bytes, 256-byte aligned; its
+ *   contents need no initialisation, and calls that may overlap on the GPU need one each. o, lse and the workspace may
+ *   overlap no other argument (FA_ERR_INVALID_ARG).
+ *   Keys and values inside a sequence must be finite; pool rows past a sequence's end are never used, whatever they
+ *   hold. A query row with a score that is NaN or +inf gets NaN in O and lse; scores of -inf weigh nothing, and a row
+ *   that has no other gets what one without keys gets: O = 0 and lse = -inf.
+ *   A table entry outside [0, num_pages) is not dereferenced: FA_ERR_BOUNDS is recorded and the output of the
+ *   sequences that it belongs to is undefined. Lengths are clamped to [0, max_pages * 16].
+ */
+FA_API fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                        const int* block_table, const int* seqlens, const int* group_starts,
+                                        const int* prefix_lens, int groups, void* o, float* lse, int B, int Hq,
+                                        int Hkv, int T, int max_pages, int page_size, int num_pages, int d,
+                                        float scale, int causal, void* workspace, size_t ws_bytes, void* stream);
+
+/* fa_prefix_workspace_bytes -- fp32 partials (O, max, sums): two rows for each query row, and 512 for each CTA that the
+ * call launches on num_sms SMs, 4 * d + 16 bytes each; and 16 bytes for each 128 rows of a sequence and KV head. 0 for
+ * sizes that the call does not take. */
+FA_API size_t fa_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
 
 /*
  * fa_get_last_device_error -- synchronise `stream`, read and clear the

@@ -99,6 +99,33 @@ def test_rope_axes(L):
     _cases(L.fa_rope_axes_append_paged, base, wrong)
 
 
+PREFIX = dict(q=P, kp=P, vp=P, table=P, seqlens=P, starts=P, lens=P, groups=3, o=P, lse=None, B=2, Hq=4, Hkv=2, T=3, max_pages=64,
+              page_size=16, num_pages=9, d=64, scale=0.125, causal=1, ws=P, ws_bytes=1 << 40, stream=None)
+
+
+def test_prefix(L):
+    ptrs = ("q", "kp", "vp", "table", "seqlens", "starts", "lens", "o", "ws")
+    wrong = [({n: None}, INV) for n in ptrs] + [({n: ODD}, INV) for n in ptrs + ("lse",)]
+    wrong += [({n: 0}, INV) for n in ("B", "Hq", "Hkv", "T", "max_pages", "num_pages", "groups")]
+    wrong += [({"Hq": 5}, INV), ({"scale": 0.0}, INV), ({"scale": math.nan}, INV), ({"scale": math.inf}, INV), ({"d": 96}, UNS),
+              ({"page_size": 32}, UNS), ({"num_pages": 1 << 27}, UNS), ({"max_pages": (1 << 27) - 1}, UNS),
+              ({"B": 1 << 20, "T": 1 << 10}, UNS), ({"groups": _lib.FA_PREFIX_MAX_GROUPS + 1}, UNS)]
+    for out in ("o", "lse", "ws"):
+        wrong += [({out: AT, other: AT, "ws_bytes": 256}, INV) for other in ("q", "kp", "vp", "table", "seqlens", "starts", "lens")]
+        wrong += [({out: AT, other: AT, "ws_bytes": 256}, INV) for other in ("o", "lse", "ws") if other != out]
+    # the last entry of the groups' starts
+    wrong += [({"o": AT, "starts": ctypes.c_void_p((1 << 20) - 12)}, INV)]
+    _cases(L.fa_prefix_decode_paged, PREFIX, wrong)
+
+
+def test_prefix_workspace(L):
+    assert L.fa_prefix_workspace_bytes(0, 4, 2, 3, 4, 64, 152) == 0 and L.fa_prefix_workspace_bytes(1, 5, 2, 3, 4, 64, 152) == 0
+    # 64 sequences of 8 heads on each of 8 KV heads: two partial rows each, 512 for each of 152 CTAs, and 16 bytes a head
+    assert L.fa_prefix_workspace_bytes(64, 64, 8, 1, 512, 128, 152) == (2 * 4096 + 512 * 152) * (4 * 128 + 16) + 16 * 64 * 8
+    # a line's cost is an int: 2^20 sequences over 2^20 keys each
+    assert L.fa_prefix_workspace_bytes(1 << 20, 1, 1, 1, 1 << 16, 64, 152) == 0
+
+
 def test_pair_axis():
     assert fa.fa_rope_pair_axis((2, 1, 1), device="cpu").tolist() == [0, 0, 1, 2]
     assert fa.fa_rope_pair_axis((3, 2, 2), cyclic=True, device="cpu").tolist() == [0, 1, 2, 0, 1, 2, 0]
@@ -118,6 +145,7 @@ def test_python_calls_refuse_cpu_tensors_and_other_objects():
     for bad in (lambda: fa.fa_pages_fork(i2, i, i, i, i), lambda: fa.fa_pages_fork(1, 2, 3, 4, 5), lambda: fa.fa_pages_copy(pool, pool, i, i),
                 lambda: fa.fa_pages_copy(None, pool, i, i), lambda: fa.fa_pages_copy(1, 2, 3, 4, 5), lambda: fa.fa_pages_free(i2, i, i),
                 lambda: fa.fa_pages_free(None, i, None), lambda: fa.fa_pages_compact(i2, i, i), lambda: fa.fa_pages_compact(0, 1, 2),
+                lambda: fa.fa_prefix_decode_paged(x, pool, pool, i2, i, i, i), lambda: fa.fa_prefix_decode_paged(1, 2, 3, 4, 5, 6, 7),
                 lambda: fa.fa_rope_axes(x, x, i3, f, i), lambda: fa.fa_rope_axes_bwd(None, x, i3, f, i),
                 lambda: fa.fa_rope_axes_append_paged(x, x, x, i3, i2, f, i, pool, pool)):
         with pytest.raises(ValueError):
@@ -126,7 +154,7 @@ def test_python_calls_refuse_cpu_tensors_and_other_objects():
 
 def test_limits_are_those_of_the_header():
     text = open(_lib._HEADER).read()
-    for name in ("FA_PAGES_MAX", "FA_ROPE_MAX_AXES"):
+    for name in ("FA_PAGES_MAX", "FA_PREFIX_MAX_GROUPS", "FA_ROPE_MAX_AXES"):
         assert f"#define {name} {getattr(_lib, name)} " in text
 
 
