@@ -52,6 +52,7 @@ enum ErrSite : unsigned {
   SITE_PX_TABLE = 32,
   SITE_PX_GROUPS = 33,
   SITE_PX_SMEM = 34,
+  SITE_PX_WALK = 35,
 };
 
 __device__ __forceinline__ void record_error(unsigned* err, unsigned code, unsigned site) {

@@ -56,13 +56,13 @@ struct PxCfg {
   static constexpr int OFF_K = 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + K_STAGES * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + V_STAGES * KV_BYTES;
-  static constexpr int OFF_EX = OFF_BAR + 384;
+  static constexpr int OFF_EX = OFF_BAR + 512;
   static constexpr int SMEM = OFF_EX + kPxTile * 5 * 4;
   static_assert(SMEM <= 232448, "shared memory of an SM");
   static_assert(OFF_BAR - OFF_K >= (2 * FA_PREFIX_MAX_GROUPS + 1) * 4, "the groups, before the rings are in use");
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
-  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, K producer, MMA issuer, V producer, an idle warp
+  static constexpr int THREADS = 384;  // 2 x 4 softmax warps, K producer, MMA issuer, V producer, the walk
   static constexpr int SOFTMAX_REGS = 192;  // 256 * 192 + 128 * 120 = 384 * 168
   static constexpr int AUX_REGS = 120;
 };
@@ -98,19 +98,35 @@ struct PxParams {
 };
 constexpr int kPxDone = -1;  // the rows are written
 
+// A run of steps of one unit inside a CTA's share, as all roles get it.
+struct PxSeg {
+  int s0, n;   // the item's sequences
+  int k0, k1;  // its keys
+  int tile;    // first row tile of the unit
+  int hu;      // KV head of the place
+  int x0, nt;  // first key tile and how many; none: the share is done
+  int flags;
+  int ctas;    // CTAs that share the unit, from the one that begins it on (known to that one)
+  __device__ __forceinline__ bool wide() const { return flags & 1; }
+  __device__ __forceinline__ bool own() const { return flags & 2; }  // a sequence's own keys
+  __device__ __forceinline__ bool from_start() const { return flags & 4; }
+  __device__ __forceinline__ bool to_end() const { return flags & 8; }
+};
+constexpr int kPxQueue = 3;  // segments on their way from the warp that walks the share to the others
+constexpr int kPxReaders = 11;  // warps that take them: producers, MMA issuer, softmax
+
 struct PxBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[6], v_full[6], k_empty[6], v_empty[6];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t drain;
+  uint64_t seg_full[kPxQueue], seg_empty[kPxQueue];
   uint32_t tmem_base;
   int abort_flag;
-  // where this CTA's share begins
-  int it0, off0, group0, begin, end, total, grid;
-  int no_groups;  // the groups are not what they should be: every sequence by itself
-  PxCost cost;
+  int it0, off0, group0;  // where this CTA's share begins
+  PxSeg seg[kPxQueue];
 };
-static_assert(sizeof(PxBars) <= 384, "barrier area");
+static_assert(sizeof(PxBars) <= 512, "barrier area");
 
 __device__ __forceinline__ int px_len(const PxParams& p, int b) {
   return max(0, min(__ldg(p.seqlens + b), p.max_pages * 16));
@@ -143,65 +159,53 @@ __device__ __forceinline__ PxItem px_sequence(const PxParams& p, int b, int pref
   return PxItem{b, b + 1, prefix, px_len(p, b), p.TS};
 }
 
-// A run of steps of one unit inside a CTA's share.
-struct PxSeg {
-  PxItem item;
-  int hu, kvh;   // KV head of the place, and of all
-  int tile;      // first row tile
-  bool wide, own;  // own: a sequence's own keys
-  int x0, nt;    // first key tile and how many
-  bool from_start, to_end;
-  int unit_end;  // where the unit ends on the cost line
-};
+// The group that b is in, the last that begins at or before it: its first and last sequence
+// and its prefix for a sequence in it, 0 for others. `g`: a group at or before it.
+__device__ __forceinline__ int px_prefix_of(const PxParams& p, int b, int& g) {
+  while (g + 1 < p.G && __ldg(p.starts + g + 1) <= b) ++g;
+  const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
+  return b >= s0 && b < s1 ? px_prefix(p, s0, s1, __ldg(p.prefix_lens + g)) : 0;
+}
 
-// Walks a share segment by segment; each role walks by itself. Items: the groups, then the
-// sequences.
+// Walks a share segment by segment. Items: the groups, then the sequences.
 struct PxWalk {
   int it, off, at, g;  // item, cost into it, cost into the line, the group that is looked at
-  const volatile PxBars* s;
-  __device__ __forceinline__ PxWalk(const PxBars* bars)
-      : it(bars->it0), off(bars->off0), at(bars->begin), g(bars->group0), s(bars) {}
+  int end, total, shares;
+  bool no_groups;
+  PxCost c;
   __device__ __forceinline__ PxItem item(const PxParams& p, int i) {
-    const bool none = s->no_groups;
     if (i < p.G) {
       const int s0 = __ldg(p.starts + i), s1 = __ldg(p.starts + i + 1);
-      return none ? PxItem{0, 0, 0, 0, 0} : px_group(p, s0, s1, px_prefix(p, s0, s1, __ldg(p.prefix_lens + i)));
+      return no_groups ? PxItem{0, 0, 0, 0, 0} : px_group(p, s0, s1, px_prefix(p, s0, s1, __ldg(p.prefix_lens + i)));
     }
-    const int b = i - p.G;
-    int prefix = 0;
-    if (!none) {
-      while (g + 1 < p.G && __ldg(p.starts + g + 1) <= b) ++g;
-      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
-      if (b >= s0 && b < s1) prefix = px_prefix(p, s0, s1, __ldg(p.prefix_lens + g));
-    }
-    return px_sequence(p, b, prefix);
+    return px_sequence(p, i - p.G, no_groups ? 0 : px_prefix_of(p, i - p.G, g));
   }
-  __device__ __forceinline__ bool next(const PxParams& p, PxSeg& w) {
-    const PxCost c = {s->cost.narrow_step, s->cost.narrow_front, s->cost.wide_step, s->cost.wide_front};
-    const int end = s->end;
-    int from, to, j0, j1, cost;
+  __device__ __forceinline__ bool next(const PxParams& p, int me, PxSeg& w) {
+    PxItem x;
+    int from, to, j0, j1, cost, unit_end;
+    bool wide;
     do {
       if (at >= end) return false;
-      w.item = item(p, it);
-      const int head = w.item.head(c);
+      x = item(p, it);
+      const int head = x.head(c);
       if (head == 0) {  // nothing to do (its cost is 0)
         ++it;
         off = 0;
         j0 = j1 = 0;
         continue;
       }
-      w.own = it >= p.G;
       w.hu = off / head;
-      const int rest = off - w.hu * head, pair = w.item.wide(c), u = min(w.item.tiles / 2, rest / pair);
+      const int rest = off - w.hu * head, pair = x.wide(c), u = min(x.tiles / 2, rest / pair);
       w.tile = 2 * u;
-      w.wide = u < w.item.tiles / 2;
+      wide = u < x.tiles / 2;
       from = rest - u * pair;
-      cost = w.wide ? pair : w.item.narrow(c);
+      cost = wide ? pair : x.narrow(c);
       to = min(cost, from + end - at);
-      const int step = w.wide ? c.wide_step : c.narrow_step, front = w.wide ? c.wide_front : c.narrow_front;
+      const int step = wide ? c.wide_step : c.narrow_step, front = wide ? c.wide_front : c.narrow_front;
       j0 = from < front ? 0 : (from - front) / step;
       j1 = to < front ? 0 : (to - front) / step;
-      w.unit_end = at - from + cost;
+      unit_end = at - from + cost;
+      w.flags = (wide ? 1 : 0) | (it >= p.G ? 2 : 0) | (j0 == 0 ? 4 : 0) | (to == cost ? 8 : 0);
       off += to - from;
       at += to - from;
       if (off == head * p.units) {
@@ -210,12 +214,30 @@ struct PxWalk {
       }
       // a share that ends inside a unit's first step leaves all of it to the next CTA
     } while (j0 == j1);
-    const int per = w.wide ? 1 : 2;
-    w.kvh = w.hu * p.V + static_cast<int>(blockIdx.x) % p.V;
+    const int per = wide ? 1 : 2;
+    w.s0 = x.s0;
+    w.n = x.s1 - x.s0;
+    w.k0 = x.k0;
+    w.k1 = x.k1;
     w.x0 = j0 * per;
-    w.nt = min(w.item.key_tiles(), j1 * per) - w.x0;
-    w.from_start = j0 == 0;
-    w.to_end = to == cost;
+    w.nt = min(x.key_tiles(), j1 * per) - w.x0;
+    // the last CTA with a share of the unit is the one whose share holds its end
+    w.ctas = static_cast<int>((static_cast<long long>(unit_end) * shares - 1) / total) - me + 1;
+    return true;
+  }
+};
+
+// Takes the segments that the walking warp leaves, one after the other.
+struct PxTake {
+  uint32_t i = 0;
+  // a whole warp; false: the wait ran out
+  __device__ __forceinline__ bool next(PxBars* bars, PxSeg& w, uint64_t tmo, const volatile int* abort_flag) {
+    const uint32_t e = i % kPxQueue;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return false;
+    w = bars->seg[e];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->seg_empty[e]);
+    ++i;
     return true;
   }
 };
@@ -258,7 +280,12 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&bars->pv_done[t], 1);
     }
     mbar_init(&bars->drain, 1);
+    for (int e = 0; e < kPxQueue; ++e) {
+      mbar_init(&bars->seg_full[e], 1);
+      mbar_init(&bars->seg_empty[e], kPxReaders);
+    }
     bars->abort_flag = 0;
+    bars->it0 = bars->off0 = bars->group0 = 0;
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(&bars->tmem_base, 512);
@@ -266,110 +293,104 @@ __global__ void __launch_bounds__(384, 1)
 
   // ---- this CTA's share of its line's cost: a block-wide scan over the items. The groups go
   // through shared memory that the rings use later.
+  PxWalk walk;
   {
+    const int items = p.G + p.B;
+    const int per = (items + C::THREADS - 1) / C::THREADS;
+    const int lo = min(items, static_cast<int>(threadIdx.x) * per), hi = min(items, lo + per);
+    // a thread's first sequence, on its way while the groups are looked at
+    const int len = lo >= p.G && lo < hi ? px_len(p, lo - p.G) : 0;
     int* gs = reinterpret_cast<int*>(sK);  // [G + 1]: starts
     int* gp = gs + p.G + 1;                // [G]: prefixes
     bool bad = false;
     for (int g = threadIdx.x; g < p.G; g += C::THREADS) {
-      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
+      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1), asked = __ldg(p.prefix_lens + g);
       gs[g] = s0;
       if (g == p.G - 1) gs[p.G] = s1;
       const bool fine = 0 <= s0 && s0 <= s1 && s1 <= p.B;
       bad |= !fine;
-      gp[g] = fine ? px_prefix(p, s0, s1, __ldg(p.prefix_lens + g)) : 0;
+      gp[g] = fine ? px_prefix(p, s0, s1, asked) : 0;
     }
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
-    auto group_of = [&](int b) {  // the last that begins at or before b
-      int g = 0, hi = p.G;
-      while (hi - g > 1) {
-        const int mid = (g + hi) / 2;
-        if (gs[mid] <= b) g = mid; else hi = mid;
-      }
-      return g;
-    };
     auto item = [&](int i, int& g) {
       if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0} : px_group(p, gs[i], gs[i + 1], gp[i]);
       const int b = i - p.G;
-      if (bad) return px_sequence(p, b, 0);
-      if (g < 0) g = group_of(b);
-      while (g + 1 < p.G && gs[g + 1] <= b) ++g;
-      return px_sequence(p, b, b >= gs[g] && b < gs[g + 1] ? gp[g] : 0);
+      int prefix = 0;
+      if (!bad) {
+        if (g < 0) {  // the last that begins at or before b
+          int top = p.G;
+          for (g = 0; top - g > 1;) {
+            const int mid = (g + top) / 2;
+            if (gs[mid] <= b) g = mid; else top = mid;
+          }
+        }
+        while (g + 1 < p.G && gs[g + 1] <= b) ++g;
+        if (b >= gs[g] && b < gs[g + 1]) prefix = gp[g];
+      }
+      return PxItem{b, b + 1, prefix, i == lo ? len : px_len(p, b), p.TS};
     };
-    const int items = p.G + p.B;
-    const int per = (items + C::THREADS - 1) / C::THREADS;
-    const int lo = min(items, static_cast<int>(threadIdx.x) * per), hi = min(items, lo + per);
-    int steps = 0, mine = 0, g = -1;  // a line's whole cost is below 2^31
+    // steps of the items before this thread's, and their cost; a line's whole cost is below 2^31
+    int steps = 0, mine = 0, g = -1;
     for (int i = lo; i < hi; ++i) {
       const PxItem x = item(i, g);
       steps += x.head(PxCost{1, 0, 1, 0});
       mine += x.head(p.cost);
     }
-    // block-wide sums through the exchange area, which nothing uses yet
-    int* wsum = reinterpret_cast<int*>(ex);
-    auto scan = [&](int v, int& total) {
-      int inc = v;
+    steps *= p.units;
+    mine *= p.units;
+    int steps_inc = steps, inc = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, steps_inc, o);
+      if (lane >= o) {
+        inc += y;
+        steps_inc += z;
       }
-      if (lane == 31) wsum[warp] = inc;
-      __syncthreads();
-      int before = inc - v;
-      total = 0;
+    }
+    // totals per warp go through the exchange area, which nothing uses yet
+    int2* wsum = reinterpret_cast<int2*>(ex);
+    if (lane == 31) wsum[warp] = make_int2(inc, steps_inc);
+    __syncthreads();
+    int before = inc - mine, steps_before = steps_inc - steps, total = 0, all_steps = 0;
 #pragma unroll
-      for (int w = 0; w < 12; ++w) {
-        if (w < warp) before += wsum[w];
-        total += wsum[w];
+    for (int w = 0; w < 12; ++w) {
+      const int2 v = wsum[w];
+      if (w < warp) {
+        before += v.x;
+        steps_before += v.y;
       }
-      __syncthreads();
-      return before;
-    };
-    int all_steps, total;
-    scan(steps * p.units, all_steps);
+      total += v.x;
+      all_steps += v.y;
+    }
     const int grid = static_cast<int>(gridDim.x) / p.V;
     // lines of so few steps that a CTA has hardly more than one are cut by steps alone; a
     // share is a step's cost or more either way, so that every CTA between a unit's first and
     // last has a step of it
     const bool few = all_steps <= 2 * grid;
-    const PxCost cost = few ? PxCost{1, 0, 1, 0} : p.cost;
-    mine = (few ? steps : mine) * p.units;
-    const int before = scan(mine, total);
-    const int shares = few ? min(grid, max(1, all_steps)) : grid;
-    const int begin = me < shares ? static_cast<int>(static_cast<long long>(me) * total / shares) : total;
-    const int end = me < shares ? static_cast<int>((me + 1ll) * total / shares) : total;
-    if (threadIdx.x == 0) {
-      bars->begin = begin;
-      bars->end = end;
-      bars->total = total;
-      bars->grid = shares;
-      bars->cost = cost;
-      bars->no_groups = bad;
-      if (begin >= end) bars->it0 = bars->off0 = bars->group0 = 0;
+    walk.c = p.cost;
+    if (few) {
+      walk.c = PxCost{1, 0, 1, 0};
+      before = steps_before;
+      mine = steps;
+      total = all_steps;
     }
-    if (begin < end && begin >= before && begin < before + mine) {  // one thread: its items hold the share's start
-      int off = begin - before, i = lo;
+    walk.total = total;
+    walk.shares = few ? min(grid, max(1, all_steps)) : grid;
+    walk.no_groups = bad;
+    walk.at = me < walk.shares ? static_cast<int>(static_cast<long long>(me) * total / walk.shares) : total;
+    walk.end = me < walk.shares ? static_cast<int>((me + 1ll) * total / walk.shares) : total;
+    if (walk.at < walk.end && walk.at >= before && walk.at < before + mine) {  // one thread: its items hold the share's start
+      int off = walk.at - before, i = lo;
       g = -1;
       for (; i < hi; ++i) {
-        const int s = item(i, g).head(cost) * p.units;
+        const int s = item(i, g).head(walk.c) * p.units;
         if (off < s) break;
         off -= s;
       }
       bars->it0 = i;
       bars->off0 = off;
       bars->group0 = max(g, 0);
-    }
-    // rows that a kind has no partials of: somebody has to say so
-    for (int b = cta; b < p.B; b += gridDim.x) {
-      int gb = -1;
-      const PxItem x = item(p.G + b, gb);
-      const int n = p.Hkv * p.TS;
-      const size_t at = static_cast<size_t>(b) * n;
-      if (x.k0 == 0)
-        for (int i = threadIdx.x; i < n; i += C::THREADS) p.desc[at + i] = make_int2(0, 0);
-      if (x.k1 <= x.k0)
-        for (int i = threadIdx.x; i < n; i += C::THREADS) p.desc[static_cast<size_t>(p.B) * n + at + i] = make_int2(0, 0);
     }
   }
   fence_async_smem();  // the rings' memory was read and written by plain accesses
@@ -398,17 +419,23 @@ __global__ void __launch_bounds__(384, 1)
         if (is_k) tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(my_map);
       }
-      PxWalk walk(bars);
+      PxTake take;
       PxSeg w;
       uint32_t g = 0;  // key tiles loaded so far (ring position)
       uint32_t stage = 0, lap = 0;
       uint32_t q_loads = 0;
       const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
       bool ok = true;
-      while (ok && !*abort_flag && walk.next(p, w)) {
-        const int* trow = p.block_table + static_cast<size_t>(w.item.s0) * p.max_pages;
-        const int page0 = w.item.k0 >> 4;  // (k0 is a page's start)
-        const int n_pages = (w.item.k1 + 15) >> 4;
+      while (ok && !*abort_flag) {
+        if (!take.next(bars, w, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (w.nt == 0) break;
+        const int* trow = p.block_table + static_cast<size_t>(w.s0) * p.max_pages;
+        const int kvh = w.hu * p.V + cta % p.V;
+        const int page0 = w.k0 >> 4;  // (k0 is a page's start)
+        const int n_pages = (w.k1 + 15) >> 4;
         // a lane holds one of 32 entries, four tiles' worth; the next 32 are fetched meanwhile
         auto fetch = [&](int x) -> int {
           const int pg = page0 + (w.x0 + x) * 8 + lane;
@@ -421,13 +448,13 @@ __global__ void __launch_bounds__(384, 1)
         auto load_q = [&]() {
           if (lane == 0) {
             const int rows = min(p.R, kPxTile) * p.spt;  // of a box; those behind the batch's end are zeros
-            const int tiles = w.wide ? 2 : 1;
+            const int tiles = w.wide() ? 2 : 1;
             mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(tiles * C::KCH * rows * 128));
             for (int t = 0; t < tiles; ++t) {
               const int tile = w.tile + t, seq = tile / p.TS;
               for (int c = 0; c < C::KCH; ++c)
                 tma_load_4d(sQ + t * C::Q_BYTES + c * C::CHUNK_BYTES, &tmQ, &bars->q_full, c * 64,
-                            (tile - seq * p.TS) * kPxTile, w.kvh, w.item.s0 + seq * p.spt);
+                            (tile - seq * p.TS) * kPxTile, kvh, w.s0 + seq * p.spt);
             }
           }
           ++q_loads;
@@ -467,7 +494,7 @@ __global__ void __launch_bounds__(384, 1)
           __syncwarp();
           if (pi < npg)
             tma_load_3d(my_ring + stage * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, my_map, &my_full[stage], pc * 64,
-                        w.kvh, pe * 16);
+                        kvh, pe * 16);
           if (++stage == ST) {
             stage = 0;
             ++lap;
@@ -537,19 +564,24 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         return r;
       };
-      PxWalk walk(bars);
+      PxTake take;
       PxSeg w;
       uint32_t g = 0;  // key tiles of earlier segments (ring position)
       uint32_t seg_i = 0;
       bool ok = true;
-      for (; ok && walk.next(p, w); ++seg_i, g += w.nt) {
-        const int nt = w.nt;  // (one at least)
+      for (; ok; ++seg_i, g += w.nt) {
+        if (!take.next(bars, w, tmo, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int nt = w.nt;
+        if (nt == 0) break;
         if (!wwait(&bars->q_full, seg_i & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (!w.wide) {
+        if (!w.wide()) {
           // slots take the tiles in turn: tile x in slot x & 1
           for (int x = 0; x < 2 && x < nt; ++x) {
             if (!wait_k(g + x)) {
@@ -625,6 +657,46 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok && leader) fail(SITE_PX_MMA);
       commit(&bars->drain);  // every MMA must finish before TMEM is released
       mbar_wait(&bars->drain, 0, tmo_unwind);
+    } else {
+      // ======================= the walk =======================
+      // Lengths and groups come from L2 and a step of the walk takes some divisions, 0.9 us: one
+      // warp does it ahead of the others, which take the segments from shared memory.
+      if (lane == 0) {
+        walk.it = bars->it0;
+        walk.off = bars->off0;
+        walk.g = bars->group0;
+        bool ok = true;
+        for (uint32_t i = 0;; ++i) {
+          PxSeg w;
+          const bool more = walk.next(p, me, w);
+          if (!more) w.nt = 0;
+          const uint32_t e = i % kPxQueue;
+          if (i >= kPxQueue && !mbar_wait(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag)) {
+            ok = false;
+            break;
+          }
+          bars->seg[e] = w;
+          mbar_arrive(&bars->seg_full[e]);
+          if (!more) break;
+        }
+        if (!ok) fail(SITE_PX_WALK);
+      }
+      __syncwarp();
+      // rows that a kind has no partials of: somebody has to say so
+      for (int b = cta; b < p.B; b += gridDim.x) {
+        int gb = 0, top = p.G;
+        while (!walk.no_groups && top - gb > 1) {
+          const int mid = (gb + top) / 2;
+          if (__ldg(p.starts + mid) <= b) gb = mid; else top = mid;
+        }
+        const int prefix = walk.no_groups ? 0 : px_prefix_of(p, b, gb);
+        const int n = p.Hkv * p.TS;
+        const size_t at = static_cast<size_t>(b) * n;
+        if (prefix == 0)
+          for (int i = lane; i < n; i += 32) p.desc[at + i] = make_int2(0, 0);
+        if (px_len(p, b) <= prefix)
+          for (int i = lane; i < n; i += 32) p.desc[static_cast<size_t>(p.B) * n + at + i] = make_int2(0, 0);
+      }
     }
   } else {
     // ======================= softmax: warps 0-3 (slot 0), 4-7 (slot 1) =======================
@@ -643,24 +715,31 @@ __global__ void __launch_bounds__(384, 1)
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
     };
-    PxWalk walk(bars);
+    PxTake take;
     PxSeg w;
     uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
     uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
     uint32_t gkv = 0;   // ring position at the segment's start
-    while (walk.next(p, w)) {
+    // where a thread's row lies in a tile of whole sequences
+    const int seq_in = p.R <= kPxTile ? r / p.R : 0, row_in = p.R <= kPxTile ? r - seq_in * p.R : r;
+    while (true) {
+      if (!take.next(bars, w, tmo, abort_flag)) {
+        ok = false;
+        w = PxSeg{};  // nothing, and out by the vote at its end
+        fail(SITE_PX_SOFTMAX);
+      } else if (w.nt == 0) {
+        break;
+      }
       // this thread's row: sequence, and row of its R; -1: none
-      const int tile = w.tile + (w.wide ? t : 0);
-      int seq, rr;
+      const int tile = w.tile + (w.wide() ? t : 0);
+      int seq = w.s0, rr = row_in;
       if (p.R <= kPxTile) {
-        const int q = r / p.R;
-        seq = w.item.s0 + tile * p.spt + q;
-        rr = r - q * p.R;
-        if (q >= p.spt || seq >= w.item.s1) rr = -1;
+        seq += tile * p.spt + seq_in;
+        if (seq_in >= p.spt || seq >= w.s0 + w.n) rr = -1;
       } else {
         const int q = tile / p.TS;
-        seq = w.item.s0 + q;
-        rr = (tile - q * p.TS) * kPxTile + r;
+        seq += q;
+        rr += (tile - q * p.TS) * kPxTile;
         if (rr >= p.R) rr = -1;
       }
       const bool valid = rr >= 0;
@@ -668,11 +747,11 @@ __global__ void __launch_bounds__(384, 1)
       // keys of the item that the row sees; rows of nobody are not masked
       int sees = 0x7fffffff;
       if (valid) {
-        const int S = px_len(p, seq);
-        sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w.item.k1) - w.item.k0;
+        const int S = w.own() ? w.k1 : px_len(p, seq);
+        sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w.k1) - w.k0;
       }
-      const int step = w.wide ? 1 : 2;
-      const int x_first = w.wide ? 0 : t;
+      const int step = w.wide() ? 1 : 2;
+      const int x_first = w.wide() ? 0 : t;
       const int mine = w.nt <= x_first ? 0 : (w.nt - x_first + step - 1) / step;  // tiles of this slot
       float m = -INFINITY;
       float l = 0.f;   // sum of the unrounded p: the lse's
@@ -761,8 +840,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         // V rows past the item's end hold whatever the pool or an earlier tile left there, and
         // 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
-        const int rows_there = w.item.k1 - w.item.k0 - key0;
-        if (rows_there < kPxTile && (!w.wide || t == 0)) {
+        const int rows_there = w.k1 - w.k0 - key0;
+        if (rows_there < kPxTile && (!w.wide() || t == 0)) {
           const uint32_t xg = gkv + x;
           if (!wwait(&bars->v_full[xg % VST], (xg / VST) & 1)) {
             ok = false;
@@ -797,17 +876,17 @@ __global__ void __launch_bounds__(384, 1)
       // A score that is NaN (a query that is not finite) may have left m at -inf, which would
       // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
       if (l != l) m = INFINITY;
-      const bool whole = w.own && w.item.k0 == 0 && w.from_start && w.to_end;
+      const bool whole = w.own() && w.k0 == 0 && w.from_start() && w.to_end();
       float m_all = m, sum = l + lc, lsum = l;
       float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
-      if (!w.wide) {
+      if (!w.wide()) {
         ex[t * 128 + r] = m;
         ex[(2 + t) * 128 + r] = l + lc;
         if (t == 1) ex[4 * 128 + r] = l;
       }
       ok = vote_all(1, 256, ok);
       if (!ok) break;  // all eight warps leave in the same segment
-      if (!w.wide) {
+      if (!w.wide()) {
         const float m0 = ex[r], m1 = ex[128 + r];
         m_all = fmaxf(m0, m1);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
@@ -823,20 +902,21 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (has_rows) {
         // the row's place in its item's partials, and in the output
-        const int at_row = p.units * p.R * w.item.s0 + (w.hu * (w.item.s1 - w.item.s0) + seq - w.item.s0) * p.R + rr;
-        const long long base = (static_cast<long long>(w.own) * p.V + cta % p.V) * p.area;
+        const int at_row = p.units * p.R * w.s0 + (w.hu * w.n + seq - w.s0) * p.R + rr;
+        const int kvh = w.hu * p.V + cta % p.V;
+        const long long base = (static_cast<long long>(w.own()) * p.V + cta % p.V) * p.area;
         const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
-        const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + w.kvh) * p.R + rr;
+        const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + kvh) * p.R + rr;
         // narrow: each slot's warps write half the columns of the joined O
         const bool take0 = f0 != 0.f;
-        const bool take1 = !w.wide && w.nt > 1 && f1 != 0.f;
-        const uint32_t o_base = tmem + lane_base + (w.wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
-        const int c_lo = w.wide ? 0 : t * (D / 64), c_hi = w.wide ? D / 32 : c_lo + D / 64;
+        const bool take1 = !w.wide() && w.nt > 1 && f1 != 0.f;
+        const uint32_t o_base = tmem + lane_base + (w.wide() ? t * C::SLOT_COLS : 0) + C::O_OFF;
+        const int c_lo = w.wide() ? 0 : t * (D / 64), c_hi = w.wide() ? D / 32 : c_lo + D / 64;
 #pragma unroll 1
         for (int cc = c_lo; cc < c_hi; ++cc) {
           uint32_t a[32], b[32];
           tmem_ld32(o_base + cc * 32, a);
-          if (!w.wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
+          if (!w.wide()) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
           tmem_ld_wait();
           float o[32];
           // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
@@ -865,25 +945,22 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         }
-        if (valid && (w.wide || t == 0)) {
+        if (valid && (w.wide() || t == 0)) {
           if (whole) {
             if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
           } else {
             p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
           }
-          if (w.from_start && rr % kPxTile == 0) {
-            // this CTA begins the unit: the last with a share of it is the one whose share holds its end
-            const long long last = (static_cast<long long>(w.unit_end) * bars->grid - 1) / bars->total;
-            const size_t at = ((static_cast<size_t>(w.own) * p.B + seq) * p.Hkv + w.kvh) * p.TS + rr / kPxTile;
-            p.desc[at] = whole ? make_int2(kPxDone, 0)
-                               : make_int2(me << 16 | (static_cast<int>(last) - me + 1), static_cast<int>(base + at_row));
+          if (w.from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
+            const size_t at = ((static_cast<size_t>(w.own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
+            p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w.ctas, static_cast<int>(base + at_row));
           }
         }
       }
       tc_fence_before();
       // narrow: both slots' O have been read by all before either is overwritten, and the
       // exchange area before the next segment fills it
-      if (!w.wide) named_bar_sync(2, 256);
+      if (!w.wide()) named_bar_sync(2, 256);
     }
   }
 
