@@ -26,6 +26,7 @@
 // K/V, the producer warp fetches 32 block-table entries at a time (one per
 // lane) one batch ahead, and issues one TMA box per 16-token page.
 #include "common.cuh"
+#include "warp_mma.cuh"
 
 namespace fa {
 
@@ -58,33 +59,6 @@ struct DecParams {
   unsigned* err;
   unsigned long long timeout_ns;
 };
-
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-
-// byte offset of (row, d) inside a tile stored as KCH chunks of [64 rows][128 B], 128-byte swizzle
-__device__ __forceinline__ uint32_t sw_off(int row, int d, int chunk_bytes) {
-  const int ch = d >> 6;
-  const int piece = (d & 63) >> 3;
-  return ch * chunk_bytes + row * 128 + ((piece ^ (row & 7)) << 4) + ((d & 7) << 1);
-}
 
 // Paged decode runs two CTAs per SM (3-stage ring, 96 KB each): with 16-token
 // pages a sequence is many small boxes, and two independent streams per SM keep

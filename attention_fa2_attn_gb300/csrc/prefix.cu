@@ -34,6 +34,7 @@
 
 #include "join.cuh"
 #include "launch.cuh"
+#include "warp_mma.cuh"
 
 namespace fa {
 
@@ -44,6 +45,7 @@ EncodeTiledFn get_encode_tiled();  // defined in api.cu
 
 constexpr int kPxTile = 128;  // rows of a tile, keys of a tile
 constexpr int kPxUnit = 2 * kPxTile;  // rows of a unit, at most
+constexpr int kPxSlim = 16;           // rows of a sequence whose own keys are taken as slim units, at most
 
 template <int D>
 struct PxCfg {
@@ -60,18 +62,20 @@ struct PxCfg {
   static constexpr int SMEM = OFF_EX + kPxTile * 5 * 4;
   static_assert(SMEM <= 232448, "shared memory of an SM");
   static_assert(OFF_BAR - OFF_K >= (2 * FA_PREFIX_MAX_GROUPS + 1) * 4, "the groups, before the rings are in use");
+  static_assert(8 * 8 * D * 4 <= Q_BYTES, "slim: eight warps' O for eight rows, in the second Q tile");
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
   static constexpr int THREADS = 384;  // 2 x 4 softmax warps, K producer, MMA issuer, V producer, the walk
-  static constexpr int SOFTMAX_REGS = 192;  // 256 * 192 + 128 * 120 = 384 * 168
-  static constexpr int AUX_REGS = 120;
+  static constexpr int SOFTMAX_REGS = 208;  // 256 * 208 + 128 * 88 = 384 * 168
+  static constexpr int AUX_REGS = 88;
 };
 
 // What shares are cut in: `step` for a step of a unit and, ahead of its first, `front` for what
 // it costs beside its keys.
 struct PxCost {
-  int narrow_step, narrow_front, wide_step, wide_front;
+  int narrow_step, narrow_front, wide_step, wide_front, own_step, own_front;  // own: narrow or slim
 };
+#define PX_BY_STEPS PxCost{1, 0, 1, 0, 1, 0}
 constexpr int kPxMostCost = 10;  // of a step with its unit's start
 
 struct PxParams {
@@ -107,10 +111,10 @@ struct PxSeg {
   int x0, nt;  // first key tile and how many; none: the share is done
   int flags;
   int ctas;    // CTAs that share the unit, from the one that begins it on (known to that one)
-  __device__ __forceinline__ bool wide() const { return flags & 1; }
-  __device__ __forceinline__ bool own() const { return flags & 2; }  // a sequence's own keys
-  __device__ __forceinline__ bool from_start() const { return flags & 4; }
-  __device__ __forceinline__ bool to_end() const { return flags & 8; }
+  __device__ __forceinline__ bool wide() const volatile { return flags & 1; }
+  __device__ __forceinline__ bool own() const volatile { return flags & 2; }  // a sequence's own keys
+  __device__ __forceinline__ bool from_start() const volatile { return flags & 4; }
+  __device__ __forceinline__ bool to_end() const volatile { return flags & 8; }
 };
 constexpr int kPxQueue = 3;  // segments on their way from the warp that walks the share to the others
 constexpr int kPxReaders = 11;  // warps that take them: producers, MMA issuer, softmax
@@ -141,11 +145,13 @@ struct PxItem {
   int s0, s1;  // its sequences
   int k0, k1;  // its keys
   int tiles;   // row tiles
+  bool own;    // a sequence's own keys
   __device__ __forceinline__ int key_tiles() const { return k1 > k0 ? (k1 - k0 + kPxTile - 1) / kPxTile : 0; }
   // cost of a wide and of a narrow unit, and of a KV head's units together
   __device__ __forceinline__ int wide(const PxCost& c) const { return c.wide_front + c.wide_step * key_tiles(); }
   __device__ __forceinline__ int narrow(const PxCost& c) const {
-    return c.narrow_front + c.narrow_step * ((key_tiles() + 1) / 2);
+    const int pairs = (key_tiles() + 1) / 2;
+    return own ? c.own_front + c.own_step * pairs : c.narrow_front + c.narrow_step * pairs;
   }
   __device__ __forceinline__ int head(const PxCost& c) const {
     return k1 > k0 ? tiles / 2 * wide(c) + (tiles & 1) * narrow(c) : 0;
@@ -153,10 +159,10 @@ struct PxItem {
 };
 __device__ __forceinline__ PxItem px_group(const PxParams& p, int s0, int s1, int prefix) {
   const int n = max(0, s1 - s0);
-  return PxItem{s0, s1, 0, prefix, p.R <= kPxTile ? (n + p.spt - 1) / p.spt : n * p.TS};
+  return PxItem{s0, s1, 0, prefix, p.R <= kPxTile ? (n + p.spt - 1) / p.spt : n * p.TS, false};
 }
 __device__ __forceinline__ PxItem px_sequence(const PxParams& p, int b, int prefix) {
-  return PxItem{b, b + 1, prefix, px_len(p, b), p.TS};
+  return PxItem{b, b + 1, prefix, px_len(p, b), p.TS, true};
 }
 
 // The group that b is in, the last that begins at or before it: its first and last sequence
@@ -176,7 +182,7 @@ struct PxWalk {
   __device__ __forceinline__ PxItem item(const PxParams& p, int i) {
     if (i < p.G) {
       const int s0 = __ldg(p.starts + i), s1 = __ldg(p.starts + i + 1);
-      return no_groups ? PxItem{0, 0, 0, 0, 0} : px_group(p, s0, s1, px_prefix(p, s0, s1, __ldg(p.prefix_lens + i)));
+      return no_groups ? PxItem{0, 0, 0, 0, 0, false} : px_group(p, s0, s1, px_prefix(p, s0, s1, __ldg(p.prefix_lens + i)));
     }
     return px_sequence(p, i - p.G, no_groups ? 0 : px_prefix_of(p, i - p.G, g));
   }
@@ -201,11 +207,12 @@ struct PxWalk {
       from = rest - u * pair;
       cost = wide ? pair : x.narrow(c);
       to = min(cost, from + end - at);
-      const int step = wide ? c.wide_step : c.narrow_step, front = wide ? c.wide_front : c.narrow_front;
+      const int step = wide ? c.wide_step : x.own ? c.own_step : c.narrow_step;
+      const int front = wide ? c.wide_front : x.own ? c.own_front : c.narrow_front;
       j0 = from < front ? 0 : (from - front) / step;
       j1 = to < front ? 0 : (to - front) / step;
       unit_end = at - from + cost;
-      w.flags = (wide ? 1 : 0) | (it >= p.G ? 2 : 0) | (j0 == 0 ? 4 : 0) | (to == cost ? 8 : 0);
+      w.flags = (wide ? 1 : 0) | (x.own ? 2 : 0) | (j0 == 0 ? 4 : 0) | (to == cost ? 8 : 0);
       off += to - from;
       at += to - from;
       if (off == head * p.units) {
@@ -227,20 +234,249 @@ struct PxWalk {
   }
 };
 
-// Takes the segments that the walking warp leaves, one after the other.
+// Takes the segments that the walking warp leaves, one after the other. A segment stays where
+// it is until `done`, and its parts are read from there when they are needed: in registers they
+// are spilled by the loops over the keys, to memory that a busy L1 has no room for.
 struct PxTake {
   uint32_t i = 0;
-  // a whole warp; false: the wait ran out
-  __device__ __forceinline__ bool next(PxBars* bars, PxSeg& w, uint64_t tmo, const volatile int* abort_flag) {
+  // a whole warp; null: the wait ran out
+  __device__ __forceinline__ const volatile PxSeg* next(PxBars* bars, uint64_t tmo, const volatile int* abort_flag) const {
     const uint32_t e = i % kPxQueue;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return false;
-    w = bars->seg[e];
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return nullptr;
+    return &bars->seg[e];
+  }
+  __device__ __forceinline__ void done(PxBars* bars) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->seg_empty[e]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->seg_empty[i % kPxQueue]);
     ++i;
-    return true;
   }
 };
+
+// A segment of a sequence's own keys for up to 16 rows, by the eight softmax warps alone. What
+// decides here is latency: with 128 rows a tile, 8 of them in use, a unit cost 3 us beside its
+// keys and a tile 0.75 us, of which the tensor cores had little. So warp-level MMAs, as in the
+// decode kernel: a warp takes 16 keys of every tile with a running maximum, sum and O of its
+// own, and no warp waits for another until the unit's end, where the eight are joined through
+// shared memory, eight rows at a time. Returns what all eight warps voted.
+template <int D>
+__device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg* w, PxBars* bars, uint8_t* sQ, uint8_t* sK,
+                                        uint8_t* sV, float* ex, uint32_t seg_i, uint32_t& gkv, uint64_t tmo) {
+  using C = PxCfg<D>;
+  constexpr int KST = C::K_STAGES, VST = C::V_STAGES;
+  const volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;  // row of the MMA fragment (and + 8), column pair
+  const int cta = blockIdx.x, me = cta / p.V;
+  auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+  };
+  // keys that the thread's two rows see (what rows from R on get goes nowhere)
+  int sees[2];
+#pragma unroll
+  for (int ri = 0; ri < 2; ++ri) {
+    const int n = gid + 8 * ri;
+    sees[ri] = w->k1 - w->k0 - (p.causal ? p.T - 1 - (p.T == 1 ? 0 : n % p.T) : 0);
+  }
+  bool ok = wwait(&bars->q_full, seg_i & 1);
+  uint32_t qa[D / 16][4];
+  if (ok) {
+    const uint32_t q0 = smem_u32(sQ);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      ldsm_x4(q0 + sw_off((lane & 7) + 8 * ((lane >> 3) & 1), kk * 16 + 8 * (lane >> 4), C::CHUNK_BYTES), qa[kk][0],
+              qa[kk][1], qa[kk][2], qa[kk][3]);
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars->q_empty);
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  const int key_of = warp * 16;  // this warp's first key of a tile
+  uint32_t ks = gkv % KST, kl = gkv / KST, vs = gkv % VST, vl = gkv / VST;
+  const int nt = w->nt;
+  for (int x = 0; ok && x < nt; ++x) {
+    if (!wwait(&bars->k_full[ks], kl & 1)) {
+      ok = false;
+      break;
+    }
+    const uint32_t k0 = smem_u32(sK + ks * C::KV_BYTES);
+    float s[2][4] = {}, odd[2][4] = {};  // two sums each, so that eight MMAs do not wait in a row
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const int mi = lane >> 3;  // matrix of the four: (keys half, d half)
+      uint32_t b00, b01, b10, b11;
+      ldsm_x4(k0 + sw_off(key_of + 8 * (mi >> 1) + (lane & 7), kk * 16 + 8 * (mi & 1), C::CHUNK_BYTES), b00, b01, b10, b11);
+      mma_bf16_16816(kk & 1 ? odd[0] : s[0], qa[kk], b00, b01);
+      mma_bf16_16816(kk & 1 ? odd[1] : s[1], qa[kk], b10, b11);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->k_empty[ks]);
+    if (++ks == KST) {
+      ks = 0;
+      ++kl;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] += odd[e >> 2][e & 3];
+    const int key0 = (w->x0 + x) * kPxTile + key_of;
+    const int there = w->k1 - w->k0 - key0;  // keys of the item from this warp's first one on
+    if (p.causal ? there < 16 + p.T - 1 : there < 16) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key0 + 8 * h + 2 * tig + (e & 1) >= sees[e >> 1]) s[h][e] = -INFINITY;
+    }
+    // two rows a thread; four neighbours share a row
+    float alpha[2];
+#pragma unroll
+    for (int ri = 0; ri < 2; ++ri) {
+      float mx = fmaxf(fmaxf(s[0][2 * ri], s[0][2 * ri + 1]), fmaxf(s[1][2 * ri], s[1][2 * ri + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float m_new = fmaxf(m[ri], mx * p.c);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      alpha[ri] = ex2_approx(m[ri] - m_use);
+      float sum = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float pv = ex2_approx(fmaf(s[h][2 * ri + e], p.c, -m_use));
+          s[h][2 * ri + e] = pv;
+          sum += pv;
+        }
+      l[ri] = l[ri] * alpha[ri] + sum;
+      m[ri] = m_new;
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= alpha[0];
+        o[n][1] *= alpha[0];
+        o[n][2] *= alpha[1];
+        o[n][3] *= alpha[1];
+      }
+    }
+    const uint32_t pa[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]), pack_bf16x2(s[1][0], s[1][1]),
+                            pack_bf16x2(s[1][2], s[1][3])};
+    if (!wwait(&bars->v_full[vs], vl & 1)) {
+      ok = false;
+      break;
+    }
+    uint8_t* vt = sV + vs * C::KV_BYTES;
+    if (there < 16) {
+      // V rows past the item's end hold whatever the pool or an earlier tile left there, and
+      // 0 * NaN is not 0
+      for (int idx = lane; idx < 16 * (D / 8); idx += 32)
+        if (idx / (D / 8) >= there)
+          *reinterpret_cast<uint4*>(vt + sw_off(key_of + idx / (D / 8), idx % (D / 8) * 8, C::CHUNK_BYTES)) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_smem();  // before the next copy into the stage
+      __syncwarp();
+    }
+    const uint32_t v0 = smem_u32(vt);
+#pragma unroll
+    for (int np = 0; np < D / 16; ++np) {
+      const int mi = lane >> 3;  // (keys half, d half)
+      uint32_t a, b, c, d;
+      ldsm_x4_t(v0 + sw_off(key_of + 8 * (mi & 1) + (lane & 7), np * 16 + 8 * (mi >> 1), C::CHUNK_BYTES), a, b, c, d);
+      mma_bf16_16816(o[2 * np], pa, a, b);
+      mma_bf16_16816(o[2 * np + 1], pa, c, d);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
+    if (++vs == VST) {
+      vs = 0;
+      ++vl;
+    }
+  }
+  gkv += nt;
+  if (!ok) {
+    record_error(p.err, FA_ERR_TIMEOUT, SITE_PX_SOFTMAX);
+    bars->abort_flag = 1;
+  }
+
+  // ---- the end: the eight warps' rows joined
+  float* part_o = reinterpret_cast<float*>(sQ + C::Q_BYTES);  // [8 warps][8 rows][D], no unit after a slim one is wide
+  float* part_m = ex;                                         // [8 warps][16 rows]
+  float* part_l = ex + 8 * 16;
+#pragma unroll
+  for (int ri = 0; ri < 2; ++ri) {
+    float x = l[ri];
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if (tig == 0) {
+      // a score that is NaN may have left the maximum at -inf, which would weigh the row 0
+      part_m[warp * 16 + gid + 8 * ri] = x != x ? INFINITY : m[ri];
+      part_l[warp * 16 + gid + 8 * ri] = x;
+    }
+  }
+  const bool whole = w->k0 == 0 && w->from_start() && w->to_end();
+  const int kvh = w->hu * p.V + cta % p.V;
+  const int at_row = (p.units * w->s0 + w->hu) * p.R;
+  const long long base = (static_cast<long long>(p.V) + cta % p.V) * p.area;
+  const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
+  const size_t out_row = (static_cast<size_t>(w->s0) * p.Hkv + kvh) * p.R;
+  constexpr int COLS = D / 32;  // columns of a thread in the joined rows, a row to a warp
+#pragma unroll
+  for (int ri = 0; ri < 2; ++ri) {
+    if (ri == 1) {
+      if (p.R <= 8) break;
+      named_bar_sync(2, 256);  // the first eight rows have been read
+    }
+    // (columns are turned round by the row, so that eight rows fall on all banks)
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+      *reinterpret_cast<float2*>(part_o + (warp * 8 + gid) * D + ((n * 8 + 2 * tig) ^ ((gid & 3) << 3))) =
+          make_float2(o[n][2 * ri], o[n][2 * ri + 1]);
+    if (ri == 0) {
+      ok = vote_all(1, 256, ok);
+      if (!ok) return false;
+    } else {
+      named_bar_sync(2, 256);
+    }
+    const int row = warp + 8 * ri, col = lane * COLS;
+    if (row >= p.R) continue;
+    float mw[8], m_all = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      mw[k] = part_m[k * 16 + row];
+      m_all = fmaxf(m_all, mw[k]);
+    }
+    const float m_use = m_all == -INFINITY ? 0.f : m_all;
+    float sum = 0.f, acc[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = ex2_approx(mw[k] - m_use);
+      sum = fmaf(f, part_l[k * 16 + row], sum);
+      const float* of = part_o + (k * 8 + warp) * D + (col ^ ((warp & 3) << 3));
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) acc[c] = fmaf(f, of[c], acc[c]);
+    }
+    if (whole) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
+      __nv_bfloat16* dst = p.o + (out_row + row) * D + col;
+      if constexpr (COLS == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+      if (p.lse && lane == 0) p.lse[out_row + row] = sum == 0.f ? -INFINITY : (m_all + log2f(sum)) * kLn2;
+    } else {
+      float* dst = p.part + (part_row + row) * D + col;
+      if constexpr (COLS == 4)
+        *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      else
+        *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
+      if (lane == 0) p.part_ml[part_row + row] = make_float4(m_all, sum, sum, 0.f);
+    }
+  }
+  if (threadIdx.x == 0 && w->from_start())
+    p.desc[(static_cast<size_t>(p.B) + w->s0) * p.Hkv + kvh] =
+        whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w->ctas, static_cast<int>(base + at_row));
+  return true;
+}
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
@@ -267,12 +503,12 @@ __global__ void __launch_bounds__(384, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 8);
     for (int s = 0; s < 6; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->k_empty[s], 8);
+      mbar_init(&bars->v_empty[s], 8);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
@@ -314,7 +550,7 @@ __global__ void __launch_bounds__(384, 1)
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
     auto item = [&](int i, int& g) {
-      if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0} : px_group(p, gs[i], gs[i + 1], gp[i]);
+      if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0, false} : px_group(p, gs[i], gs[i + 1], gp[i]);
       const int b = i - p.G;
       int prefix = 0;
       if (!bad) {
@@ -328,13 +564,13 @@ __global__ void __launch_bounds__(384, 1)
         while (g + 1 < p.G && gs[g + 1] <= b) ++g;
         if (b >= gs[g] && b < gs[g + 1]) prefix = gp[g];
       }
-      return PxItem{b, b + 1, prefix, i == lo ? len : px_len(p, b), p.TS};
+      return PxItem{b, b + 1, prefix, i == lo ? len : px_len(p, b), p.TS, true};
     };
     // steps of the items before this thread's, and their cost; a line's whole cost is below 2^31
     int steps = 0, mine = 0, g = -1;
     for (int i = lo; i < hi; ++i) {
       const PxItem x = item(i, g);
-      steps += x.head(PxCost{1, 0, 1, 0});
+      steps += x.head(PX_BY_STEPS);
       mine += x.head(p.cost);
     }
     steps *= p.units;
@@ -370,7 +606,7 @@ __global__ void __launch_bounds__(384, 1)
     const bool few = all_steps <= 2 * grid;
     walk.c = p.cost;
     if (few) {
-      walk.c = PxCost{1, 0, 1, 0};
+      walk.c = PX_BY_STEPS;
       before = steps_before;
       mine = steps;
       total = all_steps;
@@ -420,16 +656,28 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(my_map);
       }
       PxTake take;
-      PxSeg w;
       uint32_t g = 0;  // key tiles loaded so far (ring position)
       uint32_t stage = 0, lap = 0;
       uint32_t q_loads = 0;
       const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
       bool ok = true;
       while (ok && !*abort_flag) {
-        if (!take.next(bars, w, tmo, abort_flag)) {
-          ok = false;
-          break;
+        PxSeg w;
+        {
+          const volatile PxSeg* from = take.next(bars, tmo, abort_flag);
+          if (!from) {
+            ok = false;
+            break;
+          }
+          w.s0 = from->s0;
+          w.k0 = from->k0;
+          w.k1 = from->k1;
+          w.tile = from->tile;
+          w.hu = from->hu;
+          w.x0 = from->x0;
+          w.nt = from->nt;
+          w.flags = from->flags;
+          take.done(bars);
         }
         if (w.nt == 0) break;
         const int* trow = p.block_table + static_cast<size_t>(w.s0) * p.max_pages;
@@ -546,6 +794,13 @@ __global__ void __launch_bounds__(384, 1)
       auto commit = [=](uint64_t* bar) {
         if (leader) tc_commit(bar);
       };
+      // what slim units free by eight warps' arrivals
+      auto release = [=](uint64_t* bar) {
+        if (leader) {
+          mbar_arrive_n(bar, 7);
+          tc_commit(bar);
+        }
+      };
       auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, tmo, abort_flag); };
       auto wait_k = [&](uint32_t x) -> bool {
         const bool r = wwait(&bars->k_full[x % KST], (x / KST) & 1);
@@ -565,23 +820,26 @@ __global__ void __launch_bounds__(384, 1)
         return r;
       };
       PxTake take;
-      PxSeg w;
       uint32_t g = 0;  // key tiles of earlier segments (ring position)
-      uint32_t seg_i = 0;
       bool ok = true;
-      for (; ok; ++seg_i, g += w.nt) {
-        if (!take.next(bars, w, tmo, abort_flag)) {
+      for (int nt; ok; g += nt) {
+        const volatile PxSeg* from = take.next(bars, tmo, abort_flag);
+        if (!from) {
           ok = false;
           break;
         }
-        const int nt = w.nt;
+        nt = from->nt;
+        const bool wide = from->wide(), slim = from->own() && p.R <= kPxSlim;
+        const uint32_t seg_i = take.i;
+        take.done(bars);
         if (nt == 0) break;
+        if (slim) continue;  // the softmax warps do those by themselves
         if (!wwait(&bars->q_full, seg_i & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (!w.wide()) {
+        if (!wide) {
           // slots take the tiles in turn: tile x in slot x & 1
           for (int x = 0; x < 2 && x < nt; ++x) {
             if (!wait_k(g + x)) {
@@ -590,8 +848,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             qk(x, 0, (g + x) % KST);
             commit(&bars->s_full[x]);
-            commit(&bars->k_empty[(g + x) % KST]);
-            if (x + 1 == nt) commit(&bars->q_empty);
+            release(&bars->k_empty[(g + x) % KST]);
+            if (x + 1 == nt) release(&bars->q_empty);
           }
           for (int x = 0; ok && x < nt; ++x) {
             const int t = x & 1;
@@ -600,7 +858,7 @@ __global__ void __launch_bounds__(384, 1)
               break;
             }
             pv(t, (g + x) % VST, x < 2);
-            commit(&bars->v_empty[(g + x) % VST]);
+            release(&bars->v_empty[(g + x) % VST]);
             if (x + 2 >= nt) {
               commit(&bars->pv_done[t]);
             } else {
@@ -611,8 +869,8 @@ __global__ void __launch_bounds__(384, 1)
               }
               qk(t, 0, (g + x + 2) % KST);
               commit(&bars->s_full[t]);
-              commit(&bars->k_empty[(g + x + 2) % KST]);
-              if (x + 3 == nt) commit(&bars->q_empty);  // the segment's last S
+              release(&bars->k_empty[(g + x + 2) % KST]);
+              if (x + 3 == nt) release(&bars->q_empty);  // the segment's last S
             }
           }
         } else {
@@ -624,8 +882,8 @@ __global__ void __launch_bounds__(384, 1)
           commit(&bars->s_full[0]);
           qk(1, 1, g % KST);
           commit(&bars->s_full[1]);
-          commit(&bars->k_empty[g % KST]);
-          if (nt == 1) commit(&bars->q_empty);
+          release(&bars->k_empty[g % KST]);
+          if (nt == 1) release(&bars->q_empty);
           for (int x = 0; ok && x < nt; ++x) {
             const uint32_t sv = (g + x) % VST, sk = (g + x + 1) % KST;
             const bool more = x + 1 < nt;
@@ -635,7 +893,7 @@ __global__ void __launch_bounds__(384, 1)
                 break;
               }
               pv(t, sv, x == 0);
-              if (t == 1) commit(&bars->v_empty[sv]);
+              if (t == 1) release(&bars->v_empty[sv]);
               if (more) {
                 if (t == 0 && !wait_k(g + x + 1)) {
                   ok = false;
@@ -648,8 +906,8 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
             if (ok && more) {
-              commit(&bars->k_empty[sk]);
-              if (x + 2 == nt) commit(&bars->q_empty);
+              release(&bars->k_empty[sk]);
+              if (x + 2 == nt) release(&bars->q_empty);
             }
           }
         }
@@ -716,50 +974,60 @@ __global__ void __launch_bounds__(384, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
     };
     PxTake take;
-    PxSeg w;
     uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
     uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
     uint32_t gkv = 0;   // ring position at the segment's start
-    // where a thread's row lies in a tile of whole sequences
-    const int seq_in = p.R <= kPxTile ? r / p.R : 0, row_in = p.R <= kPxTile ? r - seq_in * p.R : r;
-    while (true) {
-      if (!take.next(bars, w, tmo, abort_flag)) {
-        ok = false;
-        w = PxSeg{};  // nothing, and out by the vote at its end
-        fail(SITE_PX_SOFTMAX);
-      } else if (w.nt == 0) {
-        break;
-      }
-      // this thread's row: sequence, and row of its R; -1: none
-      const int tile = w.tile + (w.wide() ? t : 0);
-      int seq = w.s0, rr = row_in;
+    // This thread's row of a segment: its sequence, and its place among the R; -1: none.
+    auto row_of = [&](const volatile PxSeg* w, int& seq) -> int {
+      int x = r;
+      asm volatile("" : "+r"(x));  // formed anew where it is needed
+      const int tile = w->tile + (w->wide() ? t : 0);
       if (p.R <= kPxTile) {
-        seq += tile * p.spt + seq_in;
-        if (seq_in >= p.spt || seq >= w.s0 + w.n) rr = -1;
-      } else {
-        const int q = tile / p.TS;
-        seq += q;
-        rr += (tile - q * p.TS) * kPxTile;
-        if (rr >= p.R) rr = -1;
+        const int q = x / p.R;
+        seq = w->s0 + tile * p.spt + q;
+        return q < p.spt && seq < w->s0 + w->n ? x - q * p.R : -1;
       }
-      const bool valid = rr >= 0;
-      const bool has_rows = __any_sync(0xffffffffu, valid);
-      // keys of the item that the row sees; rows of nobody are not masked
-      int sees = 0x7fffffff;
-      if (valid) {
-        const int S = w.own() ? w.k1 : px_len(p, seq);
-        sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w.k1) - w.k0;
+      const int q = tile / p.TS;
+      seq = w->s0 + q;
+      const int rr = (tile - q * p.TS) * kPxTile + x;
+      return rr < p.R ? rr : -1;
+    };
+    while (true) {
+      const volatile PxSeg* w = take.next(bars, tmo, abort_flag);
+      if (!w) ok = false;
+      if (!ok) fail(SITE_PX_SOFTMAX);
+      // All eight warps go on or leave together. And both slots' O and the exchange area have
+      // been read by all before this segment overwrites them.
+      ok = vote_all(1, 256, ok);
+      if (!ok || w->nt == 0) break;
+      if (w->own() && p.R <= kPxSlim) {
+        ok = px_slim<D>(p, w, bars, sQ, sK, sV, ex, take.i, gkv, tmo);
+        if (!ok) break;  // (as all eight warps voted)
+        take.done(bars);
+        continue;
       }
-      const int step = w.wide() ? 1 : 2;
-      const int x_first = w.wide() ? 0 : t;
-      const int mine = w.nt <= x_first ? 0 : (w.nt - x_first + step - 1) / step;  // tiles of this slot
+      const bool wide = w->wide();
+      int sees = 0x7fffffff;  // keys of the item that the row sees; rows of nobody are not masked
+      bool has_rows;
+      {
+        int seq;
+        const int rr = row_of(w, seq);
+        has_rows = __any_sync(0xffffffffu, rr >= 0);
+        if (rr >= 0) {
+          const int S = w->own() ? w->k1 : px_len(p, seq);
+          sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w->k1) - w->k0;
+        }
+      }
+      const int nt = w->nt;
+      const int x_first = wide ? 0 : t, step = wide ? 1 : 2;
+      const int mine = wide ? nt : (nt - t + 1) / 2;  // tiles of this slot
       float m = -INFINITY;
       float l = 0.f;   // sum of the unrounded p: the lse's
       float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
 
       for (int i = 0; i < mine; ++i, ++cnt) {
         const int x = x_first + i * step;  // tile of the segment
-        const int key0 = (w.x0 + x) * kPxTile;  // from k0
+        const int key0 = (w->x0 + x) * kPxTile;  // from k0
         if (!wwait(&bars->s_full[t], cnt & 1)) {
           ok = false;
           break;
@@ -791,7 +1059,7 @@ __global__ void __launch_bounds__(384, 1)
           const float m_tile = mx * p.c;
           const float m_new = (m_tile > m + kRescaleSlack) ? m_tile : m;
           const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-          const float alpha = valid ? ex2_approx(m - m_use) : 1.f;
+          const float alpha = sees == 0x7fffffff ? 1.f : ex2_approx(m - m_use);
           // the largest p is not 1 against a stale reference: O's normaliser counts it as the
           // bf16 product sees it, so that a nearly one-hot row is not off by its rounding
           const float p_top = ex2_approx(fmaf(mx, p.c, -m_use));
@@ -840,8 +1108,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         // V rows past the item's end hold whatever the pool or an earlier tile left there, and
         // 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
-        const int rows_there = w.k1 - w.k0 - key0;
-        if (rows_there < kPxTile && (!w.wide() || t == 0)) {
+        const int rows_there = w->k1 - w->k0 - key0;
+        if (rows_there < kPxTile && (!wide || t == 0)) {
           const uint32_t xg = gkv + x;
           if (!wwait(&bars->v_full[xg % VST], (xg / VST) & 1)) {
             ok = false;
@@ -860,15 +1128,17 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_before();
         mbar_arrive(&bars->p_full[t]);
       }
-      gkv += w.nt;
+      gkv += nt;
       if (ok && mine > 0) {
         if (!wwait(&bars->pv_done[t], ecnt & 1)) ok = false;
         ++ecnt;
         tc_fence_after();
       }
-      if (!ok) fail(SITE_PX_SOFTMAX);
 
       // ---- the segment's end: final rows, or a partial
+      int seq;
+      const int rr = row_of(w, seq);
+      const bool valid = rr >= 0;
       if (!valid) {
         m = -INFINITY;
         l = lc = 0.f;
@@ -876,17 +1146,16 @@ __global__ void __launch_bounds__(384, 1)
       // A score that is NaN (a query that is not finite) may have left m at -inf, which would
       // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
       if (l != l) m = INFINITY;
-      const bool whole = w.own() && w.k0 == 0 && w.from_start() && w.to_end();
+      const bool whole = w->own() && w->k0 == 0 && w->from_start() && w->to_end();
       float m_all = m, sum = l + lc, lsum = l;
       float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
-      if (!w.wide()) {
+      if (!wide) {
         ex[t * 128 + r] = m;
         ex[(2 + t) * 128 + r] = l + lc;
         if (t == 1) ex[4 * 128 + r] = l;
-      }
-      ok = vote_all(1, 256, ok);
-      if (!ok) break;  // all eight warps leave in the same segment
-      if (!w.wide()) {
+        if (!ok) fail(SITE_PX_SOFTMAX);
+        ok = vote_all(1, 256, ok);
+        if (!ok) break;  // all eight warps leave in the same segment
         const float m0 = ex[r], m1 = ex[128 + r];
         m_all = fmaxf(m0, m1);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
@@ -902,21 +1171,21 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (has_rows) {
         // the row's place in its item's partials, and in the output
-        const int at_row = p.units * p.R * w.s0 + (w.hu * w.n + seq - w.s0) * p.R + rr;
-        const int kvh = w.hu * p.V + cta % p.V;
-        const long long base = (static_cast<long long>(w.own()) * p.V + cta % p.V) * p.area;
+        const int at_row = p.units * p.R * w->s0 + (w->hu * w->n + seq - w->s0) * p.R + rr;
+        const int kvh = w->hu * p.V + cta % p.V;
+        const long long base = (static_cast<long long>(w->own()) * p.V + cta % p.V) * p.area;
         const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
         const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + kvh) * p.R + rr;
         // narrow: each slot's warps write half the columns of the joined O
         const bool take0 = f0 != 0.f;
-        const bool take1 = !w.wide() && w.nt > 1 && f1 != 0.f;
-        const uint32_t o_base = tmem + lane_base + (w.wide() ? t * C::SLOT_COLS : 0) + C::O_OFF;
-        const int c_lo = w.wide() ? 0 : t * (D / 64), c_hi = w.wide() ? D / 32 : c_lo + D / 64;
+        const bool take1 = !wide && nt > 1 && f1 != 0.f;
+        const uint32_t o_base = tmem + lane_base + (wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
+        const int c_lo = wide ? 0 : t * (D / 64), c_hi = wide ? D / 32 : c_lo + D / 64;
 #pragma unroll 1
         for (int cc = c_lo; cc < c_hi; ++cc) {
           uint32_t a[32], b[32];
           tmem_ld32(o_base + cc * 32, a);
-          if (!w.wide()) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
+          if (!wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
           tmem_ld_wait();
           float o[32];
           // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
@@ -945,22 +1214,20 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         }
-        if (valid && (w.wide() || t == 0)) {
+        if (valid && (wide || t == 0)) {
           if (whole) {
             if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
           } else {
             p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
           }
-          if (w.from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
-            const size_t at = ((static_cast<size_t>(w.own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
-            p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w.ctas, static_cast<int>(base + at_row));
+          if (w->from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
+            const size_t at = ((static_cast<size_t>(w->own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
+            p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w->ctas, static_cast<int>(base + at_row));
           }
         }
       }
       tc_fence_before();
-      // narrow: both slots' O have been read by all before either is overwritten, and the
-      // exchange area before the next segment fills it
-      if (!w.wide()) named_bar_sync(2, 256);
+      take.done(bars);
     }
   }
 
@@ -1221,7 +1488,10 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.c = scale * kLog2e;
-  p.cost = d == 128 ? PxCost{4, 5, 3, 6} : PxCost{3, 4, 3, 6};
+  if (s.R <= kPxSlim)
+    p.cost = d == 128 ? PxCost{5, 6, 3, 6, 4, 2} : PxCost{3, 6, 3, 6, 3, 2};
+  else
+    p.cost = d == 128 ? PxCost{4, 5, 3, 6, 4, 5} : PxCost{3, 4, 3, 6, 3, 4};
   p.area = s.area;
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float4*>(ws + s.part);
