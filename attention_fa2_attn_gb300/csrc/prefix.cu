@@ -94,7 +94,9 @@ struct PxParams {
   float c;  // scale * log2(e)
   PxCost cost;
   long long area;   // rows of partials of one place and kind
-  float* part;      // [2 kinds][V][area][D]: unnormalised O
+  long long part_rows;  // 2 kinds * V * area
+  float* part;      // [D / 8][part_rows][8]: unnormalised O; the rows of a tile lie side by side, so that lanes
+                    // with a row each write whole lines (rows of D, 32 bytes a lane: 4.3 us a tile pair; 2 so)
   float4* part_ml;  // (max in log2 units, sum as P V saw it, sum, -)
   int2* desc;       // [2 kinds][B][Hkv][TS]: (first CTA << 16 | CTAs, first row), or kPxDone
   unsigned* err;
@@ -464,7 +466,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
       if (p.lse && lane == 0) p.lse[out_row + row] = sum == 0.f ? -INFINITY : (m_all + log2f(sum)) * kLn2;
     } else {
-      float* dst = p.part + (part_row + row) * D + col;
+      float* dst = p.part + ((col >> 3) * p.part_rows + part_row + row) * 8 + (col & 7);
       if constexpr (COLS == 4)
         *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       else
@@ -1204,13 +1206,12 @@ __global__ void __launch_bounds__(384, 1)
                   make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
                              pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
           } else {
-            float* dst = p.part + part_row * D + cc * 32;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t v[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
-              st32(dst + 8 * q, v);
+              st32(p.part + ((4 * cc + q) * p.part_rows + part_row) * 8, v);
             }
           }
         }
@@ -1240,8 +1241,9 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Joins the partials of each row that is not written yet, of its prefix and of its own keys:
-// lse = log2 sum 2^(m_s - m) l_s + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. A row has
-// D / 4 lanes; 1, 2, 4 or 8 warps take its partials in turn, four of each in flight.
+// lse = log2 sum 2^(m_s - m) l_s + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Four rows
+// to a warp: eight lanes read a line of the four, four such groups of lanes a line each. 1, 2,
+// 4 or 8 warps take the rows' partials in turn, two of each in flight.
 struct PxJoin {
   const float* part;
   const float4* part_ml;
@@ -1256,14 +1258,14 @@ struct PxJoin {
 
 template <int D, int WPR>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
-  constexpr int LANES = D / 4, PER = 32 / LANES, IN = 4;
-  __shared__ float4 red[8][32];
-  __shared__ float red_m[8][PER], red_s[8][PER], red_l[8][PER];
+  constexpr int NV = D / 32, IN = 2;  // a lane's vectors of four columns
+  __shared__ float4 red[WPR > 1 ? 8 : 1][NV][32];
+  __shared__ float red_ml[WPR > 1 ? 8 : 1][3][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch();
-  const int sub = warp % WPR, my = lane / LANES, col = lane % LANES * 4;
-  const long long row = (static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR) * PER + my;
+  const int sub = warp % WPR, my = (lane & 7) >> 1, col = (lane >> 3) * 8 + (lane & 1) * 4;
+  const long long row = (static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR) * 4 + my;
   int2 d[2] = {make_int2(kPxDone, 0), make_int2(kPxDone, 0)};
   long long r_in_tile = 0;
   if (row < p.rows) {
@@ -1275,22 +1277,39 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
     r_in_tile = rr % kPxTile;
   }
   const bool todo = d[1].x != kPxDone;
-  int first[2], count[2];
+  int count[2];
   long long at[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    first[k] = d[k].x >> 16;
+    const int first = d[k].x >> 16;
     count[k] = d[k].x & 0xffff;
-    at[k] = d[k].y + r_in_tile + static_cast<long long>(kPxUnit) * first[k];
+    at[k] = d[k].y + r_in_tile + static_cast<long long>(kPxUnit) * first;
     // (after a wait that ran out a descriptor may be anything)
-    if (!todo || first[k] < 0 || first[k] + count[k] > p.grid || at[k] < 0 ||
+    if (!todo || first < 0 || first + count[k] > p.grid || at[k] < 0 ||
         at[k] + static_cast<long long>(kPxUnit) * count[k] >= p.part_rows + kPxUnit)
       count[k] = 0;
   }
   const int n = count[0] + count[1];
-  RowJoin acc;
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float4 acc[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A partial whose maximum is +inf (its scores were NaN) makes all of them NaN; one of -inf
+  // had no key that the row sees.
+  auto add = [&](float m2, float s2, float l2, const float4* o2) {
+    if (m2 == -INFINITY) return;
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      acc[j] = make_float4(acc[j].x * fa + o2[j].x * fb, acc[j].y * fa + o2[j].y * fb, acc[j].z * fa + o2[j].z * fb,
+                           acc[j].w * fa + o2[j].w * fb);
+    m = mn;
+  };
   for (int i0 = sub; i0 < n; i0 += WPR * IN) {
-    float4 ml[IN], v[IN];
+    float4 ml[IN], v[IN][NV];
 #pragma unroll
     for (int k = 0; k < IN; ++k) {
       const int i = i0 + WPR * k;
@@ -1299,28 +1318,38 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
         const long long x = i < count[0] ? at[0] + static_cast<long long>(kPxUnit) * i
                                          : at[1] + static_cast<long long>(kPxUnit) * (i - count[0]);
         ml[k] = p.part_ml[x];
-        v[k] = *reinterpret_cast<const float4*>(p.part + x * D + col);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          v[k][j] = *reinterpret_cast<const float4*>(p.part + ((4 * j + (lane >> 3)) * p.part_rows + x) * 8 + (lane & 1) * 4);
       }
     }
 #pragma unroll
-    for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
+    for (int k = 0; k < IN; ++k) add(ml[k].x, ml[k].y, ml[k].z, v[k]);
   }
   if constexpr (WPR > 1) {
-    red[warp][lane] = acc.o;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) red[warp][j][lane] = acc[j];
     if (col == 0) {
-      red_m[warp][my] = acc.m;
-      red_s[warp][my] = acc.s;
-      red_l[warp][my] = acc.l;
+      red_ml[warp][0][my] = m;
+      red_ml[warp][1][my] = s;
+      red_ml[warp][2][my] = l;
     }
     __syncthreads();
     if (sub == 0)
-      for (int k = warp + 1; k < warp + WPR; ++k) acc.add(red_m[k][my], red_s[k][my], red_l[k][my], red[k][lane]);
+      for (int k = warp + 1; k < warp + WPR; ++k) {
+        float4 v[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = red[k][j][lane];
+        add(red_ml[k][0][my], red_ml[k][1][my], red_ml[k][2][my], v);
+      }
   }
   if (todo && sub == 0) {
-    const float inv = acc.s == 0.f ? 0.f : 1.f / acc.s;
-    *reinterpret_cast<uint2*>(p.o + row * D + col) =
-        make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
-    if (p.lse && col == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * kLn2;
+    const float inv = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      *reinterpret_cast<uint2*>(p.o + row * D + 32 * j + col) =
+          make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+    if (p.lse && col == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 
@@ -1379,9 +1408,8 @@ static int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   }
   const int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
   if (rc != FA_OK) return rc;
-  // warps to a row: as many as rows leave of some 24 an SM
-  constexpr int PER = 128 / D;
-  const long long warps = (j.rows + PER - 1) / PER;
+  // warps to four rows: as many as there are of some 24 an SM
+  const long long warps = (j.rows + 3) / 4;
   int wpr = 8;
   while (wpr > 1 && warps * wpr > 24ll * sms) wpr >>= 1;
   const dim3 blocks(static_cast<unsigned>((warps * wpr + 7) / 8));
@@ -1493,6 +1521,7 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   else
     p.cost = d == 128 ? PxCost{4, 5, 3, 6, 4, 5} : PxCost{3, 4, 3, 6, 3, 4};
   p.area = s.area;
+  p.part_rows = 2 * s.V * s.area;
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float4*>(ws + s.part);
   p.desc = reinterpret_cast<int2*>(ws + s.part + s.ml);
