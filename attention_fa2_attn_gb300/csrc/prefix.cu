@@ -76,7 +76,7 @@ struct PxCost {
   int narrow_step, narrow_front, wide_step, wide_front, own_step, own_front;  // own: narrow or slim
 };
 #define PX_BY_STEPS PxCost{1, 0, 1, 0, 1, 0}
-constexpr int kPxMostCost = 10;  // of a step with its unit's start
+constexpr int kPxMostCost = 28;  // of a step with its unit's start
 
 struct PxParams {
   __nv_bfloat16* o;
@@ -266,7 +266,9 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   using C = PxCfg<D>;
   constexpr int KST = C::K_STAGES, VST = C::V_STAGES;
   const volatile int* abort_flag = &bars->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int tid = threadIdx.x;
+  asm volatile("" : "+r"(tid));  // (as in px_rows)
+  const int warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;  // row of the MMA fragment (and + 8), column pair
   const int cta = blockIdx.x, me = cta / p.V;
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -478,6 +480,272 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     p.desc[(static_cast<size_t>(p.B) + w->s0) * p.Hkv + kvh] =
         whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w->ctas, static_cast<int>(base + at_row));
   return true;
+}
+
+// A segment of a wide or narrow unit, by one of the two softmax slots: thread r has row r of the
+// slot's tile, TMEM lane r. False: a wait ran out (in narrow units as all eight warps voted).
+template <int D>
+__device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg* w, PxBars* bars, uint8_t* sV, float* ex,
+                                        uint32_t& phases, uint32_t& gkv, uint64_t tmo) {
+  using C = PxCfg<D>;
+  constexpr int VST = C::V_STAGES;
+  // The reference maximum m is raised only when a row's maximum climbs more than this above it;
+  // until then the exponentials stay below 2^8 and carry one constant factor that O / l cancels.
+  constexpr float kRescaleSlack = 8.f;
+  // formed anew in each segment: kept over both kinds of segments these are spilled in their loops
+  int tid = threadIdx.x;
+  asm volatile("" : "+r"(tid));
+  const int t = tid >> 7, r = tid & 127;
+  const volatile int* abort_flag = &bars->abort_flag;
+  const uint32_t tmem = *const_cast<const volatile uint32_t*>(&bars->tmem_base);
+  const uint32_t lane_base = static_cast<uint32_t>(r & 96) << 16;
+  const uint32_t tS = tmem + lane_base + t * C::SLOT_COLS;
+  const uint32_t tO = tS + C::O_OFF;
+  const float2 c2 = make_float2(p.c, p.c);
+  bool ok = true;
+  auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+  };
+  // This thread's row of the segment: its sequence, and its place among the R; -1: none.
+  auto row_of = [&](int& seq) -> int {
+    int x = r;
+    asm volatile("" : "+r"(x));
+    const int tile = w->tile + (w->wide() ? t : 0);
+    if (p.R <= kPxTile) {
+      const int q = x / p.R;
+      seq = w->s0 + tile * p.spt + q;
+      return q < p.spt && seq < w->s0 + w->n ? x - q * p.R : -1;
+    }
+    const int q = tile / p.TS;
+    seq = w->s0 + q;
+    const int rr = (tile - q * p.TS) * kPxTile + x;
+    return rr < p.R ? rr : -1;
+  };
+  const bool wide = w->wide();
+  int sees = 0x7fffffff;  // keys that the row sees from the segment's first on; rows of nobody are not masked
+  bool has_rows;
+  {
+    int seq;
+    const int rr = row_of(seq);
+    has_rows = __any_sync(0xffffffffu, rr >= 0);
+    if (rr >= 0) {
+      const int S = w->own() ? w->k1 : px_len(p, seq);
+      sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w->k1) - w->k0 - w->x0 * kPxTile;
+    }
+  }
+  const int keys = w->k1 - w->k0 - w->x0 * kPxTile;  // of the item, from the segment's first one on
+  const int nt = w->nt;
+  const int x_first = wide ? 0 : t, step = wide ? 1 : 2;
+  const int mine = wide ? nt : (nt - t + 1) / 2;  // tiles of this slot
+  float m = -INFINITY;
+  float l = 0.f;   // sum of the unrounded p: the lse's
+  float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
+
+  for (int i = 0; i < mine; ++i, phases ^= 1) {
+    const int x = x_first + i * step;  // tile of the segment
+    const int key0 = x * kPxTile;
+    if (!wwait(&bars->s_full[t], phases & 1)) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    if (has_rows) {
+      uint32_t raw[4][32];
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, raw[cc]);
+      tmem_ld_wait();
+      float s[128];
+#pragma unroll
+      for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(raw[k >> 5][k & 31]);
+      if (__any_sync(0xffffffffu, sees < key0 + kPxTile)) {
+        const int left = sees - key0;
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= left) s[k] = -INFINITY;
+      }
+      float mx8[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float a = fmax3(s[16 * k], s[16 * k + 1], s[16 * k + 2]);
+#pragma unroll
+        for (int e = 3; e < 15; e += 2) a = fmax3(a, s[16 * k + e], s[16 * k + e + 1]);
+        mx8[k] = fmaxf(a, s[16 * k + 15]);
+      }
+      const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+      const float m_tile = mx * p.c;
+      const float m_new = (m_tile > m + kRescaleSlack) ? m_tile : m;
+      const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
+      const float alpha = sees == 0x7fffffff ? 1.f : ex2_approx(m - m_use);
+      // the largest p is not 1 against a stale reference: O's normaliser counts it as the
+      // bf16 product sees it, so that a nearly one-hot row is not off by its rounding
+      const float p_top = ex2_approx(fmaf(mx, p.c, -m_use));
+      const float p_top_err = __bfloat162float(__float2bfloat16_rn(p_top)) - p_top;
+      const float2 nm2 = make_float2(-m_use, -m_use);
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = cc * 32 + 2 * k;
+          const float2 v = ffma2(make_float2(s[e], s[e + 1]), c2, nm2);
+          const float2 ev = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+          acc[k & 3] = fadd2(acc[k & 3], ev);
+          pk[k] = pack_bf16x2(ev.x, ev.y);
+        }
+        tmem_st16(tS + cc * 16, pk);
+      }
+      const float2 at = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+      l = fmaf(l, alpha, at.x + at.y);
+      lc = fmaf(lc, alpha, p_top_err);
+      m = m_new;
+      // PV of this slot's previous tile is complete: S of this one was issued behind it
+      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+        for (int cc = 0; cc < D / 32; cc += 2) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32(tO + cc * 32, o0);
+          tmem_ld32(tO + cc * 32 + 32, o1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 v0 = fmul2(make_float2(__uint_as_float(o0[k]), __uint_as_float(o0[k + 1])), al2);
+            const float2 v1 = fmul2(make_float2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), al2);
+            o0[k] = __float_as_uint(v0.x);
+            o0[k + 1] = __float_as_uint(v0.y);
+            o1[k] = __float_as_uint(v1.x);
+            o1[k + 1] = __float_as_uint(v1.y);
+          }
+          tmem_st32(tO + cc * 32, o0);
+          tmem_st32(tO + cc * 32 + 32, o1);
+        }
+      }
+    }
+    // V rows past the item's end hold whatever the pool or an earlier tile left there, and
+    // 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
+    const int rows_there = keys - key0;
+    if (rows_there < kPxTile && (!wide || t == 0)) {
+      const uint32_t xg = gkv + x;
+      if (!wwait(&bars->v_full[xg % VST], (xg / VST) & 1)) {
+        ok = false;
+        break;
+      }
+      uint8_t* vt = sV + (xg % VST) * C::KV_BYTES;
+      for (int idx = r; idx < (kPxTile - rows_there) * C::KCH * 8; idx += 128) {
+        const int vr = rows_there + idx / (C::KCH * 8);
+        const int rem = idx % (C::KCH * 8);
+        *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::CHUNK_BYTES + vr * 128 + (rem & 7) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&bars->p_full[t]);
+  }
+  gkv += nt;
+  if (ok && mine > 0) {
+    if (!wwait(&bars->pv_done[t], (phases >> 1) & 1)) ok = false;
+    phases ^= 2;
+    tc_fence_after();
+  }
+
+  // ---- the segment's end: final rows, or a partial
+  int seq;
+  const int rr = row_of(seq);
+  const bool valid = rr >= 0;
+  if (!valid) {
+    m = -INFINITY;
+    l = lc = 0.f;
+  }
+  // A score that is NaN (a query that is not finite) may have left m at -inf, which would
+  // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
+  if (l != l) m = INFINITY;
+  const bool whole = w->own() && w->k0 == 0 && w->from_start() && w->to_end();
+  float m_all = m, sum = l + lc, lsum = l;
+  float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
+  if (!wide) {
+    ex[t * 128 + r] = m;
+    ex[(2 + t) * 128 + r] = l + lc;
+    if (t == 1) ex[4 * 128 + r] = l;
+    if (!ok) {
+      record_error(p.err, FA_ERR_TIMEOUT, SITE_PX_SOFTMAX);
+      bars->abort_flag = 1;
+    }
+    ok = vote_all(1, 256, ok);
+    if (!ok) return false;  // all eight warps leave in the same segment
+    const float m0 = ex[r], m1 = ex[128 + r];
+    m_all = fmaxf(m0, m1);
+    const float m_use = m_all == -INFINITY ? 0.f : m_all;
+    f0 = ex2_approx(m0 - m_use);
+    f1 = ex2_approx(m1 - m_use);
+    sum = f0 * ex[256 + r] + f1 * ex[384 + r];
+    if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
+  }
+  if (whole) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
+    f0 *= inv;
+    f1 *= inv;
+  }
+  if (has_rows) {
+    // the row's place in its item's partials, and in the output
+    const int at_row = p.units * p.R * w->s0 + (w->hu * w->n + seq - w->s0) * p.R + rr;
+    const int kvh = w->hu * p.V + static_cast<int>(blockIdx.x) % p.V;
+    const long long base = (static_cast<long long>(w->own()) * p.V + static_cast<int>(blockIdx.x) % p.V) * p.area;
+    const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * (blockIdx.x / p.V);
+    const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + kvh) * p.R + rr;
+    // narrow: each slot's warps write half the columns of the joined O
+    const bool take0 = f0 != 0.f;
+    const bool take1 = !wide && nt > 1 && f1 != 0.f;
+    const uint32_t o_base = tmem + lane_base + (wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
+    const int c_lo = wide ? 0 : t * (D / 64), c_hi = wide ? D / 32 : c_lo + D / 64;
+#pragma unroll 1
+    for (int cc = c_lo; cc < c_hi; ++cc) {
+      uint32_t a[32], b[32];
+      tmem_ld32(o_base + cc * 32, a);
+      if (!wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
+      tmem_ld_wait();
+      float o[32];
+      // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
+        o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
+      }
+      if (!valid) continue;
+      if (whole) {
+        // (o may start on any 16-byte border)
+        __nv_bfloat16* dst = p.o + out_row * D + cc * 32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(dst + 8 * q) =
+              make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                         pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
+          st32(p.part + ((4 * cc + q) * p.part_rows + part_row) * 8, v);
+        }
+      }
+    }
+    if (valid && (wide || t == 0)) {
+      if (whole) {
+        if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
+      } else {
+        p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
+      }
+      if (w->from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
+        const size_t at = ((static_cast<size_t>(w->own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
+        p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(static_cast<int>(blockIdx.x) / p.V << 16 | w->ctas, static_cast<int>(base + at_row));
+      }
+    }
+  }
+  tc_fence_before();
+  return ok;
 }
 
 template <int D>
@@ -961,275 +1229,33 @@ __global__ void __launch_bounds__(384, 1)
   } else {
     // ======================= softmax: warps 0-3 (slot 0), 4-7 (slot 1) =======================
     warpgroup_reg_alloc<C::SOFTMAX_REGS>();
-    const int t = warp >> 2;
-    const int r = threadIdx.x & 127;  // row of the tile == TMEM lane
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + t * C::SLOT_COLS;
-    const uint32_t tO = tS + C::O_OFF;
-    const float2 c2 = make_float2(p.c, p.c);
-    // The reference maximum m is raised only when a row's maximum climbs more than this above
-    // it; until then the exponentials stay below 2^8 and carry one constant factor that O / l
-    // cancels.
-    constexpr float kRescaleSlack = 8.f;
     bool ok = true;
-    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
-    };
     PxTake take;
-    uint32_t cnt = 0;   // tiles of this slot done so far (s_full phases)
-    uint32_t ecnt = 0;  // segments with at least one tile in this slot (pv_done phases)
-    uint32_t gkv = 0;   // ring position at the segment's start
-    // This thread's row of a segment: its sequence, and its place among the R; -1: none.
-    auto row_of = [&](const volatile PxSeg* w, int& seq) -> int {
-      int x = r;
-      asm volatile("" : "+r"(x));  // formed anew where it is needed
-      const int tile = w->tile + (w->wide() ? t : 0);
-      if (p.R <= kPxTile) {
-        const int q = x / p.R;
-        seq = w->s0 + tile * p.spt + q;
-        return q < p.spt && seq < w->s0 + w->n ? x - q * p.R : -1;
-      }
-      const int q = tile / p.TS;
-      seq = w->s0 + q;
-      const int rr = (tile - q * p.TS) * kPxTile + x;
-      return rr < p.R ? rr : -1;
-    };
-    while (true) {
-      const volatile PxSeg* w = take.next(bars, tmo, abort_flag);
+    uint32_t phases = 0;  // parities of this slot's s_full (bit 0) and pv_done (bit 1)
+    uint32_t gkv = 0;     // ring position at the segment's start
+    const volatile PxSeg* w;
+    // All eight warps go on or leave together. And both slots' O and the exchange area have been
+    // read by all before the next segment overwrites them.
+    auto next = [&]() -> bool {
+      w = take.next(bars, tmo, abort_flag);
       if (!w) ok = false;
       if (!ok) fail(SITE_PX_SOFTMAX);
-      // All eight warps go on or leave together. And both slots' O and the exchange area have
-      // been read by all before this segment overwrites them.
       ok = vote_all(1, 256, ok);
-      if (!ok || w->nt == 0) break;
-      if (w->own() && p.R <= kPxSlim) {
-        ok = px_slim<D>(p, w, bars, sQ, sK, sV, ex, take.i, gkv, tmo);
-        if (!ok) break;  // (as all eight warps voted)
-        take.done(bars);
-        continue;
-      }
-      const bool wide = w->wide();
-      int sees = 0x7fffffff;  // keys of the item that the row sees; rows of nobody are not masked
-      bool has_rows;
-      {
-        int seq;
-        const int rr = row_of(w, seq);
-        has_rows = __any_sync(0xffffffffu, rr >= 0);
-        if (rr >= 0) {
-          const int S = w->own() ? w->k1 : px_len(p, seq);
-          sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w->k1) - w->k0;
-        }
-      }
-      const int nt = w->nt;
-      const int x_first = wide ? 0 : t, step = wide ? 1 : 2;
-      const int mine = wide ? nt : (nt - t + 1) / 2;  // tiles of this slot
-      float m = -INFINITY;
-      float l = 0.f;   // sum of the unrounded p: the lse's
-      float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
-
-      for (int i = 0; i < mine; ++i, ++cnt) {
-        const int x = x_first + i * step;  // tile of the segment
-        const int key0 = (w->x0 + x) * kPxTile;  // from k0
-        if (!wwait(&bars->s_full[t], cnt & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (has_rows) {
-          uint32_t raw[4][32];
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, raw[cc]);
-          tmem_ld_wait();
-          float s[128];
-#pragma unroll
-          for (int k = 0; k < 128; ++k) s[k] = __uint_as_float(raw[k >> 5][k & 31]);
-          if (__any_sync(0xffffffffu, sees < key0 + kPxTile)) {
-            const int left = sees - key0;
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k >= left) s[k] = -INFINITY;
-          }
-          float mx8[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float a = fmax3(s[16 * k], s[16 * k + 1], s[16 * k + 2]);
-#pragma unroll
-            for (int e = 3; e < 15; e += 2) a = fmax3(a, s[16 * k + e], s[16 * k + e + 1]);
-            mx8[k] = fmaxf(a, s[16 * k + 15]);
-          }
-          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
-          const float m_tile = mx * p.c;
-          const float m_new = (m_tile > m + kRescaleSlack) ? m_tile : m;
-          const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-          const float alpha = sees == 0x7fffffff ? 1.f : ex2_approx(m - m_use);
-          // the largest p is not 1 against a stale reference: O's normaliser counts it as the
-          // bf16 product sees it, so that a nearly one-hot row is not off by its rounding
-          const float p_top = ex2_approx(fmaf(mx, p.c, -m_use));
-          const float p_top_err = __bfloat162float(__float2bfloat16_rn(p_top)) - p_top;
-          const float2 nm2 = make_float2(-m_use, -m_use);
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int e = cc * 32 + 2 * k;
-              const float2 v = ffma2(make_float2(s[e], s[e + 1]), c2, nm2);
-              const float2 ev = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-              acc[k & 3] = fadd2(acc[k & 3], ev);
-              pk[k] = pack_bf16x2(ev.x, ev.y);
-            }
-            tmem_st16(tS + cc * 16, pk);
-          }
-          const float2 at = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-          l = fmaf(l, alpha, at.x + at.y);
-          lc = fmaf(lc, alpha, p_top_err);
-          m = m_new;
-          // PV of this slot's previous tile is complete: S of this one was issued behind it
-          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            const float2 al2 = make_float2(alpha, alpha);
-#pragma unroll
-            for (int cc = 0; cc < D / 32; cc += 2) {
-              uint32_t o0[32], o1[32];
-              tmem_ld32(tO + cc * 32, o0);
-              tmem_ld32(tO + cc * 32 + 32, o1);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float2 v0 = fmul2(make_float2(__uint_as_float(o0[k]), __uint_as_float(o0[k + 1])), al2);
-                const float2 v1 = fmul2(make_float2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), al2);
-                o0[k] = __float_as_uint(v0.x);
-                o0[k + 1] = __float_as_uint(v0.y);
-                o1[k] = __float_as_uint(v1.x);
-                o1[k + 1] = __float_as_uint(v1.y);
-              }
-              tmem_st32(tO + cc * 32, o0);
-              tmem_st32(tO + cc * 32 + 32, o1);
-            }
-          }
-        }
-        // V rows past the item's end hold whatever the pool or an earlier tile left there, and
-        // 0 * NaN is not 0: the slot whose PV on this tile comes first zeroes them
-        const int rows_there = w->k1 - w->k0 - key0;
-        if (rows_there < kPxTile && (!wide || t == 0)) {
-          const uint32_t xg = gkv + x;
-          if (!wwait(&bars->v_full[xg % VST], (xg / VST) & 1)) {
-            ok = false;
-            break;
-          }
-          uint8_t* vt = sV + (xg % VST) * C::KV_BYTES;
-          for (int idx = r; idx < (kPxTile - rows_there) * C::KCH * 8; idx += 128) {
-            const int vr = rows_there + idx / (C::KCH * 8);
-            const int rem = idx % (C::KCH * 8);
-            *reinterpret_cast<uint4*>(vt + (rem >> 3) * C::CHUNK_BYTES + vr * 128 + (rem & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[t]);
-      }
-      gkv += nt;
-      if (ok && mine > 0) {
-        if (!wwait(&bars->pv_done[t], ecnt & 1)) ok = false;
-        ++ecnt;
-        tc_fence_after();
-      }
-
-      // ---- the segment's end: final rows, or a partial
-      int seq;
-      const int rr = row_of(w, seq);
-      const bool valid = rr >= 0;
-      if (!valid) {
-        m = -INFINITY;
-        l = lc = 0.f;
-      }
-      // A score that is NaN (a query that is not finite) may have left m at -inf, which would
-      // weigh the row 0: at +inf its weight, 2^(m - m), is NaN, here and in every join.
-      if (l != l) m = INFINITY;
-      const bool whole = w->own() && w->k0 == 0 && w->from_start() && w->to_end();
-      float m_all = m, sum = l + lc, lsum = l;
-      float f0 = 1.f, f1 = 0.f;  // weights of this slot's O (wide), or of slot 0's and slot 1's (narrow)
-      if (!wide) {
-        ex[t * 128 + r] = m;
-        ex[(2 + t) * 128 + r] = l + lc;
-        if (t == 1) ex[4 * 128 + r] = l;
-        if (!ok) fail(SITE_PX_SOFTMAX);
-        ok = vote_all(1, 256, ok);
-        if (!ok) break;  // all eight warps leave in the same segment
-        const float m0 = ex[r], m1 = ex[128 + r];
-        m_all = fmaxf(m0, m1);
-        const float m_use = m_all == -INFINITY ? 0.f : m_all;
-        f0 = ex2_approx(m0 - m_use);
-        f1 = ex2_approx(m1 - m_use);
-        sum = f0 * ex[256 + r] + f1 * ex[384 + r];
-        if (t == 0) lsum = f0 * l + f1 * ex[512 + r];
-      }
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
-        f0 *= inv;
-        f1 *= inv;
-      }
-      if (has_rows) {
-        // the row's place in its item's partials, and in the output
-        const int at_row = p.units * p.R * w->s0 + (w->hu * w->n + seq - w->s0) * p.R + rr;
-        const int kvh = w->hu * p.V + cta % p.V;
-        const long long base = (static_cast<long long>(w->own()) * p.V + cta % p.V) * p.area;
-        const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
-        const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + kvh) * p.R + rr;
-        // narrow: each slot's warps write half the columns of the joined O
-        const bool take0 = f0 != 0.f;
-        const bool take1 = !wide && nt > 1 && f1 != 0.f;
-        const uint32_t o_base = tmem + lane_base + (wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
-        const int c_lo = wide ? 0 : t * (D / 64), c_hi = wide ? D / 32 : c_lo + D / 64;
-#pragma unroll 1
-        for (int cc = c_lo; cc < c_hi; ++cc) {
-          uint32_t a[32], b[32];
-          tmem_ld32(o_base + cc * 32, a);
-          if (!wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
-          tmem_ld_wait();
-          float o[32];
-          // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
-            o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
-          }
-          if (!valid) continue;
-          if (whole) {
-            // (o may start on any 16-byte border)
-            __nv_bfloat16* dst = p.o + out_row * D + cc * 32;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(dst + 8 * q) =
-                  make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                             pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
-              st32(p.part + ((4 * cc + q) * p.part_rows + part_row) * 8, v);
-            }
-          }
-        }
-        if (valid && (wide || t == 0)) {
-          if (whole) {
-            if (p.lse) p.lse[out_row] = lsum == 0.f ? -INFINITY : (m_all + log2f(lsum)) * kLn2;
-          } else {
-            p.part_ml[part_row] = make_float4(m_all, sum, lsum, 0.f);
-          }
-          if (w->from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
-            const size_t at = ((static_cast<size_t>(w->own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
-            p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w->ctas, static_cast<int>(base + at_row));
-          }
-        }
-      }
-      tc_fence_before();
+      return ok && w->nt > 0;
+    };
+    // The slim segments are a share's last ones. A loop of their own: in one with the others,
+    // values of both are spilled, to memory that a busy L1 has no room for (64 sequences of 4096
+    // keys: 186 us, 169 without).
+    bool more;
+    while ((more = next()) && !(w->own() && p.R <= kPxSlim)) {
+      ok = px_rows<D>(p, w, bars, sV, ex, phases, gkv, tmo);
       take.done(bars);
     }
+    for (; more; more = next()) {
+      if (!px_slim<D>(p, w, bars, sQ, sK, sV, ex, take.i, gkv, tmo)) break;  // (as all eight warps voted)
+      take.done(bars);
+    }
+    tc_fence_before();
   }
 
   tc_fence_before();
@@ -1517,9 +1543,9 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.num_pages = num_pages;
   p.c = scale * kLog2e;
   if (s.R <= kPxSlim)
-    p.cost = d == 128 ? PxCost{5, 6, 3, 6, 4, 2} : PxCost{3, 6, 3, 6, 3, 2};
+    p.cost = d == 128 ? PxCost{10, 14, 8, 18, 10, 5} : PxCost{9, 14, 8, 20, 8, 6};
   else
-    p.cost = d == 128 ? PxCost{4, 5, 3, 6, 4, 5} : PxCost{3, 4, 3, 6, 3, 4};
+    p.cost = d == 128 ? PxCost{10, 14, 8, 18, 10, 14} : PxCost{9, 14, 8, 20, 9, 14};
   p.area = s.area;
   p.part_rows = 2 * s.V * s.area;
   p.part = reinterpret_cast<float*>(ws);
