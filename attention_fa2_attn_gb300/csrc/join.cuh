@@ -19,6 +19,21 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// mbar_wait in a quarter of its code, for kernels with many kinds of work: what a CTA runs for
+// the first time comes from L2, a microsecond or more for a few KB while that is busy.
+__device__ __forceinline__ bool mbar_wait_lean(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                               const volatile int* abort = nullptr) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  int i = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(a, parity)) {
+    if ((++i & 31) == 0 && ((abort && *abort) || globaltimer_ns() - t0 > timeout_ns)) return false;
+  }
+  return true;
+}
+
 // 32 bytes in one store: a warp whose threads each write a row of their own spends a
 // wavefront per row and store, so half as many as with 16 bytes.
 __device__ __forceinline__ void st32(void* p, const uint32_t (&v)[8]) {

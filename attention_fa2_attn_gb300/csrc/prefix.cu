@@ -104,6 +104,13 @@ struct PxParams {
 };
 constexpr int kPxDone = -1;  // the rows are written
 
+// Where share c of `shares` begins on a line of cost `total`: c * total / shares, in 32 bits.
+struct PxCut {
+  int whole, rest, shares;
+  __device__ __forceinline__ PxCut(int total = 0, int n = 1) : whole(total / n), rest(total % n), shares(n) {}
+  __device__ __forceinline__ int begin(int c) const { return c * whole + static_cast<int>(static_cast<unsigned>(c * rest) / static_cast<unsigned>(shares)); }
+};
+
 // A run of steps of one unit inside a CTA's share, as all roles get it.
 struct PxSeg {
   int s0, n;   // the item's sequences
@@ -170,6 +177,7 @@ __device__ __forceinline__ PxItem px_sequence(const PxParams& p, int b, int pref
 // The group that b is in, the last that begins at or before it: its first and last sequence
 // and its prefix for a sequence in it, 0 for others. `g`: a group at or before it.
 __device__ __forceinline__ int px_prefix_of(const PxParams& p, int b, int& g) {
+#pragma unroll 1
   while (g + 1 < p.G && __ldg(p.starts + g + 1) <= b) ++g;
   const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1);
   return b >= s0 && b < s1 ? px_prefix(p, s0, s1, __ldg(p.prefix_lens + g)) : 0;
@@ -178,7 +186,8 @@ __device__ __forceinline__ int px_prefix_of(const PxParams& p, int b, int& g) {
 // Walks a share segment by segment. Items: the groups, then the sequences.
 struct PxWalk {
   int it, off, at, g;  // item, cost into it, cost into the line, the group that is looked at
-  int end, total, shares;
+  int end;
+  PxCut cut;
   bool no_groups;
   PxCost c;
   __device__ __forceinline__ PxItem item(const PxParams& p, int i) {
@@ -192,6 +201,7 @@ struct PxWalk {
     PxItem x;
     int from, to, j0, j1, cost, unit_end;
     bool wide;
+#pragma unroll 1
     do {
       if (at >= end) return false;
       x = item(p, it);
@@ -230,8 +240,10 @@ struct PxWalk {
     w.k1 = x.k1;
     w.x0 = j0 * per;
     w.nt = min(x.key_tiles(), j1 * per) - w.x0;
-    // the last CTA with a share of the unit is the one whose share holds its end
-    w.ctas = static_cast<int>((static_cast<long long>(unit_end) * shares - 1) / total) - me + 1;
+    // CTAs up to the one whose share holds the unit's end
+    w.ctas = 1;
+#pragma unroll 1
+    while (cut.begin(me + w.ctas) < unit_end) ++w.ctas;
     return true;
   }
 };
@@ -244,7 +256,7 @@ struct PxTake {
   // a whole warp; null: the wait ran out
   __device__ __forceinline__ const volatile PxSeg* next(PxBars* bars, uint64_t tmo, const volatile int* abort_flag) const {
     const uint32_t e = i % kPxQueue;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return nullptr;
+    if (!__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return nullptr;
     return &bars->seg[e];
   }
   __device__ __forceinline__ void done(PxBars* bars) {
@@ -272,7 +284,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   const int gid = lane >> 2, tig = lane & 3;  // row of the MMA fragment (and + 8), column pair
   const int cta = blockIdx.x, me = cta / p.V;
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+    return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, tmo, abort_flag));
   };
   // keys that the thread's two rows see (what rows from R on get goes nowhere)
   int sees[2];
@@ -299,6 +311,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   const int key_of = warp * 16;  // this warp's first key of a tile
   uint32_t ks = gkv % KST, kl = gkv / KST, vs = gkv % VST, vl = gkv / VST;
   const int nt = w->nt;
+#pragma unroll 1
   for (int x = 0; ok && x < nt; ++x) {
     if (!wwait(&bars->k_full[ks], kl & 1)) {
       ok = false;
@@ -372,6 +385,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     if (there < 16) {
       // V rows past the item's end hold whatever the pool or an earlier tile left there, and
       // 0 * NaN is not 0
+#pragma unroll 1
       for (int idx = lane; idx < 16 * (D / 8); idx += 32)
         if (idx / (D / 8) >= there)
           *reinterpret_cast<uint4*>(vt + sw_off(key_of + idx / (D / 8), idx % (D / 8) * 8, C::CHUNK_BYTES)) = make_uint4(0u, 0u, 0u, 0u);
@@ -422,17 +436,21 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
   const size_t out_row = (static_cast<size_t>(w->s0) * p.Hkv + kvh) * p.R;
   constexpr int COLS = D / 32;  // columns of a thread in the joined rows, a row to a warp
-#pragma unroll
-  for (int ri = 0; ri < 2; ++ri) {
+#pragma unroll 1
+  for (int ri = 0; 8 * ri < p.R; ++ri) {
     if (ri == 1) {
-      if (p.R <= 8) break;
       named_bar_sync(2, 256);  // the first eight rows have been read
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] = o[n][2];
+        o[n][1] = o[n][3];
+      }
     }
     // (columns are turned round by the row, so that eight rows fall on all banks)
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
       *reinterpret_cast<float2*>(part_o + (warp * 8 + gid) * D + ((n * 8 + 2 * tig) ^ ((gid & 3) << 3))) =
-          make_float2(o[n][2 * ri], o[n][2 * ri + 1]);
+          make_float2(o[n][0], o[n][1]);
     if (ri == 0) {
       ok = vote_all(1, 256, ok);
       if (!ok) return false;
@@ -504,7 +522,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
   const float2 c2 = make_float2(p.c, p.c);
   bool ok = true;
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, tmo, abort_flag));
+    return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, tmo, abort_flag));
   };
   // This thread's row of the segment: its sequence, and its place among the R; -1: none.
   auto row_of = [&](int& seq) -> int {
@@ -541,6 +559,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
   float l = 0.f;   // sum of the unrounded p: the lse's
   float lc = 0.f;  // bf16(p_top) - p_top of each tile's largest p, rescaled like l
 
+#pragma unroll 1
   for (int i = 0; i < mine; ++i, phases ^= 1) {
     const int x = x_first + i * step;  // tile of the segment
     const int key0 = x * kPxTile;
@@ -602,23 +621,18 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
       // PV of this slot's previous tile is complete: S of this one was issued behind it
       if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         const float2 al2 = make_float2(alpha, alpha);
-#pragma unroll
-        for (int cc = 0; cc < D / 32; cc += 2) {
-          uint32_t o0[32], o1[32];
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o0[32];
           tmem_ld32(tO + cc * 32, o0);
-          tmem_ld32(tO + cc * 32 + 32, o1);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
             const float2 v0 = fmul2(make_float2(__uint_as_float(o0[k]), __uint_as_float(o0[k + 1])), al2);
-            const float2 v1 = fmul2(make_float2(__uint_as_float(o1[k]), __uint_as_float(o1[k + 1])), al2);
             o0[k] = __float_as_uint(v0.x);
             o0[k + 1] = __float_as_uint(v0.y);
-            o1[k] = __float_as_uint(v1.x);
-            o1[k + 1] = __float_as_uint(v1.y);
           }
           tmem_st32(tO + cc * 32, o0);
-          tmem_st32(tO + cc * 32 + 32, o1);
         }
       }
     }
@@ -632,6 +646,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
         break;
       }
       uint8_t* vt = sV + (xg % VST) * C::KV_BYTES;
+#pragma unroll 1
       for (int idx = r; idx < (kPxTile - rows_there) * C::KCH * 8; idx += 128) {
         const int vr = rows_there + idx / (C::KCH * 8);
         const int rem = idx % (C::KCH * 8);
@@ -699,37 +714,30 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
     const bool take0 = f0 != 0.f;
     const bool take1 = !wide && nt > 1 && f1 != 0.f;
     const uint32_t o_base = tmem + lane_base + (wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
-    const int c_lo = wide ? 0 : t * (D / 64), c_hi = wide ? D / 32 : c_lo + D / 64;
+    const int c_lo = wide ? 0 : t * (D / 16), c_hi = wide ? D / 8 : c_lo + D / 16;  // chunks of eight columns
 #pragma unroll 1
     for (int cc = c_lo; cc < c_hi; ++cc) {
-      uint32_t a[32], b[32];
-      tmem_ld32(o_base + cc * 32, a);
-      if (!wide) tmem_ld32(o_base + C::SLOT_COLS + cc * 32, b);
+      uint32_t a[8], b[8];
+      tmem_ld8(o_base + cc * 8, a);
+      tmem_ld8(o_base + (wide ? 0 : C::SLOT_COLS) + cc * 8, b);
       tmem_ld_wait();
-      float o[32];
       // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+      float o[8];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < 8; ++k) {
         o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
         o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
       }
       if (!valid) continue;
       if (whole) {
         // (o may start on any 16-byte border)
-        __nv_bfloat16* dst = p.o + out_row * D + cc * 32;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(dst + 8 * q) =
-              make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                         pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
+        *reinterpret_cast<uint4*>(p.o + out_row * D + cc * 8) =
+            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
       } else {
+        uint32_t v[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
-          st32(p.part + ((4 * cc + q) * p.part_rows + part_row) * 8, v);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[k]);
+        st32(p.part + (cc * p.part_rows + part_row) * 8, v);
       }
     }
     if (valid && (wide || t == 0)) {
@@ -774,6 +782,7 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 8);
+#pragma unroll 1
     for (int s = 0; s < 6; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
@@ -809,6 +818,7 @@ __global__ void __launch_bounds__(384, 1)
     int* gs = reinterpret_cast<int*>(sK);  // [G + 1]: starts
     int* gp = gs + p.G + 1;                // [G]: prefixes
     bool bad = false;
+#pragma unroll 1
     for (int g = threadIdx.x; g < p.G; g += C::THREADS) {
       const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1), asked = __ldg(p.prefix_lens + g);
       gs[g] = s0;
@@ -826,77 +836,82 @@ __global__ void __launch_bounds__(384, 1)
       if (!bad) {
         if (g < 0) {  // the last that begins at or before b
           int top = p.G;
+#pragma unroll 1
           for (g = 0; top - g > 1;) {
             const int mid = (g + top) / 2;
             if (gs[mid] <= b) g = mid; else top = mid;
           }
         }
+#pragma unroll 1
         while (g + 1 < p.G && gs[g + 1] <= b) ++g;
         if (b >= gs[g] && b < gs[g + 1]) prefix = gp[g];
       }
       return PxItem{b, b + 1, prefix, i == lo ? len : px_len(p, b), p.TS, true};
     };
-    // steps of the items before this thread's, and their cost; a line's whole cost is below 2^31
-    int steps = 0, mine = 0, g = -1;
-    for (int i = lo; i < hi; ++i) {
-      const PxItem x = item(i, g);
-      steps += x.head(PX_BY_STEPS);
-      mine += x.head(p.cost);
-    }
-    steps *= p.units;
-    mine *= p.units;
-    int steps_inc = steps, inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, steps_inc, o);
-      if (lane >= o) {
-        inc += y;
-        steps_inc += z;
-      }
-    }
-    // totals per warp go through the exchange area, which nothing uses yet
-    int2* wsum = reinterpret_cast<int2*>(ex);
-    if (lane == 31) wsum[warp] = make_int2(inc, steps_inc);
-    __syncthreads();
-    int before = inc - mine, steps_before = steps_inc - steps, total = 0, all_steps = 0;
-#pragma unroll
-    for (int w = 0; w < 12; ++w) {
-      const int2 v = wsum[w];
-      if (w < warp) {
-        before += v.x;
-        steps_before += v.y;
-      }
-      total += v.x;
-      all_steps += v.y;
-    }
-    const int grid = static_cast<int>(gridDim.x) / p.V;
-    // lines of so few steps that a CTA has hardly more than one are cut by steps alone; a
-    // share is a step's cost or more either way, so that every CTA between a unit's first and
-    // last has a step of it
-    const bool few = all_steps <= 2 * grid;
+    // Twice over the thread's items: for the sums of steps and cost (a line's whole cost is below
+    // 2^31), and for the one that holds the share's start, if it is here.
+    int2* wsum = reinterpret_cast<int2*>(ex);  // totals per warp, in the exchange area that nothing uses yet
+    int steps = 0, mine = 0, off = -1;
     walk.c = p.cost;
-    if (few) {
-      walk.c = PX_BY_STEPS;
-      before = steps_before;
-      mine = steps;
-      total = all_steps;
-    }
-    walk.total = total;
-    walk.shares = few ? min(grid, max(1, all_steps)) : grid;
-    walk.no_groups = bad;
-    walk.at = me < walk.shares ? static_cast<int>(static_cast<long long>(me) * total / walk.shares) : total;
-    walk.end = me < walk.shares ? static_cast<int>((me + 1ll) * total / walk.shares) : total;
-    if (walk.at < walk.end && walk.at >= before && walk.at < before + mine) {  // one thread: its items hold the share's start
-      int off = walk.at - before, i = lo;
-      g = -1;
-      for (; i < hi; ++i) {
-        const int s = item(i, g).head(walk.c) * p.units;
-        if (off < s) break;
-        off -= s;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int g = -1;
+#pragma unroll 1
+      for (int i = lo; i < hi; ++i) {
+        const PxItem x = item(i, g);
+        const int cost = x.head(walk.c) * p.units;
+        if (pass == 0) {
+          steps += x.head(PX_BY_STEPS) * p.units;
+          mine += cost;
+        } else if (off >= 0) {
+          if (off < cost) {
+            bars->it0 = i;
+            bars->off0 = off;
+            bars->group0 = max(g, 0);
+          }
+          off -= cost;
+        }
       }
-      bars->it0 = i;
-      bars->off0 = off;
-      bars->group0 = max(g, 0);
+      if (pass == 1) break;
+      int2 inc = make_int2(mine, steps);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc.x, o), z = __shfl_up_sync(0xffffffffu, inc.y, o);
+        if (lane >= o) {
+          inc.x += y;
+          inc.y += z;
+        }
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      int2 before = make_int2(inc.x - mine, inc.y - steps), all = make_int2(0, 0);
+#pragma unroll 1
+      for (int w = 0; w < 12; ++w) {
+        const int2 v = wsum[w];
+        if (w < warp) {
+          before.x += v.x;
+          before.y += v.y;
+        }
+        all.x += v.x;
+        all.y += v.y;
+      }
+      const int grid = static_cast<int>(gridDim.x) / p.V;
+      // Lines of so few steps that a CTA has hardly more than one are cut by steps alone. A share
+      // is a step's cost or more either way, so that every CTA between a unit's first and last
+      // has a step of it.
+      int shares = grid;
+      if (all.y <= 2 * grid) {
+        walk.c = PX_BY_STEPS;
+        before.x = before.y;
+        mine = steps;
+        all.x = all.y;
+        shares = min(grid, max(1, all.y));
+      }
+      walk.cut = PxCut(all.x, shares);
+      walk.no_groups = bad;
+      walk.at = me < shares ? walk.cut.begin(me) : all.x;
+      walk.end = me < shares ? walk.cut.begin(me + 1) : all.x;
+      if (walk.at < walk.end && walk.at >= before.x && walk.at < before.x + mine) off = walk.at - before.x;  // one thread
     }
   }
   fence_async_smem();  // the rings' memory was read and written by plain accesses
@@ -931,6 +946,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t q_loads = 0;
       const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
       bool ok = true;
+#pragma unroll 1
       while (ok && !*abort_flag) {
         PxSeg w;
         {
@@ -968,6 +984,7 @@ __global__ void __launch_bounds__(384, 1)
             const int rows = min(p.R, kPxTile) * p.spt;  // of a box; those behind the batch's end are zeros
             const int tiles = w.wide() ? 2 : 1;
             mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(tiles * C::KCH * rows * 128));
+#pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
               const int tile = w.tile + t, seq = tile / p.TS;
               for (int c = 0; c < C::KCH; ++c)
@@ -981,12 +998,13 @@ __global__ void __launch_bounds__(384, 1)
         auto q_free = [&]() {  // uniform: every lane asks, and one answer counts
           return q_loads == 0 || __all_sync(0xffffffffu, mbar_test(&bars->q_empty, (q_loads - 1) & 1));
         };
+#pragma unroll 1
         for (int x = 0; x < w.nt; ++x, ++g) {
           if (q_due) {
             if (q_free()) {
               load_q();
             } else if (x == KST - 1) {
-              if (!mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
+              if (!mbar_wait_lean(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -1004,7 +1022,7 @@ __global__ void __launch_bounds__(384, 1)
             record_error(p.err, FA_ERR_BOUNDS, SITE_PX_TABLE);
             pe = 0;
           }
-          if (g >= ST && !mbar_wait(&my_empty[stage], (lap & 1) ^ 1, tmo, abort_flag)) {
+          if (g >= ST && !mbar_wait_lean(&my_empty[stage], (lap & 1) ^ 1, tmo, abort_flag)) {
             ok = false;
             break;
           }
@@ -1019,7 +1037,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         if (ok && q_due) {
-          if (q_loads > 0 && !mbar_wait(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
+          if (q_loads > 0 && !mbar_wait_lean(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
             ok = false;
           else
             load_q();
@@ -1028,8 +1046,9 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) fail(SITE_PX_PRODUCER);
       // Copies in flight must land before the CTA exits. Waited for whether or not a wait has
       // run out so far: another role's may after this warp has issued its last copy.
-      if (q_loads > 0) mbar_wait(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
-      for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) mbar_wait(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
+      if (q_loads > 0) mbar_wait_lean(&bars->q_full, (q_loads - 1) & 1, tmo_unwind);
+#pragma unroll 1
+      for (uint32_t x = g > ST ? g - ST : 0; x < g; ++x) mbar_wait_lean(&my_full[x % ST], (x / ST) & 1, tmo_unwind);
     } else if (warp == 9) {
       // ======================= MMA issuer =======================
       const bool leader = elect_one();
@@ -1071,7 +1090,7 @@ __global__ void __launch_bounds__(384, 1)
           tc_commit(bar);
         }
       };
-      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, tmo, abort_flag); };
+      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait_lean(bar, parity, tmo, abort_flag); };
       auto wait_k = [&](uint32_t x) -> bool {
         const bool r = wwait(&bars->k_full[x % KST], (x / KST) & 1);
         tc_fence_after();
@@ -1092,6 +1111,7 @@ __global__ void __launch_bounds__(384, 1)
       PxTake take;
       uint32_t g = 0;  // key tiles of earlier segments (ring position)
       bool ok = true;
+#pragma unroll 1
       for (int nt; ok; g += nt) {
         const volatile PxSeg* from = take.next(bars, tmo, abort_flag);
         if (!from) {
@@ -1111,59 +1131,47 @@ __global__ void __launch_bounds__(384, 1)
         tc_fence_after();
         if (!wide) {
           // slots take the tiles in turn: tile x in slot x & 1
-          for (int x = 0; x < 2 && x < nt; ++x) {
-            if (!wait_k(g + x)) {
-              ok = false;
-              break;
-            }
-            qk(x, 0, (g + x) % KST);
-            commit(&bars->s_full[x]);
+          auto score = [&](int x) -> bool {
+            if (!wait_k(g + x)) return false;
+            qk(x & 1, 0, (g + x) % KST);
+            commit(&bars->s_full[x & 1]);
             release(&bars->k_empty[(g + x) % KST]);
-            if (x + 1 == nt) release(&bars->q_empty);
-          }
-          for (int x = 0; ok && x < nt; ++x) {
-            const int t = x & 1;
-            if (!wait_p(t) || !wait_v(g + x)) {
-              ok = false;
-              break;
-            }
-            pv(t, (g + x) % VST, x < 2);
-            release(&bars->v_empty[(g + x) % VST]);
-            if (x + 2 >= nt) {
-              commit(&bars->pv_done[t]);
-            } else {
-              // S of this slot overwrites the columns P was read from; one thread's MMAs run in order
-              if (!wait_k(g + x + 2)) {
+            if (x + 1 == nt) release(&bars->q_empty);  // the segment's last S
+            return true;
+          };
+          // the first two tiles' S, then PV of each with the S of the next but one right behind it:
+          // that overwrites the columns P was read from, and one thread's MMAs run in order
+#pragma unroll 1
+          for (int x = -2; ok && x < nt; ++x) {
+            if (x >= 0) {
+              const int t = x & 1;
+              if (!wait_p(t) || !wait_v(g + x)) {
                 ok = false;
                 break;
               }
-              qk(t, 0, (g + x + 2) % KST);
-              commit(&bars->s_full[t]);
-              release(&bars->k_empty[(g + x + 2) % KST]);
-              if (x + 3 == nt) release(&bars->q_empty);  // the segment's last S
+              pv(t, (g + x) % VST, x < 2);
+              release(&bars->v_empty[(g + x) % VST]);
+              if (x + 2 >= nt) commit(&bars->pv_done[t]);
             }
+            if (x + 2 < nt) ok = score(x + 2);
           }
         } else {
-          if (!wait_k(g)) {
-            ok = false;
-            break;
-          }
-          qk(0, 0, g % KST);
-          commit(&bars->s_full[0]);
-          qk(1, 1, g % KST);
-          commit(&bars->s_full[1]);
-          release(&bars->k_empty[g % KST]);
-          if (nt == 1) release(&bars->q_empty);
-          for (int x = 0; ok && x < nt; ++x) {
+          // the first tile's S for both row tiles, then PV of each with the S of the next behind it
+#pragma unroll 1
+          for (int x = -1; ok && x < nt; ++x) {
             const uint32_t sv = (g + x) % VST, sk = (g + x + 1) % KST;
             const bool more = x + 1 < nt;
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-              if (!wait_p(t) || (t == 0 && !wait_v(g + x))) {
-                ok = false;
-                break;
+              if (x >= 0) {
+                if (!wait_p(t) || (t == 0 && !wait_v(g + x))) {
+                  ok = false;
+                  break;
+                }
+                pv(t, sv, x == 0);
+                if (t == 1) release(&bars->v_empty[sv]);
+                if (!more) commit(&bars->pv_done[t]);
               }
-              pv(t, sv, x == 0);
-              if (t == 1) release(&bars->v_empty[sv]);
               if (more) {
                 if (t == 0 && !wait_k(g + x + 1)) {
                   ok = false;
@@ -1171,8 +1179,6 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 qk(t, t, sk);
                 commit(&bars->s_full[t]);
-              } else {
-                commit(&bars->pv_done[t]);
               }
             }
             if (ok && more) {
@@ -1184,7 +1190,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok && leader) fail(SITE_PX_MMA);
       commit(&bars->drain);  // every MMA must finish before TMEM is released
-      mbar_wait(&bars->drain, 0, tmo_unwind);
+      mbar_wait_lean(&bars->drain, 0, tmo_unwind);
     } else {
       // ======================= the walk =======================
       // Lengths and groups come from L2 and a step of the walk takes some divisions, 0.9 us: one
@@ -1194,12 +1200,13 @@ __global__ void __launch_bounds__(384, 1)
         walk.off = bars->off0;
         walk.g = bars->group0;
         bool ok = true;
+#pragma unroll 1
         for (uint32_t i = 0;; ++i) {
           PxSeg w;
           const bool more = walk.next(p, me, w);
           if (!more) w.nt = 0;
           const uint32_t e = i % kPxQueue;
-          if (i >= kPxQueue && !mbar_wait(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag)) {
+          if (i >= kPxQueue && !mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag)) {
             ok = false;
             break;
           }
@@ -1211,8 +1218,10 @@ __global__ void __launch_bounds__(384, 1)
       }
       __syncwarp();
       // rows that a kind has no partials of: somebody has to say so
+#pragma unroll 1
       for (int b = cta; b < p.B; b += gridDim.x) {
         int gb = 0, top = p.G;
+#pragma unroll 1
         while (!walk.no_groups && top - gb > 1) {
           const int mid = (gb + top) / 2;
           if (__ldg(p.starts + mid) <= b) gb = mid; else top = mid;
@@ -1221,8 +1230,10 @@ __global__ void __launch_bounds__(384, 1)
         const int n = p.Hkv * p.TS;
         const size_t at = static_cast<size_t>(b) * n;
         if (prefix == 0)
+#pragma unroll 1
           for (int i = lane; i < n; i += 32) p.desc[at + i] = make_int2(0, 0);
         if (px_len(p, b) <= prefix)
+#pragma unroll 1
           for (int i = lane; i < n; i += 32) p.desc[static_cast<size_t>(p.B) * n + at + i] = make_int2(0, 0);
       }
     }
@@ -1247,10 +1258,12 @@ __global__ void __launch_bounds__(384, 1)
     // values of both are spilled, to memory that a busy L1 has no room for (64 sequences of 4096
     // keys: 186 us, 169 without).
     bool more;
+#pragma unroll 1
     while ((more = next()) && !(w->own() && p.R <= kPxSlim)) {
       ok = px_rows<D>(p, w, bars, sV, ex, phases, gkv, tmo);
       take.done(bars);
     }
+#pragma unroll 1
     for (; more; more = next()) {
       if (!px_slim<D>(p, w, bars, sQ, sK, sV, ex, take.i, gkv, tmo)) break;  // (as all eight warps voted)
       take.done(bars);
