@@ -61,7 +61,9 @@ struct PxCfg {
   static constexpr int OFF_EX = OFF_BAR + 512;
   static constexpr int SMEM = OFF_EX + kPxTile * 5 * 4;
   static_assert(SMEM <= 232448, "shared memory of an SM");
-  static_assert(OFF_BAR - OFF_K >= (2 * FA_PREFIX_MAX_GROUPS + 1) * 4, "the groups, before the rings are in use");
+  // sequences whose lengths fit into the rings beside the most groups, before the rings are in use
+  static constexpr int MOST_LENS = (OFF_BAR - OFF_K) / 4 - 2 * FA_PREFIX_MAX_GROUPS - 1;
+  static_assert(MOST_LENS > 0, "the groups");
   static_assert(8 * 8 * D * 4 <= Q_BYTES, "slim: eight warps' O for eight rows, in the second Q tile");
   static constexpr int SLOT_COLS = 256;  // a slot's columns: S/P, then O
   static constexpr int O_OFF = 128;
@@ -212,8 +214,9 @@ struct PxWalk {
         j0 = j1 = 0;
         continue;
       }
-      w.hu = off / head;
-      const int rest = off - w.hu * head, pair = x.wide(c), u = min(x.tiles / 2, rest / pair);
+      // (a division is some 40 instructions in a row: none where the answer is plain)
+      w.hu = p.units > 1 ? off / head : 0;
+      const int rest = off - w.hu * head, pair = x.wide(c), u = x.tiles < 2 ? 0 : min(x.tiles / 2, rest / pair);
       w.tile = 2 * u;
       wide = u < x.tiles / 2;
       from = rest - u * pair;
@@ -221,8 +224,8 @@ struct PxWalk {
       to = min(cost, from + end - at);
       const int step = wide ? c.wide_step : x.own ? c.own_step : c.narrow_step;
       const int front = wide ? c.wide_front : x.own ? c.own_front : c.narrow_front;
-      j0 = from < front ? 0 : (from - front) / step;
-      j1 = to < front ? 0 : (to - front) / step;
+      j0 = from <= front ? 0 : (from - front) / step;
+      j1 = to == cost ? (wide ? x.key_tiles() : (x.key_tiles() + 1) / 2) : to < front ? 0 : (to - front) / step;
       unit_end = at - from + cost;
       w.flags = (wide ? 1 : 0) | (x.own ? 2 : 0) | (j0 == 0 ? 4 : 0) | (to == cost ? 8 : 0);
       off += to - from;
@@ -242,8 +245,10 @@ struct PxWalk {
     w.nt = min(x.key_tiles(), j1 * per) - w.x0;
     // CTAs up to the one whose share holds the unit's end
     w.ctas = 1;
+    if (!(w.flags & 8)) {
 #pragma unroll 1
-    while (cut.begin(me + w.ctas) < unit_end) ++w.ctas;
+      while (cut.begin(me + w.ctas) < unit_end) ++w.ctas;
+    }
     return true;
   }
 };
@@ -806,31 +811,38 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 9) tmem_alloc(&bars->tmem_base, 512);
   pdl_wait();
 
-  // ---- this CTA's share of its line's cost: a block-wide scan over the items. The groups go
-  // through shared memory that the rings use later.
+  // ---- this CTA's share of its line's cost: a block-wide scan over the items. Groups and lengths
+  // go through shared memory that the rings use later: one round trip to L2 for all of them.
   PxWalk walk;
   {
     const int items = p.G + p.B;
     const int per = (items + C::THREADS - 1) / C::THREADS;
     const int lo = min(items, static_cast<int>(threadIdx.x) * per), hi = min(items, lo + per);
-    // a thread's first sequence, on its way while the groups are looked at
-    const int len = lo >= p.G && lo < hi ? px_len(p, lo - p.G) : 0;
     int* gs = reinterpret_cast<int*>(sK);  // [G + 1]: starts
-    int* gp = gs + p.G + 1;                // [G]: prefixes
-    bool bad = false;
+    int* gp = gs + p.G + 1;                // [G]: prefixes as they were asked for
+    int* ls = gp + p.G;                    // [B]: lengths, where there is room for them
+    const bool lens_here = p.B <= C::MOST_LENS;
 #pragma unroll 1
-    for (int g = threadIdx.x; g < p.G; g += C::THREADS) {
-      const int s0 = __ldg(p.starts + g), s1 = __ldg(p.starts + g + 1), asked = __ldg(p.prefix_lens + g);
-      gs[g] = s0;
-      if (g == p.G - 1) gs[p.G] = s1;
-      const bool fine = 0 <= s0 && s0 <= s1 && s1 <= p.B;
-      bad |= !fine;
-      gp[g] = fine ? px_prefix(p, s0, s1, asked) : 0;
+    for (int i = threadIdx.x; i <= p.G; i += C::THREADS) {
+      gs[i] = __ldg(p.starts + i);
+      if (i < p.G) gp[i] = __ldg(p.prefix_lens + i);
     }
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
+    if (lens_here) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < p.B; i += C::THREADS) ls[i] = px_len(p, i);
+    }
+    __syncthreads();
+    bool bad = false, wrong = false;  // the groups are not what they should be; seen by this thread
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.G; i += C::THREADS) wrong |= gs[i] < 0 || gs[i] > gs[i + 1] || gs[i + 1] > p.B;
+    auto len = [&](int b) { return lens_here ? ls[b] : px_len(p, b); };
+    auto prefix_of = [&](int g) {
+      const int s0 = gs[g], s1 = gs[g + 1];
+      // (until the sums are made it is not known whether the starts are in order)
+      return s1 - s0 < 2 || s0 < 0 || s1 > p.B ? 0 : max(0, min(gp[g], len(s0))) & ~15;
+    };
     auto item = [&](int i, int& g) {
-      if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0, false} : px_group(p, gs[i], gs[i + 1], gp[i]);
+      if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0, false} : px_group(p, gs[i], gs[i + 1], prefix_of(i));
       const int b = i - p.G;
       int prefix = 0;
       if (!bad) {
@@ -844,35 +856,37 @@ __global__ void __launch_bounds__(384, 1)
         }
 #pragma unroll 1
         while (g + 1 < p.G && gs[g + 1] <= b) ++g;
-        if (b >= gs[g] && b < gs[g + 1]) prefix = gp[g];
+        if (b >= gs[g] && b < gs[g + 1]) prefix = prefix_of(g);
       }
-      return PxItem{b, b + 1, prefix, i == lo ? len : px_len(p, b), p.TS, true};
+      return PxItem{b, b + 1, prefix, len(b), p.TS, true};
     };
-    // Twice over the thread's items: for the sums of steps and cost (a line's whole cost is below
-    // 2^31), and for the one that holds the share's start, if it is here.
-    int2* wsum = reinterpret_cast<int2*>(ex);  // totals per warp, in the exchange area that nothing uses yet
-    int steps = 0, mine = 0, off = -1;
+    // Over the thread's items for the sums of steps and cost (a line's whole cost is below 2^31),
+    // again where the groups turn out to be wrong; and, in the thread whose items hold the share's
+    // start, where there are several, for the one that does.
+    int4* wsum = reinterpret_cast<int4*>(ex);  // totals per warp, in the exchange area that nothing uses yet
+    int off = -1, g;
     walk.c = p.cost;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      int g = -1;
+    while (true) {
+      int steps = 0, mine = 0;
+      g = -1;
 #pragma unroll 1
       for (int i = lo; i < hi; ++i) {
         const PxItem x = item(i, g);
         const int cost = x.head(walk.c) * p.units;
-        if (pass == 0) {
+        if (off < 0) {
           steps += x.head(PX_BY_STEPS) * p.units;
           mine += cost;
-        } else if (off >= 0) {
+        } else {
           if (off < cost) {
             bars->it0 = i;
             bars->off0 = off;
             bars->group0 = max(g, 0);
+            break;
           }
           off -= cost;
         }
       }
-      if (pass == 1) break;
+      if (off >= 0) break;
       int2 inc = make_int2(mine, steps);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -882,18 +896,27 @@ __global__ void __launch_bounds__(384, 1)
           inc.y += z;
         }
       }
-      if (lane == 31) wsum[warp] = inc;
+      const bool warp_wrong = __any_sync(0xffffffffu, wrong);
+      if (lane == 31) wsum[warp] = make_int4(inc.x, inc.y, warp_wrong, 0);
       __syncthreads();
       int2 before = make_int2(inc.x - mine, inc.y - steps), all = make_int2(0, 0);
-#pragma unroll 1
+      int any_wrong = 0;
+#pragma unroll
       for (int w = 0; w < 12; ++w) {
-        const int2 v = wsum[w];
+        const int4 v = wsum[w];
         if (w < warp) {
           before.x += v.x;
           before.y += v.y;
         }
         all.x += v.x;
         all.y += v.y;
+        any_wrong |= v.z;
+      }
+      if (any_wrong && !bad) {  // every sequence by itself then
+        bad = true;
+        if (threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
+        __syncthreads();
+        continue;
       }
       const int grid = static_cast<int>(gridDim.x) / p.V;
       // Lines of so few steps that a CTA has hardly more than one are cut by steps alone. A share
@@ -911,7 +934,14 @@ __global__ void __launch_bounds__(384, 1)
       walk.no_groups = bad;
       walk.at = me < shares ? walk.cut.begin(me) : all.x;
       walk.end = me < shares ? walk.cut.begin(me + 1) : all.x;
-      if (walk.at < walk.end && walk.at >= before.x && walk.at < before.x + mine) off = walk.at - before.x;  // one thread
+      if (!(walk.at < walk.end && walk.at >= before.x && walk.at < before.x + mine)) break;
+      off = walk.at - before.x;  // one thread
+      if (hi - lo == 1) {
+        bars->it0 = lo;
+        bars->off0 = off;
+        bars->group0 = max(g, 0);
+        break;
+      }
     }
   }
   fence_async_smem();  // the rings' memory was read and written by plain accesses
@@ -1282,7 +1312,7 @@ __global__ void __launch_bounds__(384, 1)
 // Joins the partials of each row that is not written yet, of its prefix and of its own keys:
 // lse = log2 sum 2^(m_s - m) l_s + m, O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s. Four rows
 // to a warp: eight lanes read a line of the four, four such groups of lanes a line each. 1, 2,
-// 4 or 8 warps take the rows' partials in turn, two of each in flight.
+// 4 or 8 warps take the rows' partials in turn, three or four of each in flight.
 struct PxJoin {
   const float* part;
   const float4* part_ml;
@@ -1297,7 +1327,7 @@ struct PxJoin {
 
 template <int D, int WPR>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
-  constexpr int NV = D / 32, IN = 2;  // a lane's vectors of four columns
+  constexpr int NV = D / 32, IN = D == 64 ? 4 : 3;  // a lane's vectors of four columns, partials in flight
   __shared__ float4 red[WPR > 1 ? 8 : 1][NV][32];
   __shared__ float red_ml[WPR > 1 ? 8 : 1][3][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
