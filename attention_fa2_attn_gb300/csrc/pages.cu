@@ -12,7 +12,8 @@
 // trips to L2 (parent -> length -> table row).
 //
 // fa_pages_copy. Bound by HBM: every copied byte is read once and written once. A warp moves
-// 4 KB of a page at a time, eight 16-byte vectors a lane in flight (64 warps an SM: 256 KB).
+// 8 KB of a page at a time, sixteen 16-byte vectors a lane in flight (1.07 GB read and written:
+// 163 us, 6.6 TB/s; 167 us with eight, 172 with four).
 //
 // fa_pages_free, fa_pages_compact. Both need sets of pages in ascending order, so that the
 // lists they give do not depend on which atomic came first: a bit for each page of the pool.
@@ -20,7 +21,10 @@
 // memory, all of them set bits there from their entries of the table, and cluster barriers
 // stand where three or five launches would.
 //   free: shares[p] is counted down for each of the entries; who finds it at 0 already sets
-//   p's bit. Bits in order are the freed list.
+//   p's bit. Bits in order are the freed list. An SM does one count in about two cycles, so
+//   many entries are counted down by the whole GPU first, which leaves -1 where nobody holds a
+//   page any more, and the cluster takes its bits from there: three launches (256 of 512 rows,
+//   164 000 entries, 524 000 pages: one cluster alone 32 us).
 //   compact: a bit for each live page. With n live pages from `first` on, they end up in
 //   [first, first + n): a live page behind that moves into a hole before it, the i-th of
 //   these into the i-th of those. Sources and holes are apart, so the copies need no order.
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(kForkWarps * 32) pages_fork_kernel(const ForkP
 // ---------------------------------------------------------------------------
 // copy
 // ---------------------------------------------------------------------------
-constexpr int kCopyVecs = 8;  // 16-byte vectors of a lane in flight
+constexpr int kCopyVecs = 16;  // 16-byte vectors of a lane in flight
 constexpr int kCopyThreads = 256;
 
 struct CopyParams {
@@ -152,7 +156,7 @@ struct CopyParams {
   const int* dst;
   const int* count;       // may be null
   int n, num_pages;
-  unsigned parts;         // 4 KB parts of a page
+  unsigned parts;         // 8 KB parts of a page
   long long page_vecs;    // 16-byte vectors of a page
   long long layer_vecs;   // and of a layer
   int sides;              // layers * 2
@@ -239,13 +243,13 @@ constexpr int kSetRows = 4;  // chunks of 32 entries of a warp, in flight togeth
 // Calls f(row of the table, place in it, entry, whether the row's sequence holds it) for the
 // entries of the rows; those behind a sequence's pages only with ALL (the compact call copies
 // them).
-template <bool ALL, typename F>
+template <bool ALL, int THREADS = kSetThreads, typename F>
 __device__ __forceinline__ void set_entries(const SetParams& p, bool& bad, const F& f) {
   const int lane = threadIdx.x & 31;
   const unsigned chunks = (p.max_pages + 31) / 32;
   const unsigned long long items = static_cast<unsigned long long>(p.n) * chunks;
-  const unsigned warps = gridDim.x * (kSetThreads / 32);
-  const unsigned warp = blockIdx.x * (kSetThreads / 32) + (threadIdx.x >> 5);
+  const unsigned warps = gridDim.x * (THREADS / 32);
+  const unsigned warp = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
   for (unsigned long long at = warp; at < items; at += static_cast<unsigned long long>(warps) * kSetRows) {
     int row[kSetRows], j[kSetRows], pages[kSetRows], e[kSetRows];
 #pragma unroll
@@ -279,8 +283,10 @@ __device__ __forceinline__ void set_entries(const SetParams& p, bool& bad, const
   }
 }
 
-template <bool COMPACT>
+// MODE 0: free; 1: compact; 2: free, the entries counted down already.
+template <int MODE>
 __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetParams p) {
+  constexpr bool COMPACT = MODE == 1;
   extern __shared__ uint32_t set_smem[];
   uint32_t* bits = set_smem;              // [words]: this CTA's part of the pool
   uint32_t* pre = set_smem + p.words;     // [words]: bits of the part before each word
@@ -295,6 +301,23 @@ __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetPara
   pdl_launch();
   bool bad = false;
 
+  if constexpr (MODE == 2) {
+    constexpr int IN = 4;  // words of a warp in flight
+    for (int w = warp; w < p.words; w += IN * (kSetThreads / 32)) {
+      int left[IN];
+#pragma unroll
+      for (int k = 0; k < IN; ++k) {
+        const int x = w + k * (kSetThreads / 32), page = page0 + x * 32 + lane;
+        left[k] = x < p.words && page < p.num_pages ? p.shares_out[page] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < IN; ++k) {
+        const unsigned v = __ballot_sync(0xffffffffu, left[k] < 0);
+        if (lane == 0 && w + k * (kSetThreads / 32) < p.words) bits[w + k * (kSetThreads / 32)] = v;
+      }
+    }
+    __syncthreads();
+  } else {
   for (int w = tid; w < p.words; w += kSetThreads) bits[w] = 0u;
   if (!COMPACT && p.shares_out != p.shares) {
     const int last = min(p.num_pages, page0 + part_pages);
@@ -322,6 +345,7 @@ __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetPara
   });
   if (bad) record_error(p.err, FA_ERR_BOUNDS, COMPACT ? SITE_PAGES_COMPACT : SITE_PAGES_FREE);
   set_cluster_sync();
+  }
 
   // bits before each word, of the part and of the parts before it
   {
@@ -373,8 +397,9 @@ __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetPara
         p.shares_out[page] = 0;
       }
     }
-    for (long long x = all + static_cast<long long>(rank) * kSetThreads + tid; x < p.cap; x += static_cast<long long>(p.C) * kSetThreads)
-      p.list0[x] = -1;
+    if (MODE == 0)
+      for (long long x = all + static_cast<long long>(rank) * kSetThreads + tid; x < p.cap; x += static_cast<long long>(p.C) * kSetThreads)
+        p.list0[x] = -1;
     if (rank == 0 && tid == 0) p.counts[0] = all;
   } else {
     // live pages before page x
@@ -429,6 +454,33 @@ __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetPara
   set_cluster_sync();  // nobody leaves while others read its shared memory
 }
 
+// What the whole GPU does of a large free: the copy of the shares and the list's -1, then the
+// counts.
+constexpr int kFreeThreads = 256;
+__global__ void __launch_bounds__(kFreeThreads) pages_free_begin_kernel(const SetParams p) {
+  pdl_wait();
+  pdl_launch();
+  const long long at = static_cast<long long>(blockIdx.x) * kFreeThreads + threadIdx.x, step = static_cast<long long>(gridDim.x) * kFreeThreads;
+  if (p.shares_out != p.shares)
+    for (long long x = at; x < p.num_pages; x += step) p.shares_out[x] = __ldg(p.shares + x);
+  for (long long x = at; x < p.cap; x += step) p.list0[x] = -1;
+}
+__global__ void __launch_bounds__(kFreeThreads) pages_free_count_kernel(const SetParams p) {
+  pdl_wait();
+  pdl_launch();
+  bool bad = false;
+  set_entries<false, kFreeThreads>(p, bad, [&](int, int, int e, bool) {
+    if (e < 0 || e >= p.num_pages)
+      bad = true;
+    else
+      bad |= atomicSub(p.shares_out + e, 1) < 0;
+  });
+  if (bad) record_error(p.err, FA_ERR_BOUNDS, SITE_PAGES_FREE);
+}
+// Entries from which on that is done: one cluster / three launches, us: 64 000 entries 14.1 / 16.9,
+// 262 144 entries 32.1 / 18.5, 524 288 entries 51.4 / 19.6.
+constexpr long long kFreeLarge = 131072;
+
 // CTAs of the cluster: enough warps that one has a few chunks of 32 entries, and 32 words of
 // the pool, at most.
 static int set_cluster(long long rows, int max_pages, int num_pages) {
@@ -438,12 +490,12 @@ static int set_cluster(long long rows, int max_pages, int num_pages) {
   return c;
 }
 
-template <bool COMPACT>
+template <int MODE>
 static int launch_set(SetParams& p, cudaStream_t stream) {
-  p.C = set_cluster(p.n, p.max_pages, p.num_pages);
+  p.C = set_cluster(MODE == 2 ? 0 : p.n, p.max_pages, p.num_pages);
   p.words = (p.num_pages + 32 * p.C - 1) / (32 * p.C);
   const size_t smem = static_cast<size_t>(p.words) * 8;
-  auto kfn = pages_set_kernel<COMPACT>;
+  auto kfn = pages_set_kernel<MODE>;
   // the attributes hold for the life of the device's context: asked for once per device
   static std::atomic<unsigned long long> asked{0};
   int dev = 0;
@@ -577,7 +629,19 @@ fa_status fa_pages_free(const int* block_table, const int* seqlens, const int* r
   p.num_pages = num_pages;
   p.err = device_error_word();
   if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
-  return static_cast<fa_status>(launch_set<false>(p, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (mp * n < kFreeLarge) return static_cast<fa_status>(launch_set<0>(p, cs));
+  const int sms = device_sm_count();
+  if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
+  auto blocks = [&](long long work) {
+    const long long b = (work + kFreeThreads - 1) / kFreeThreads;
+    return dim3(static_cast<unsigned>(b < 8ll * sms ? b : 8ll * sms));
+  };
+  int rc = launch_dependent(pages_free_begin_kernel, blocks(p.cap > num_pages ? p.cap : num_pages), dim3(kFreeThreads), 0, cs, p);
+  const long long chunks = (mp + 31) / 32 * n;
+  if (rc == FA_OK) rc = launch_dependent(pages_free_count_kernel, blocks((chunks + kSetRows - 1) / kSetRows * 32), dim3(kFreeThreads), 0, cs, p);
+  if (rc == FA_OK) rc = launch_set<2>(p, cs);
+  return static_cast<fa_status>(rc);
 }
 
 fa_status fa_pages_compact(const int* block_table, const int* seqlens, const int* shares, int* table_out,
@@ -615,7 +679,7 @@ fa_status fa_pages_compact(const int* block_table, const int* seqlens, const int
   p.first = first;
   p.err = device_error_word();
   if (!p.err) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
-  return static_cast<fa_status>(launch_set<true>(p, static_cast<cudaStream_t>(stream)));
+  return static_cast<fa_status>(launch_set<1>(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
