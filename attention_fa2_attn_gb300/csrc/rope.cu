@@ -142,13 +142,13 @@ __device__ __forceinline__ bool turns_of(double f, unsigned long long& turns) {
 }
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeMostRows = 4;  // of a warp
+constexpr int kRopeMostRows = 4;  // of a warp, five where that saves a cut
 
 // U: rows of a warp, all in flight at once. The sines stay in shared memory: in registers
 // they would cost a block's worth of occupancy (64 registers a thread: four blocks an SM;
 // b1 hq64 hkv8 n8192 d128 52.9 us with them there, 47.2 us without).
 template <typename E, int VEC, bool INTER, bool APPEND, int U>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, U > 4 ? 3 : 4) rope_kernel(const RopeParams p) {
   __shared__ float cs[2][VEC][32];
   pdl_wait();
   pdl_launch();
@@ -287,6 +287,7 @@ static int launch_rope_rows(const RopeParams& p, bool interleaved, int rows, dim
       if (rows == 1) return go(inter, std::integral_constant<int, 1>{});
       if (rows == 2) return go(inter, std::integral_constant<int, 2>{});
       if (rows == 3) return go(inter, std::integral_constant<int, 3>{});
+      if (rows == 5) return go(inter, std::integral_constant<int, 5>{});
     }
     return go(inter, std::integral_constant<int, kRopeMostRows>{});
   };
@@ -313,7 +314,10 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   int cuts = (heads + kRopeMostRows * kRopeWarps - 1) / (kRopeMostRows * kRopeWarps);
   const int most = (heads + kRopeWarps - 1) / kRopeWarps;
   while (cuts < most && blocks * cuts < 2ll * device_sm_count()) cuts = cuts * 2 < most ? cuts * 2 : most;
-  const int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
+  int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
+  // Heads that two cuts of three rows each would hold, but one of five as well: three blocks an SM
+  // with all rows in use (b2 h32+8 n8192 d128 bf16: 56.2 us in two cuts, 52.9 in one).
+  if (w == V && cuts == 2 && heads > 4 * kRopeWarps && heads <= 5 * kRopeWarps && blocks >= 2ll * device_sm_count()) rows = 5;
   p.head_chunk = rows * kRopeWarps;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.head_chunk - 1) / p.head_chunk));
   if (w == V) return launch_rope_rows<E, V, APPEND>(p, interleaved, rows, grid, stream);
