@@ -313,7 +313,8 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   float o[D / 8][4];
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-  const int key_of = warp * 16;  // this warp's first key of a tile
+  const int key_of = warp * 16;  // this warp's first key of a tile: its page, [d / 64][16 keys][128 bytes]
+  constexpr int PAGE_BYTES = 16 * D * 2, PAGE_CHUNK = 16 * 128;
   uint32_t ks = gkv % KST, kl = gkv / KST, vs = gkv % VST, vl = gkv / VST;
   const int nt = w->nt;
 #pragma unroll 1
@@ -322,13 +323,13 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
       ok = false;
       break;
     }
-    const uint32_t k0 = smem_u32(sK + ks * C::KV_BYTES);
+    const uint32_t k0 = smem_u32(sK + ks * C::KV_BYTES + warp * PAGE_BYTES);
     float s[2][4] = {}, odd[2][4] = {};  // two sums each, so that eight MMAs do not wait in a row
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const int mi = lane >> 3;  // matrix of the four: (keys half, d half)
       uint32_t b00, b01, b10, b11;
-      ldsm_x4(k0 + sw_off(key_of + 8 * (mi >> 1) + (lane & 7), kk * 16 + 8 * (mi & 1), C::CHUNK_BYTES), b00, b01, b10, b11);
+      ldsm_x4(k0 + sw_off(8 * (mi >> 1) + (lane & 7), kk * 16 + 8 * (mi & 1), PAGE_CHUNK), b00, b01, b10, b11);
       mma_bf16_16816(kk & 1 ? odd[0] : s[0], qa[kk], b00, b01);
       mma_bf16_16816(kk & 1 ? odd[1] : s[1], qa[kk], b10, b11);
     }
@@ -386,14 +387,14 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
       ok = false;
       break;
     }
-    uint8_t* vt = sV + vs * C::KV_BYTES;
+    uint8_t* vt = sV + vs * C::KV_BYTES + warp * PAGE_BYTES;
     if (there < 16) {
       // V rows past the item's end hold whatever the pool or an earlier tile left there, and
       // 0 * NaN is not 0
 #pragma unroll 1
       for (int idx = lane; idx < 16 * (D / 8); idx += 32)
         if (idx / (D / 8) >= there)
-          *reinterpret_cast<uint4*>(vt + sw_off(key_of + idx / (D / 8), idx % (D / 8) * 8, C::CHUNK_BYTES)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(vt + sw_off(idx / (D / 8), idx % (D / 8) * 8, PAGE_CHUNK)) = make_uint4(0u, 0u, 0u, 0u);
       fence_async_smem();  // before the next copy into the stage
       __syncwarp();
     }
@@ -402,7 +403,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     for (int np = 0; np < D / 16; ++np) {
       const int mi = lane >> 3;  // (keys half, d half)
       uint32_t a, b, c, d;
-      ldsm_x4_t(v0 + sw_off(key_of + 8 * (mi & 1) + (lane & 7), np * 16 + 8 * (mi >> 1), C::CHUNK_BYTES), a, b, c, d);
+      ldsm_x4_t(v0 + sw_off(8 * (mi & 1) + (lane & 7), np * 16 + 8 * (mi >> 1), PAGE_CHUNK), a, b, c, d);
       mma_bf16_16816(o[2 * np], pa, a, b);
       mma_bf16_16816(o[2 * np + 1], pa, c, d);
     }
@@ -764,7 +765,8 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
 template <int D>
 __global__ void __launch_bounds__(384, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const PxParams p) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKp,
+                  const __grid_constant__ CUtensorMap tmVp, const PxParams p) {
   using C = PxCfg<D>;
   constexpr int KST = C::K_STAGES, VST = C::V_STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -962,6 +964,7 @@ __global__ void __launch_bounds__(384, 1)
       // ======================= producers: K (and Q), V =======================
       const bool is_k = warp == 8;
       const CUtensorMap* my_map = is_k ? &tmK : &tmV;
+      const CUtensorMap* my_pages = is_k ? &tmKp : &tmVp;  // slim: a page with all of d
       uint8_t* my_ring = is_k ? sK : sV;
       uint64_t* my_full = is_k ? bars->k_full : bars->v_full;
       uint64_t* my_empty = is_k ? bars->k_empty : bars->v_empty;
@@ -969,12 +972,12 @@ __global__ void __launch_bounds__(384, 1)
       if (lane == 0) {
         if (is_k) tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(my_map);
+        tma_prefetch_desc(my_pages);
       }
       PxTake take;
       uint32_t g = 0;  // key tiles loaded so far (ring position)
       uint32_t stage = 0, lap = 0;
       uint32_t q_loads = 0;
-      const int pi = lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
       bool ok = true;
 #pragma unroll 1
       while (ok && !*abort_flag) {
@@ -998,6 +1001,7 @@ __global__ void __launch_bounds__(384, 1)
         if (w.nt == 0) break;
         const int* trow = p.block_table + static_cast<size_t>(w.s0) * p.max_pages;
         const int kvh = w.hu * p.V + cta % p.V;
+        const bool slim = w.own() && p.R <= kPxSlim;
         const int page0 = w.k0 >> 4;  // (k0 is a page's start)
         const int n_pages = (w.k1 + 15) >> 4;
         // a lane holds one of 32 entries, four tiles' worth; the next 32 are fetched meanwhile
@@ -1046,6 +1050,7 @@ __global__ void __launch_bounds__(384, 1)
             ent_next = fetch(x + 4);
           }
           const int npg = min(8, n_pages - page0 - (w.x0 + x) * 8);  // pages past the end are not loaded
+          const int pi = slim ? lane : lane / C::KCH, pc = lane % C::KCH;  // the box of this lane: page and d-chunk
           int pe = __shfl_sync(0xffffffffu, ent, (x & 3) * 8 + (pi & 7));
           if (pi < npg && (pe < 0 || pe >= p.num_pages)) {
             // never dereferenced: page 0 is loaded in its place, the output is undefined
@@ -1058,7 +1063,9 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (lane == 0) mbar_arrive_expect_tx(&my_full[stage], static_cast<uint32_t>(npg) * 16 * 128 * C::KCH);
           __syncwarp();
-          if (pi < npg)
+          if (slim && pi < npg)
+            tma_load_4d(my_ring + stage * C::KV_BYTES + pi * (16 * D * 2), my_pages, &my_full[stage], 0, kvh, pe * 16, 0);
+          else if (pi < npg)
             tma_load_3d(my_ring + stage * C::KV_BYTES + pc * C::CHUNK_BYTES + pi * 2048, my_map, &my_full[stage], pc * 64,
                         kvh, pe * 16);
           if (++stage == ST) {
@@ -1460,7 +1467,7 @@ static bool px_shape(int B, int Hq, int Hkv, int T, int max_pages, int d, int sm
 }
 
 template <int D>
-static int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PxParams& p,
+static int launch_prefix(const CUtensorMap& tq, const CUtensorMap (&tk)[2], const CUtensorMap (&tv)[2], const PxParams& p,
                          const PxJoin& j, int grid, int sms, cudaStream_t stream) {
   using C = PxCfg<D>;
   auto kfn = prefix_kernel<D>;
@@ -1475,7 +1482,7 @@ static int launch_prefix(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     if (e != cudaSuccess) return record_cuda_failure(e);
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
-  const int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk, tv, p);
+  const int rc = launch_dependent(kfn, dim3(grid), dim3(C::THREADS), C::SMEM, stream, tq, tk[0], tv[0], tk[1], tv[1], p);
   if (rc != FA_OK) return rc;
   // warps to four rows: as many as there are of some 24 an SM
   const long long warps = (j.rows + 3) / 4;
@@ -1540,7 +1547,7 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   if (2 * s.V * s.area >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk[2], tv[2];
   {
     // a KV head's R rows are dense; a box is the rows of a tile, of several sequences or of one
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)s.R, (cuuint64_t)Hkv, (cuuint64_t)B};
@@ -1552,16 +1559,19 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
   }
-  for (int i = 0; i < 2; ++i) {
-    // one 16-token page of one KV head per box; L2 fetches what a row is, no neighbour's
+  for (int i = 0; i < 4; ++i) {
+    // K, V: one 16-token page of one KV head per box, 64 of its d (what a tile of 128 rows is made
+    // of), or all of it (what a warp of a slim unit takes: half the boxes at d = 128). L2 fetches
+    // what a row is, no neighbour's.
+    const bool pages = i & 2;
     const CUtensorMapL2promotion fetch = d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)num_pages * 16};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2};
-    cuuint32_t box[3] = {64, 1, 16};
-    cuuint32_t es[3] = {1, 1, 1};
-    if (enc(i == 0 ? &tk : &tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(i == 0 ? k_pages : v_pages),
-            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    cuuint64_t dims[4] = {(cuuint64_t)(pages ? 64 : d), (cuuint64_t)Hkv, (cuuint64_t)num_pages * 16, (cuuint64_t)d / 64};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)Hkv * d * 2, 128};
+    cuuint32_t box[4] = {64, 1, 16, (cuuint32_t)d / 64};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    if (enc(i & 1 ? &tv[i >> 1] : &tk[i >> 1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pages ? 4 : 3,
+            const_cast<void*>(i & 1 ? v_pages : k_pages), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return static_cast<fa_status>(record_cuda_failure(cudaErrorInvalidValue));
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1585,10 +1595,16 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.c = scale * kLog2e;
-  if (s.R <= kPxSlim)
-    p.cost = d == 128 ? PxCost{10, 14, 8, 18, 10, 5} : PxCost{9, 14, 8, 20, 8, 6};
-  else
-    p.cost = d == 128 ? PxCost{10, 14, 8, 18, 10, 14} : PxCost{9, 14, 8, 20, 9, 14};
+  // In eighths of a wide step (some 0.2 us); narrow and slim steps are two tiles of keys, which
+  // at d = 128 wait for HBM. What a unit costs beside its steps: Q and the first S, a slim one's
+  // join, the partials of 128 or 256 rows. (Swept over seven batches from 24 to 170 us: within 2 %
+  // of the best for each; off by half, up to 15 % slower.)
+  p.cost = d == 128 ? PxCost{9, 12, 8, 20, 9, 12} : PxCost{9, 12, 8, 12, 9, 12};
+  if (s.R <= kPxSlim) {
+    p.cost.own_step = d == 128 ? 10 : 7;
+    p.cost.own_front = d == 128 ? 4 : 8;
+    p.cost.wide_front = d == 128 ? 8 : 12;
+  }
   p.area = s.area;
   p.part_rows = 2 * s.V * s.area;
   p.part = reinterpret_cast<float*>(ws);
