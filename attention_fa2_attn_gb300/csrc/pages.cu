@@ -481,13 +481,14 @@ __global__ void __launch_bounds__(kFreeThreads) pages_free_count_kernel(const Se
 // 262 144 entries 32.1 / 18.5, 524 288 entries 51.4 / 19.6.
 constexpr long long kFreeLarge = 131072;
 
-// CTAs of the cluster: enough warps that one has a few chunks of 32 entries, and 32 words of
-// the pool, at most.
+// CTAs of the cluster. A cluster's barriers cost a microsecond that a few chunks of 32 entries do
+// not make up for; many are done faster by more SMs (compact, us, 1 / 4 / 16 CTAs: 16 chunks 6.2 /
+// 7.7 / 7.2, 128 chunks 11.3 / 9.2 / 8.7, 512 chunks 31.8 / 16.6 / 11.8; free: 32 chunks 5.7 / 6.7 /
+// 6.5, 256 chunks 13.4 / 9.3 / 7.5).
 static int set_cluster(long long rows, int max_pages, int num_pages) {
   const long long chunks = rows * ((max_pages + 31) / 32);
-  int c = 1;
-  while (c < kSetMaxCluster && (chunks > 32ll * kSetRows * c || num_pages > 32 * 1024 * c)) c *= 2;
-  return c;
+  if (chunks > 128 || num_pages > 32768) return kSetMaxCluster;
+  return chunks > 32 ? 8 : 1;
 }
 
 template <int MODE>
