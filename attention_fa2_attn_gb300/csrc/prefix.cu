@@ -13,23 +13,36 @@
 // has 8. So the prefix costs tensor-core and softmax time, what a sequence has of its own HBM
 // time.
 //
-// How. As the tree kernel: 128 rows a tile on the tensor cores, one CTA to an SM, equal shares
-// of the batch's cost whatever the lengths, partials joined by a second kernel.
+// How. 128 rows a tile on the tensor cores, one CTA to an SM, equal shares of the batch's cost
+// whatever the lengths, partials joined by a second kernel.
 //   * An item is a group (its prefix) or a sequence (its own keys). Its row tiles hold the
 //     rows of as many whole sequences as fit, in q's order, so one 4-D box brings a tile of Q:
 //     [sequences][R rows] behind one another. With R > 128 a sequence is several tiles.
 //   * Two row tiles make a wide unit, which goes over the keys with one tile of keys against
-//     both. A last tile alone is a narrow unit: two tiles of keys at a time, each with its own
-//     S, P and O. A CTA takes units of both kinds as its share has them: most rows of a batch's
-//     prefix are wide, every sequence's own are narrow (R <= 128).
+//     both. A last tile alone, and own keys of more than 16 rows, are narrow units: two tiles of
+//     keys at a time, each with its own S, P and O. Own keys of up to 16 rows are slim units, on
+//     warp-level MMAs (px_slim).
+//   * A share is a stretch of the line of all units' costs, groups first. One warp walks it ahead
+//     of the others and leaves its segments in a queue in shared memory.
 //   * The CTAs that are neighbours take the KV heads of one cost line side by side.
 //   * A share of a unit leaves fp32 partials at (the rows before the unit + 256 times the
 //     CTA's number): no two shares meet there, since along the line either the unit or the CTA
 //     goes up. A sequence without a prefix whose keys lie in one share is written at once.
+//   * Code and spills cost more than usual: what a CTA runs for the first time comes from L2 while
+//     that is busy, and a spilled value waits in a busy L1. So few unrolled
+//     copies, one loop to a kind of segment, and no spills at 208 and 88 registers.
+// Measured, both kernels in a graph, d = 128 but where it says 64: 8 sequences of 2000 + 1..200
+// keys, 32 over 8 heads, 13.4 us (the launches, the lengths' scan and the first keys are 5);
+// 64 of 16384 + 9..1024, 64 over 8 heads, 59 us, 205 MB read once, where the paged decode
+// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 35.2 us
+// (64); 32 of 1000 + up to 8192, 16 heads, 168 us, 6.55 TB/s (232). Prefix steps are bound by
+// a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
+// under way), own keys by HBM where they are long and by the units' ends where they are short.
+// Two slim units at a time, four warps on each, took the same (62.7 and 169 us).
 // P is rounded to bf16 for the tensor cores (by at most 2^-8 of a weight; fp32 would take twice
 // the MMAs), O once at the end; sums and maxima are fp32.
 // Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the CTA
-// unwinds. The softmax warps leave together, by a vote in every unit.
+// unwinds. A warp's lanes leave together, and the softmax warps by a vote in every unit.
 #include <atomic>
 
 #include "join.cuh"
@@ -975,12 +988,16 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(my_pages);
       }
       PxTake take;
+      // one answer for all lanes, which go on or leave together
+      auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, tmo, abort_flag));
+      };
       uint32_t g = 0;  // key tiles loaded so far (ring position)
       uint32_t stage = 0, lap = 0;
       uint32_t q_loads = 0;
       bool ok = true;
 #pragma unroll 1
-      while (ok && !*abort_flag) {
+      while (__all_sync(0xffffffffu, ok && !*abort_flag)) {
         PxSeg w;
         {
           const volatile PxSeg* from = take.next(bars, tmo, abort_flag);
@@ -1029,7 +1046,7 @@ __global__ void __launch_bounds__(384, 1)
           ++q_loads;
           q_due = false;
         };
-        auto q_free = [&]() {  // uniform: every lane asks, and one answer counts
+        auto q_free = [&]() {
           return q_loads == 0 || __all_sync(0xffffffffu, mbar_test(&bars->q_empty, (q_loads - 1) & 1));
         };
 #pragma unroll 1
@@ -1038,7 +1055,7 @@ __global__ void __launch_bounds__(384, 1)
             if (q_free()) {
               load_q();
             } else if (x == KST - 1) {
-              if (!mbar_wait_lean(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag)) {
+              if (!wwait(&bars->q_empty, (q_loads - 1) & 1)) {
                 ok = false;
                 break;
               }
@@ -1057,7 +1074,7 @@ __global__ void __launch_bounds__(384, 1)
             record_error(p.err, FA_ERR_BOUNDS, SITE_PX_TABLE);
             pe = 0;
           }
-          if (g >= ST && !mbar_wait_lean(&my_empty[stage], (lap & 1) ^ 1, tmo, abort_flag)) {
+          if (g >= ST && !wwait(&my_empty[stage], (lap & 1) ^ 1)) {
             ok = false;
             break;
           }
@@ -1074,7 +1091,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         if (ok && q_due) {
-          if (q_loads > 0 && !mbar_wait_lean(&bars->q_empty, (q_loads - 1) & 1, tmo, abort_flag))
+          if (q_loads > 0 && !wwait(&bars->q_empty, (q_loads - 1) & 1))
             ok = false;
           else
             load_q();
@@ -1149,7 +1166,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t g = 0;  // key tiles of earlier segments (ring position)
       bool ok = true;
 #pragma unroll 1
-      for (int nt; ok; g += nt) {
+      for (int nt; __all_sync(0xffffffffu, ok); g += nt) {  // (a wait may run out for some of the lanes only)
         const volatile PxSeg* from = take.next(bars, tmo, abort_flag);
         if (!from) {
           ok = false;
@@ -1163,7 +1180,7 @@ __global__ void __launch_bounds__(384, 1)
         if (slim) continue;  // the softmax warps do those by themselves
         if (!wwait(&bars->q_full, seg_i & 1)) {
           ok = false;
-          break;
+          continue;
         }
         tc_fence_after();
         if (!wide) {
@@ -1225,7 +1242,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
       }
-      if (!ok && leader) fail(SITE_PX_MMA);
+      if (!ok) fail(SITE_PX_MMA);
       commit(&bars->drain);  // every MMA must finish before TMEM is released
       mbar_wait_lean(&bars->drain, 0, tmo_unwind);
     } else {
