@@ -1,5 +1,6 @@
 """GB300 (sm_103a) fused attention: prefill, backward, split-KV and paged decode, and the
-calls around the paged cache (plans, rotary positions, trees of drafted tokens).
+calls around the paged cache (plans, rotary positions, trees of drafted tokens, shared
+pages and prefixes).
 
 The computation runs in the CUDA library ``libfa_gb300.so`` (C ABI in
 ``include/fa_gb300.h``); ``api`` holds thin PyTorch-facing wrappers with the
