@@ -38,7 +38,8 @@
 // (64); 32 of 1000 + up to 8192, 16 heads, 168 us, 6.55 TB/s (232). Prefix steps are bound by
 // a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
 // under way), own keys by HBM where they are long and by the units' ends where they are short.
-// Two slim units at a time, four warps on each, took the same (62.7 and 169 us).
+// Tried and taken back: two slim units at a time, four warps on each (62 and 167 us); a slim unit's
+// Q with its first keys, and the next segment's table entries fetched ahead (58.9 and 168.8).
 // P is rounded to bf16 for the tensor cores (by at most 2^-8 of a weight; fp32 would take twice
 // the MMAs), O once at the end; sums and maxima are fp32.
 // Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the CTA
@@ -135,6 +136,8 @@ struct PxSeg {
   int x0, nt;  // first key tile and how many; none: the share is done
   int flags;
   int ctas;    // CTAs that share the unit, from the one that begins it on (known to that one)
+  int kvh, me;    // KV head, this CTA's number on its line
+  int out, part;  // of a sequence's own keys: its first row in the output, and (but for 256 * me) of its partials
   __device__ __forceinline__ bool wide() const volatile { return flags & 1; }
   __device__ __forceinline__ bool own() const volatile { return flags & 2; }  // a sequence's own keys
   __device__ __forceinline__ bool from_start() const volatile { return flags & 4; }
@@ -300,7 +303,6 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
   asm volatile("" : "+r"(tid));  // (as in px_rows)
   const int warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;  // row of the MMA fragment (and + 8), column pair
-  const int cta = blockIdx.x, me = cta / p.V;
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, tmo, abort_flag));
   };
@@ -364,9 +366,10 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
           if (key0 + 8 * h + 2 * tig + (e & 1) >= sees[e >> 1]) s[h][e] = -INFINITY;
     }
     // two rows a thread; four neighbours share a row
-    float alpha[2];
+    float alpha[2] = {1.f, 1.f};
 #pragma unroll
     for (int ri = 0; ri < 2; ++ri) {
+      if (ri == 1 && p.R <= 8) break;
       float mx = fmaxf(fmaxf(s[0][2 * ri], s[0][2 * ri + 1]), fmaxf(s[1][2 * ri], s[1][2 * ri + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -400,25 +403,18 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
       ok = false;
       break;
     }
-    uint8_t* vt = sV + vs * C::KV_BYTES + warp * PAGE_BYTES;
-    if (there < 16) {
-      // V rows past the item's end hold whatever the pool or an earlier tile left there, and
-      // 0 * NaN is not 0
-#pragma unroll 1
-      for (int idx = lane; idx < 16 * (D / 8); idx += 32)
-        if (idx / (D / 8) >= there)
-          *reinterpret_cast<uint4*>(vt + sw_off(idx / (D / 8), idx % (D / 8) * 8, PAGE_CHUNK)) = make_uint4(0u, 0u, 0u, 0u);
-      fence_async_smem();  // before the next copy into the stage
-      __syncwarp();
-    }
-    const uint32_t v0 = smem_u32(vt);
+    // V rows past the item's end hold whatever the pool or an earlier tile left there, and
+    // 0 * NaN is not 0: this thread's keys of the two halves, as masks of their fragments
+    const uint32_t in_lo = (2 * tig < there ? 0xffffu : 0u) | (2 * tig + 1 < there ? 0xffff0000u : 0u);
+    const uint32_t in_hi = (2 * tig + 8 < there ? 0xffffu : 0u) | (2 * tig + 9 < there ? 0xffff0000u : 0u);
+    const uint32_t v0 = smem_u32(sV + vs * C::KV_BYTES + warp * PAGE_BYTES);
 #pragma unroll
     for (int np = 0; np < D / 16; ++np) {
       const int mi = lane >> 3;  // (keys half, d half)
       uint32_t a, b, c, d;
       ldsm_x4_t(v0 + sw_off(8 * (mi & 1) + (lane & 7), np * 16 + 8 * (mi >> 1), PAGE_CHUNK), a, b, c, d);
-      mma_bf16_16816(o[2 * np], pa, a, b);
-      mma_bf16_16816(o[2 * np + 1], pa, c, d);
+      mma_bf16_16816(o[2 * np], pa, a & in_lo, b & in_hi);
+      mma_bf16_16816(o[2 * np + 1], pa, c & in_lo, d & in_hi);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->v_empty[vs]);
@@ -449,11 +445,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     }
   }
   const bool whole = w->k0 == 0 && w->from_start() && w->to_end();
-  const int kvh = w->hu * p.V + cta % p.V;
-  const int at_row = (p.units * w->s0 + w->hu) * p.R;
-  const long long base = (static_cast<long long>(p.V) + cta % p.V) * p.area;
-  const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * me;
-  const size_t out_row = (static_cast<size_t>(w->s0) * p.Hkv + kvh) * p.R;
+  const int part_row = w->part + kPxUnit * w->me, out_row = w->out;
   constexpr int COLS = D / 32;  // columns of a thread in the joined rows, a row to a warp
 #pragma unroll 1
   for (int ri = 0; 8 * ri < p.R; ++ri) {
@@ -498,7 +490,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     }
     if (whole) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (NaN stays NaN)
-      __nv_bfloat16* dst = p.o + (out_row + row) * D + col;
+      __nv_bfloat16* dst = p.o + static_cast<size_t>(out_row + row) * D + col;
       if constexpr (COLS == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
       else
@@ -514,8 +506,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
     }
   }
   if (threadIdx.x == 0 && w->from_start())
-    p.desc[(static_cast<size_t>(p.B) + w->s0) * p.Hkv + kvh] =
-        whole ? make_int2(kPxDone, 0) : make_int2(me << 16 | w->ctas, static_cast<int>(base + at_row));
+    p.desc[(static_cast<size_t>(p.B) + w->s0) * p.Hkv + w->kvh] = whole ? make_int2(kPxDone, 0) : make_int2(w->me << 16 | w->ctas, w->part);
   return true;
 }
 
@@ -725,9 +716,9 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
   if (has_rows) {
     // the row's place in its item's partials, and in the output
     const int at_row = p.units * p.R * w->s0 + (w->hu * w->n + seq - w->s0) * p.R + rr;
-    const int kvh = w->hu * p.V + static_cast<int>(blockIdx.x) % p.V;
-    const long long base = (static_cast<long long>(w->own()) * p.V + static_cast<int>(blockIdx.x) % p.V) * p.area;
-    const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * (blockIdx.x / p.V);
+    const int kvh = w->kvh, place = kvh - w->hu * p.V;
+    const long long base = (static_cast<long long>(w->own()) * p.V + place) * p.area;
+    const long long part_row = base + at_row + static_cast<long long>(kPxUnit) * w->me;
     const size_t out_row = (static_cast<size_t>(seq) * p.Hkv + kvh) * p.R + rr;
     // narrow: each slot's warps write half the columns of the joined O
     const bool take0 = f0 != 0.f;
@@ -767,7 +758,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
       }
       if (w->from_start() && rr % kPxTile == 0) {  // this CTA begins the unit
         const size_t at = ((static_cast<size_t>(w->own()) * p.B + seq) * p.Hkv + kvh) * p.TS + rr / kPxTile;
-        p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(static_cast<int>(blockIdx.x) / p.V << 16 | w->ctas, static_cast<int>(base + at_row));
+        p.desc[at] = whole ? make_int2(kPxDone, 0) : make_int2(w->me << 16 | w->ctas, static_cast<int>(base + at_row));
       }
     }
   }
@@ -1013,11 +1004,12 @@ __global__ void __launch_bounds__(384, 1)
           w.x0 = from->x0;
           w.nt = from->nt;
           w.flags = from->flags;
+          w.kvh = from->kvh;
           take.done(bars);
         }
         if (w.nt == 0) break;
         const int* trow = p.block_table + static_cast<size_t>(w.s0) * p.max_pages;
-        const int kvh = w.hu * p.V + cta % p.V;
+        const int kvh = w.kvh;
         const bool slim = w.own() && p.R <= kPxSlim;
         const int page0 = w.k0 >> 4;  // (k0 is a page's start)
         const int n_pages = (w.k1 + 15) >> 4;
@@ -1254,11 +1246,19 @@ __global__ void __launch_bounds__(384, 1)
         walk.off = bars->off0;
         walk.g = bars->group0;
         bool ok = true;
+        const int place = cta % p.V;
 #pragma unroll 1
         for (uint32_t i = 0;; ++i) {
           PxSeg w;
           const bool more = walk.next(p, me, w);
-          if (!more) w.nt = 0;
+          if (more) {  // (here, since a division or two is a tenth of what a slim unit takes)
+            w.kvh = w.hu * p.V + place;
+            w.me = me;
+            w.out = (w.s0 * p.Hkv + w.kvh) * p.R;
+            w.part = static_cast<int>((p.V + place) * p.area) + (p.units * w.s0 + w.hu) * p.R;
+          } else {
+            w.nt = 0;
+          }
           const uint32_t e = i % kPxQueue;
           if (i >= kPxQueue && !mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag)) {
             ok = false;
@@ -1614,12 +1614,12 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.c = scale * kLog2e;
   // In eighths of a wide step (some 0.2 us); narrow and slim steps are two tiles of keys, which
   // at d = 128 wait for HBM. What a unit costs beside its steps: Q and the first S, a slim one's
-  // join, the partials of 128 or 256 rows. (Swept over seven batches from 24 to 170 us: within 2 %
+  // join, the partials of 128 or 256 rows. (Swept over nine batches from 13 to 170 us: within 3 %
   // of the best for each; off by half, up to 15 % slower.)
   p.cost = d == 128 ? PxCost{9, 12, 8, 20, 9, 12} : PxCost{9, 12, 8, 12, 9, 12};
   if (s.R <= kPxSlim) {
-    p.cost.own_step = d == 128 ? 10 : 7;
-    p.cost.own_front = d == 128 ? 4 : 8;
+    p.cost.own_step = d == 128 ? 9 : 5;
+    p.cost.own_front = d == 128 ? 2 : 12;
     p.cost.wide_front = d == 128 ? 8 : 12;
   }
   p.area = s.area;
