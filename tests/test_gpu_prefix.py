@@ -374,3 +374,19 @@ def test_wrong_arguments_are_named(way):
     with pytest.raises(fa.FAError) as e:
         _call(dict(c, starts=_i32(np.zeros(4098)), lens=_i32(np.zeros(4097))))
     assert e.value.status == _lib.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("d,n", [(64, 45_000), (128, 33_000)])
+def test_more_sequences_than_a_block_has_room_for_the_lengths_of(d, n):
+    rng = np.random.default_rng(d)
+    groups = [(int(rng.integers(0, 34)), [int(x) for x in rng.integers(0, 15, 11)]) for _ in range(n // 11)]
+    c = _case(2, 1, 1, d, groups, 31)
+    o, lse = _call(c)
+    o2, lse2 = fa.fa_decode_paged(c["q"], c["kp"], c["vp"], c["table"], c["seqlens"])
+    same = torch.isneginf(lse) == torch.isneginf(lse2)
+    assert bool(same.all()) and (o.float() - o2.float()).abs().max() <= 1e-2
+    assert torch.nan_to_num(lse - lse2).abs().max() <= 1e-3
+    some = torch.as_tensor(np.sort(rng.choice(c["q"].shape[0], 300, replace=False))).to(DEV)
+    part = dict(c, q=c["q"][some], table=c["table"][some], seqlens=c["seqlens"][some])
+    compare(o[some], lse[some], *_ref(part))
+    assert fa.fa_get_last_device_error()[0] == 0
