@@ -37,6 +37,7 @@ FA_PLAN_MAX_T = 8388480
 FA_TREE_MASK_MAX_T = 8192
 FA_TREE_MASK_MAX_B = 65535
 FA_PAGES_MAX = 4194304
+FA_FORK_MAX = 65536
 FA_PREFIX_MAX_GROUPS = 4096
 FA_ROPE_MAX_AXES = 8
 FA_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}

@@ -17,6 +17,7 @@ from ._lib import (
     FA_DTYPE_BF16,
     FA_DTYPE_F32,
     FA_ERR_UNSUPPORTED,
+    FA_FORK_MAX,
     FA_PAGES_MAX,
     FA_PLAN_MAX_T,
     FA_ROPE_MAX_AXES,
@@ -594,7 +595,7 @@ def fa_pages_fork(block_table, seqlens, parents, free_pages, shares, table_out=N
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}")
     n, P = parents.shape[0], shares.shape[0]
-    if n * max_pages >= 2**31:  # before outputs of that size are made
+    if n > FA_FORK_MAX or n * max_pages >= 2**31:  # before outputs of that size are made
         check(FA_ERR_UNSUPPORTED, "fa_pages_fork")
     table_out = _out(table_out, "table_out", (n, max_pages), _I32, block_table)
     lens_out = _out(lens_out, "lens_out", (n,), _I32, block_table)

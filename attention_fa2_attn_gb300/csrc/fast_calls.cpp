@@ -427,7 +427,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !dense(free_pages, at::kInt, 1, dev))
     Py_RETURN_NONE;
   const int64_t B = table.size(0), pages = table.size(1), N = parents.size(0), F = free_pages.size(0);
-  if (!fits(N) || !fits(F) || !fits(N * pages)) Py_RETURN_NONE;  // refused before its outputs are made
+  if (N > FA_FORK_MAX || !fits(F) || !fits(N * pages)) Py_RETURN_NONE;  // refused before its outputs are made
   std::array<Tensor, 5> out;  // table, lengths, sources, destinations, pages used
   fa_status st;
   {

@@ -8,8 +8,9 @@
 // fa_pages_fork. Child i gets the whole pages of its parent (shares + 1 each) and, where the
 // parent's last page is not full, a page of its own from the free list, in the order of i.
 // One launch without any exchange between blocks: a warp takes a child, and its block counts
-// by itself how many of the children before it need a page. Bound by launch and by two round
-// trips to L2 (parent -> length -> table row).
+// by itself how many of the children before it need a page (work that grows with the square of
+// their number, so that is limited). Bound by launch and by two round trips to L2 (parent ->
+// length -> table row).
 //
 // fa_pages_copy. Bound by HBM: every copied byte is read once and written once. A warp moves
 // 8 KB of a page at a time, sixteen 16-byte vectors a lane in flight (1.07 GB read and written:
@@ -393,14 +394,18 @@ __global__ void __launch_bounds__(kSetThreads, 1) pages_set_kernel(const SetPara
       const uint32_t v = bits[w];
       if ((v >> lane) & 1u) {
         const int page = page0 + w * 32 + lane;
-        p.list0[base + static_cast<int>(pre[w]) + __popc(v & ((1u << lane) - 1u))] = page;
+        const int at = base + static_cast<int>(pre[w]) + __popc(v & ((1u << lane) - 1u));
+        if (at < p.cap) p.list0[at] = page;  // (as many as were given back, unless shares were negative)
         p.shares_out[page] = 0;
       }
     }
     if (MODE == 0)
       for (long long x = all + static_cast<long long>(rank) * kSetThreads + tid; x < p.cap; x += static_cast<long long>(p.C) * kSetThreads)
         p.list0[x] = -1;
-    if (rank == 0 && tid == 0) p.counts[0] = all;
+    if (rank == 0 && tid == 0) {
+      p.counts[0] = static_cast<int>(min(static_cast<long long>(all), p.cap));
+      if (all > p.cap) record_error(p.err, FA_ERR_BOUNDS, SITE_PAGES_FREE);
+    }
   } else {
     // live pages before page x
     auto rank_of = [&](int x) -> int {
@@ -549,7 +554,7 @@ fa_status fa_pages_fork(const int* block_table, const int* seqlens, const int* p
   if (page_size != kPgTokens) return FA_ERR_UNSUPPORTED;
   const long long mp = max_pages;
   if (mp * kPgTokens >= (1ll << 31) || mp * B >= (1ll << 31) || mp * n >= (1ll << 31) ||
-      num_pages * 16ll >= (1ll << 31) || mp > 65535ll * kForkChunk)
+      num_pages * 16ll >= (1ll << 31) || mp > 65535ll * kForkChunk || n > FA_FORK_MAX)
     return FA_ERR_UNSUPPORTED;
   if (pg_meet({{table_out, 4 * mp * n}, {lens_out, 4ll * n}, {copy_src, 4ll * n}, {copy_dst, 4ll * n}, {pages_used, 4},
                {shares, 4ll * num_pages}},

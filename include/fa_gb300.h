@@ -91,6 +91,7 @@ typedef enum {
 #define FA_TREE_MASK_MAX_T 8192    /* nodes of a tree in fa_tree_mask */
 #define FA_TREE_MASK_MAX_B 65535   /* trees of a call */
 #define FA_PAGES_MAX 4194304       /* pages of a pool in fa_pages_free and fa_pages_compact */
+#define FA_FORK_MAX 65536            /* children of a call of fa_pages_fork */
 #define FA_PREFIX_MAX_GROUPS 4096  /* groups of a call of fa_prefix_decode_paged */
 #define FA_ROPE_MAX_AXES 8         /* axes of the positions in the fa_rope_axes calls */
 
@@ -488,7 +489,7 @@ FA_API fa_status fa_rope_axes_append_paged(const void* q, const void* k, const v
  *   Where the free list is too short, or names a page outside the pool, FA_ERR_BOUNDS is recorded and the child's
  *   last page is -1, in the table and among the copies.
  *   The parents' rows go on to hold their pages; fa_pages_free gives them back. A row may be forked any number of
- *   times in one call.
+ *   times in one call. n <= FA_FORK_MAX.
  */
 FA_API fa_status fa_pages_fork(const int* block_table, const int* seqlens, const int* parents,
                                const int* free_pages, int num_free, int* shares, int* table_out, int* lens_out,
@@ -514,7 +515,8 @@ FA_API fa_status fa_pages_copy(void* k_pages, void* v_pages, const int* src, con
  *   shares.
  *   freed [min(num_pages, n * max_pages)] int32 out: the pages that nobody holds any more, ascending, -1 behind
  *   them; num_freed [1] out: how many.
- *   A page that is given back more often than it is held is freed once, and FA_ERR_BOUNDS is recorded.
+ *   A page that is given back more often than it is held is freed once, and FA_ERR_BOUNDS is recorded. Shares may
+ *   not be negative: what is freed of such pages is undefined (the outputs hold all the same).
  *   The rows and their lengths are left as they are: a caller takes them out of its batch.
  *   num_pages <= FA_PAGES_MAX.
  */

@@ -397,3 +397,24 @@ def test_wrong_arguments_are_named(way):
             call()
         assert e.value.status == _lib.FA_ERR_INVALID_ARG
     _ok()
+
+
+def test_large_free_keeps_to_its_outputs_where_shares_are_negative(way):
+    # more negative shares than entries are given back: none of the pages goes behind the list's end
+    B, max_pages, pages = 2048, 64, 400_000
+    table = torch.zeros(B, max_pages, dtype=torch.int32, device=DEV)
+    shares = torch.full((pages,), -5, dtype=torch.int32, device=DEV)
+    cap = B * max_pages
+    buf = torch.full((cap + 4096,), 77, dtype=torch.int32, device=DEV)
+    num = torch.zeros(1, dtype=torch.int32, device=DEV)
+    fa.fa_pages_free(table, torch.ones(B, dtype=torch.int32, device=DEV), shares, freed=buf[:cap], num_freed=num)
+    _ok(5)
+    assert int(num) == cap and bool((buf[cap:] == 77).all())
+    assert torch.equal(buf[:cap], torch.arange(cap, dtype=torch.int32, device=DEV))
+
+
+def test_fork_of_as_many_children_as_a_call_takes(way):
+    lens = np.array([33, 16, 0])
+    table, lens, shares, free = _pool(3, 3, lens, 6, spare=_lib.FA_FORK_MAX)
+    parents = np.random.default_rng(6).integers(-1, 3, _lib.FA_FORK_MAX)
+    _check_fork(table, lens, shares, free, _i32(parents))

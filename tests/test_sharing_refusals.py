@@ -202,3 +202,8 @@ def test_rope_axes_is_rope_where_the_axes_agree():
     two = oracle.rope_axes(x, np.stack([pos, 0 * pos]), f, [0, 1, 1, 0])
     assert np.array_equal(two[..., [1, 2, 5, 6]], x[..., [1, 2, 5, 6]])
     assert np.abs(two[..., [0, 3, 4, 7]] - oracle.rope(x, pos, f)[..., [0, 3, 4, 7]]).max() <= 1e-14
+
+
+def test_fork_of_more_children_than_a_call_takes(L):
+    # each block counts the children before its own, so that the work grows with the square of their number
+    _cases(L.fa_pages_fork, FORK, [({"n": _lib.FA_FORK_MAX + 1, "max_pages": 1}, UNS), ({"n": 2**31 - 1, "max_pages": 1}, UNS)])
