@@ -208,6 +208,7 @@ struct PxWalk {
   PxCut cut;
   bool no_groups;
   PxCost c;
+  const PxItem* first;  // the item that the share begins in; null: it is past that
   __device__ __forceinline__ PxItem item(const PxParams& p, int i) {
     if (i < p.G) {
       const int s0 = __ldg(p.starts + i), s1 = __ldg(p.starts + i + 1);
@@ -222,7 +223,8 @@ struct PxWalk {
 #pragma unroll 1
     do {
       if (at >= end) return false;
-      x = item(p, it);
+      x = first ? *first : item(p, it);
+      first = nullptr;
       const int head = x.head(c);
       if (head == 0) {  // nothing to do (its cost is 0)
         ++it;
@@ -820,6 +822,7 @@ __global__ void __launch_bounds__(384, 1)
   // ---- this CTA's share of its line's cost: a block-wide scan over the items. Groups and lengths
   // go through shared memory that the rings use later: one round trip to L2 for all of them.
   PxWalk walk;
+  PxItem* item0 = reinterpret_cast<PxItem*>(ex + 128);  // what it begins in, until the walk has read it
   {
     const int items = p.G + p.B;
     const int per = (items + C::THREADS - 1) / C::THREADS;
@@ -871,13 +874,14 @@ __global__ void __launch_bounds__(384, 1)
     // start, where there are several, for the one that does.
     int4* wsum = reinterpret_cast<int4*>(ex);  // totals per warp, in the exchange area that nothing uses yet
     int off = -1, g;
+    PxItem x = {0, 0, 0, 0, 0, false};
     walk.c = p.cost;
     while (true) {
       int steps = 0, mine = 0;
       g = -1;
 #pragma unroll 1
       for (int i = lo; i < hi; ++i) {
-        const PxItem x = item(i, g);
+        x = item(i, g);
         const int cost = x.head(walk.c) * p.units;
         if (off < 0) {
           steps += x.head(PX_BY_STEPS) * p.units;
@@ -887,6 +891,7 @@ __global__ void __launch_bounds__(384, 1)
             bars->it0 = i;
             bars->off0 = off;
             bars->group0 = max(g, 0);
+            *item0 = x;
             break;
           }
           off -= cost;
@@ -946,6 +951,7 @@ __global__ void __launch_bounds__(384, 1)
         bars->it0 = lo;
         bars->off0 = off;
         bars->group0 = max(g, 0);
+        *item0 = x;
         break;
       }
     }
@@ -1245,6 +1251,7 @@ __global__ void __launch_bounds__(384, 1)
         walk.it = bars->it0;
         walk.off = bars->off0;
         walk.g = bars->group0;
+        walk.first = item0;
         bool ok = true;
         const int place = cta % p.V;
 #pragma unroll 1
