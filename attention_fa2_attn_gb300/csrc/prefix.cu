@@ -144,6 +144,7 @@ struct PxSeg {
   __device__ __forceinline__ bool to_end() const volatile { return flags & 8; }
 };
 constexpr int kPxQueue = 3;  // segments on their way from the warp that walks the share to the others
+constexpr int kPxWalker = 11;   // the warp that walks
 constexpr int kPxReaders = 11;  // warps that take them: producers, MMA issuer, softmax
 
 struct PxBars {
@@ -817,33 +818,36 @@ __global__ void __launch_bounds__(384, 1)
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(&bars->tmem_base, 512);
-  pdl_wait();
 
   // ---- this CTA's share of its line's cost: a block-wide scan over the items. Groups and lengths
   // go through shared memory that the rings use later: one round trip to L2 for all of them.
-  PxWalk walk;
+  // The walking warp is not in it: its code is on its way meanwhile.
   PxItem* item0 = reinterpret_cast<PxItem*>(ex + 128);  // what it begins in, until the walk has read it
-  {
+  PxWalk* walk0 = reinterpret_cast<PxWalk*>(ex + 160);  // and how the line is cut
+  if (warp != kPxWalker) {
+    constexpr int kScan = kPxWalker * 32;
+    PxWalk walk;
+    pdl_wait();
     const int items = p.G + p.B;
-    const int per = (items + C::THREADS - 1) / C::THREADS;
+    const int per = (items + kScan - 1) / kScan;
     const int lo = min(items, static_cast<int>(threadIdx.x) * per), hi = min(items, lo + per);
     int* gs = reinterpret_cast<int*>(sK);  // [G + 1]: starts
     int* gp = gs + p.G + 1;                // [G]: prefixes as they were asked for
     int* ls = gp + p.G;                    // [B]: lengths, where there is room for them
     const bool lens_here = p.B <= C::MOST_LENS;
 #pragma unroll 1
-    for (int i = threadIdx.x; i <= p.G; i += C::THREADS) {
+    for (int i = threadIdx.x; i <= p.G; i += kScan) {
       gs[i] = __ldg(p.starts + i);
       if (i < p.G) gp[i] = __ldg(p.prefix_lens + i);
     }
     if (lens_here) {
 #pragma unroll 1
-      for (int i = threadIdx.x; i < p.B; i += C::THREADS) ls[i] = px_len(p, i);
+      for (int i = threadIdx.x; i < p.B; i += kScan) ls[i] = px_len(p, i);
     }
-    __syncthreads();
+    named_bar_sync(3, kScan);
     bool bad = false, wrong = false;  // the groups are not what they should be; seen by this thread
 #pragma unroll 1
-    for (int i = threadIdx.x; i < p.G; i += C::THREADS) wrong |= gs[i] < 0 || gs[i] > gs[i + 1] || gs[i + 1] > p.B;
+    for (int i = threadIdx.x; i < p.G; i += kScan) wrong |= gs[i] < 0 || gs[i] > gs[i + 1] || gs[i + 1] > p.B;
     auto len = [&](int b) { return lens_here ? ls[b] : px_len(p, b); };
     auto prefix_of = [&](int g) {
       const int s0 = gs[g], s1 = gs[g + 1];
@@ -909,11 +913,11 @@ __global__ void __launch_bounds__(384, 1)
       }
       const bool warp_wrong = __any_sync(0xffffffffu, wrong);
       if (lane == 31) wsum[warp] = make_int4(inc.x, inc.y, warp_wrong, 0);
-      __syncthreads();
+      named_bar_sync(3, kScan);
       int2 before = make_int2(inc.x - mine, inc.y - steps), all = make_int2(0, 0);
       int any_wrong = 0;
 #pragma unroll
-      for (int w = 0; w < 12; ++w) {
+      for (int w = 0; w < kPxWalker; ++w) {
         const int4 v = wsum[w];
         if (w < warp) {
           before.x += v.x;
@@ -926,7 +930,7 @@ __global__ void __launch_bounds__(384, 1)
       if (any_wrong && !bad) {  // every sequence by itself then
         bad = true;
         if (threadIdx.x == 0) record_error(p.err, FA_ERR_BOUNDS, SITE_PX_GROUPS);
-        __syncthreads();
+        named_bar_sync(3, kScan);
         continue;
       }
       const int grid = static_cast<int>(gridDim.x) / p.V;
@@ -955,9 +959,10 @@ __global__ void __launch_bounds__(384, 1)
         break;
       }
     }
+    if (threadIdx.x == 0) *walk0 = walk;
   }
   fence_async_smem();  // the rings' memory was read and written by plain accesses
-  __syncthreads();
+  if (warp != kPxWalker) __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
@@ -1247,37 +1252,57 @@ __global__ void __launch_bounds__(384, 1)
       // ======================= the walk =======================
       // Lengths and groups come from L2 and a step of the walk takes some divisions, 0.9 us: one
       // warp does it ahead of the others, which take the segments from shared memory.
-      if (lane == 0) {
-        walk.it = bars->it0;
-        walk.off = bars->off0;
-        walk.g = bars->group0;
-        walk.first = item0;
-        bool ok = true;
-        const int place = cta % p.V;
+      // A first step, whose result nobody takes, brings its code from L2 while the others make the scan.
+      PxWalk walk;
+      walk.it = walk.off = walk.at = walk.g = 0;
+      walk.end = 1;
+      walk.cut = PxCut(2, 2);
+      walk.no_groups = true;
+      walk.c = PX_BY_STEPS;
+      walk.first = item0 + 1;
+      if (lane == 0) item0[1] = PxItem{0, 1, 0, 3 * kPxTile, 1, true};  // two steps: half of them each
+      __syncwarp();
+      bool ok = true;
+      const int place = cta % p.V;
 #pragma unroll 1
-        for (uint32_t i = 0;; ++i) {
-          PxSeg w;
-          const bool more = walk.next(p, me, w);
-          if (more) {  // (here, since a division or two is a tenth of what a slim unit takes)
-            w.kvh = w.hu * p.V + place;
-            w.me = me;
-            w.out = (w.s0 * p.Hkv + w.kvh) * p.R;
-            w.part = static_cast<int>((p.V + place) * p.area) + (p.units * w.s0 + w.hu) * p.R;
-          } else {
-            w.nt = 0;
-          }
-          const uint32_t e = i % kPxQueue;
-          if (i >= kPxQueue && !mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag)) {
-            ok = false;
-            break;
-          }
+      for (int i = -1;; ++i) {
+        if (i == 0) {
+          pdl_wait();
+          __syncthreads();
+          walk = *walk0;
+          walk.it = bars->it0;
+          walk.off = bars->off0;
+          walk.g = bars->group0;
+          walk.first = item0;
+          __syncwarp();
+        }
+        PxSeg w;
+        const bool more = walk.next(p, me, w);
+        if (more) {  // (here, since a division or two is a tenth of what a slim unit takes)
+          w.kvh = w.hu * p.V + place;
+          w.me = me;
+          w.out = (w.s0 * p.Hkv + w.kvh) * p.R;
+          w.part = static_cast<int>((p.V + place) * p.area) + (p.units * w.s0 + w.hu) * p.R;
+        } else {
+          w.nt = 0;
+        }
+        if (i < 0) {
+          asm volatile("" ::"r"(w.nt), "r"(w.ctas), "r"(w.out), "r"(w.part), "r"(w.tile));
+          continue;
+        }
+        const uint32_t e = static_cast<uint32_t>(i) % kPxQueue;
+        if (i >= kPxQueue && !__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
           bars->seg[e] = w;
           mbar_arrive(&bars->seg_full[e]);
-          if (!more) break;
         }
-        if (!ok) fail(SITE_PX_WALK);
+        __syncwarp();
+        if (!more) break;
       }
-      __syncwarp();
+      if (!ok) fail(SITE_PX_WALK);
       // rows that a kind has no partials of: somebody has to say so
 #pragma unroll 1
       for (int b = cta; b < p.B; b += gridDim.x) {
