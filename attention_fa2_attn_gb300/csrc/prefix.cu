@@ -729,28 +729,34 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
     const uint32_t o_base = tmem + lane_base + (wide ? t * C::SLOT_COLS : 0) + C::O_OFF;
     const int c_lo = wide ? 0 : t * (D / 16), c_hi = wide ? D / 8 : c_lo + D / 16;  // chunks of eight columns
 #pragma unroll 1
-    for (int cc = c_lo; cc < c_hi; ++cc) {
-      uint32_t a[8], b[8];
-      tmem_ld8(o_base + cc * 8, a);
-      tmem_ld8(o_base + (wide ? 0 : C::SLOT_COLS) + cc * 8, b);
-      tmem_ld_wait();
-      // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
-      float o[8];
+    for (int cc = c_lo; cc < c_hi; cc += 2) {  // (two at a time: a chunk's loads and stores one behind the other are 0.13 us)
+      uint32_t a[2][8], b[2][8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
-        o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
+      for (int i = 0; i < 2; ++i) {
+        tmem_ld8(o_base + (cc + i) * 8, a[i]);
+        tmem_ld8(o_base + (wide ? 0 : C::SLOT_COLS) + (cc + i) * 8, b[i]);
       }
+      tmem_ld_wait();
       if (!valid) continue;
-      if (whole) {
-        // (o may start on any 16-byte border)
-        *reinterpret_cast<uint4*>(p.o + out_row * D + cc * 8) =
-            make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-      } else {
-        uint32_t v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[k]);
-        st32(p.part + (cc * p.part_rows + part_row) * 8, v);
+      for (int i = 0; i < 2; ++i) {
+        // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          o[k] = take0 ? f0 * __uint_as_float(a[i][k]) : 0.f;
+          o[k] = take1 ? fmaf(f1, __uint_as_float(b[i][k]), o[k]) : o[k];
+        }
+        if (whole) {
+          // (o may start on any 16-byte border)
+          *reinterpret_cast<uint4*>(p.o + out_row * D + (cc + i) * 8) =
+              make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+        } else {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[k]);
+          st32(p.part + ((cc + i) * p.part_rows + part_row) * 8, v);
+        }
       }
     }
     if (valid && (wide || t == 0)) {
