@@ -23,7 +23,8 @@
 //     keys at a time, each with its own S, P and O. Own keys of up to 16 rows are slim units, on
 //     warp-level MMAs (px_slim).
 //   * A share is a stretch of the line of all units' costs, groups first. One warp walks it ahead
-//     of the others and leaves its segments in a queue in shared memory.
+//     of the others and leaves its segments in a queue in shared memory. It takes no part in the
+//     scan of the costs: meanwhile it runs a step of no consequence, which fetches its code (0.6 us).
 //   * The CTAs that are neighbours take the KV heads of one cost line side by side.
 //   * A share of a unit leaves fp32 partials at (the rows before the unit + 256 times the
 //     CTA's number): no two shares meet there, since along the line either the unit or the CTA
@@ -32,10 +33,10 @@
 //     that is busy, and a spilled value waits in a busy L1. So few unrolled
 //     copies, one loop to a kind of segment, and no spills at 208 and 88 registers.
 // Measured, both kernels in a graph, d = 128 but where it says 64: 8 sequences of 2000 + 1..200
-// keys, 32 over 8 heads, 13.4 us (the launches, the lengths' scan and the first keys are 5);
-// 64 of 16384 + 9..1024, 64 over 8 heads, 59 us, 205 MB read once, where the paged decode
-// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 35.2 us
-// (64); 32 of 1000 + up to 8192, 16 heads, 168 us, 6.55 TB/s (232). Prefix steps are bound by
+// keys, 32 over 8 heads, 12.7 us (the launches, the lengths' scan and the first keys are 5);
+// 64 of 16384 + 9..1024, 64 over 8 heads, 58.6 us, 205 MB read once, where the paged decode
+// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 34.2 us
+// (64); 32 of 1000 + up to 8192, 16 heads, 167 us, 6.6 TB/s (232). Prefix steps are bound by
 // a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
 // under way), own keys by HBM where they are long and by the units' ends where they are short.
 // Tried and taken back: two slim units at a time, four warps on each (62 and 167 us); a slim unit's
