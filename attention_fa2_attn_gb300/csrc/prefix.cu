@@ -1653,13 +1653,13 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.c = scale * kLog2e;
   // In eighths of a wide step (some 0.2 us); narrow and slim steps are two tiles of keys, which
   // at d = 128 wait for HBM. What a unit costs beside its steps: Q and the first S, a slim one's
-  // join, the partials of 128 or 256 rows. (Swept over nine batches from 13 to 170 us: within 3 %
-  // of the best for each; off by half, up to 15 % slower.)
+  // join, the partials of 128 or 256 rows. (Swept over batches from 13 to 170 us, for slim
+  // units 25 of drawn sizes: 2.5 % on average from the best for each, 8 % at most.)
   p.cost = d == 128 ? PxCost{9, 12, 8, 20, 9, 12} : PxCost{9, 12, 8, 12, 9, 12};
   if (s.R <= kPxSlim) {
-    p.cost.own_step = d == 128 ? 9 : 5;
-    p.cost.own_front = d == 128 ? 2 : 12;
-    p.cost.wide_front = d == 128 ? 8 : 12;
+    p.cost.own_step = d == 128 ? 7 : 6;
+    p.cost.own_front = d == 128 ? 4 : 6;
+    p.cost.wide_front = d == 128 ? 4 : 12;
   }
   p.area = s.area;
   p.part_rows = 2 * s.V * s.area;
