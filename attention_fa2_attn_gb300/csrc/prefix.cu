@@ -33,8 +33,8 @@
 //     that is busy, and a spilled value waits in a busy L1. So few unrolled
 //     copies, one loop to a kind of segment, and no spills at 208 and 88 registers.
 // Measured, both kernels in a graph, d = 128 but where it says 64: 8 sequences of 2000 + 1..200
-// keys, 32 over 8 heads, 12.7 us (the launches, the lengths' scan and the first keys are 5);
-// 64 of 16384 + 9..1024, 64 over 8 heads, 58.6 us, 205 MB read once, where the paged decode
+// keys, 32 over 8 heads, 12.6 us (the launches, the lengths' scan and the first keys are 5);
+// 64 of 16384 + 9..1024, 64 over 8 heads, 59.4 us, 205 MB read once, where the paged decode
 // reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 34.2 us
 // (64); 32 of 1000 + up to 8192, 16 heads, 167 us, 6.6 TB/s (232). Prefix steps are bound by
 // a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
@@ -1653,9 +1653,9 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.c = scale * kLog2e;
   // In eighths of a wide step (some 0.2 us); narrow and slim steps are two tiles of keys, which
   // at d = 128 wait for HBM. What a unit costs beside its steps: Q and the first S, a slim one's
-  // join, the partials of 128 or 256 rows. (Swept over batches from 13 to 170 us, for slim
-  // units 25 of drawn sizes: 2.5 % on average from the best for each, 8 % at most.)
-  p.cost = d == 128 ? PxCost{9, 12, 8, 20, 9, 12} : PxCost{9, 12, 8, 12, 9, 12};
+  // join, the partials of 128 or 256 rows. (Swept over batches from 13 to 170 us, 51 of
+  // them of drawn sizes: 2.5 % on average from the best for each, 8 % at most.)
+  p.cost = d == 128 ? PxCost{9, 16, 8, 20, 10, 9} : PxCost{9, 16, 8, 20, 8, 15};
   if (s.R <= kPxSlim) {
     p.cost.own_step = d == 128 ? 7 : 6;
     p.cost.own_front = d == 128 ? 4 : 6;
