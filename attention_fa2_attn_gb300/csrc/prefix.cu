@@ -33,9 +33,9 @@
 //     that is busy, and a spilled value waits in a busy L1. So few unrolled
 //     copies, one loop to a kind of segment, and no spills at 208 and 88 registers.
 // Measured, both kernels in a graph, d = 128 but where it says 64: 8 sequences of 2000 + 1..200
-// keys, 32 over 8 heads, 12.6 us (the launches, the lengths' scan and the first keys are 5);
+// keys, 32 over 8 heads, 12.5 us (the launches, the lengths' scan and the first keys are 5);
 // 64 of 16384 + 9..1024, 64 over 8 heads, 59.4 us, 205 MB read once, where the paged decode
-// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 34.2 us
+// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 33.8 us
 // (64); 32 of 1000 + up to 8192, 16 heads, 167 us, 6.6 TB/s (232). Prefix steps are bound by
 // a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
 // under way), own keys by HBM where they are long and by the units' ends where they are short.
@@ -105,6 +105,7 @@ struct PxParams {
   int B, G, Hkv, T, R, causal;
   int spt;    // sequences of a row tile (1 where R > 128)
   int TS;     // row tiles of a sequence (1 where R <= 128)
+  int r_mul, t_mul;  // floor(2^16 / R) + 1, of T: x times that >> 16 is x / R for x < 128 and R <= 128
   int V;      // KV heads side by side
   int units;  // KV heads of each of these places
   int max_pages, num_pages;
@@ -315,7 +316,7 @@ __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg*
 #pragma unroll
   for (int ri = 0; ri < 2; ++ri) {
     const int n = gid + 8 * ri;
-    sees[ri] = w->k1 - w->k0 - (p.causal ? p.T - 1 - (p.T == 1 ? 0 : n % p.T) : 0);
+    sees[ri] = w->k1 - w->k0 - (p.causal ? p.T - 1 - (n - p.T * (n * p.t_mul >> 16)) : 0);
   }
   bool ok = wwait(&bars->q_full, seg_i & 1);
   uint32_t qa[D / 16][4];
@@ -544,7 +545,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
     asm volatile("" : "+r"(x));
     const int tile = w->tile + (w->wide() ? t : 0);
     if (p.R <= kPxTile) {
-      const int q = x / p.R;
+      const int q = x * p.r_mul >> 16;  // x / R
       seq = w->s0 + tile * p.spt + q;
       return q < p.spt && seq < w->s0 + w->n ? x - q * p.R : -1;
     }
@@ -562,7 +563,8 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
     has_rows = __any_sync(0xffffffffu, rr >= 0);
     if (rr >= 0) {
       const int S = w->own() ? w->k1 : px_len(p, seq);
-      sees = min(p.causal ? S - p.T + rr % p.T + 1 : S, w->k1) - w->k0 - w->x0 * kPxTile;
+      const int pos = p.R <= kPxTile ? rr - p.T * (rr * p.t_mul >> 16) : rr % p.T;
+      sees = min(p.causal ? S - p.T + pos + 1 : S, w->k1) - w->k0 - w->x0 * kPxTile;
     }
   }
   const int keys = w->k1 - w->k0 - w->x0 * kPxTile;  // of the item, from the segment's first one on
@@ -1646,6 +1648,8 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.causal = causal ? 1 : 0;
   p.spt = s.spt;
   p.TS = s.TS;
+  p.r_mul = (1 << 16) / s.R + 1;
+  p.t_mul = (1 << 16) / T + 1;
   p.V = s.V;
   p.units = Hkv / s.V;
   p.max_pages = max_pages;
