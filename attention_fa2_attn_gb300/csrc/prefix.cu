@@ -47,6 +47,7 @@
 // unwinds. A warp's lanes leave together, and the softmax warps by a vote in every unit.
 #include <atomic>
 
+#include "groups.h"
 #include "join.cuh"
 #include "launch.cuh"
 #include "warp_mma.cuh"
@@ -167,7 +168,7 @@ __device__ __forceinline__ int px_len(const PxParams& p, int b) {
 }
 // Keys that a group reads once: whole pages, of two sequences or more, which its first one has.
 __device__ __forceinline__ int px_prefix(const PxParams& p, int s0, int s1, int asked) {
-  return s1 - s0 < 2 ? 0 : max(0, min(asked, px_len(p, s0))) & ~15;
+  return group_of_several(s0, s1, p.B) ? max(0, min(asked, px_len(p, s0))) & ~15 : 0;
 }
 
 // A group's prefix or a sequence's own keys.
@@ -188,7 +189,7 @@ struct PxItem {
   }
 };
 __device__ __forceinline__ PxItem px_group(const PxParams& p, int s0, int s1, int prefix) {
-  const int n = max(0, s1 - s0);
+  const int n = prefix > 0 ? s1 - s0 : 0;  // (a group without one has no units, and its ends may be anything)
   return PxItem{s0, s1, 0, prefix, p.R <= kPxTile ? (n + p.spt - 1) / p.spt : n * p.TS, false};
 }
 __device__ __forceinline__ PxItem px_sequence(const PxParams& p, int b, int prefix) {
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(384, 1)
     auto prefix_of = [&](int g) {
       const int s0 = gs[g], s1 = gs[g + 1];
       // (until the sums are made it is not known whether the starts are in order)
-      return s1 - s0 < 2 || s0 < 0 || s1 > p.B ? 0 : max(0, min(gp[g], len(s0))) & ~15;
+      return group_of_several(s0, s1, p.B) ? max(0, min(gp[g], len(s0))) & ~15 : 0;
     };
     auto item = [&](int i, int& g) {
       if (i < p.G) return bad ? PxItem{0, 0, 0, 0, 0, false} : px_group(p, gs[i], gs[i + 1], prefix_of(i));
