@@ -671,6 +671,7 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
             make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
+      __syncwarp();  // lanes may have made one store more than others, and what follows is the whole warp's
     }
     tmem_st_wait();
     tc_fence_before();
@@ -705,8 +706,10 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
       record_error(p.err, FA_ERR_TIMEOUT, SITE_PX_SOFTMAX);
       bars->abort_flag = 1;
     }
+    tc_fence_before();
     ok = vote_all(1, 256, ok);
     if (!ok) return false;  // all eight warps leave in the same segment
+    tc_fence_after();  // the other slot's O, whose end its own warps waited for
     const float m0 = ex[r], m1 = ex[128 + r];
     m_all = fmaxf(m0, m1);
     const float m_use = m_all == -INFINITY ? 0.f : m_all;
@@ -741,27 +744,29 @@ __device__ __forceinline__ bool px_rows(const PxParams& p, const volatile PxSeg*
         tmem_ld8(o_base + (wide ? 0 : C::SLOT_COLS) + (cc + i) * 8, b[i]);
       }
       tmem_ld_wait();
-      if (!valid) continue;
+      if (valid) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
-        float o[8];
+        for (int i = 0; i < 2; ++i) {
+          // TMEM that no PV wrote, and rows whose weight is 0 over whatever P held, are not taken in
+          float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          o[k] = take0 ? f0 * __uint_as_float(a[i][k]) : 0.f;
-          o[k] = take1 ? fmaf(f1, __uint_as_float(b[i][k]), o[k]) : o[k];
-        }
-        if (whole) {
-          // (o may start on any 16-byte border)
-          *reinterpret_cast<uint4*>(p.o + out_row * D + (cc + i) * 8) =
-              make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-        } else {
-          uint32_t v[8];
+          for (int k = 0; k < 8; ++k) {
+            o[k] = take0 ? f0 * __uint_as_float(a[i][k]) : 0.f;
+            o[k] = take1 ? fmaf(f1, __uint_as_float(b[i][k]), o[k]) : o[k];
+          }
+          if (whole) {
+            // (o may start on any 16-byte border)
+            *reinterpret_cast<uint4*>(p.o + out_row * D + (cc + i) * 8) =
+                make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+          } else {
+            uint32_t v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[k]);
-          st32(p.part + ((cc + i) * p.part_rows + part_row) * 8, v);
+            for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[k]);
+            st32(p.part + ((cc + i) * p.part_rows + part_row) * 8, v);
+          }
         }
       }
+      __syncwarp();  // lanes without a row wait: the next loads are the whole warp's
     }
     if (valid && (wide || t == 0)) {
       if (whole) {
