@@ -823,6 +823,7 @@ __global__ void __launch_bounds__(384, 1)
                 make_uint4(0u, 0u, 0u, 0u);
           }
           fence_async_smem();
+          __syncwarp();  // lanes may have made one store more than others, and what follows is the whole warp's
         }
         tmem_st_wait();
         tc_fence_before();
@@ -863,8 +864,10 @@ __global__ void __launch_bounds__(384, 1)
         ex[t * 128 + r] = m;
         ex[(2 + t) * 128 + r] = l + lc;
         if (t == 1) ex[4 * 128 + r] = l;
+        tc_fence_before();
         ok = vote_all(1, 256, ok);
         if (!ok) break;  // all eight warps leave in the same segment
+        tc_fence_after();  // the other slot's O, whose end its own warps waited for
         const float m0 = ex[r], m1 = ex[128 + r];
         m_all = fmaxf(m0, m1);
         const float m_use = m_all == -INFINITY ? 0.f : m_all;
@@ -905,33 +908,35 @@ __global__ void __launch_bounds__(384, 1)
             o[k] = take0 ? f0 * __uint_as_float(a[k]) : 0.f;
             if constexpr (!WIDE) o[k] = take1 ? fmaf(f1, __uint_as_float(b[k]), o[k]) : o[k];
           }
-          if (!write) continue;
-          if (whole) {
-            // (o may start on any 16-byte border)
-            __nv_bfloat16* dst = p.o + out_row * D + col0 + cc * 32;
+          if (write) {
+            if (whole) {
+              // (o may start on any 16-byte border)
+              __nv_bfloat16* dst = p.o + out_row * D + col0 + cc * 32;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(dst + 8 * q) =
-                  live ? make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
-                                    pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]))
-                       : make_uint4(0u, 0u, 0u, 0u);
-          } else if (CL) {
-            if (m_all != -INFINITY) {  // else its weight is 0 and nobody reads it (nor has Q necessarily come)
-              float* dst = reinterpret_cast<float*>(smem + (WIDE ? t * kTrTile + r : r) * C::PART_PITCH) + col0 + cc * 32;
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + 8 * q) =
+                    live ? make_uint4(pack_bf16x2(o[8 * q], o[8 * q + 1]), pack_bf16x2(o[8 * q + 2], o[8 * q + 3]),
+                                      pack_bf16x2(o[8 * q + 4], o[8 * q + 5]), pack_bf16x2(o[8 * q + 6], o[8 * q + 7]))
+                         : make_uint4(0u, 0u, 0u, 0u);
+            } else if (CL) {
+              if (m_all != -INFINITY) {  // else its weight is 0 and nobody reads it (nor has Q necessarily come)
+                float* dst = reinterpret_cast<float*>(smem + (WIDE ? t * kTrTile + r : r) * C::PART_PITCH) + col0 + cc * 32;
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-            }
-          } else if (live) {
-            float* dst = p.part + part_row * D + col0 + cc * 32;
+                for (int q = 0; q < 8; ++q)
+                  *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+              }
+            } else if (live) {
+              float* dst = p.part + part_row * D + col0 + cc * 32;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t v[8];
+              for (int q = 0; q < 4; ++q) {
+                uint32_t v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
-              st32(dst + 8 * q, v);
+                for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[8 * q + k]);
+                st32(dst + 8 * q, v);
+              }
             }
           }
+          __syncwarp();  // lanes without a row wait: the next loads are the whole warp's
         }
         if (write && (WIDE || t == 0)) {
           if (whole) {

@@ -26,7 +26,7 @@ def _body(code, at):
     raise AssertionError("no end")
 
 
-@pytest.mark.parametrize("name", ["prefix.cu"])
+@pytest.mark.parametrize("name", ["prefix.cu", "tree.cu"])
 def test_stores_of_some_lanes_between_loads_of_all(name):
     # loops over columns that load from tensor memory and store the rows that a warp's lanes have
     code = _code(name)
@@ -42,7 +42,7 @@ def test_stores_of_some_lanes_between_loads_of_all(name):
     assert seen == 1
 
 
-@pytest.mark.parametrize("name", ["prefix.cu"])
+@pytest.mark.parametrize("name", ["prefix.cu", "tree.cu"])
 def test_loops_of_unequal_length_before_what_the_whole_warp_does(name):
     # V's rows past the end are set to 0 by each lane as often as there is something for it
     code = _code(name)
@@ -54,7 +54,7 @@ def test_loops_of_unequal_length_before_what_the_whole_warp_does(name):
         assert "__syncwarp();" in code[end:next_one.start()]
 
 
-@pytest.mark.parametrize("name", ["prefix.cu"])
+@pytest.mark.parametrize("name", ["prefix.cu", "tree.cu"])
 def test_the_other_slots_sums_are_read_between_fences(name):
     code = _code(name)
     votes = [m for m in re.finditer(r"ok = vote_all\(1, 256, ok\);", code) if "ex[r]" in code[m.end():m.end() + 200]]
