@@ -43,8 +43,9 @@
 // Q with its first keys, and the next segment's table entries fetched ahead (58.9 and 168.8).
 // P is rounded to bf16 for the tensor cores (by at most 2^-8 of a weight; fp32 would take twice
 // the MMAs), O once at the end; sums and maxima are fp32.
-// Every mbarrier wait is bounded; a wait that runs out records FA_ERR_TIMEOUT and the CTA
-// unwinds. A warp's lanes leave together, and the softmax warps by a vote in every unit.
+// Every mbarrier wait is bounded (one for a whole segment by as much for each of its tiles); a
+// wait that runs out records FA_ERR_TIMEOUT and the CTA unwinds. A warp's lanes leave together,
+// and the softmax warps by a vote in every unit.
 #include <atomic>
 
 #include "groups.h"
@@ -275,6 +276,11 @@ struct PxWalk {
   }
 };
 
+// What bounds a wait for all of a segment: each of its tiles may take as long as any other wait.
+__device__ __forceinline__ uint64_t px_bound(uint64_t tmo, int tiles) {
+  return tmo >> 38 ? tmo : tmo * static_cast<uint64_t>(tiles + 2);  // (longer ones than four minutes are long enough)
+}
+
 // Takes the segments that the walking warp leaves, one after the other. A segment stays where
 // it is until `done`, and its parts are read from there when they are needed: in registers they
 // are spilled by the loops over the keys, to memory that a busy L1 has no room for.
@@ -283,8 +289,11 @@ struct PxTake {
   // a whole warp; null: the wait ran out
   __device__ __forceinline__ const volatile PxSeg* next(PxBars* bars, uint64_t tmo, const volatile int* abort_flag) const {
     const uint32_t e = i % kPxQueue;
-    if (!__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_full[e], (i / kPxQueue) & 1, tmo, abort_flag))) return nullptr;
-    return &bars->seg[e];
+    const volatile PxSeg* at = &bars->seg[e];
+    // It comes when the last of the readers has done the one before it in its place.
+    const uint64_t bound = i < kPxQueue ? tmo : px_bound(tmo, at->nt);
+    if (!__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_full[e], (i / kPxQueue) & 1, bound, abort_flag))) return nullptr;
+    return at;
   }
   __device__ __forceinline__ void done(PxBars* bars) {
     __syncwarp();
@@ -1306,9 +1315,12 @@ __global__ void __launch_bounds__(384, 1)
           continue;
         }
         const uint32_t e = static_cast<uint32_t>(i) % kPxQueue;
-        if (i >= kPxQueue && !__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, tmo, abort_flag))) {
-          ok = false;
-          break;
+        if (i >= kPxQueue) {
+          const uint64_t bound = px_bound(tmo, bars->seg[e].nt);  // the one that is still there is waited for
+          if (!__all_sync(0xffffffffu, mbar_wait_lean(&bars->seg_empty[e], ((i / kPxQueue) & 1) ^ 1, bound, abort_flag))) {
+            ok = false;
+            break;
+          }
         }
         if (lane == 0) {
           bars->seg[e] = w;

@@ -622,7 +622,9 @@ FA_API fa_status fa_get_last_device_error(void* stream, int* detail);
 /*
  * fa_set_wait_timeout_ns -- bound, in nanoseconds of %globaltimer, for every
  * wait of one role of a CTA on another inside the kernels launched after this
- * call (default 4e9 = 4 s). Values below 1e6 (1 ms) are raised to 1e6. The
+ * call (default 4e9 = 4 s). Values below 1e6 (1 ms) are raised to 1e6. Where a
+ * role waits until others have gone over a stretch of keys, it is the bound for
+ * each tile of them, so that it need not grow with the lengths. The
  * waits a CTA makes before it exits or frees its tensor memory (its own bulk
  * copies landing, its own MMAs draining) are bounded by max(this, 1e9): a
  * short setting never lets a CTA leave with copies or MMAs still running.
