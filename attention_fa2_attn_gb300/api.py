@@ -16,6 +16,7 @@ import torch
 from ._lib import (
     FA_DTYPE_BF16,
     FA_DTYPE_F32,
+    FA_ERR_INVALID_ARG,
     FA_ERR_UNSUPPORTED,
     FA_FORK_MAX,
     FA_PAGES_MAX,
@@ -790,6 +791,9 @@ def fa_prefix_decode_paged(q, k_pages, v_pages, block_table, seqlens, group_star
     _need_ints("group_starts", group_starts, (groups + 1,), dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     nbytes = fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, device=dev)
+    if nbytes == 0:  # before a workspace and outputs are made
+        whole = min(B, Hq, Hkv, T, max_pages) > 0 and Hq % Hkv == 0
+        check(FA_ERR_UNSUPPORTED if whole else FA_ERR_INVALID_ARG, "fa_prefix_decode_paged")
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     ws_bytes = _ws_bytes(workspace, nbytes, dev)

@@ -386,14 +386,14 @@ PyObject* prefix_decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !fits(G))
     Py_RETURN_NONE;
   if (a[8] == Py_None) scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+  const size_t bytes = fa_prefix_workspace_bytes(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv),
+                                                 static_cast<int>(T), static_cast<int>(pages), static_cast<int>(d),
+                                                 at::cuda::getCurrentDeviceProperties()->multiProcessorCount);
+  if (bytes == 0) Py_RETURN_NONE;  // refused before its outputs are made
   Tensor o, lse;
   fa_status st;
   {
     NoInterpreter released;
-    const int sms = at::cuda::getCurrentDeviceProperties()->multiProcessorCount;
-    const size_t bytes =
-        fa_prefix_workspace_bytes(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(T),
-                                  static_cast<int>(pages), static_cast<int>(d), sms);
     const Tensor ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
     o = make({B, Hq, T, d}, at::kBFloat16, dev);
     lse = make({B, Hq, T}, at::kFloat, dev);

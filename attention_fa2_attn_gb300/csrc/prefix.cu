@@ -1547,10 +1547,12 @@ struct PxShape {
   size_t part, ml, all;     // bytes
 };
 
-// How the problem is laid out on `sms` SMs; false: its cost could reach 2^31.
+// How the problem is laid out on `sms` SMs; false: sizes that the call does not take.
 static bool px_shape(int B, int Hq, int Hkv, int T, int max_pages, int d, int sms, PxShape& s) {
   const long long R = static_cast<long long>(Hq / Hkv) * T;
-  if (R >= (1ll << 30) || B * R * Hkv > (1ll << 30)) return false;
+  if (d != 64 && d != 128) return false;
+  if (R >= (1ll << 30) || B * R > (1ll << 30) / Hkv || sms > 32767) return false;
+  if (static_cast<long long>(max_pages) * 16 > (1ll << 31) - 256) return false;  // (a key's index, rounded up to whole tiles, has 32 bits)
   s.R = static_cast<int>(R);
   s.spt = R <= kPxTile ? static_cast<int>(kPxTile / R) : 1;
   s.TS = static_cast<int>((R + kPxTile - 1) / kPxTile);
@@ -1565,9 +1567,10 @@ static bool px_shape(int B, int Hq, int Hkv, int T, int max_pages, int d, int sm
   const long long units = Hkv / s.V, tiles = (static_cast<long long>(max_pages) * 16 + kPxTile - 1) / kPxTile;
   // steps of a line: a row tile of every sequence over all keys, of its prefix and of its own
   const long long rows = 2ll * B * s.TS * units;
-  if (rows > (1ll << 31) / kPxMostCost / tiles) return false;
+  if (rows > (1ll << 31) / kPxMostCost / tiles) return false;  // (their cost has 32 bits)
   s.grid = static_cast<int>(rows * tiles < sms / s.V ? rows * tiles : sms / s.V);
   s.area = units * R * B + static_cast<long long>(kPxUnit) * s.grid;
+  if (2 * s.V * s.area >= (1ll << 31)) return false;  // (as have the partials' rows)
   s.desc = static_cast<long long>(B) * Hkv * s.TS;
   s.part = static_cast<size_t>(2 * s.V * s.area) * d * 4;
   s.ml = static_cast<size_t>(2 * s.V * s.area) * 16;
@@ -1622,7 +1625,7 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
                                  int num_pages, int d, float scale, int causal, void* workspace, size_t ws_bytes,
                                  void* stream) {
   auto mis = [](const void* x, uintptr_t m) { return (reinterpret_cast<uintptr_t>(x) & (m - 1)) != 0; };
-  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !group_starts || !prefix_lens || !o || !workspace)
+  if (!q || !k_pages || !v_pages || !block_table || !seqlens || !group_starts || !prefix_lens || !o)
     return FA_ERR_INVALID_ARG;
   if (mis(q, 16) || mis(k_pages, 16) || mis(v_pages, 16) || mis(o, 16) || mis(block_table, 4) || mis(seqlens, 4) ||
       mis(group_starts, 4) || mis(prefix_lens, 4) || (lse && mis(lse, 4)) || mis(workspace, 256))
@@ -1633,7 +1636,7 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   if (page_size != 16 || (d != 64 && d != 128) || groups > FA_PREFIX_MAX_GROUPS) return FA_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * 16 >= (1ll << 31) ||
       static_cast<long long>(max_pages) * 16 > (1ll << 31) - 256 || static_cast<long long>(B) * Hq * T >= (1ll << 31))
-    return FA_ERR_UNSUPPORTED;  // (a key's index, rounded up to whole tiles, is a 32-bit number)
+    return FA_ERR_UNSUPPORTED;
   {
     // o, lse and the workspace are written while other CTAs still read the rest
     const long long rows = static_cast<long long>(B) * Hq * T, q_bytes = rows * d * 2;
@@ -1649,11 +1652,11 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
     }
   }
   const int sms = device_sm_count();
-  if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
   PxShape s;
-  if (sms > 32767 || !px_shape(B, Hq, Hkv, T, max_pages, d, sms, s)) return FA_ERR_UNSUPPORTED;
+  if (sms && !px_shape(B, Hq, Hkv, T, max_pages, d, sms, s)) return FA_ERR_UNSUPPORTED;
+  if (!workspace) return FA_ERR_INVALID_ARG;  // (of 0 bytes, which may be null, for sizes that are not taken)
+  if (!sms) return static_cast<fa_status>(record_cuda_failure(cudaGetLastError()));
   if (ws_bytes < s.all) return FA_ERR_INVALID_ARG;
-  if (2 * s.V * s.area >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return FA_ERR_CUDA;
   CUtensorMap tq, tk[2], tv[2];

@@ -590,7 +590,9 @@ FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pag
  *   every sequence is read by itself, so that the result is the same. prefix_lens [groups] int32 (device): any value,
  *   0 and less for none. 1 <= groups <= FA_PREFIX_MAX_GROUPS.
  *   q, pools, block_table, seqlens, o, lse (may be NULL), scale, causal: as fa_decode_paged, and the same result, for
- *   any Hq / Hkv and T with B * Hq * T <= 2^30. d in {64, 128}, page_size == 16.
+ *   any Hq / Hkv and T. d in {64, 128}, page_size == 16. FA_ERR_UNSUPPORTED past these sizes: B * Hq * T + 256 * SM count
+ *   < 2^30, and B * ceil(Hq / Hkv * T / 128) * (Hkv / V) * ceil(max_pages / 8) <= 38347922, whatever the lengths are,
+ *   where V is the largest divisor of Hkv up to 16 that leaves no more than a 24th of the SMs over.
  *   workspace: at least fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count) bytes, 256-byte aligned; its
  *   contents need no initialisation, and calls that may overlap on the GPU need one each. o, lse and the workspace may
  *   overlap no other argument (FA_ERR_INVALID_ARG).
@@ -608,7 +610,7 @@ FA_API fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, cons
 
 /* fa_prefix_workspace_bytes -- fp32 partials (O, max, sums): two rows for each query row, and 512 for each CTA that the
  * call launches on num_sms SMs, 4 * d + 16 bytes each; and 16 bytes for each 128 rows of a sequence and KV head. 0 for
- * sizes that the call does not take. */
+ * sizes that the call does not take, d other than 64 and 128 among them. */
 FA_API size_t fa_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pages, int d, int num_sms);
 
 /*
