@@ -311,13 +311,26 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   // Heads of a block: up to four rows to each of its eight warps (a warp's heads are
   // kRopeWarps apart), in even cuts; fewer where the blocks would leave SMs idle (a decode
   // step).
+  const long long sms = device_sm_count();
   int cuts = (heads + kRopeMostRows * kRopeWarps - 1) / (kRopeMostRows * kRopeWarps);
   const int most = (heads + kRopeWarps - 1) / kRopeWarps;
-  while (cuts < most && blocks * cuts < 2ll * device_sm_count()) cuts = cuts * 2 < most ? cuts * 2 : most;
+  while (cuts < most && blocks * cuts < 2 * sms) cuts = cuts * 2 < most ? cuts * 2 : most;
   int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
-  // Heads that two cuts of three rows each would hold, but one of five as well: three blocks an SM
-  // with all rows in use (b2 h32+8 n8192 d128 bf16: 56.2 us in two cuts, 52.9 in one).
-  if (w == V && cuts == 2 && heads > 4 * kRopeWarps && heads <= 5 * kRopeWarps && blocks >= 2ll * device_sm_count()) rows = 5;
+  // 33 to 40 heads: two cuts of three rows, four blocks an SM, or one of five (rows from the last
+  // heads on are empty), three. One is better where its blocks fit the GPU at once and two cuts' do
+  // not, or where three rounds of its blocks and more leave a small part of the last one empty. Two
+  // cuts / one, us, d = 128, by heads and tokens (blocks of one cut an SM):
+  //   bf16  1216 (2)   1500 (2.5)  2048 (3.4)  4096 (6.7)   6000 (9.9)   16384 (27)
+  //     33  6.2 / 6.4  7.6 / 6.8   8.8 / 9.9   15.7 / 15.3  21.1 / 20.2  51.1 / 46.6
+  //     36  6.2 / 6.6  7.8 / 7.2   9.2 / 10.4  16.2 / 16.2  21.7 / 21.1  53.2 / 49.4
+  //     40  6.3 / 7.1  8.3 / 7.8   9.9 / 11.1  17.2 / 17.3  23.2 / 22.8  57.0 / 53.2
+  //   fp32  900 (3)    1216 (4)    2048 (6.7)  3001 (9.9)   8192 (27)
+  //     33  7.6 / 7.0  9.2 / 10.0  14.1 / 13.9 19.1 / 18.5  47.0 / 43.3
+  //     40  8.4 / 8.1  10.1 / 11.2 15.3 / 15.6 21.1 / 21.3  52.1 / 51.5
+  // Backward, interleaved pairs, several axes and appends go the same way. From 65 heads on one cut less
+  // in three gains 2 % at most and loses as much.
+  const bool pays = (blocks > 2 * sms && blocks <= 3 * sms) || blocks >= 9 * sms;
+  if (w == V && cuts == 2 && heads > 4 * kRopeWarps && heads <= 5 * kRopeWarps && pays) rows = 5;
   p.head_chunk = rows * kRopeWarps;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((heads + p.head_chunk - 1) / p.head_chunk));
   if (w == V) return launch_rope_rows<E, V, APPEND>(p, interleaved, rows, grid, stream);
