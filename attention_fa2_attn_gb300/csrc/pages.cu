@@ -25,7 +25,9 @@
 //   p's bit. Bits in order are the freed list. An SM does one count in about two cycles, so
 //   many entries are counted down by the whole GPU first, which leaves -1 where nobody holds a
 //   page any more, and the cluster takes its bits from there: three launches (256 of 512 rows,
-//   164 000 entries, 524 000 pages: one cluster alone 32 us).
+//   164 000 entries, 524 000 pages: one cluster alone 32 us). Counts that meet on few addresses
+//   are no slower (512 rows of 640 pages: 20.3 us where all hold the same 600, 20.0 where none
+//   holds another's).
 //   compact: a bit for each live page. With n live pages from `first` on, they end up in
 //   [first, first + n): a live page behind that moves into a hole before it, the i-th of
 //   these into the i-th of those. Sources and holes are apart, so the copies need no order.
