@@ -7,10 +7,12 @@
 //
 // fa_pages_fork. Child i gets the whole pages of its parent (shares + 1 each) and, where the
 // parent's last page is not full, a page of its own from the free list, in the order of i.
-// One launch without any exchange between blocks: a warp takes a child, and its block counts
-// by itself how many of the children before it need a page (work that grows with the square of
-// their number, so that is limited). Bound by launch and by two round trips to L2 (parent ->
-// length -> table row).
+// One launch without any exchange between blocks: a warp takes a child, and of the blocks that
+// write a row (128 entries each) the first counts by itself how many of the children before it
+// need a page. That is work that grows with the square of their number, so it is limited. Bound
+// by launch and by two round trips to L2 (parent -> length -> table row); in a graph 16 children
+// of tables of 64 pages 2.5 us, 1024 of 512 pages 3.6, 16384 of 1024 75, 65536 of 2048 751 (2034
+// where every block of a row counted).
 //
 // fa_pages_copy. Bound by HBM: every copied byte is read once and written once. A warp moves
 // 8 KB of a page at a time, sixteen 16-byte vectors a lane in flight (1.07 GB read and written:
@@ -85,10 +87,16 @@ __global__ void __launch_bounds__(kForkWarps * 32) pages_fork_kernel(const ForkP
   pdl_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i0 = blockIdx.x * kForkWarps, i = i0 + warp;
-  // this child's parent and row, on their way while the children before it are counted
+  // The block of a row's first entries alone counts, and writes the child's last page wherever that
+  // is. What it counts first is on its way with this child's parent, length and row.
+  const bool first = blockIdx.y == 0;
   const int parent = i < p.n ? __ldg(p.parents + i) : -1;
-  bool bad = false;
+  const int far = first && static_cast<int>(threadIdx.x) < i0 ? __ldg(p.parents + threadIdx.x) : -1;
+  const int near = first && lane < warp && i0 + lane < p.n ? __ldg(p.parents + i0 + lane) : -1;
+  bool bad = false, ignored = false;
   const int len = fork_len(p, parent, bad);
+  int sum = fork_len(p, far, ignored) % kPgTokens != 0;
+  const int beside = fork_len(p, near, ignored) % kPgTokens != 0;
   const int full = len / kPgTokens, part = len % kPgTokens != 0;
   const int* row = p.table + static_cast<size_t>(parent >= 0 && parent < p.B ? parent : 0) * p.max_pages;
   const int j0 = blockIdx.y * kForkChunk + lane;
@@ -96,55 +104,52 @@ __global__ void __launch_bounds__(kForkWarps * 32) pages_fork_kernel(const ForkP
 #pragma unroll
   for (int k = 0; k < kForkRows; ++k) {
     const int j = j0 + 32 * k;
-    e[k] = i < p.n && j < full + part ? __ldg(row + j) : 0;
+    e[k] = i < p.n && j < full ? __ldg(row + j) : 0;
   }
-  bool ignored = false;
-  int sum = 0;
+  const int copied = first && part ? __ldg(row + full) : -1;
+  int before = 0;
+  if (first) {
 #pragma unroll 4
-  for (int c = threadIdx.x; c < i0; c += kForkWarps * 32)
-    sum += fork_len(p, __ldg(p.parents + c), ignored) % kPgTokens != 0;
+    for (int c = threadIdx.x + kForkWarps * 32; c < i0; c += kForkWarps * 32)
+      sum += fork_len(p, __ldg(p.parents + c), ignored) % kPgTokens != 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) partial[warp] = sum;
-  __syncthreads();
-  int before = lane < kForkWarps ? partial[lane] : 0;
-  if (lane < warp && i0 + lane < p.n) before += fork_len(p, __ldg(p.parents + i0 + lane), ignored) % kPgTokens != 0;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) partial[warp] = sum;
+    __syncthreads();
+    before = beside + (lane < kForkWarps ? partial[lane] : 0);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if (i >= p.n) return;
-  int fresh = -1;
-  if (part) {
-    if (before < p.num_free) fresh = __ldg(p.free_pages + before);
-    if (fresh < 0 || fresh >= p.num_pages) {
-      fresh = -1;
-      bad = true;
-    }
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   }
+  if (i >= p.n) return;
   int* out = p.table_out + static_cast<size_t>(i) * p.max_pages;
 #pragma unroll
   for (int k = 0; k < kForkRows; ++k) {
     const int j = j0 + 32 * k;
-    if (j >= p.max_pages) continue;
-    int v = 0;
+    if (j >= p.max_pages || (part && j == full)) continue;
     if (j < full) {
-      v = e[k];
-      if (v >= 0 && v < p.num_pages) atomicAdd(p.shares + v, 1); else bad = true;
-    } else if (j == full && part) {
-      v = fresh;
-      // the lane that has the parent's last page names the copy
-      const bool ok = e[k] >= 0 && e[k] < p.num_pages;
-      bad |= !ok;
-      p.src[i] = ok && fresh >= 0 ? e[k] : -1;
-      p.dst[i] = ok ? fresh : -1;
+      if (e[k] >= 0 && e[k] < p.num_pages) atomicAdd(p.shares + e[k], 1); else bad = true;
     }
-    out[j] = v;
+    out[j] = e[k];
   }
-  if (bad) record_error(p.err, FA_ERR_BOUNDS, SITE_PAGES_FORK);
-  if (blockIdx.y == 0 && lane == 0) {
+  if (first && lane == 0) {
+    int from = -1, to = -1;
+    if (part) {
+      int fresh = before < p.num_free ? __ldg(p.free_pages + before) : -1;
+      if (fresh < 0 || fresh >= p.num_pages) fresh = -1;
+      const bool there = copied >= 0 && copied < p.num_pages;
+      bad |= fresh < 0 || !there;
+      if (fresh >= 0 && there) {
+        from = copied;
+        to = fresh;
+      }
+      out[full] = fresh;
+    }
+    p.src[i] = from;
+    p.dst[i] = to;
     p.lens_out[i] = len;
-    if (!part) p.src[i] = p.dst[i] = -1;
     if (i == p.n - 1) *p.used = before + part;
   }
+  if (bad) record_error(p.err, FA_ERR_BOUNDS, SITE_PAGES_FORK);
 }
 
 // ---------------------------------------------------------------------------
