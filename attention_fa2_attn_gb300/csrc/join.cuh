@@ -56,26 +56,18 @@ __device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
   return r != 0;
 }
 
-// A row's partials joined: maximum, sums, and a lane's columns of O, four to a vector. A partial
-// whose maximum is +inf (its scores were NaN) makes all of them NaN.
-template <int NV>
+// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
+// maximum is +inf (its scores were NaN) makes all of them NaN.
 struct RowJoin {
   float m = -INFINITY, s = 0.f, l = 0.f;
-  float4 o[NV];
-  __device__ __forceinline__ RowJoin() {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4* o2) {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
     if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
     const float mn = fmaxf(m, m2);
     const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
     s = s * fa + s2 * fb;
     l = l * fa + l2 * fb;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      o[j] = make_float4(o[j].x * fa + o2[j].x * fb, o[j].y * fa + o2[j].y * fb, o[j].z * fa + o2[j].z * fb,
-                         o[j].w * fa + o2[j].w * fb);
+    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
     m = mn;
   }
 };

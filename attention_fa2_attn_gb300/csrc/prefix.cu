@@ -1475,7 +1475,24 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
       count[k] = 0;
   }
   const int n = count[0] + count[1];
-  RowJoin<NV> acc;
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float4 acc[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A partial whose maximum is +inf (its scores were NaN) makes all of them NaN; one of -inf
+  // had no key that the row sees.
+  auto add = [&](float m2, float s2, float l2, const float4* o2) {
+    if (m2 == -INFINITY) return;
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      acc[j] = make_float4(acc[j].x * fa + o2[j].x * fb, acc[j].y * fa + o2[j].y * fb, acc[j].z * fa + o2[j].z * fb,
+                           acc[j].w * fa + o2[j].w * fb);
+    m = mn;
+  };
   for (int i0 = sub; i0 < n; i0 += WPR * IN) {
     float4 ml[IN], v[IN][NV];
 #pragma unroll
@@ -1492,15 +1509,15 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
       }
     }
 #pragma unroll
-    for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
+    for (int k = 0; k < IN; ++k) add(ml[k].x, ml[k].y, ml[k].z, v[k]);
   }
   if constexpr (WPR > 1) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) red[warp][j][lane] = acc.o[j];
+    for (int j = 0; j < NV; ++j) red[warp][j][lane] = acc[j];
     if (col == 0) {
-      red_ml[warp][0][my] = acc.m;
-      red_ml[warp][1][my] = acc.s;
-      red_ml[warp][2][my] = acc.l;
+      red_ml[warp][0][my] = m;
+      red_ml[warp][1][my] = s;
+      red_ml[warp][2][my] = l;
     }
     __syncthreads();
     if (sub == 0)
@@ -1508,16 +1525,16 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PxJoin p) {
         float4 v[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) v[j] = red[k][j][lane];
-        acc.add(red_ml[k][0][my], red_ml[k][1][my], red_ml[k][2][my], v);
+        add(red_ml[k][0][my], red_ml[k][1][my], red_ml[k][2][my], v);
       }
   }
   if (todo && sub == 0) {
-    const float inv = acc.s == 0.f ? 0.f : 1.f / acc.s;
+    const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       *reinterpret_cast<uint2*>(p.o + row * D + 32 * j + col) =
-          make_uint2(pack_bf16x2(acc.o[j].x * inv, acc.o[j].y * inv), pack_bf16x2(acc.o[j].z * inv, acc.o[j].w * inv));
-    if (p.lse && col == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * kLn2;
+          make_uint2(pack_bf16x2(acc[j].x * inv, acc[j].y * inv), pack_bf16x2(acc[j].z * inv, acc[j].w * inv));
+    if (p.lse && col == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 

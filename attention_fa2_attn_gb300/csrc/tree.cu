@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(384, 1)
       bool all = true;
       for (int c = 0; c < p.C; ++c) all &= ld_cluster_int(in_cta(&bars->finished, c)) != 0;
       for (int row = rank * per + warp * PER + my; all && row < last; row += 8 * PER) {
-        RowJoin<1> acc;
+        RowJoin acc;
         for (int c0 = 0; c0 < p.C; c0 += 4) {  // four CTAs' loads in flight
           float4 ml[4], o[4];
 #pragma unroll
@@ -977,12 +977,12 @@ __global__ void __launch_bounds__(384, 1)
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (c0 + c < p.C) acc.add(ml[c].x, ml[c].y, ml[c].z, &o[c]);
+            if (c0 + c < p.C) acc.add(ml[c].x, ml[c].y, ml[c].z, o[c]);
         }
         const float inv = acc.s == 0.f ? 0.f : 1.f / acc.s;
         const size_t out = (static_cast<size_t>(w.b) * p.Hkv + w.kvh) * p.R + w.u * C::QT * kTrTile + row;
         *reinterpret_cast<uint2*>(p.o + out * D + col) =
-            make_uint2(pack_bf16x2(acc.o[0].x * inv, acc.o[0].y * inv), pack_bf16x2(acc.o[0].z * inv, acc.o[0].w * inv));
+            make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
         if (p.lse && col == 0) p.lse[out] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * kLn2;
       }
       cluster_sync();  // nobody leaves while others read its shared memory
@@ -1094,16 +1094,16 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       ml = part_ml[row_at];
       v = *reinterpret_cast<const float4*>(part + row_at * D + col);
     };
-    auto put = [&](const RowJoin<1>& r, int row) {
+    auto put = [&](const RowJoin& r, int row) {
       const float inv = r.s == 0.f ? 0.f : 1.f / r.s;
       const size_t out = static_cast<size_t>(un.row0) + row;
       *reinterpret_cast<uint2*>(o + out * D + col) =
-          make_uint2(pack_bf16x2(r.o[0].x * inv, r.o[0].y * inv), pack_bf16x2(r.o[0].z * inv, r.o[0].w * inv));
+          make_uint2(pack_bf16x2(r.o.x * inv, r.o.y * inv), pack_bf16x2(r.o.z * inv, r.o.w * inv));
       if (lse && col == 0) lse[out] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * kLn2;
     };
     if (un.parts <= kTrFewParts) {
       const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
-      RowJoin<1> acc[2];
+      RowJoin acc[2];
       float4 ml[kTrFewParts][2], v[kTrFewParts][2];
 #pragma unroll
       for (int k = 0; k < kTrFewParts; ++k)
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
 #pragma unroll
       for (int k = 0; k < kTrFewParts; ++k)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, &v[k][r]);
+        for (int r = 0; r < 2; ++r) acc[r].add(ml[k][r].x, ml[k][r].y, ml[k][r].z, v[k][r]);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
         if (row0 + r * PER < un.rows) put(acc[r], row0 + r * PER);
@@ -1123,7 +1123,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       constexpr int IN = 4;
       const int sub = warp & (wpr - 1);
       const int row = (item - un.first_item) * many_step + warp / wpr * PER + my;
-      RowJoin<1> acc;
+      RowJoin acc;
       for (int i0 = sub; i0 < un.parts; i0 += wpr * IN) {
         float4 ml[IN], v[IN];
 #pragma unroll
@@ -1132,10 +1132,10 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
           if (i0 + wpr * k < un.parts && row < un.rows) get(ml[k], v[k], at(i0 + wpr * k) + row);
         }
 #pragma unroll
-        for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, &v[k]);
+        for (int k = 0; k < IN; ++k) acc.add(ml[k].x, ml[k].y, ml[k].z, v[k]);
       }
       if (wpr > 1) {  // block-uniform
-        red[warp][lane] = acc.o[0];
+        red[warp][lane] = acc.o;
         if (col == 0) {
           red_m[warp][my] = acc.m;
           red_s[warp][my] = acc.s;
@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
         }
         __syncthreads();
         if (sub == 0)
-          for (int k = warp + 1; k < warp + wpr; ++k) acc.add(red_m[k][my], red_s[k][my], red_l[k][my], &red[k][lane]);
+          for (int k = warp + 1; k < warp + wpr; ++k) acc.add(red_m[k][my], red_s[k][my], red_l[k][my], red[k][lane]);
         __syncthreads();
       }
       if (sub == 0 && row < un.rows) put(acc, row);
