@@ -1,5 +1,6 @@
-// join.cuh -- what the kernels share that cut a row's keys over several CTAs and join the
-// partial results.
+// join.cuh -- waits, votes and stores of the kernels that cut a row's keys over several CTAs. (How
+// they join the partial results differs: tree.cu takes a lane's columns as one vector, prefix.cu as
+// several. One text for both gave prefix attention other last bits and no time.)
 #pragma once
 
 #include "common.cuh"
@@ -55,21 +56,5 @@ __device__ __forceinline__ bool vote_all(int id, int nthreads, bool ok) {
       : "memory");
   return r != 0;
 }
-
-// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
-// maximum is +inf (its scores were NaN) makes all of them NaN.
-struct RowJoin {
-  float m = -INFINITY, s = 0.f, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
-  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
-    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
-    const float mn = fmaxf(m, m2);
-    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
-    s = s * fa + s2 * fb;
-    l = l * fa + l2 * fb;
-    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
-    m = mn;
-  }
-};
 
 }  // namespace fa

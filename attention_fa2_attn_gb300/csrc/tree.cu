@@ -283,6 +283,22 @@ __device__ __forceinline__ uint32_t tr_bits(const int* row, int words, int n, in
   return left < 32 ? v & ((1u << left) - 1u) : v;
 }
 
+// A row's partials joined: maximum, sums, and a lane's four columns of O. A partial whose
+// maximum is +inf (its scores were NaN) makes all of them NaN.
+struct TrRow {
+  float m = -INFINITY, s = 0.f, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);  // a lane's four columns
+  __device__ __forceinline__ void add(float m2, float s2, float l2, const float4& o2) {
+    if (m2 == -INFINITY) return;  // a share without a key that this row sees: its O was not written
+    const float mn = fmaxf(m, m2);
+    const float fa = ex2_approx(m - mn), fb = ex2_approx(m2 - mn);
+    s = s * fa + s2 * fb;
+    l = l * fa + l2 * fb;
+    o = make_float4(o.x * fa + o2.x * fb, o.y * fa + o2.y * fb, o.z * fa + o2.z * fb, o.w * fa + o2.w * fb);
+    m = mn;
+  }
+};
+
 template <int D, bool WIDE, bool CL>
 __global__ void __launch_bounds__(384, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -966,7 +982,7 @@ __global__ void __launch_bounds__(384, 1)
       bool all = true;
       for (int c = 0; c < p.C; ++c) all &= ld_cluster_int(in_cta(&bars->finished, c)) != 0;
       for (int row = rank * per + warp * PER + my; all && row < last; row += 8 * PER) {
-        RowJoin acc;
+        TrRow acc;
         for (int c0 = 0; c0 < p.C; c0 += 4) {  // four CTAs' loads in flight
           float4 ml[4], o[4];
 #pragma unroll
@@ -1094,7 +1110,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       ml = part_ml[row_at];
       v = *reinterpret_cast<const float4*>(part + row_at * D + col);
     };
-    auto put = [&](const RowJoin& r, int row) {
+    auto put = [&](const TrRow& r, int row) {
       const float inv = r.s == 0.f ? 0.f : 1.f / r.s;
       const size_t out = static_cast<size_t>(un.row0) + row;
       *reinterpret_cast<uint2*>(o + out * D + col) =
@@ -1103,7 +1119,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
     };
     if (un.parts <= kTrFewParts) {
       const int row0 = (item - un.first_item) * few_rows + warp * 2 * PER + my;
-      RowJoin acc[2];
+      TrRow acc[2];
       float4 ml[kTrFewParts][2], v[kTrFewParts][2];
 #pragma unroll
       for (int k = 0; k < kTrFewParts; ++k)
@@ -1123,7 +1139,7 @@ __global__ void __launch_bounds__(256, kTrMergeBlocks) tree_merge_kernel(const f
       constexpr int IN = 4;
       const int sub = warp & (wpr - 1);
       const int row = (item - un.first_item) * many_step + warp / wpr * PER + my;
-      RowJoin acc;
+      TrRow acc;
       for (int i0 = sub; i0 < un.parts; i0 += wpr * IN) {
         float4 ml[IN], v[IN];
 #pragma unroll
