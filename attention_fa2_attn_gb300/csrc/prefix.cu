@@ -33,12 +33,15 @@
 //     that is busy, and a spilled value waits in a busy L1. So few unrolled
 //     copies, one loop to a kind of segment, and no spills at 208 and 88 registers.
 // Measured, both kernels in a graph, d = 128 but where it says 64: 8 sequences of 2000 + 1..200
-// keys, 32 over 8 heads, 12.5 us (the launches, the lengths' scan and the first keys are 5);
-// 64 of 16384 + 9..1024, 64 over 8 heads, 59.4 us, 205 MB read once, where the paged decode
-// reads 549 us' worth; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 33.8 us
-// (64); 32 of 1000 + up to 8192, 16 heads, 167 us, 6.6 TB/s (232). Prefix steps are bound by
-// a step's S, softmax and PV behind one another (1.6 us for 256 rows and 128 keys, two steps
-// under way), own keys by HBM where they are long and by the units' ends where they are short.
+// keys, 32 over 8 heads, 12.6 us (the launches, the lengths' scan and the first keys are 5);
+// 64 of 16384 + 9..1024, 64 over 8 heads, 59.4 us, for 205 MB of keys (231 to 255 MB from DRAM: two
+// units of 256 rows go over the prefix, on CTAs that are not at the same keys), where the paged
+// decode takes 548; 48 in 6 groups of 4000 + 4..1500, T = 4, 64 over 4 heads, d = 64, 34.0 us (63.6);
+// 32 of 1000 + up to 8192, 16 heads, 167.6 us, 6.6 TB/s (233). Prompts are bound by the tensor cores
+// and their softmax alone, and fa_decode_paged is faster: 8 of 512 positions behind 8192 keys, 64 over
+// 8 heads, 920 us (725), at d = 64 730 (600). Prefix steps are bound by a step's S, softmax and PV
+// behind one another (1.6 us for 256 rows and 128 keys, two steps under way), own keys by HBM where
+// they are long and by the units' ends where they are short.
 // Tried and taken back: two slim units at a time, four warps on each (62 and 167 us); a slim unit's
 // Q with its first keys, and the next segment's table entries fetched ahead (58.9 and 168.8).
 // P is rounded to bf16 for the tensor cores (by at most 2^-8 of a weight; fp32 would take twice
@@ -339,7 +342,9 @@ struct PxTake {
 // keys and a tile 0.75 us, of which the tensor cores had little. So warp-level MMAs, as in the
 // decode kernel: a warp takes 16 keys of every tile with a running maximum, sum and O of its
 // own, and no warp waits for another until the unit's end, where the eight are joined through
-// shared memory, eight rows at a time. Returns what all eight warps voted.
+// shared memory, eight rows at a time. The maximum is the keys' own, never a stale one, so that a
+// warp's largest weight is 1, which bf16 holds: px_rows' correction of it has nothing to do here.
+// Returns what all eight warps voted.
 template <int D>
 __device__ __forceinline__ bool px_slim(const PxParams& p, const volatile PxSeg* w, PxBars* bars, uint8_t* sQ, uint8_t* sK,
                                         uint8_t* sV, float* ex, uint32_t seg_i, uint32_t& gkv, uint64_t tmo) {
@@ -1711,8 +1716,8 @@ fa_status fa_prefix_decode_paged(const void* q, const void* k_pages, const void*
   p.c = scale * kLog2e;
   // In eighths of a wide step (some 0.2 us); narrow and slim steps are two tiles of keys, which
   // at d = 128 wait for HBM. What a unit costs beside its steps: Q and the first S, a slim one's
-  // join, the partials of 128 or 256 rows. (Swept over batches from 13 to 170 us, 51 of
-  // them of drawn sizes: 2.5 % on average from the best for each, 8 % at most.)
+  // join, the partials of 128 or 256 rows. Swept one or two at a time over batches from 10 to 170 us:
+  // on 84 drawn ones 0.8 % on average from the best of 20 to 30 others for each, 8 % at most.
   p.cost = d == 128 ? PxCost{9, 16, 8, 20, 10, 9} : PxCost{9, 16, 8, 20, 8, 15};
   if (s.R <= kPxSlim) {
     p.cost.own_step = d == 128 ? 7 : 6;
