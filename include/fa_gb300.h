@@ -590,8 +590,8 @@ FA_API size_t fa_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int max_pag
  *   every sequence is read by itself, so that the result is the same. prefix_lens [groups] int32 (device): any value,
  *   0 and less for none. 1 <= groups <= FA_PREFIX_MAX_GROUPS.
  *   q, pools, block_table, seqlens, o, lse (may be NULL), scale, causal: as fa_decode_paged, and the same result, for
- *   any Hq / Hkv and T (it is for decodes and drafts: prompts of hundreds of positions take fa_decode_paged four fifths
- *   of the time). d in {64, 128}, page_size == 16. FA_ERR_UNSUPPORTED past these sizes: B * Hq * T + 256 * SM count
+ *   any Hq / Hkv and T. (It is for decodes and drafts: prompts of hundreds of positions take fa_decode_paged four fifths
+ *   of the time, where it takes their heads.) d in {64, 128}, page_size == 16. FA_ERR_UNSUPPORTED past these sizes: B * Hq * T + 256 * SM count
  *   < 2^30, and B * ceil(Hq / Hkv * T / 128) * (Hkv / V) * ceil(max_pages / 8) <= 38347922, whatever the lengths are,
  *   where V is the largest divisor of Hkv up to 16 that leaves no more than a 24th of the SMs over.
  *   workspace: at least fa_prefix_workspace_bytes(B, Hq, Hkv, T, max_pages, d, SM count) bytes, 256-byte aligned; its
