@@ -316,10 +316,10 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   const int most = (heads + kRopeWarps - 1) / kRopeWarps;
   while (cuts < most && blocks * cuts < 2 * sms) cuts = cuts * 2 < most ? cuts * 2 : most;
   int rows = ((heads + cuts - 1) / cuts + kRopeWarps - 1) / kRopeWarps;
-  // 33 to 40 heads: two cuts of three rows, four blocks an SM, or one of five (rows from the last
-  // heads on are empty), three. One is better where its blocks fit the GPU at once and two cuts' do
-  // not, or where three rounds of its blocks and more leave a small part of the last one empty. Two
-  // cuts / one, us, d = 128, by heads and tokens (blocks of one cut an SM):
+  // 33 to 40 heads: two cuts of three rows, four blocks an SM, or one of five (rows behind the last
+  // head are empty), three. One is better where its blocks fit the GPU at once and two cuts' do not,
+  // and from three rounds of its blocks on, where a last round in part weighs little. Two cuts / one,
+  // us, d = 128, by heads and tokens (blocks of one cut an SM):
   //   bf16  1216 (2)   1500 (2.5)  2048 (3.4)  4096 (6.7)   6000 (9.9)   16384 (27)
   //     33  6.2 / 6.4  7.6 / 6.8   8.8 / 9.9   15.7 / 15.3  21.1 / 20.2  51.1 / 46.6
   //     36  6.2 / 6.6  7.8 / 7.2   9.2 / 10.4  16.2 / 16.2  21.7 / 21.1  53.2 / 49.4
@@ -328,7 +328,7 @@ static int launch_rope(RopeParams& p, bool interleaved, cudaStream_t stream) {
   //     33  7.6 / 7.0  9.2 / 10.0  14.1 / 13.9 19.1 / 18.5  47.0 / 43.3
   //     40  8.4 / 8.1  10.1 / 11.2 15.3 / 15.6 21.1 / 21.3  52.1 / 51.5
   // Backward, interleaved pairs, several axes and appends go the same way. From 65 heads on one cut less
-  // in three gains 2 % at most and loses as much.
+  // of three or more gains 2 % at most in large calls and loses up to 9 % in smaller ones.
   const bool pays = (blocks > 2 * sms && blocks <= 3 * sms) || blocks >= 9 * sms;
   if (w == V && cuts == 2 && heads > 4 * kRopeWarps && heads <= 5 * kRopeWarps && pays) rows = 5;
   p.head_chunk = rows * kRopeWarps;
